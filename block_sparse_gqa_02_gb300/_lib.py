@@ -38,6 +38,24 @@ class MsaShape(ctypes.Structure):
         return "MsaShape(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
 
 
+class MsaRope(ctypes.Structure):
+    """Mirror of ``msa_rope_desc``."""
+    _fields_ = [("batch", _i32), ("seq", _i32), ("dtype", _i32), ("pos_offset", _i32),
+                ("interleaved", _i32), ("inverse", _i32), ("scale", ctypes.c_float)]
+
+
+class MsaRopeTensor(ctypes.Structure):
+    """Mirror of ``msa_rope_tensor``."""
+    _fields_ = [("x", _vp), ("y", _vp), ("freqs", _vp), ("n_heads", _i32), ("head_dim", _i32),
+                ("rotary_dim", _i32), ("head_major", _i32)]
+
+
+class MsaGatherTensor(ctypes.Structure):
+    """Mirror of ``msa_gather_tensor``."""
+    _fields_ = [("src", _vp), ("dst", _vp), ("src_rows", ctypes.c_int64),
+                ("dst_rows", ctypes.c_int64), ("n_heads", _i32), ("row_bytes", _i32)]
+
+
 _SHAPE_P = ctypes.POINTER(MsaShape)
 SIGNATURES = {
     "msa_index_scores": (_i32, [_SHAPE_P, _vp, _vp, _vp, _vp]),
@@ -55,6 +73,17 @@ SIGNATURES = {
     "msa_block_topk_ragged": (_i32, [_SHAPE_P, _vp, _vp, _vp, _vp]),
     "msa_sparse_decode_paged": (_i32, [_SHAPE_P, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
                                        _vp, _sz, _vp]),
+    "msa_rope": (_i32, [ctypes.POINTER(MsaRope), ctypes.POINTER(MsaRopeTensor), _i32, _vp, _vp]),
+    "msa_cache_pack": (_i32, [_SHAPE_P, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp]),
+    "msa_cache_unpack": (_i32, [_SHAPE_P, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp]),
+    "msa_sparse_decode_packed": (_i32, [_SHAPE_P, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
+                                        _vp]),
+    "msa_sparse_decode_mass": (_i32, [_SHAPE_P, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
+                                      _vp, _vp, _sz, _vp]),
+    "msa_cache_evict": (_i32, [_SHAPE_P, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                               _vp]),
+    "msa_cache_gather": (_i32, [_i32, ctypes.POINTER(MsaGatherTensor), _i32, _vp, _i32, _i32,
+                                _vp]),
     "msa_workspace_bytes": (_sz, [_SHAPE_P, ctypes.c_int]),
     "msa_get_device_status": (_i32, [_vp]),
     "msa_status_string": (ctypes.c_char_p, [_i32]),
@@ -245,6 +274,195 @@ def msa_sparse_decode_paged(shape: MsaShape, seq_lens, block_table, n_phys, q, k
                                           int(n_phys), _ptr(q), _ptr(k_pool), _ptr(v_pool),
                                           _ptr(sel), _ptr(out), _ptr(lse), _ptr(workspace),
                                           ws_bytes, _stream(stream)), "msa_sparse_decode_paged")
+
+
+# ----------------------------- rotary positions, the 4-bit cache, eviction by weight
+
+def _arg(x, name, dtype=None, numel=None):
+    """Device pointer of a tensor that must be contiguous, of `dtype` and (at least) `numel`
+    elements, and on the current CUDA device (the one the kernels run on); of an int (a raw
+    pointer) or None as they are."""
+    if x is None or isinstance(x, int):
+        return x
+    import torch
+    if not x.is_cuda or x.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {x.device}, not on the current CUDA device")
+    if dtype is not None and x.dtype is not _torch_dtype(dtype):
+        raise ValueError(f"{name} is {x.dtype}, expected {_torch_dtype(dtype)}")
+    if numel is not None and x.numel() < numel:
+        raise ValueError(f"{name} has {x.numel()} elements, expected {numel}")
+    return _ptr(x)
+
+
+_TORCH_DTYPES = {}
+
+
+def _torch_dtype(code):
+    if not _TORCH_DTYPES:
+        import torch
+        _TORCH_DTYPES.update({MSA_F32: torch.float32, MSA_BF16: torch.bfloat16,
+                              "f32": torch.float32, "i32": torch.int32, "i64": torch.int64,
+                              "u8": torch.uint8})
+    return _TORCH_DTYPES[code]
+
+
+def make_rope(batch, seq, dtype="bf16", pos_offset=0, scale=0.0, interleaved=False,
+              inverse=False) -> MsaRope:
+    """The description of a msa_rope call (see include/msa.h; scale 0 means 1)."""
+    code = _DTYPE_CODES[dtype] if isinstance(dtype, str) else int(dtype)
+    return MsaRope(batch, seq, code, pos_offset, int(interleaved), int(inverse), scale)
+
+
+class RopeTensors:
+    """The tensors of a msa_rope call: rows (x, y, freqs, head_major) with x and y
+    [batch, seq, heads, d] (or [batch, seq, d], one head), or [batch, heads, seq, d] with
+    head_major; freqs int64 [rotary_dim / 2].  Holds the tensors, and may be kept and used for
+    every call on them."""
+
+    def __init__(self, rows):
+        rows = list(rows)
+        self.rows = rows
+        self.array = (MsaRopeTensor * max(1, len(rows)))()
+        self.sizes = []
+        for i, (x, y, freqs, head_major) in enumerate(rows):
+            heads = 1 if x.dim() == 3 else x.shape[1 if head_major else 2]
+            if x.dim() not in (3, 4) or y.shape != x.shape or y.dtype != x.dtype:
+                raise ValueError(f"rope tensor {i}: x and y need the same [batch, seq, (heads,) d] "
+                                 f"shape and type, got {tuple(x.shape)} and {tuple(y.shape)}")
+            self.array[i] = MsaRopeTensor(
+                _arg(x, f"x of rope tensor {i}"), _arg(y, f"y of rope tensor {i}"),
+                _arg(freqs, f"freqs of rope tensor {i}", "i64"), heads, x.shape[-1],
+                2 * freqs.numel(), int(bool(head_major)))
+            seq = x.shape[2] if head_major and x.dim() == 4 else x.shape[1]
+            self.sizes.append((x.shape[0], seq, x.dtype))
+
+    def __len__(self):
+        return len(self.rows)
+
+
+def make_rope_tensors(rows) -> RopeTensors:
+    return RopeTensors(rows)
+
+
+def msa_rope(desc: MsaRope, tensors: RopeTensors, positions=None, stream=None):
+    want = (desc.batch, desc.seq, _torch_dtype(desc.dtype))
+    for i, size in enumerate(tensors.sizes):
+        if size != want:
+            raise ValueError(f"rope tensor {i} has (batch, seq, dtype) {size}, the call {want}")
+    _check(load().msa_rope(ctypes.byref(desc), tensors.array, len(tensors),
+                           _arg(positions, "positions", "i32", desc.batch * desc.seq),
+                           _stream(stream)), "msa_rope")
+
+
+def _cache_args(shape, seq_lens, block_table, n_phys, cache):
+    return (_arg(seq_lens, "seq_lens", "i32", shape.batch),
+            _arg(block_table, "block_table", "i32", shape.batch * shape.n_blocks), int(n_phys),
+            _arg(cache, "cache", "u8", int(n_phys) * shape.n_heads_kv * 160 * shape.head_dim))
+
+
+def msa_cache_pack(shape: MsaShape, n_new, starts, seq_lens, block_table, n_phys, k, v, cache,
+                   stream=None):
+    sl, bt, n_phys, c = _cache_args(shape, seq_lens, block_table, n_phys, cache)
+    n = shape.batch * shape.n_heads_kv * int(n_new) * shape.head_dim
+    _check(load().msa_cache_pack(ctypes.byref(shape), int(n_new),
+                                 _arg(starts, "starts", "i32", shape.batch), sl, bt, n_phys,
+                                 _arg(k, "k", shape.dtype, n), _arg(v, "v", shape.dtype, n), c,
+                                 _stream(stream)), "msa_cache_pack")
+
+
+def msa_cache_unpack(shape: MsaShape, n_out, starts, seq_lens, block_table, n_phys, cache, k, v,
+                     stream=None):
+    sl, bt, n_phys, c = _cache_args(shape, seq_lens, block_table, n_phys, cache)
+    n = shape.batch * shape.n_heads_kv * int(n_out) * shape.head_dim
+    _check(load().msa_cache_unpack(ctypes.byref(shape), int(n_out),
+                                   _arg(starts, "starts", "i32", shape.batch), sl, bt, n_phys, c,
+                                   _arg(k, "k", shape.dtype, n), _arg(v, "v", shape.dtype, n),
+                                   _stream(stream)), "msa_cache_unpack")
+
+
+def _decode_args(shape, q, sel, out, lse, mass):
+    n = shape.batch * shape.n_heads_q * shape.head_dim
+    rows = shape.batch * shape.n_heads_kv
+    return (_arg(q, "q", shape.dtype, n), _arg(sel, "sel", "i32", rows * shape.top_k),
+            _arg(out, "out", shape.dtype, n),
+            _arg(lse, "lse", "f32", shape.batch * shape.n_heads_q),
+            _arg(mass, "mass", "f32", rows * shape.n_blocks))
+
+
+def msa_sparse_decode_packed(shape: MsaShape, seq_lens, block_table, n_phys, q, cache, sel, out,
+                             lse=None, mass=None, stream=None):
+    sl, bt, n_phys, c = _cache_args(shape, seq_lens, block_table, n_phys, cache)
+    q, sel, out, lse, mass = _decode_args(shape, q, sel, out, lse, mass)
+    _check(load().msa_sparse_decode_packed(ctypes.byref(shape), sl, bt, n_phys, q, c, sel, out,
+                                           lse, mass, _stream(stream)),
+           "msa_sparse_decode_packed")
+
+
+def msa_sparse_decode_mass(shape: MsaShape, seq_lens, block_table, n_phys, q, k, v, sel, out, lse,
+                           mass, workspace, ws_bytes=None, stream=None):
+    if ws_bytes is None:
+        ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    n = (int(n_phys) * shape.block_size if block_table is not None
+         else shape.batch * shape.seq_k) * shape.n_heads_kv * shape.head_dim
+    q, sel, out, lse, mass = _decode_args(shape, q, sel, out, lse, mass)
+    _check(load().msa_sparse_decode_mass(
+        ctypes.byref(shape), _arg(seq_lens, "seq_lens", "i32", shape.batch),
+        _arg(block_table, "block_table", "i32", shape.batch * shape.n_blocks), int(n_phys), q,
+        _arg(k, "k", shape.dtype, n), _arg(v, "v", shape.dtype, n), sel, out, lse, mass,
+        _arg(workspace, "workspace"), ws_bytes, _stream(stream)), "msa_sparse_decode_mass")
+
+
+def msa_cache_evict(shape: MsaShape, keep, n_first, n_recent, seq_lens, mass, block_table, kept,
+                    new_lens, mass_out, table_out=None, stream=None):
+    B, n = shape.batch, shape.batch * shape.n_blocks
+    _check(load().msa_cache_evict(
+        ctypes.byref(shape), int(keep), int(n_first), int(n_recent),
+        _arg(seq_lens, "seq_lens", "i32", B), _arg(mass, "mass", "f32", n * shape.n_heads_kv),
+        _arg(block_table, "block_table", "i32", n), _arg(kept, "kept", "i32", B * int(keep)),
+        _arg(new_lens, "new_lens", "i32", B),
+        _arg(mass_out, "mass_out", "f32", n * shape.n_heads_kv),
+        _arg(table_out, "table_out", "i32", n), _stream(stream)), "msa_cache_evict")
+
+
+class GatherTensors:
+    """The caches of a msa_cache_gather call: rows (src, dst), each [batch, heads, rows, ...]
+    or [batch, rows, d] (one head).  Holds the tensors, and may be kept and used for every call
+    on them."""
+
+    def __init__(self, rows):
+        rows = list(rows)
+        self.rows = rows
+        self.array = (MsaGatherTensor * max(1, len(rows)))()
+        self.batches = []
+        for i, (src, dst) in enumerate(rows):
+            lead = 1 if src.dim() == 3 else 2
+            if src.dim() not in (3, 4) or dst.dim() != src.dim() or dst.dtype != src.dtype or \
+                    dst.shape[:lead] != src.shape[:lead] or dst.shape[-1] != src.shape[-1]:
+                raise ValueError(f"gather tensor {i}: src and dst differ in more than their rows: "
+                                 f"{tuple(src.shape)} and {tuple(dst.shape)}")
+            self.array[i] = MsaGatherTensor(
+                _arg(src, f"src of gather tensor {i}"), _arg(dst, f"dst of gather tensor {i}"),
+                src.shape[lead], dst.shape[lead], 1 if lead == 1 else src.shape[1],
+                src.shape[-1] * src.element_size())
+            self.batches.append(src.shape[0])
+
+    def __len__(self):
+        return len(self.rows)
+
+
+def make_gather_tensors(rows) -> GatherTensors:
+    return GatherTensors(rows)
+
+
+def msa_cache_gather(batch, tensors: GatherTensors, kept, block_size=128, stream=None):
+    for i, n in enumerate(tensors.batches):
+        if n != batch:
+            raise ValueError(f"gather tensor {i} has batch {n}, the call {batch}")
+    if kept.dim() != 2 or kept.shape[0] != batch:
+        raise ValueError(f"kept is {tuple(kept.shape)}, expected [{batch}, keep]")
+    _check(load().msa_cache_gather(int(batch), tensors.array, len(tensors),
+                                   _arg(kept, "kept", "i32"), kept.shape[1], int(block_size),
+                                   _stream(stream)), "msa_cache_gather")
 
 
 def msa_workspace_bytes(shape: MsaShape, which: int) -> int:

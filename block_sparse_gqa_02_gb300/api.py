@@ -3,11 +3,17 @@ MSA stages (index block scores -> per-KV-head block top-k -> sparse attention) a
 library calls on the current stream, with no host synchronisation in between."""
 from __future__ import annotations
 
+import math
+from dataclasses import dataclass
+
 import torch
 
 from . import _lib
-from ._lib import (make_shape, msa_block_topk, msa_index_scores, msa_sparse_decode,
-                   msa_sparse_prefill, msa_workspace_bytes)
+from ._lib import (make_gather_tensors, make_rope, make_rope_tensors, make_shape, msa_block_topk,
+                   msa_block_topk_ragged, msa_cache_evict, msa_cache_gather, msa_cache_pack,
+                   msa_index_scores, msa_index_scores_paged, msa_rope, msa_sparse_decode,
+                   msa_sparse_decode_mass, msa_sparse_decode_packed, msa_sparse_prefill,
+                   msa_workspace_bytes)
 
 _DT = {torch.float32: "f32", torch.bfloat16: "bf16"}
 
@@ -45,33 +51,177 @@ def run_decode(shape, q, k_cache, v_cache, idx_q, idx_k, bufs, stream=None):
                       bufs["ws"], None, stream)
 
 
-def prefill(q, k, v, idx_q, idx_k, block_size=128, top_k=16, q_tile=64, sm_scale=0.0,
-            index_scale=0.0):
-    """MSA prefill.  q [B,T,Hq,d], k/v [B,Hkv,T,d], idx_q [B,T,Hkv,dI], idx_k [B,T,dI].
+@dataclass(frozen=True)
+class Rope:
+    """Rotary positions of a model: frequencies of the main heads (int64 [rotary_dim / 2],
+    turns per position in units of 2^-64 turns, see rope_freqs), of the index heads (None: the
+    same), the factor on the rotated dims, and the pairing of the dims."""
+    freqs: torch.Tensor
+    index_freqs: torch.Tensor | None = None
+    scale: float = 1.0
+    interleaved: bool = False
 
-    Returns a dict with out [B,T,Hq,d], lse [B,Hq,T], scores and sel."""
+
+def rope_freqs(rotary_dim, base=10000.0, scaling="none", factor=1.0, original_len=0,
+               ramp=(1.0, 32.0), device=None):
+    """Frequencies base^(-2 i / rotary_dim) radians per position as a table for msa_rope, and
+    the factor for the rotated dims: (int64 [rotary_dim / 2], scale).  For contexts `factor`
+    times the trained length: scaling "linear" divides the positions, "ntk" raises the base so
+    that the lowest frequency is divided by `factor`, "yarn" divides the frequencies that turn
+    less than ramp[0] times in original_len positions, keeps those that turn more than ramp[1]
+    times, ramps in between, and gives the scale 0.1 ln(factor) + 1."""
+    if rotary_dim < 16 or rotary_dim % 16:
+        raise ValueError(f"rotary_dim {rotary_dim} is not a multiple of 16")
+    if not (factor >= 1.0 and math.isfinite(factor)) or not (base > 1.0 and math.isfinite(base)):
+        raise ValueError("factor must be >= 1 and base > 1")
+    scale = 1.0
+    if scaling == "ntk":
+        base = base * factor ** (rotary_dim / (rotary_dim - 2))
+    i = torch.arange(0, rotary_dim, 2, dtype=torch.float64)
+    turns = base ** (-i / rotary_dim) / (2 * math.pi)
+    if scaling == "linear":
+        turns = turns / factor
+    elif scaling == "yarn":
+        if original_len < 1 or not 0 < ramp[0] < ramp[1]:
+            raise ValueError("yarn needs original_len >= 1 and an ascending ramp")
+        keep = ((turns * original_len - ramp[0]) / (ramp[1] - ramp[0])).clamp(0, 1)
+        turns = turns * keep + turns / factor * (1 - keep)
+        scale = 0.1 * math.log(factor) + 1.0
+    elif scaling not in ("none", "ntk"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return (turns * 2.0 ** 64).to(torch.int64).to(device), scale
+
+
+def rope(tensors, positions=None, pos_offset=0, scale=1.0, interleaved=False, inverse=False):
+    """Rotates tensors that share their positions in one launch: rows (x, freqs, head_major),
+    x [batch, seq, heads, d] or [batch, seq, d], or [batch, heads, seq, d] with head_major.
+    Returns new tensors; inverse=True is the gradient of the same call without it."""
+    rows = [(x, torch.empty_like(x), freqs, head_major) for x, freqs, head_major in tensors]
+    x, _, _, head_major = rows[0]
+    seq = x.shape[2] if head_major and x.dim() == 4 else x.shape[1]
+    msa_rope(make_rope(x.shape[0], seq, _DT[x.dtype], pos_offset, scale, interleaved, inverse),
+             make_rope_tensors(rows), positions)
+    return [y for _, y, _, _ in rows]
+
+
+def _rotate(rope_, q, k, idx_q, idx_k, pos_offset=0):
+    """The given tensors (None: left out) at positions pos_offset, pos_offset + 1, ..."""
+    index = rope_.freqs if rope_.index_freqs is None else rope_.index_freqs
+    rows = [(q, rope_.freqs, False), (k, rope_.freqs, True), (idx_q, index, False),
+            (idx_k, index, False)]
+    got = iter(rope([r for r in rows if r[0] is not None], None, pos_offset, rope_.scale,
+                    rope_.interleaved))
+    return [None if r[0] is None else next(got) for r in rows]
+
+
+def prefill(q, k, v, idx_q, idx_k, block_size=128, top_k=16, q_tile=64, sm_scale=0.0,
+            index_scale=0.0, rope=None):
+    """MSA prefill.  q [B,T,Hq,d], k/v [B,Hkv,T,d], idx_q [B,T,Hkv,dI], idx_k [B,T,dI].
+    With a Rope, q, k, idx_q and idx_k are rotated to positions 0 .. T-1 first (copies).
+
+    Returns a dict with out [B,T,Hq,d], lse [B,Hq,T], scores and sel, and with a Rope the
+    rotated keys for the caches (k, idx_k)."""
     shape = _shape_of(q, k, idx_q, block_size, top_k, q_tile, sm_scale, index_scale)
     bufs = alloc_prefill_outputs(shape, q.device, q.dtype)
+    if rope is not None:
+        q, k, idx_q, idx_k = _rotate(rope, q, k, idx_q, idx_k)
+        bufs.update(k=k, idx_k=idx_k)
     run_prefill(shape, q, k, v, idx_q, idx_k, bufs)
     return bufs
 
 
-def alloc_decode_outputs(shape, device, dtype):
+def alloc_decode_outputs(shape, device, dtype, mass=False):
+    """Outputs and workspace of a decode step (of msa_sparse_decode_mass with mass)."""
     bufs = alloc_prefill_outputs(shape, device, dtype)
-    nbytes = max(16, msa_workspace_bytes(shape, 1))
+    nbytes = max(16, msa_workspace_bytes(shape, 4 if mass else 1))
     bufs["ws"] = torch.empty((nbytes + 15) // 16 * 4, device=device, dtype=torch.float32)
     return bufs
 
 
 def decode(q, k_cache, v_cache, idx_q, idx_k, block_size=128, top_k=64, sm_scale=0.0,
-           index_scale=0.0):
+           index_scale=0.0, rope=None, mass=None):
     """One MSA decode step.  q [B,1,Hq,d], caches [B,Hkv,L,d], idx_q [B,1,Hkv,dI],
-    idx_k [B,L,dI]; the new token is at position L-1 and already in the caches."""
+    idx_k [B,L,dI]; the new token is at position L-1 and already in the caches.  With a Rope,
+    q and idx_q are rotated to that position (the caches hold rotated keys).  With mass
+    (float32 [B,Hkv,blocks]) the attention weight of every selected block is added to it."""
     shape = _shape_of(q, k_cache, idx_q, block_size, top_k, 1, sm_scale, index_scale)
-    bufs = alloc_decode_outputs(shape, q.device, q.dtype)
-    run_decode(shape, q, k_cache, v_cache, idx_q, idx_k, bufs)
+    bufs = alloc_decode_outputs(shape, q.device, q.dtype, mass is not None)
+    if rope is not None:
+        q, _, idx_q, _ = _rotate(rope, q, None, idx_q, None, shape.seq_k - 1)
+    if mass is None:
+        run_decode(shape, q, k_cache, v_cache, idx_q, idx_k, bufs)
+    else:
+        msa_index_scores(shape, idx_q, idx_k, bufs["scores"])
+        msa_block_topk(shape, bufs["scores"], bufs["sel"])
+        msa_sparse_decode_mass(shape, None, None, 0, q, k_cache, v_cache, bufs["sel"], bufs["out"],
+                               bufs["lse"], mass, bufs["ws"])
     return bufs
 
 
+def alloc_packed_cache(n_phys, n_heads_kv, head_dim, device="cuda"):
+    """A 4-bit cache of n_phys blocks of 128 keys (layout in include/msa.h)."""
+    return torch.zeros((n_phys, n_heads_kv, 160 * head_dim), dtype=torch.uint8, device=device)
+
+
+def decode_packed(q, k, v, cache, idx_q, idx_k_pool, seq_lens, block_table, capacity, top_k=64,
+                  sm_scale=0.0, index_scale=0.0, rope=None, mass=None):
+    """One MSA decode step over a paged cache whose K and V are held in 4 bits.  q [B,1,Hq,d];
+    k, v [B,Hkv,1,d]: the new token's rows, packed into the cache at position seq_lens - 1;
+    cache from alloc_packed_cache; idx_q [B,1,Hkv,128]; idx_k_pool [P,128,128] 16-bit index keys
+    (rotated, the new token's among them); seq_lens int32 [B] (the new token counted);
+    block_table int32 [B, ceil(capacity / 128)].  With a Rope, q, k and idx_q are rotated to
+    position seq_lens - 1 first.  With mass, the blocks' attention weights are added to it."""
+    B, _, Hq, d = q.shape
+    Hkv, n_phys = cache.shape[1], cache.shape[0]
+    shape = make_shape(B, 1, capacity, Hq, Hkv, d, idx_q.shape[-1], 128, top_k, 1, _DT[q.dtype],
+                       sm_scale, index_scale)
+    bufs = alloc_prefill_outputs(shape, q.device, q.dtype)
+    if rope is not None:
+        index = rope.freqs if rope.index_freqs is None else rope.index_freqs
+        rows = [(x, torch.empty_like(x), f, h)
+                for x, f, h in ((q, rope.freqs, False), (k, rope.freqs, True), (idx_q, index, False))]
+        msa_rope(make_rope(B, 1, _DT[q.dtype], -1, rope.scale, rope.interleaved),
+                 make_rope_tensors(rows), seq_lens)
+        q, k, idx_q = (y for _, y, _, _ in rows)
+    msa_cache_pack(shape, 1, None, seq_lens, block_table, n_phys, k, v, cache)
+    msa_index_scores_paged(shape, seq_lens, block_table, n_phys, idx_q, idx_k_pool, bufs["scores"])
+    msa_block_topk_ragged(shape, seq_lens, bufs["scores"], bufs["sel"])
+    msa_sparse_decode_packed(shape, seq_lens, block_table, n_phys, q, cache, bufs["sel"],
+                             bufs["out"], bufs["lse"], mass)
+    return bufs
+
+
+def evict_paged(seq_lens, mass, block_table, capacity, keep, n_first=1, n_recent=2, block_size=128):
+    """Cuts every sequence of a paged cache to at most `keep` blocks, in place: seq_lens, mass
+    [B,Hkv,blocks] and block_table are updated (the dropped physical blocks follow the kept
+    ones in the table).  Returns kept int32 [B, keep], the old indices of what stays."""
+    B, Hkv, _ = mass.shape
+    shape = make_shape(B, 1, capacity, Hkv, Hkv, 128, 128, block_size, 1, 1)
+    kept = torch.empty((B, keep), dtype=torch.int32, device=mass.device)
+    msa_cache_evict(shape, keep, n_first, n_recent, seq_lens, mass, block_table, kept, seq_lens,
+                    mass, block_table)
+    return kept
+
+
+def evict(k_cache, v_cache, idx_k, mass, keep, n_first=1, n_recent=2, block_size=128):
+    """Cuts contiguous caches (k, v [B,Hkv,L,d], idx_k [B,L,dI]) to at most `keep` blocks.
+    Returns a dict with the shorter caches k, v, idx_k, their mass, and kept int32 [B, keep]."""
+    B, Hkv, L, d = k_cache.shape
+    shape = make_shape(B, 1, L, Hkv, Hkv, d, 128, block_size, 1, 1)
+    n = shape.n_blocks
+    rows = L - (n - min(n, keep)) * block_size
+    new = lambda x: torch.empty((*x.shape[:-2], rows, x.shape[-1]), dtype=x.dtype, device=x.device)  # noqa: E731
+    kept = torch.empty((B, keep), dtype=torch.int32, device=mass.device)
+    lens = torch.empty((B,), dtype=torch.int32, device=mass.device)
+    out = torch.empty_like(mass)
+    msa_cache_evict(shape, keep, n_first, n_recent, None, mass, None, kept, lens, out)
+    pairs = [(x, new(x)) for x in (k_cache, v_cache, idx_k)]
+    msa_cache_gather(B, make_gather_tensors(pairs), kept, block_size)
+    blocks = -(-rows // block_size)
+    return dict(k=pairs[0][1], v=pairs[1][1], idx_k=pairs[2][1],
+                mass=out[:, :, :blocks].contiguous(), kept=kept)
+
+
 __all__ = ["prefill", "decode", "run_prefill", "run_decode", "alloc_prefill_outputs",
-           "alloc_decode_outputs", "_lib"]
+           "alloc_decode_outputs", "Rope", "rope", "rope_freqs", "alloc_packed_cache",
+           "decode_packed", "evict", "evict_paged", "_lib"]

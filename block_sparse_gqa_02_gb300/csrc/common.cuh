@@ -6,6 +6,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "msa.h"
+
 namespace msa {
 
 // Shape after validation, with the derived sizes every kernel needs.
@@ -139,6 +141,34 @@ size_t index_kl_workspace_bytes(const Dims& p);
 // the scratch it needs (partial outputs and partial log-sum-exps, fp32).
 int decode_num_splits(const Dims& p);
 size_t decode_workspace_bytes(const Dims& p);
+
+// Rotary positions of up to MSA_ROPE_MAX_TENSORS tensors in one launch (rope.cu).
+cudaError_t launch_rope(const msa_rope_desc& desc, const msa_rope_tensor* tensors, int n,
+                        const int32_t* positions, cudaStream_t st);
+
+// The 4-bit KV cache (packed_cache.cu, packed_decode.cu); p.block_table may be null.
+cudaError_t launch_cache_pack(const Dims& p, int n, const int32_t* starts, const void* k,
+                              const void* v, void* cache, cudaStream_t st);
+cudaError_t launch_cache_unpack(const Dims& p, int n, const int32_t* starts, const void* cache,
+                                void* k, void* v, cudaStream_t st);
+cudaError_t launch_sparse_decode_packed(const Dims& p, const void* q, const void* cache,
+                                        const int32_t* sel, void* out, float* lse, float* mass,
+                                        cudaStream_t st);
+// Selected blocks per row that decode can accumulate weights for over the 4-bit cache.
+constexpr int kMaxPackedMassBlocks = 1024;
+
+// Decode with accumulated attention weights, and eviction by them (decode_mass.cu,
+// cache_evict.cu).
+cudaError_t launch_sparse_decode_mass(const Dims& p, const void* q, const void* k, const void* v,
+                                      const int32_t* sel, void* out, float* lse, float* mass,
+                                      float* ws, cudaStream_t st, int* dev_status);
+size_t decode_mass_workspace_bytes(const Dims& p);
+cudaError_t launch_cache_evict(const Dims& p, int keep, int n_first, int n_recent,
+                               const float* mass, const int32_t* table, int32_t* kept,
+                               int32_t* new_lens, float* mass_out, int32_t* table_out,
+                               cudaStream_t st);
+cudaError_t launch_cache_gather(int batch, const msa_gather_tensor* tensors, int n,
+                                const int32_t* kept, int keep, int block, cudaStream_t st);
 
 // Largest candidate count the top-k kernel keeps in shared memory.
 constexpr int kMaxBlocks = 32768;

@@ -1,0 +1,112 @@
+// The attention weight that every selected block of a decode step receives, added up per KV
+// head: mass[b, g, blk] += sum over the group's heads h and the block's keys j of
+// exp(z_hj - lse_h), from the step's log-sum-exps.
+//
+// CTA = one selection entry of one (sequence, KV head): its keys' logits are formed in fp32
+// from K in shared memory, a thread per key, and the block's weight is one atomic addition, the
+// only one to its address in a call, so results repeat bit for bit.
+#include "common.cuh"
+
+namespace msa {
+
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kKeys = 128;             // keys of a pass, one thread each
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads)
+mass_kernel(const T* __restrict__ q, const T* __restrict__ k, const int32_t* __restrict__ sel,
+            const float* __restrict__ lse, float* __restrict__ mass, Dims p) {
+  constexpr int kRow = D + 4;                              // floats of a staged key
+  extern __shared__ float smem[];
+  float* ks = smem;                                        // [kKeys][kRow]
+  float* qs = smem + kKeys * kRow;                         // [G][D]
+  float* ls = qs + p.G * D;                                // [G] lse in log2 units
+  __shared__ float part[kThreads / 32];
+  const int bg = blockIdx.y, b = bg / p.Hkv, g = bg % p.Hkv;
+  const int L = seq_len_of(p, b), nB_b = (L + p.Bk - 1) / p.Bk;
+  const int blk = sel[(size_t)bg * p.k + blockIdx.x];
+  if (blk < 0 || blk >= nB_b) return;
+  const T* kb;
+  if (p.block_table) {
+    const int phys = p.block_table[(size_t)b * p.nB + blk];
+    // the paged attention reads zeros there; an entry that is no block gets no weight
+    if (phys < 0 || phys >= p.n_phys) return;
+    kb = k + ((size_t)phys * p.Hkv + g) * p.Bk * D;
+  } else {
+    kb = k + ((size_t)bg * p.Sk + (size_t)blk * p.Bk) * D;
+  }
+  const int seen = min(p.Bk, L - blk * p.Bk);
+  for (int e = threadIdx.x; e < p.G * D; e += kThreads)
+    qs[e] = to_f32(q[((size_t)b * p.Hq + g * p.G) * D + e]) * (p.sm_scale * kLog2e);
+  for (int h = threadIdx.x; h < p.G; h += kThreads)
+    ls[h] = lse[(size_t)b * p.Hq + g * p.G + h] * kLog2e;
+  float sum = 0.f;
+  for (int j0 = 0; j0 < seen; j0 += kKeys) {
+    const int n = min(kKeys, seen - j0);
+    __syncthreads();
+    for (int e = threadIdx.x * Vec16<T>::N; e < n * D; e += kThreads * Vec16<T>::N)
+      Vec16<T>::load(kb + (size_t)j0 * D + e, ks + e / D * kRow + e % D);
+    __syncthreads();
+    const int j = threadIdx.x;
+    if (j < n)
+      for (int h = 0; h < p.G; ++h) {
+        float dot = 0.f;
+#pragma unroll 8
+        for (int d0 = 0; d0 < D; d0 += 4) {
+          const float4 kx = *reinterpret_cast<const float4*>(ks + j * kRow + d0);
+          const float4 qx = *reinterpret_cast<const float4*>(qs + h * D + d0);
+          dot = fmaf(qx.x, kx.x, dot);
+          dot = fmaf(qx.y, kx.y, dot);
+          dot = fmaf(qx.z, kx.z, dot);
+          dot = fmaf(qx.w, kx.w, dot);
+        }
+        if (ls[h] != -INFINITY) sum += exp2f(dot - ls[h]);
+      }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kThreads / 32; ++w) sum += part[w];
+    atomicAdd(mass + (size_t)bg * p.nB + blk, sum);
+  }
+}
+
+template <typename T, int D>
+cudaError_t run_mass(const Dims& p, const void* q, const void* k, const int32_t* sel,
+                     const float* lse, float* mass, cudaStream_t st) {
+  auto kern = mass_kernel<T, D>;
+  const size_t smem = sizeof(float) * (kKeys * (D + 4) + (size_t)p.G * (D + 1));
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)smem);
+  if (e != cudaSuccess) return e;
+  kern<<<dim3(p.k, p.B * p.Hkv), kThreads, smem, st>>>((const T*)q, (const T*)k, sel, lse, mass,
+                                                       p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t decode_mass_workspace_bytes(const Dims& p) {
+  // the decode's scratch, and the log-sum-exps when the caller takes none
+  return (decode_workspace_bytes(p) + 15) / 16 * 16 + sizeof(float) * (size_t)p.B * p.Hq;
+}
+
+cudaError_t launch_sparse_decode_mass(const Dims& p, const void* q, const void* k, const void* v,
+                                      const int32_t* sel, void* out, float* lse, float* mass,
+                                      float* ws, cudaStream_t st, int* dev_status) {
+  if (!lse) lse = ws + (decode_workspace_bytes(p) + 15) / 16 * 4;
+  cudaError_t e = launch_sparse_decode(p, q, k, v, sel, out, lse, ws, st, dev_status);
+  if (e != cudaSuccess) return e;
+  if (p.dtype == 1)
+    return p.d == 128 ? run_mass<__nv_bfloat16, 128>(p, q, k, sel, lse, mass, st)
+                      : run_mass<__nv_bfloat16, 64>(p, q, k, sel, lse, mass, st);
+  return p.d == 128 ? run_mass<float, 128>(p, q, k, sel, lse, mass, st)
+                    : run_mass<float, 64>(p, q, k, sel, lse, mass, st);
+}
+
+}  // namespace msa

@@ -407,12 +407,265 @@ msa_status msa_sparse_decode_paged(const msa_shape* shape, const int32_t* seq_le
   return e == cudaSuccess ? MSA_OK : cuda_fail(e, "msa_sparse_decode_paged launch");
 }
 
+// ------------------------------------------------------------------ rotary positions
+
+msa_status msa_rope(const msa_rope_desc* desc, const msa_rope_tensor* tensors, int32_t n_tensors,
+                    const int32_t* positions, void* stream) {
+  g_last_error[0] = 0;
+  if (!desc || !tensors)
+    return fail(MSA_ERR_INVALID_ARG, "%s is NULL", desc ? "tensors" : "desc");
+  if (desc->batch < 1 || desc->seq < 1)
+    return fail(MSA_ERR_INVALID_ARG, "batch and seq must be >= 1 (got %d, %d)", desc->batch,
+                desc->seq);
+  if (desc->dtype != MSA_F32 && desc->dtype != MSA_BF16)
+    return fail(MSA_ERR_INVALID_ARG, "dtype must be MSA_F32 or MSA_BF16 (got %d)", desc->dtype);
+  if ((desc->interleaved != 0 && desc->interleaved != 1) ||
+      (desc->inverse != 0 && desc->inverse != 1))
+    return fail(MSA_ERR_INVALID_ARG, "interleaved and inverse must be 0 or 1");
+  if (!isfinite(desc->scale)) return fail(MSA_ERR_INVALID_ARG, "scale must be finite");
+  if (n_tensors < 1 || n_tensors > MSA_ROPE_MAX_TENSORS)
+    return fail(MSA_ERR_INVALID_ARG, "n_tensors must be in [1, %d] (got %d)", MSA_ROPE_MAX_TENSORS,
+                n_tensors);
+  MSA_TRY(check_ptr(positions, "positions", true));
+  const size_t item = desc->dtype == MSA_BF16 ? 2 : 4;
+  for (int i = 0; i < n_tensors; ++i) {
+    const msa_rope_tensor& t = tensors[i];
+    MSA_TRY(check_ptr(t.x, "x"));
+    MSA_TRY(check_ptr(t.y, "y"));
+    MSA_TRY(check_ptr(t.freqs, "freqs"));
+    if (t.n_heads < 1 || (t.head_major != 0 && t.head_major != 1))
+      return fail(MSA_ERR_INVALID_ARG, "tensor %d: n_heads must be >= 1, head_major 0 or 1", i);
+    if (t.head_dim < 16 || t.head_dim > 1024 || t.head_dim % 16 != 0)
+      return fail(MSA_ERR_UNSUPPORTED, "tensor %d: head_dim %d: a multiple of 16 of at most 1024",
+                  i, t.head_dim);
+    if (t.rotary_dim < 16 || t.rotary_dim > t.head_dim || t.rotary_dim % 16 != 0)
+      return fail(MSA_ERR_UNSUPPORTED,
+                  "tensor %d: rotary_dim %d: a multiple of 16 of at most head_dim (%d)", i,
+                  t.rotary_dim, t.head_dim);
+    // outputs stay clear of every other tensor (a tensor may be rotated in place)
+    const __int128 bytes = (__int128)desc->batch * desc->seq * t.n_heads * t.head_dim * item;
+    if (bytes >= (__int128)1 << 62)
+      return fail(MSA_ERR_UNSUPPORTED, "tensor %d is too large", i);
+    for (int j = 0; j < n_tensors; ++j) {
+      const msa_rope_tensor& o = tensors[j];
+      const __int128 size = (__int128)desc->batch * desc->seq * o.n_heads * o.head_dim * item;
+      const __int128 y0 = (uintptr_t)t.y, x0 = (uintptr_t)o.x, w0 = (uintptr_t)o.y;
+      const bool in_place = i == j && t.x == t.y;
+      if (!in_place && y0 < x0 + size && x0 < y0 + bytes)
+        return fail(MSA_ERR_INVALID_ARG, "y of tensor %d overlaps x of tensor %d", i, j);
+      if (i != j && y0 < w0 + size && w0 < y0 + bytes)
+        return fail(MSA_ERR_INVALID_ARG, "y of tensor %d overlaps y of tensor %d", i, j);
+    }
+  }
+  cudaError_t e = launch_rope(*desc, tensors, n_tensors, positions, (cudaStream_t)stream);
+  return e == cudaSuccess ? MSA_OK : cuda_fail(e, "msa_rope launch");
+}
+
+// -------------------------------------------------------------------- the 4-bit KV cache
+
+namespace {
+msa_status make_packed_dims(const msa_shape* shape, const int32_t* seq_lens,
+                            const int32_t* block_table, int32_t n_phys, Dims* d) {
+  MSA_TRY(make_dims(shape, d));
+  if (!d->decode)
+    return fail(MSA_ERR_INVALID_ARG, "the 4-bit cache takes decode shapes (seq_q == q_tile == 1)");
+  if (d->Bk != 128)
+    return fail(MSA_ERR_UNSUPPORTED, "the 4-bit cache holds blocks of 128 keys (got %d)", d->Bk);
+  MSA_TRY(check_ptr(seq_lens, "seq_lens", true));
+  MSA_TRY(check_ptr(block_table, "block_table", true));
+  if (n_phys < 1) return fail(MSA_ERR_INVALID_ARG, "n_phys must be >= 1");
+  if (!block_table && (long long)d->B * d->nB != n_phys)
+    return fail(MSA_ERR_INVALID_ARG,
+                "without a block_table n_phys (%d) must be batch * n_blocks = %lld", n_phys,
+                (long long)d->B * d->nB);
+  d->seq_lens = seq_lens;
+  d->block_table = block_table;
+  d->n_phys = n_phys;
+  return MSA_OK;
+}
+}  // namespace
+
+msa_status msa_cache_pack(const msa_shape* shape, int32_t n_new, const int32_t* starts,
+                          const int32_t* seq_lens, const int32_t* block_table, int32_t n_phys,
+                          const void* k, const void* v, void* cache, void* stream) {
+  g_last_error[0] = 0;
+  Dims d;
+  MSA_TRY(make_packed_dims(shape, seq_lens, block_table, n_phys, &d));
+  if (n_new < 1) return fail(MSA_ERR_INVALID_ARG, "n_new must be >= 1 (got %d)", n_new);
+  MSA_TRY(check_ptr(starts, "starts", true));
+  MSA_TRY(check_ptr(k, "k"));
+  MSA_TRY(check_ptr(v, "v"));
+  MSA_TRY(check_ptr(cache, "cache"));
+  {
+    const cudaError_t ve = launch_debug_validate(d, nullptr, (cudaStream_t)stream, status_ptr());
+    if (ve != cudaSuccess) return cuda_fail(ve, "msa_cache_pack debug validation");
+  }
+  cudaError_t e = launch_cache_pack(d, n_new, starts, k, v, cache, (cudaStream_t)stream);
+  return e == cudaSuccess ? MSA_OK : cuda_fail(e, "msa_cache_pack launch");
+}
+
+msa_status msa_cache_unpack(const msa_shape* shape, int32_t n_out, const int32_t* starts,
+                            const int32_t* seq_lens, const int32_t* block_table, int32_t n_phys,
+                            const void* cache, void* k, void* v, void* stream) {
+  g_last_error[0] = 0;
+  Dims d;
+  MSA_TRY(make_packed_dims(shape, seq_lens, block_table, n_phys, &d));
+  if (n_out < 1) return fail(MSA_ERR_INVALID_ARG, "n_out must be >= 1 (got %d)", n_out);
+  MSA_TRY(check_ptr(starts, "starts", true));
+  MSA_TRY(check_ptr(cache, "cache"));
+  MSA_TRY(check_ptr(k, "k"));
+  MSA_TRY(check_ptr(v, "v"));
+  {
+    const cudaError_t ve = launch_debug_validate(d, nullptr, (cudaStream_t)stream, status_ptr());
+    if (ve != cudaSuccess) return cuda_fail(ve, "msa_cache_unpack debug validation");
+  }
+  cudaError_t e = launch_cache_unpack(d, n_out, starts, cache, k, v, (cudaStream_t)stream);
+  return e == cudaSuccess ? MSA_OK : cuda_fail(e, "msa_cache_unpack launch");
+}
+
+msa_status msa_sparse_decode_packed(const msa_shape* shape, const int32_t* seq_lens,
+                                    const int32_t* block_table, int32_t n_phys, const void* q,
+                                    const void* cache, const int32_t* sel, void* out, float* lse,
+                                    float* mass, void* stream) {
+  g_last_error[0] = 0;
+  Dims d;
+  MSA_TRY(make_packed_dims(shape, seq_lens, block_table, n_phys, &d));
+  if (d.G > 64) return fail(MSA_ERR_UNSUPPORTED, "decode needs n_heads_q / n_heads_kv <= 64");
+  if (mass && d.k > kMaxPackedMassBlocks)
+    return fail(MSA_ERR_UNSUPPORTED, "mass needs top_k <= %d (got %d)", kMaxPackedMassBlocks, d.k);
+  MSA_TRY(check_ptr(q, "q"));
+  MSA_TRY(check_ptr(cache, "cache"));
+  MSA_TRY(check_ptr(sel, "sel"));
+  MSA_TRY(check_ptr(out, "out"));
+  MSA_TRY(check_ptr(lse, "lse", true));
+  MSA_TRY(check_ptr(mass, "mass", true));
+  {
+    const cudaError_t ve = launch_debug_validate(d, sel, (cudaStream_t)stream, status_ptr());
+    if (ve != cudaSuccess) return cuda_fail(ve, "msa_sparse_decode_packed debug validation");
+  }
+  cudaError_t e = launch_sparse_decode_packed(d, q, cache, sel, out, lse, mass,
+                                              (cudaStream_t)stream);
+  return e == cudaSuccess ? MSA_OK : cuda_fail(e, "msa_sparse_decode_packed launch");
+}
+
+// ------------------------------------------- eviction by accumulated attention weight
+
+msa_status msa_sparse_decode_mass(const msa_shape* shape, const int32_t* seq_lens,
+                                  const int32_t* block_table, int32_t n_phys, const void* q,
+                                  const void* k, const void* v, const int32_t* sel, void* out,
+                                  float* lse, float* mass, void* workspace, size_t ws_bytes,
+                                  void* stream) {
+  g_last_error[0] = 0;
+  Dims d;
+  if ((seq_lens == nullptr) != (block_table == nullptr))
+    return fail(MSA_ERR_INVALID_ARG, "seq_lens and block_table are given together or not at all");
+  if (block_table) {
+    MSA_TRY(make_paged_dims(shape, seq_lens, block_table, n_phys, &d, true));
+  } else {
+    MSA_TRY(make_dims(shape, &d));
+    if (!d.decode)
+      return fail(MSA_ERR_INVALID_ARG, "msa_sparse_decode_mass needs seq_q == q_tile == 1");
+  }
+  if (d.G > 64) return fail(MSA_ERR_UNSUPPORTED, "decode needs n_heads_q / n_heads_kv <= 64");
+  MSA_TRY(check_ptr(q, "q"));
+  MSA_TRY(check_ptr(k, "k"));
+  MSA_TRY(check_ptr(v, "v"));
+  MSA_TRY(check_ptr(sel, "sel"));
+  MSA_TRY(check_ptr(out, "out"));
+  MSA_TRY(check_ptr(lse, "lse", true));
+  MSA_TRY(check_ptr(mass, "mass"));
+  MSA_TRY(check_ptr(workspace, "workspace"));
+  const size_t need = decode_mass_workspace_bytes(d);
+  if (ws_bytes < need)
+    return fail(MSA_ERR_INVALID_ARG, "workspace of %zu bytes is too small: need %zu", ws_bytes,
+                need);
+  {
+    const cudaError_t ve = launch_debug_validate(d, sel, (cudaStream_t)stream, status_ptr());
+    if (ve != cudaSuccess) return cuda_fail(ve, "msa_sparse_decode_mass debug validation");
+  }
+  cudaError_t e = launch_sparse_decode_mass(d, q, k, v, sel, out, lse, mass,
+                                            static_cast<float*>(workspace), (cudaStream_t)stream,
+                                            status_ptr());
+  return e == cudaSuccess ? MSA_OK : cuda_fail(e, "msa_sparse_decode_mass launch");
+}
+
+msa_status msa_cache_evict(const msa_shape* shape, int32_t keep, int32_t n_first, int32_t n_recent,
+                           const int32_t* seq_lens, const float* mass, const int32_t* block_table,
+                           int32_t* kept, int32_t* new_lens, float* mass_out, int32_t* table_out,
+                           void* stream) {
+  g_last_error[0] = 0;
+  Dims d;
+  MSA_TRY(make_dims(shape, &d));
+  if (!d.decode)
+    return fail(MSA_ERR_INVALID_ARG, "msa_cache_evict takes decode shapes (seq_q == q_tile == 1)");
+  if (n_first < 0 || n_recent < 1 || (long long)n_first + n_recent > keep)
+    return fail(MSA_ERR_INVALID_ARG,
+                "keep (%d) must hold the first n_first (%d, >= 0) and last n_recent (%d, >= 1) "
+                "blocks", keep, n_first, n_recent);
+  MSA_TRY(check_ptr(seq_lens, "seq_lens", true));
+  MSA_TRY(check_ptr(mass, "mass"));
+  MSA_TRY(check_ptr(block_table, "block_table", true));
+  MSA_TRY(check_ptr(kept, "kept"));
+  MSA_TRY(check_ptr(new_lens, "new_lens"));
+  MSA_TRY(check_ptr(mass_out, "mass_out"));
+  if ((block_table == nullptr) != (table_out == nullptr))
+    return fail(MSA_ERR_INVALID_ARG, "block_table and table_out are given together or not at all");
+  MSA_TRY(check_ptr(table_out, "table_out", true));
+  d.seq_lens = seq_lens;
+  {
+    const cudaError_t ve = launch_debug_validate(d, nullptr, (cudaStream_t)stream, status_ptr());
+    if (ve != cudaSuccess) return cuda_fail(ve, "msa_cache_evict debug validation");
+  }
+  cudaError_t e = launch_cache_evict(d, keep, n_first, n_recent, mass, block_table, kept, new_lens,
+                                     mass_out, table_out, (cudaStream_t)stream);
+  return e == cudaSuccess ? MSA_OK : cuda_fail(e, "msa_cache_evict launch");
+}
+
+msa_status msa_cache_gather(int32_t batch, const msa_gather_tensor* tensors, int32_t n_tensors,
+                            const int32_t* kept, int32_t keep, int32_t block_size, void* stream) {
+  g_last_error[0] = 0;
+  if (!tensors) return fail(MSA_ERR_INVALID_ARG, "tensors is NULL");
+  if (batch < 1 || keep < 1 || block_size < 1)
+    return fail(MSA_ERR_INVALID_ARG, "batch, keep and block_size must be >= 1 (got %d, %d, %d)",
+                batch, keep, block_size);
+  if (n_tensors < 1 || n_tensors > MSA_GATHER_MAX_TENSORS)
+    return fail(MSA_ERR_INVALID_ARG, "n_tensors must be in [1, %d] (got %d)",
+                MSA_GATHER_MAX_TENSORS, n_tensors);
+  MSA_TRY(check_ptr(kept, "kept"));
+  for (int i = 0; i < n_tensors; ++i) {
+    const msa_gather_tensor& t = tensors[i];
+    MSA_TRY(check_ptr(t.src, "src"));
+    MSA_TRY(check_ptr(t.dst, "dst"));
+    if (t.n_heads < 1 || t.src_rows < 1 || t.dst_rows < 1 || t.src_rows > (1ll << 40) ||
+        t.dst_rows > (1ll << 40))
+      return fail(MSA_ERR_INVALID_ARG, "tensor %d: n_heads and rows must be >= 1", i);
+    if (t.row_bytes < 16 || t.row_bytes > 65536 || t.row_bytes % 16 != 0)
+      return fail(MSA_ERR_UNSUPPORTED,
+                  "tensor %d: row_bytes %d: a multiple of 16 of at most 65536", i, t.row_bytes);
+    const __int128 one = (__int128)batch * t.n_heads * t.row_bytes;
+    const __int128 d0 = (uintptr_t)t.dst, d1 = d0 + one * t.dst_rows;
+    for (int j = 0; j < n_tensors; ++j) {
+      const msa_gather_tensor& o = tensors[j];
+      const __int128 other = (__int128)batch * o.n_heads * o.row_bytes;
+      const __int128 s0 = (uintptr_t)o.src, o0 = (uintptr_t)o.dst;
+      if (d0 < s0 + other * o.src_rows && s0 < d1)
+        return fail(MSA_ERR_INVALID_ARG, "dst of tensor %d overlaps src of tensor %d", i, j);
+      if (i != j && d0 < o0 + other * o.dst_rows && o0 < d1)
+        return fail(MSA_ERR_INVALID_ARG, "dst of tensor %d overlaps dst of tensor %d", i, j);
+    }
+  }
+  cudaError_t e = launch_cache_gather(batch, tensors, n_tensors, kept, keep, block_size,
+                                      (cudaStream_t)stream);
+  return e == cudaSuccess ? MSA_OK : cuda_fail(e, "msa_cache_gather launch");
+}
+
 size_t msa_workspace_bytes(const msa_shape* shape, int which) {
   Dims d;
   if (make_dims(shape, &d) != MSA_OK) return 0;
   if (which == 1 && d.decode) return decode_workspace_bytes(d);
   if (which == 2 && !d.decode) return backward_workspace_bytes(d);
   if (which == 3 && !d.decode) return index_kl_workspace_bytes(d);
+  if (which == 4 && d.decode) return decode_mass_workspace_bytes(d);
   return 0;
 }
 

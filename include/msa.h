@@ -232,9 +232,158 @@ msa_status msa_sparse_decode_paged(const msa_shape* shape, const int32_t* seq_le
                                    void* out, float* lse, void* workspace, size_t ws_bytes,
                                    void* stream);
 
+/* ------------------------------------------------------------------ rotary positions
+ * Rotates (q, k, idx_q, idx_k before the calls above) or, with inverse = 1, rotates back
+ * (their gradients) by position-dependent angles: with p = positions[b, t] + pos_offset (or
+ * t + pos_offset without positions) and the turn a = p * freqs[i] / 2^64 of pair i,
+ *   (x0, x1) -> scale * (x0 cos - x1 sin, x0 sin + x1 cos)  of the angle 2 pi a  (-2 pi a
+ *   with inverse: scale and inverse together are the gradient of scale without inverse).
+ * Pair i of a head is dims (i, i + rotary_dim / 2), or (2 i, 2 i + 1) with interleaved = 1;
+ * dims from rotary_dim on are copied.  freqs holds turns per position in units of 2^-64
+ * turns, so the product wraps at whole turns exactly and far positions lose nothing; any
+ * scheme for long contexts (positions divided, base raised, ramped frequencies) is a choice
+ * of freqs and scale.  Angles are exact to 2^-32 turns before the sine, products are fp32,
+ * the result is rounded once to the dtype.
+ *   positions   int32 [batch, seq], device; NULL: 0, 1, ..., seq - 1 in every sequence.
+ *               With the cache lengths of a decode batch (seq = 1) and pos_offset = -1 the
+ *               new tokens sit at the end of their caches.  Sums wrap as 32-bit integers.
+ * Up to MSA_ROPE_MAX_TENSORS tensors sharing these positions go in one launch; each is
+ * [batch, seq, n_heads, head_dim], or [batch, n_heads, seq, head_dim] with head_major = 1.
+ * y may be x itself (in place); otherwise no y may overlap another tensor.
+ * head_dim: a multiple of 16, at most 1024; rotary_dim: a multiple of 16 of at most head_dim.
+ * desc and tensors are host structs, read before the call returns. */
+#define MSA_ROPE_MAX_TENSORS 8
+typedef struct msa_rope_desc {
+  int32_t batch, seq;
+  int32_t dtype;       /* msa_dtype of every tensor of the call */
+  int32_t pos_offset;
+  int32_t interleaved; /* 0 or 1 */
+  int32_t inverse;     /* 0 or 1 */
+  float scale;         /* factor on the rotated dims; finite; 0 means 1 */
+} msa_rope_desc;
+typedef struct msa_rope_tensor {
+  const void* x;
+  void* y;
+  const uint64_t* freqs; /* device, [rotary_dim / 2] */
+  int32_t n_heads, head_dim, rotary_dim;
+  int32_t head_major;    /* 0 or 1 */
+} msa_rope_tensor;
+msa_status msa_rope(const msa_rope_desc* desc, const msa_rope_tensor* tensors, int32_t n_tensors,
+                    const int32_t* positions, void* stream);
+
+/* ---------------------------------------------------------------- the 4-bit KV cache
+ * K and V in 4 bits: 5 bits a value with their scales, 160 * head_dim bytes for the 128 keys
+ * of one KV head's block against 512 * head_dim in bf16.  A group is 32 consecutive dims of one token and head.  With hi, lo its
+ * largest and smallest value (fp32 arithmetic, each operation rounded to nearest even):
+ *   step = bf16(hi * f - lo * f), f = fp32(1 / 15)    (steps below 2^-100 become 0)
+ *   mid  = bf16(lo + 8 * step)
+ *   code = clamp(rint((x - mid) * fp32(1 / step)) + 8, 0, 15), 8 when step is 0
+ *   value = mid + (code - 8) * step                   (what the cache holds)
+ * |value - x| <= step / 2 + 2^-8 |mid| + 2^-8 * 8 step; a group holding a NaN or an infinity
+ * is stored as NaN values.
+ *
+ * cache   uint8 [n_phys, n_heads_kv, 160 * head_dim], 16-byte aligned: K's record of the
+ *         block, then V's.  With a block_table (int32 [batch, n_blocks]) logical block j of
+ *         sequence b is physical block block_table[b, j], as in the paged calls above;
+ *         without one (NULL) it is b * n_blocks + j, and n_phys must be batch * n_blocks.
+ * One record (d = head_dim, ng = d / 32 groups; byte offsets):
+ *   [0, 64 d)       codes, two a byte, the lower dim in the low half;
+ *     K: key j, dim 32 g + 8 c + i (c < 4, i < 8):  j * d / 2 + c * 4 ng + g * 4 + i / 2
+ *     V: key j, dim 32 g + 4 r + i (r < 8, i < 4):
+ *        (r * 128 + 2 * P + j % 2) * 2 ng + g * 2 + i / 2,
+ *        P = (j / 2) ^ (4 * (r % 2)) for d = 128, (j / 2) ^ (4 * (r % 4)) for d = 64
+ *   [64 d, 72 d)    step, bf16, group g of key j at element g * 128 + j
+ *   [72 d, 80 d)    mid, likewise
+ * so that a thread's share of a tensor-core operand is one aligned load.
+ *
+ * shape: a decode shape (seq_q = q_tile = 1) with block_size 128 whose seq_k is the capacity
+ * (n_blocks = ceil(seq_k / 128)); n_heads_q, index_dim and top_k matter to the attention
+ * call only.  seq_lens int32 [batch], device (NULL: every length is seq_k; lengths are
+ * clamped to [0, seq_k]).  Table entries outside [0, n_phys) are skipped (nothing is read
+ * or written there). */
+
+/* Quantises tokens into the cache.  k, v: [batch, n_heads_kv, n_new, head_dim] of the
+ * shape's dtype.  Token i of sequence b goes to position starts[b] + i, or, with starts
+ * NULL, to seq_lens[b] - n_new + i (the last n_new positions); positions outside
+ * [0, seq_lens[b]) are not stored, so a batch padded on the right is passed as it is.  Only
+ * the stored tokens' bytes change.  A decode step is n_new = 1. */
+msa_status msa_cache_pack(const msa_shape* shape, int32_t n_new, const int32_t* starts,
+                          const int32_t* seq_lens, const int32_t* block_table, int32_t n_phys,
+                          const void* k, const void* v, void* cache, void* stream);
+
+/* The values of the same positions (rounded once to the dtype) into k, v
+ * [batch, n_heads_kv, n_out, head_dim]; rows of positions outside [0, seq_lens[b]) are left
+ * as they are. */
+msa_status msa_cache_unpack(const msa_shape* shape, int32_t n_out, const int32_t* starts,
+                            const int32_t* seq_lens, const int32_t* block_table, int32_t n_phys,
+                            const void* cache, void* k, void* v, void* stream);
+
+/* msa_sparse_decode over the 4-bit cache: attention of q [batch, 1, n_heads_q, head_dim] over
+ * the values that the selected blocks hold.  out, lse as there (lse may be NULL); bytes of
+ * the last block past the sequence's length are never used, whatever they hold.  No
+ * workspace.  At most 64 query heads per KV head.
+ * mass: NULL, or the accumulated attention weights below (then top_k is at most 1024). */
+msa_status msa_sparse_decode_packed(const msa_shape* shape, const int32_t* seq_lens,
+                                    const int32_t* block_table, int32_t n_phys, const void* q,
+                                    const void* cache, const int32_t* sel, void* out, float* lse,
+                                    float* mass, void* stream);
+
+/* -------------------------------------------- eviction by accumulated attention weight
+ * Decode with the attention weight that every block receives added up:
+ *   mass[b, g, sel[b, g, i]] += sum over the group's query heads h and the keys j of that
+ *   block of exp(z_hj - lse_h)                   (the weights of one head sum to 1)
+ * mass: float32 [batch, n_heads_kv, n_blocks], the caller's, zeroed when a sequence starts.
+ * out and lse (may be NULL) are bit for bit those of msa_sparse_decode, or, with seq_lens and
+ * block_table (both given), of msa_sparse_decode_paged on its shapes.  Each entry of mass
+ * gets one addition a call, so results repeat bit for bit (a block listed twice is counted
+ * twice).  workspace: msa_workspace_bytes(shape, 4) bytes, as for msa_sparse_decode. */
+msa_status msa_sparse_decode_mass(const msa_shape* shape, const int32_t* seq_lens,
+                                  const int32_t* block_table, int32_t n_phys, const void* q,
+                                  const void* k, const void* v, const int32_t* sel, void* out,
+                                  float* lse, float* mass, void* workspace, size_t ws_bytes,
+                                  void* stream);
+
+/* Chooses, for every sequence of more than `keep` blocks, the blocks that stay: the first
+ * n_first, the last n_recent (the one that is being filled among them), and of the others
+ * those of the largest score, ties to the lower block index; a block's score is the fp32 sum
+ * of its mass over the KV heads in head order (NaN counts as the lowest).  Whole blocks go
+ * and the rest keep their keys together, so the index scores of those that stay do not
+ * change; all heads of a sequence drop the same ones, as they share index keys and table.
+ *   kept      int32 [batch, keep]: the old indices of the blocks that stay, ascending, -1 padded
+ *   new_lens  int32 [batch]: the lengths without the dropped blocks
+ *   mass_out  [batch, n_heads_kv, n_blocks]: mass of the kept blocks, in their order, then 0
+ *   table_out int32 [batch, n_blocks] (NULL without a block_table): the sequence's entries
+ *             with the kept blocks first and the dropped ones after them (both ascending),
+ *             entries past the sequence's last block as they were.  A sequence grows into
+ *             the blocks it dropped, or the caller takes them back.
+ * new_lens, mass_out and table_out may be the inputs themselves (in place).  shape: a decode
+ * shape (n_blocks at most 32768); seq_lens NULL: every length is seq_k.
+ * keep >= n_first + n_recent, n_first >= 0, n_recent >= 1. */
+msa_status msa_cache_evict(const msa_shape* shape, int32_t keep, int32_t n_first, int32_t n_recent,
+                           const int32_t* seq_lens, const float* mass, const int32_t* block_table,
+                           int32_t* kept, int32_t* new_lens, float* mass_out, int32_t* table_out,
+                           void* stream);
+
+/* Contiguous caches: copies block kept[b, i] of every source to block i of its destination
+ * (entries outside the source are skipped).  Up to MSA_GATHER_MAX_TENSORS caches
+ * [batch, n_heads, rows, row_bytes] a launch (K, V, index keys; the 4-bit cache without a
+ * table is n_heads = 1, rows = 128 * n_blocks, row_bytes = n_heads_kv * 160 * head_dim / 128).
+ * Rows past src_rows are not read, rows past dst_rows not written; rows of the destination
+ * that no kept block covers stay as they are.  Sources and destinations must not overlap. */
+#define MSA_GATHER_MAX_TENSORS 8
+typedef struct msa_gather_tensor {
+  const void* src;
+  void* dst;
+  int64_t src_rows, dst_rows; /* rows per (sequence, head) */
+  int32_t n_heads;
+  int32_t row_bytes;          /* a multiple of 16, at most 65536 */
+} msa_gather_tensor;
+msa_status msa_cache_gather(int32_t batch, const msa_gather_tensor* tensors, int32_t n_tensors,
+                            const int32_t* kept, int32_t keep, int32_t block_size, void* stream);
+
 /* Scratch bytes msa_sparse_prefill (which = 0), msa_sparse_decode (which = 1),
- * msa_sparse_prefill_backward (which = 2) or msa_index_kl_loss (which = 3) needs for this
- * shape; 0 when none.  Returns 0 for an invalid shape. */
+ * msa_sparse_prefill_backward (which = 2), msa_index_kl_loss (which = 3) or
+ * msa_sparse_decode_mass (which = 4) needs for this shape; 0 when none.  Returns 0 for an invalid shape. */
 size_t msa_workspace_bytes(const msa_shape* shape, int which);
 
 /* Synchronises `stream`, then reports (and clears) the device status word and any pending

@@ -5,3 +5,4 @@ from .msa_oracle import (index_logits, pool_blocks, index_block_scores_prefill,
                          block_topk_prefill, block_topk_decode, selected_keys,
                          sparse_attention, full_causal_gqa, msa_prefill, msa_decode,
                          default_scale)
+from . import cache_ops  # noqa: F401
