@@ -153,7 +153,7 @@ cudaError_t launch_cache_unpack(const Dims& p, int n, const int32_t* starts, con
                                 void* k, void* v, cudaStream_t st);
 cudaError_t launch_sparse_decode_packed(const Dims& p, const void* q, const void* cache,
                                         const int32_t* sel, void* out, float* lse, float* mass,
-                                        cudaStream_t st);
+                                        cudaStream_t st, int* dev_status);
 // Selected blocks per row that decode can accumulate weights for over the 4-bit cache.
 constexpr int kMaxPackedMassBlocks = 1024;
 

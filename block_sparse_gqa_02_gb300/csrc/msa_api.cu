@@ -544,7 +544,7 @@ msa_status msa_sparse_decode_packed(const msa_shape* shape, const int32_t* seq_l
     if (ve != cudaSuccess) return cuda_fail(ve, "msa_sparse_decode_packed debug validation");
   }
   cudaError_t e = launch_sparse_decode_packed(d, q, cache, sel, out, lse, mass,
-                                              (cudaStream_t)stream);
+                                              (cudaStream_t)stream, status_ptr());
   return e == cudaSuccess ? MSA_OK : cuda_fail(e, "msa_sparse_decode_packed launch");
 }
 
