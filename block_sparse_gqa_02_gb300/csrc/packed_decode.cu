@@ -206,22 +206,29 @@ packed_decode_simt(const T* __restrict__ q, const uint8_t* __restrict__ cache,
 // ------------------------------------------------------------------ tensor-core kernel
 //
 // The G <= 16 heads of a group (16 of them a pass) are the M rows of mma.sync.m16n8k16.  The
-// codes become exact bf16 integers -8 .. 7 (a code or-ed into the mantissa of 128 and 136 taken
-// away), so products with them lose nothing, and steps and mids enter in fp32:
+// codes become exact bf16 integers, so products with them lose nothing, and steps and mids
+// enter in fp32:
 //   z_j = sum_g step_jg (q_g . c_jg) + sum_g mid_jg (sum of q_g),
-//   o_g = sum_j (p_j step_jg) c_jg + sum_j p_j mid_jg.
-// The scores take one accumulator per group of dims; their mid term is one more MMA whose A
-// operand is the rows' group sums of q, split in three bf16 parts (24 bits).  For the output
+//   o_g = sum_j (p_j step_jg) c_jg + sum_j p_j mid_jg,      c = code - 8.
+// K's codes are or-ed into the mantissa of 16, and the accumulators (one per group of dims) start
+// at -24 times the rows' group sums of q, which takes the 16 and the 8 away without an
+// instruction per operand; V's are or-ed into that of 128 and 136 is subtracted (its sums run
+// over thousands of keys, where the offset would cost digits).  The scores' mid term is one MMA
+// whose A operand is the group sums of q, split in three bf16 parts (24 bits).  For the output
 // p_j step_jg is formed in fp32 and rounded once to bf16, as the 16-bit cache's kernel rounds
 // p_j; the mid term is an MMA with the mids as four more columns.
 //
-// CTA = one split of a (sequence, KV head): a producer warp lists the split's blocks and keeps a
-// ring of whole records (K and V of a block, 160 D contiguous bytes, one bulk copy) filled;
-// four warps take 32 keys of every block each, with a softmax base of their own that moves only
-// when a row's maximum passes it by more than 8 (log2 units).
+// CTA = one split of a (sequence, KV head), two groups of four warps that take its blocks in
+// turn, 32 keys a warp, each warp with a softmax base of its own that moves only when a row's
+// maximum passes it by more than 8 (log2 units).  Whole records (K and V of a block, 160 D
+// contiguous bytes) come through a ring, one bulk copy each; a group's first warp refills a
+// stage in the middle of its next block, when the other warps have left the stage.  Q's
+// operands stay in shared memory: at 128 registers a thread two CTAs fit an SM.
 
-constexpr int kMmaWarps = 4;
-constexpr int kMmaThreads = (kMmaWarps + 1) * 32;
+constexpr int kMmaGroups = 4;                              // groups of warps
+constexpr int kGroupWarps = 4;
+constexpr int kMmaWarps = kMmaGroups * kGroupWarps;
+constexpr int kMmaThreads = kMmaWarps * 32;
 constexpr int kMaxList = 1024;         // blocks of a split
 constexpr int kMaxMassList = 128;      // blocks of a split whose weights are kept
 constexpr float kSlack = 8.f;
@@ -232,31 +239,66 @@ struct Entry {
 
 template <int D>
 struct MmaSmem {
-  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kStages = D == 128 ? 8 : 16;
+  static constexpr int kGroups = PackedRecord<D>::kGroups;
   union {
     __align__(128) uint8_t ring[kStages][PackedRecord<D>::kPairBytes];
     float part[kMmaWarps][kRows][D + 4];                   // the warps' outputs, after the ring
   };
   float o[kRows][D];                   // the CTA's outputs, relative to m
+  uint4 qf[kGroups][2][32];            // Q as A operands, per lane
+  float qsum[kGroups][kRows];          // sums of q over a group of dims
   float m[kRows], l[kRows], norm[kRows];
   float wm[kMmaWarps][kRows], wl[kMmaWarps][kRows];
   uint64_t full[kStages], empty[kStages];
+  int last[kStages];                   // a stage's last copy
   int abort, count;
 };
 
-__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                          uint32_t b1) {
+// d = a b + c
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1,
+                                          float c0, float c1, float c2, float c3) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
-      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2),
+        "f"(c3));
+}
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint4& a, uint32_t b0,
+                                          uint32_t b1) {
+  mma_16816(d, a, b0, b1, d[0], d[1], d[2], d[3]);
 }
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Pairs of fp32 in a 64-bit register for the paired instructions.
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void split_f32x2(uint64_t x, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Codes in bits 3-6 and 19-22 of x as a pair of bf16 integers 16 + code.
+__device__ __forceinline__ uint32_t code_pair_16(uint32_t x) {
+  return (x & 0x00780078u) | 0x41804180u;
 }
 
 // Codes in bits 0-3 and 16-19 of x as a pair of bf16 integers -8 .. 7.
@@ -271,17 +313,36 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
+__device__ __forceinline__ uint32_t bf16_pair(uint64_t x) {
+  float lo, hi;
+  split_f32x2(x, lo, hi);
+  return bf16_pair(lo, hi);
+}
 
 __device__ __forceinline__ float lo_bf16(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float hi_bf16(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+__device__ __forceinline__ uint64_t widen_bf16(uint32_t x) {
+  return f32x2(lo_bf16(x), hi_bf16(x));
+}
 
-// Keeps the halves of a pair of keys (j, j + 1) that lie before `seen`.
-__device__ __forceinline__ uint32_t keep_seen(uint32_t pair, int j, int seen) {
-  return pair & ((j < seen ? 0xffffu : 0u) | (j + 1 < seen ? 0xffff0000u : 0u));
+__device__ __forceinline__ uint32_t load_u32(const uint8_t* p) {
+  return *reinterpret_cast<const uint32_t*>(p);
+}
+
+// N = 2 or 4 consecutive words.
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
+  if (N == 4) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    w[0] = u.x, w[1] = u.y, w[2 % N] = u.z, w[3 % N] = u.w;
+  } else {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    w[0] = u.x, w[1] = u.y;
+  }
 }
 
 template <int D, bool kMass>
-__global__ void __launch_bounds__(kMmaThreads)
+__global__ void __launch_bounds__(kMmaThreads, 1)
 packed_decode_mma(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict__ cache,
                   const int32_t* __restrict__ sel, __nv_bfloat16* __restrict__ out,
                   float* __restrict__ lse, float* __restrict__ mass, Dims p, int per,
@@ -292,23 +353,40 @@ packed_decode_mma(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict
   extern __shared__ __align__(128) uint8_t smem_raw[];
   S& s = *reinterpret_cast<S*>(smem_raw);
   Entry* list = reinterpret_cast<Entry*>(smem_raw + sizeof(S));                  // [per]
-  float* weights = reinterpret_cast<float*>(list + per);   // [kMmaWarps][kRows][per], kMass only
+  float* weights = reinterpret_cast<float*>(list + per);   // [kGroupWarps][kRows][per], kMass only
   cg::cluster_group cluster = cg::this_cluster();
   const int split = (int)cluster.block_rank(), n_split = (int)cluster.num_blocks();
   const int bg = blockIdx.y, b = bg / p.Hkv, g = bg % p.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = warp / kGroupWarps, gw = warp % kGroupWarps;
   const int gr = lane >> 2, c = lane & 3;
   const volatile int* abort = &s.abort;
+  const float c1 = p.sm_scale * kLog2e;
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      ptx::mbar_init(&s.full[i], 1);
-      ptx::mbar_init(&s.empty[i], kMmaWarps);
+  // Copy number x (block x - first of the list) into its stage, once its last block has left it.
+  auto issue = [&](int x, int i) {
+    const int st = x % kStages;
+    if (!ptx::mbar_wait(&s.empty[st], ((x / kStages) & 1) ^ 1, abort)) return false;
+    if (lane == 0) {
+      s.last[st] = x;
+      ptx::mbar_arrive_expect_tx(&s.full[st], R::kPairBytes);
+      ptx::bulk_load(s.ring[st], cache + ((size_t)list[i].phys * p.Hkv + g) * R::kPairBytes,
+                     R::kPairBytes, &s.full[st]);
     }
-    s.abort = 0;
-    ptx::fence_barrier_init();
-  }
-  if (warp == kMmaWarps) {
+    __syncwarp();
+    return true;
+  };
+
+  if (warp == kMmaWarps - 1) {
+    if (lane == 0) {
+      for (int i = 0; i < kStages; ++i) {
+        ptx::mbar_init(&s.full[i], 1);
+        ptx::mbar_init(&s.empty[i], kGroupWarps);
+        s.last[i] = -1;
+      }
+      s.abort = 0;
+      ptx::fence_barrier_init();
+    }
     // the split's blocks, in order, without entries that are no block of the sequence
     const int L = seq_len_of(p, b), nB_b = (L + kPackedBlock - 1) / kPackedBlock;
     const int i0 = min(p.k, split * per), i1 = min(p.k, i0 + per);
@@ -323,314 +401,284 @@ packed_decode_mma(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict
       n += __popc(there);
     }
     if (lane == 0) s.count = n;
+    __syncwarp();
   }
-  __syncthreads();
-  const int n_blocks = s.count;
-  const float c1 = p.sm_scale * kLog2e;
-  int issued = 0, taken = 0;                               // blocks copied, blocks consumed
 
   // more than 16 heads of a group: one pass after the other, weights added up in order
+  int first = 0;                                           // copies of the passes before
   for (int h0 = 0; h0 < p.G; h0 += kRows) {
     const int rows = min(kRows, p.G - h0);
+    if (warp == kMmaWarps - 1) {
+      const int n = s.count;
+      for (int i = 0; i < min(n, kStages) && !*abort; ++i)
+        if (!issue(first + i, i)) {
+          if (lane == 0) {
+            s.abort = 1;
+            if (status) atomicExch(status, 0x411);
+          }
+          break;
+        }
+    } else if (warp < NG) {
+      // Q as A operands, dims in the order of the codes in K's words: of group x, k-step kk
+      // holds dims 32 x + 8 c + (2 kk, 2 kk + 4) and (2 kk + 1, 2 kk + 5)
+      const __nv_bfloat16* q0 = q + ((size_t)b * p.Hq + (size_t)g * p.G + h0) * D;
+      uint4 w[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = gr + 8 * r;
+        w[r] = row < rows ? *reinterpret_cast<const uint4*>(q0 + (size_t)row * D +
+                                                            warp * kPackedGroup + c * 8)
+                          : make_uint4(0, 0, 0, 0);
+        float t = lo_bf16(w[r].x) + hi_bf16(w[r].x) + lo_bf16(w[r].y) + hi_bf16(w[r].y) +
+                  lo_bf16(w[r].z) + hi_bf16(w[r].z) + lo_bf16(w[r].w) + hi_bf16(w[r].w);
+        t += __shfl_xor_sync(0xffffffffu, t, 1);
+        t += __shfl_xor_sync(0xffffffffu, t, 2);
+        if (c == 0) s.qsum[warp][row] = t;
+      }
+      // dims (0,1) (2,3) (4,5) (6,7) -> (0,4) (1,5) and (2,6) (3,7)
+      s.qf[warp][0][lane] =
+          make_uint4(__byte_perm(w[0].x, w[0].z, 0x5410), __byte_perm(w[1].x, w[1].z, 0x5410),
+                     __byte_perm(w[0].x, w[0].z, 0x7632), __byte_perm(w[1].x, w[1].z, 0x7632));
+      s.qf[warp][1][lane] =
+          make_uint4(__byte_perm(w[0].y, w[0].w, 0x5410), __byte_perm(w[1].y, w[1].w, 0x5410),
+                     __byte_perm(w[0].y, w[0].w, 0x7632), __byte_perm(w[1].y, w[1].w, 0x7632));
+    }
+    __syncthreads();
+    const int n_blocks = s.count;
+    // the group sums of q in three bf16 parts: k = part * NG + group
+    uint4 qs;
+    {
+      uint32_t w[4];
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          float v[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int k = 8 * u + 2 * c + e, part = k / NG;
+            float t = s.qsum[k % NG][gr + 8 * r];
+            for (int y = 0; y < part; ++y) t -= __bfloat162float(__float2bfloat16_rn(t));
+            v[e] = part < 3 ? t : 0.f;
+          }
+          w[2 * u + r] = bf16_pair(v[0], v[1]);
+        }
+      qs = make_uint4(w[0], w[1], w[2], w[3]);
+    }
     float o[4 * NG][4], om[4];
     float base[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
 #pragma unroll
     for (int t = 0; t < 4 * NG; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
     om[0] = om[1] = om[2] = om[3] = 0.f;
 
-    if (warp == kMmaWarps) {
-      // ------------------------------------------------------------------- producer
-      bool ok = !*abort;
-      for (int i = 0; ok && i < n_blocks; ++i) {
-        const int st = issued % kStages;
-        ok = ptx::mbar_wait(&s.empty[st], ((issued / kStages) & 1) ^ 1, abort);
-        if (!ok) break;
-        if (lane == 0) {
-          ptx::mbar_arrive_expect_tx(&s.full[st], R::kPairBytes);
-          ptx::bulk_load(s.ring[st], cache + ((size_t)list[i].phys * p.Hkv + g) * R::kPairBytes,
-                         R::kPairBytes, &s.full[st]);
-        }
-        ++issued;
+    const int key0 = gw * 32;
+    bool ok = !*abort;
+    for (int i = group; ok && i < n_blocks; i += kMmaGroups) {
+      const int st = (first + i) % kStages;
+      ok = ptx::mbar_wait(&s.full[st], ((first + i) / kStages) & 1, abort);
+      if (!ok) break;
+      uint8_t* kr = s.ring[st];
+      uint8_t* vr = kr + R::kBytes;
+      const int seen = list[i].seen;
+      if (seen < kPackedBlock) {
+        // keys past the sequence: whatever their bytes hold counts as zero
+        if (key0 + lane >= seen)
+#pragma unroll
+          for (int y = 0; y < 2 * NG; ++y) {
+            *reinterpret_cast<uint16_t*>(kr + R::plane(R::kStepOffset, key0 + lane, y)) = 0;
+            *reinterpret_cast<uint16_t*>(vr + R::plane(R::kStepOffset, key0 + lane, y)) = 0;
+          }
+        ptx::fence_proxy_async_smem();                     // before the stage's next copy
         __syncwarp();
       }
-      if (!ok && lane == 0) {
-        s.abort = 1;
-        if (status) atomicExch(status, 0x411);
-      }
-    } else {
-      // -------------------------------------------------------------- compute warps
-      // Q as A operands, dims in the order of the codes in K's words: of group x, k-step kk
-      // holds dims 32 x + 8 c + (2 kk, 2 kk + 4) and (2 kk + 1, 2 kk + 5)
-      uint32_t qa[NG][2][4], qs[4];
-      {
-        float sum[2][NG];
-        const __nv_bfloat16* q0 = q + ((size_t)b * p.Hq + (size_t)g * p.G + h0) * D;
+      // scores of 16 rows x 32 keys, two n-tiles (16 keys) at a time
+      float sc[4][4];
 #pragma unroll
-        for (int x = 0; x < NG; ++x)
+      for (int half = 0; half < 2; ++half) {
+        uint32_t w[2][NG];
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const int row = gr + 8 * r;
-            const uint4 w = row < rows ? *reinterpret_cast<const uint4*>(q0 + (size_t)row * D +
-                                                                        x * kPackedGroup + c * 8)
-                                       : make_uint4(0, 0, 0, 0);
-            // dims (0,1) (2,3) (4,5) (6,7) -> (0,4) (1,5) (2,6) (3,7)
-            qa[x][0][r] = __byte_perm(w.x, w.z, 0x5410);
-            qa[x][0][2 + r] = __byte_perm(w.x, w.z, 0x7632);
-            qa[x][1][r] = __byte_perm(w.y, w.w, 0x5410);
-            qa[x][1][2 + r] = __byte_perm(w.y, w.w, 0x7632);
-            float t = lo_bf16(w.x) + hi_bf16(w.x) + lo_bf16(w.y) + hi_bf16(w.y) + lo_bf16(w.z) +
-                      hi_bf16(w.z) + lo_bf16(w.w) + hi_bf16(w.w);
-            t += __shfl_xor_sync(0xffffffffu, t, 1);
-            t += __shfl_xor_sync(0xffffffffu, t, 2);
-            sum[r][x] = t;
-          }
-        // the three parts of the sums: k = part * NG + group
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          float part[3][NG];
-#pragma unroll
-          for (int x = 0; x < NG; ++x) {
-            part[0][x] = __bfloat162float(__float2bfloat16_rn(sum[r][x]));
-            part[1][x] = __bfloat162float(__float2bfloat16_rn(sum[r][x] - part[0][x]));
-            part[2][x] = sum[r][x] - part[0][x] - part[1][x];
-          }
-          if (NG == 4) {
-            const int x = 2 * (c & 1);
-            const float lo = c < 2 ? (x ? part[0][2 % NG] : part[0][0])
-                                   : (x ? part[1][2 % NG] : part[1][0]);
-            const float hi = c < 2 ? (x ? part[0][3 % NG] : part[0][1])
-                                   : (x ? part[1][3 % NG] : part[1][1]);
-            qs[r] = bf16_pair(lo, hi);
-            qs[2 + r] = c < 2 ? bf16_pair(x ? part[2][2 % NG] : part[2][0],
-                                          x ? part[2][3 % NG] : part[2][1])
-                              : 0u;
-          } else {
-            qs[r] = c == 0 ? bf16_pair(part[0][0], part[0][1])
-                    : c == 1 ? bf16_pair(part[1][0], part[1][1])
-                    : c == 2 ? bf16_pair(part[2][0], part[2][1]) : 0u;
-            qs[2 + r] = 0u;
-          }
-        }
-      }
-      bool ok = !*abort;
-      for (int i = 0; ok && i < n_blocks; ++i) {
-        const int st = taken % kStages;
-        ok = ptx::mbar_wait(&s.full[st], (taken / kStages) & 1, abort);
-        if (!ok) break;
-        const uint8_t* kr = s.ring[st];
-        const uint8_t* vr = kr + R::kBytes;
-        const int seen = list[i].seen;
-        const int key0 = warp * 32;
-        // scores of 16 rows x 32 keys
-        float sc[4][4];
-#pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
-          const int key = key0 + nt * 8 + gr;              // this lane's key as a B column
-          const int col = key0 + nt * 8 + 2 * c;           // its keys as accumulator columns
-          uint32_t w[NG];
-          if (NG == 4) {
-            const uint4 u = *reinterpret_cast<const uint4*>(kr + R::k_word(key, 0, c));
-            w[0] = u.x, w[1] = u.y, w[2 % NG] = u.z, w[3 % NG] = u.w;
-          } else {
-            const uint2 u = *reinterpret_cast<const uint2*>(kr + R::k_word(key, 0, c));
-            w[0] = u.x, w[1] = u.y;
-          }
+        for (int u = 0; u < 2; ++u) {
+          const int key = key0 + (2 * half + u) * 8 + gr;  // this lane's key as a B column
+          load_words<NG>(kr + R::k_word(key, 0, c), w[u]);
           const int x = NG == 4 ? 2 * (c & 1) : 0;
           const uint32_t mids =
               *reinterpret_cast<const uint16_t*>(kr + R::plane(R::kMidOffset, key, x)) |
               (uint32_t)*reinterpret_cast<const uint16_t*>(kr + R::plane(R::kMidOffset, key, x + 1))
                   << 16;
-          float acc[NG][4];
-          sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
-          mma_16816(sc[nt], qs, mids, mids);
+          mma_16816(sc[2 * half + u], qs, mids, mids, 0.f, 0.f, 0.f, 0.f);
+        }
 #pragma unroll
-          for (int y = 0; y < NG; ++y) {
-            acc[y][0] = acc[y][1] = acc[y][2] = acc[y][3] = 0.f;
-            mma_16816(acc[y], qa[y][0], code_pair(w[y]), code_pair(w[y] >> 4));
-            mma_16816(acc[y], qa[y][1], code_pair(w[y] >> 8), code_pair(w[y] >> 12));
-          }
+        for (int y = 0; y < NG; ++y) {
+          const uint4 a0 = s.qf[y][0][lane], a1 = s.qf[y][1][lane];
+          const float i0 = -24.f * s.qsum[y][gr], i1 = -24.f * s.qsum[y][gr + 8];
 #pragma unroll
-          for (int y = 0; y < NG; ++y) {
-            const uint32_t st2 =
-                *reinterpret_cast<const uint32_t*>(kr + R::plane(R::kStepOffset, col, y));
-            const float s0 = lo_bf16(st2), s1 = hi_bf16(st2);
-            sc[nt][0] = fmaf(acc[y][0], s0, sc[nt][0]);
-            sc[nt][1] = fmaf(acc[y][1], s1, sc[nt][1]);
-            sc[nt][2] = fmaf(acc[y][2], s0, sc[nt][2]);
-            sc[nt][3] = fmaf(acc[y][3], s1, sc[nt][3]);
-          }
-          if (seen < kPackedBlock) {                       // whatever the unused bytes held
-            if (col >= seen) sc[nt][0] = sc[nt][2] = -INFINITY;
-            if (col + 1 >= seen) sc[nt][1] = sc[nt][3] = -INFINITY;
+          for (int u = 0; u < 2; ++u) {
+            float acc[4];
+            mma_16816(acc, a0, code_pair_16(w[u][y] << 3), code_pair_16(w[u][y] >> 1), i0, i0, i1,
+                      i1);
+            mma_16816(acc, a1, code_pair_16(w[u][y] >> 5), code_pair_16(w[u][y] >> 9));
+            // its keys as accumulator columns: 2 c and 2 c + 1
+            const uint64_t step = widen_bf16(load_u32(
+                kr + R::plane(R::kStepOffset, key0 + (2 * half + u) * 8 + 2 * c, y)));
+            float(&t)[4] = sc[2 * half + u];
+            split_f32x2(fma_f32x2(f32x2(acc[0], acc[1]), step, f32x2(t[0], t[1])), t[0], t[1]);
+            split_f32x2(fma_f32x2(f32x2(acc[2], acc[3]), step, f32x2(t[2], t[3])), t[2], t[3]);
           }
         }
-        float mx[2] = {-INFINITY, -INFINITY};
+      }
+      // the stage of this group's block before: its other warps have most likely left it
+      if (gw == 0 && i >= kMmaGroups && i - kMmaGroups + kStages < n_blocks) {
+        ok = issue(first + i - kMmaGroups + kStages, i - kMmaGroups + kStages);
+        if (!ok) break;
+      }
+      if (seen < kPackedBlock) {
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
-          mx[0] = fmaxf(mx[0], fmaxf(sc[nt][0], sc[nt][1]));
-          mx[1] = fmaxf(mx[1], fmaxf(sc[nt][2], sc[nt][3]));
+          const int col = key0 + nt * 8 + 2 * c;
+          if (col >= seen) sc[nt][0] = sc[nt][2] = -INFINITY;
+          if (col + 1 >= seen) sc[nt][1] = sc[nt][3] = -INFINITY;
         }
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-          mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2)) * c1;
-        }
-        // -inf * 0 of a zero scale is no number: such rows stay at -inf
-        if (!(mx[0] > -INFINITY)) mx[0] = -INFINITY;
-        if (!(mx[1] > -INFINITY)) mx[1] = -INFINITY;
-        if (__any_sync(0xffffffffu, mx[0] > base[0] + kSlack || mx[1] > base[1] + kSlack)) {
-          float alpha[2];
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const float up = fmaxf(base[r], mx[r]);
-            alpha[r] = up == -INFINITY ? 1.f : ex2(base[r] - up);
-            base[r] = up;
-            l_run[r] *= alpha[r];
-          }
-#pragma unroll
-          for (int t = 0; t < 4 * NG; ++t) {
-            o[t][0] *= alpha[0];
-            o[t][1] *= alpha[0];
-            o[t][2] *= alpha[1];
-            o[t][3] *= alpha[1];
-          }
-          om[0] *= alpha[0];
-          om[1] *= alpha[0];
-          om[2] *= alpha[1];
-          om[3] *= alpha[1];
-        }
-        float sum[2] = {0.f, 0.f};
-        {
-          const float b0 = base[0] == -INFINITY ? 0.f : base[0];
-          const float b1 = base[1] == -INFINITY ? 0.f : base[1];
-#pragma unroll
-          for (int nt = 0; nt < 4; ++nt) {
-            sc[nt][0] = ex2(fmaf(sc[nt][0], c1, -b0));
-            sc[nt][1] = ex2(fmaf(sc[nt][1], c1, -b0));
-            sc[nt][2] = ex2(fmaf(sc[nt][2], c1, -b1));
-            sc[nt][3] = ex2(fmaf(sc[nt][3], c1, -b1));
-            sum[0] += sc[nt][0] + sc[nt][1];
-            sum[1] += sc[nt][2] + sc[nt][3];
-          }
-        }
-        l_run[0] += sum[0];
-        l_run[1] += sum[1];
-        if (kMass) {
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
-            sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
-          }
-          const float bs = c ? base[1] : base[0], sm = c ? sum[1] : sum[0];
-          if (c < 2)
-            weights[(warp * kRows + gr + 8 * c) * per + i] =
-                bs == -INFINITY ? -INFINITY : bs + __log2f(sm);
-        }
-        // outputs: 16 keys a step
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          const int key = key0 + ks * 16 + 2 * c;          // keys key, key + 1, key + 8, key + 9
-          const int pair = key / 2;
-          const uint8_t* v0 = vr + R::v_half(2 * pair, 0, gr);
-          const uint8_t* v1 = vr + R::v_half(2 * (pair + 4), 0, gr);
-          uint32_t va[NG], vb[NG];                         // NG / 2 words of each key of the pair
-          if (NG == 4) {
-            const uint4 u = *reinterpret_cast<const uint4*>(v0);
-            const uint4 t = *reinterpret_cast<const uint4*>(v1);
-            va[0] = u.x, va[1] = u.y, va[2 % NG] = u.z, va[3 % NG] = u.w;
-            vb[0] = t.x, vb[1] = t.y, vb[2 % NG] = t.z, vb[3 % NG] = t.w;
-          } else {
-            const uint2 u = *reinterpret_cast<const uint2*>(v0);
-            const uint2 t = *reinterpret_cast<const uint2*>(v1);
-            va[0] = u.x, va[1] = u.y;
-            vb[0] = t.x, vb[1] = t.y;
-          }
-          const float* p0 = sc[2 * ks];
-          const float* p1 = sc[2 * ks + 1];
-          {
-            uint32_t m0 = 0, m1 = 0;                       // mids of group gr as column gr
-            if (gr < NG) {
-              m0 = *reinterpret_cast<const uint32_t*>(vr + R::plane(R::kMidOffset, key, gr));
-              m1 = *reinterpret_cast<const uint32_t*>(vr + R::plane(R::kMidOffset, key + 8, gr));
-              if (seen < kPackedBlock) {
-                m0 = keep_seen(m0, key, seen);
-                m1 = keep_seen(m1, key + 8, seen);
-              }
-            }
-            const uint32_t pa[4] = {bf16_pair(p0[0], p0[1]), bf16_pair(p0[2], p0[3]),
-                                    bf16_pair(p1[0], p1[1]), bf16_pair(p1[2], p1[3])};
-            mma_16816(om, pa, m0, m1);
-          }
-#pragma unroll
-          for (int x = 0; x < NG; ++x) {
-            uint32_t w0 = *reinterpret_cast<const uint32_t*>(vr + R::plane(R::kStepOffset, key, x));
-            uint32_t w1 =
-                *reinterpret_cast<const uint32_t*>(vr + R::plane(R::kStepOffset, key + 8, x));
-            if (seen < kPackedBlock) {
-              w0 = keep_seen(w0, key, seen);
-              w1 = keep_seen(w1, key + 8, seen);
-            }
-            const float s0 = lo_bf16(w0), s1 = hi_bf16(w0), s2 = lo_bf16(w1), s3 = hi_bf16(w1);
-            const uint32_t pa[4] = {
-                bf16_pair(p0[0] * s0, p0[1] * s1), bf16_pair(p0[2] * s0, p0[3] * s1),
-                bf16_pair(p1[0] * s2, p1[1] * s3), bf16_pair(p1[2] * s2, p1[3] * s3)};
-            // the group's 16 bits of the two keys of each pair, a byte (two dims) at a time
-            const int word = x / 2, byte = 2 * (x & 1);
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const uint32_t pick = (uint32_t)(byte + y) * 0x0011u | (uint32_t)(4 + byte + y) * 0x1100u;
-              const uint32_t a = __byte_perm(va[word], va[NG / 2 + word], pick);
-              const uint32_t e = __byte_perm(vb[word], vb[NG / 2 + word], pick);
-              mma_16816(o[4 * x + 2 * y], pa, code_pair(a), code_pair(e));
-              mma_16816(o[4 * x + 2 * y + 1], pa, code_pair(a >> 4), code_pair(e >> 4));
-            }
-          }
-        }
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&s.empty[st]);
-        ++taken;
       }
-      if (!ok && lane == 0) {
-        s.abort = 1;
-        if (status) atomicExch(status, 0x412);
+      float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt) {
+        mx[0] = fmaxf(mx[0], fmaxf(sc[nt][0], sc[nt][1]));
+        mx[1] = fmaxf(mx[1], fmaxf(sc[nt][2], sc[nt][3]));
       }
-    }
-    // Every warp has left its loop.  Without an abort every copy has been consumed; after one,
-    // the producer waits for its last copies before the ring's memory is used again.
-    __syncthreads();
-    if (warp == kMmaWarps && lane == 0 && *abort)
-      for (int x = issued > kStages ? issued - kStages : 0; x < issued; ++x)
-        ptx::mbar_wait_timed(&s.full[x % kStages], (x / kStages) & 1);
-    __syncthreads();
-    if (warp < kMmaWarps) {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 1);
-        l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 2);
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2)) * c1;
       }
-      if (c == 0) {
-        s.wm[warp][gr] = base[0];
-        s.wm[warp][gr + 8] = base[1];
-        s.wl[warp][gr] = l_run[0];
-        s.wl[warp][gr + 8] = l_run[1];
-      }
-      // columns 2 c, 2 c + 1 of n-tile 4 x + i are dims 32 x + 4 column + i; the mid term of
-      // group x is in lane x / 2 of the quad, element x % 2
-#pragma unroll
-      for (int x = 0; x < NG; ++x)
+      if (__any_sync(0xffffffffu, mx[0] > base[0] + kSlack || mx[1] > base[1] + kSlack)) {
+        float alpha[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float mid = __shfl_sync(0xffffffffu, om[2 * r + (x & 1)], (lane & ~3) | (x >> 1));
+          const float up = fmaxf(base[r], mx[r]);
+          alpha[r] = up == -INFINITY ? 1.f : ex2(base[r] - up);
+          base[r] = up;
+          l_run[r] *= alpha[r];
+        }
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float4 v = make_float4(o[4 * x][2 * r + e] + mid, o[4 * x + 1][2 * r + e] + mid,
-                                         o[4 * x + 2][2 * r + e] + mid,
-                                         o[4 * x + 3][2 * r + e] + mid);
-            *reinterpret_cast<float4*>(
-                &s.part[warp][gr + 8 * r][x * kPackedGroup + 4 * (2 * c + e)]) = v;
+        for (int t = 0; t < 4 * NG; ++t) {
+          o[t][0] *= alpha[0];
+          o[t][1] *= alpha[0];
+          o[t][2] *= alpha[1];
+          o[t][3] *= alpha[1];
+        }
+        om[0] *= alpha[0];
+        om[1] *= alpha[0];
+        om[2] *= alpha[1];
+        om[3] *= alpha[1];
+      }
+      float sum[2] = {0.f, 0.f};
+      {
+        const float b0 = base[0] == -INFINITY ? 0.f : base[0];
+        const float b1 = base[1] == -INFINITY ? 0.f : base[1];
+        const uint64_t c2 = f32x2(c1, c1), n0 = f32x2(-b0, -b0), n1 = f32x2(-b1, -b1);
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) {
+          split_f32x2(fma_f32x2(f32x2(sc[nt][0], sc[nt][1]), c2, n0), sc[nt][0], sc[nt][1]);
+          split_f32x2(fma_f32x2(f32x2(sc[nt][2], sc[nt][3]), c2, n1), sc[nt][2], sc[nt][3]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[nt][e] = ex2(sc[nt][e]);
+          sum[0] += sc[nt][0] + sc[nt][1];
+          sum[1] += sc[nt][2] + sc[nt][3];
+        }
+      }
+      l_run[0] += sum[0];
+      l_run[1] += sum[1];
+      if (kMass) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
+          sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
+        }
+        const float bs = c ? base[1] : base[0], sm = c ? sum[1] : sum[0];
+        if (c < 2)
+          weights[(gw * kRows + gr + 8 * c) * per + i] =
+              bs == -INFINITY ? -INFINITY : bs + __log2f(sm);
+      }
+      // outputs: 16 keys a step
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        const int key = key0 + ks * 16 + 2 * c;            // keys key, key + 1, key + 8, key + 9
+        const int pair = key / 2;
+        uint32_t va[NG], vb[NG];                           // NG / 2 words of each key of the pair
+        load_words<NG>(vr + R::v_half(2 * pair, 0, gr), va);
+        load_words<NG>(vr + R::v_half(2 * (pair + 4), 0, gr), vb);
+        const float* p0 = sc[2 * ks];
+        const float* p1 = sc[2 * ks + 1];
+        const uint64_t p00 = f32x2(p0[0], p0[1]), p01 = f32x2(p0[2], p0[3]);
+        const uint64_t p10 = f32x2(p1[0], p1[1]), p11 = f32x2(p1[2], p1[3]);
+        {
+          uint32_t m0 = 0, m1 = 0;                         // mids of group gr as column gr
+          if (gr < NG) {
+            m0 = load_u32(vr + R::plane(R::kMidOffset, key, gr));
+            m1 = load_u32(vr + R::plane(R::kMidOffset, key + 8, gr));
+          }
+          mma_16816(om, make_uint4(bf16_pair(p00), bf16_pair(p01), bf16_pair(p10), bf16_pair(p11)),
+                    m0, m1);
+        }
+#pragma unroll
+        for (int x = 0; x < NG; ++x) {
+          const uint64_t s0 = widen_bf16(load_u32(vr + R::plane(R::kStepOffset, key, x)));
+          const uint64_t s1 = widen_bf16(load_u32(vr + R::plane(R::kStepOffset, key + 8, x)));
+          const uint4 pa = make_uint4(bf16_pair(mul_f32x2(p00, s0)), bf16_pair(mul_f32x2(p01, s0)),
+                                      bf16_pair(mul_f32x2(p10, s1)), bf16_pair(mul_f32x2(p11, s1)));
+          // the group's 16 bits of the two keys of each pair, a byte (two dims) at a time
+          const int word = x / 2, byte = 2 * (x & 1);
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t pick = (uint32_t)(byte + y) * 0x0011u | (uint32_t)(4 + byte + y) * 0x1100u;
+            const uint32_t a = __byte_perm(va[word], va[NG / 2 + word], pick);
+            const uint32_t e = __byte_perm(vb[word], vb[NG / 2 + word], pick);
+            mma_16816(o[4 * x + 2 * y], pa, code_pair(a), code_pair(e));
+            mma_16816(o[4 * x + 2 * y + 1], pa, code_pair(a >> 4), code_pair(e >> 4));
           }
         }
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&s.empty[st]);
     }
+    if (!ok && lane == 0) {
+      s.abort = 1;
+      if (status) atomicExch(status, 0x412);
+    }
+    // Every warp has left its loop.  Without an abort every copy has been consumed; after one,
+    // a warp waits for the last copy of every stage before the memory is used again.
+    __syncthreads();
+    if (*abort && warp == 0)
+      for (int x = 0; x < kStages; ++x)
+        if (s.last[x] >= 0) ptx::mbar_wait_timed(&s.full[x], (s.last[x] / kStages) & 1);
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 1);
+      l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 2);
+    }
+    if (c == 0) {
+      s.wm[warp][gr] = base[0];
+      s.wm[warp][gr + 8] = base[1];
+      s.wl[warp][gr] = l_run[0];
+      s.wl[warp][gr + 8] = l_run[1];
+    }
+    // columns 2 c, 2 c + 1 of n-tile 4 x + i are dims 32 x + 4 column + i; the mid term of
+    // group x is in lane x / 2 of the quad, element x % 2
+#pragma unroll
+    for (int x = 0; x < NG; ++x)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float mid = __shfl_sync(0xffffffffu, om[2 * r + (x & 1)], (lane & ~3) | (x >> 1));
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float4 v = make_float4(o[4 * x][2 * r + e] + mid, o[4 * x + 1][2 * r + e] + mid,
+                                       o[4 * x + 2][2 * r + e] + mid,
+                                       o[4 * x + 3][2 * r + e] + mid);
+          *reinterpret_cast<float4*>(
+              &s.part[warp][gr + 8 * r][x * kPackedGroup + 4 * (2 * c + e)]) = v;
+        }
+      }
     __syncthreads();
     // the CTA's outputs, sums and maxima
     if (threadIdx.x < kRows) {
@@ -692,12 +740,13 @@ packed_decode_mma(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict
         float sum = 0.f;
         for (int r = 0; r < rows; ++r)
           if (s.norm[r] != -INFINITY)
-            for (int w = 0; w < kMmaWarps; ++w)
+            for (int w = 0; w < kGroupWarps; ++w)
               sum += ex2(weights[(w * kRows + r) * per + i] - s.norm[r]);
         if (!*abort) atomicAdd(mass + (size_t)bg * p.nB + list[i].blk, sum);
       }
     // the next pass copies into the memory that held the warps' outputs
     if (h0 + kRows < p.G) ptx::fence_proxy_async_smem();
+    first += n_blocks;
     cluster.sync();                                        // the others have read this CTA's part
   }
 }
@@ -709,7 +758,7 @@ cudaError_t decode_mma(const Dims& p, int n_split, const void* q, const void* ca
   auto kern = packed_decode_mma<D, kMass>;
   const int per = (p.k + n_split - 1) / n_split;
   const size_t smem = sizeof(MmaSmem<D>) + sizeof(Entry) * per +
-                      (kMass ? sizeof(float) * kMmaWarps * kRows * per : 0);
+                      (kMass ? sizeof(float) * kGroupWarps * kRows * per : 0);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)smem);
   if (e != cudaSuccess) return e;
@@ -733,7 +782,7 @@ cudaError_t decode_mma(const Dims& p, int n_split, const void* q, const void* ca
 // and have a block each; with weights, as many as their lists need.
 int packed_splits(const Dims& p, bool mass) {
   int n = 1;
-  while (n < 8 && 2 * n <= p.k && 2 * n * p.B * p.Hkv <= 2 * 152) n *= 2;
+  while (n < 8 && 2 * n <= p.k && 2 * n * p.B * p.Hkv <= 152) n *= 2;
   while (n < 8 && (p.k + n - 1) / n > (mass ? kMaxMassList : kMaxList)) n *= 2;
   return n;
 }
