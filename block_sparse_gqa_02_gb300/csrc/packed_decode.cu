@@ -9,6 +9,7 @@
 // bf16 queries run on the tensor cores (packed_decode_mma), fp32 ones, and rows of more blocks
 // than its list holds, on the CUDA cores (packed_decode_simt).
 #include <cooperative_groups.h>
+#include <cuda_fp16.h>
 
 #include "packed_cache.cuh"
 #include "ptx.cuh"
@@ -206,32 +207,41 @@ packed_decode_simt(const T* __restrict__ q, const uint8_t* __restrict__ cache,
 // ------------------------------------------------------------------ tensor-core kernel
 //
 // The G <= 16 heads of a group (16 of them a pass) are the M rows of mma.sync.m16n8k16.  The
-// codes become exact bf16 integers, so products with them lose nothing, and steps and mids
-// enter in fp32:
+// codes become exact fp16 integers c = code - 8: a code or-ed into the mantissa of 1024 (or, four
+// bits further up, of 64) with 1032 (72) subtracted, so that two of them share a shift.  Steps
+// and mids enter apart from them:
 //   z_j = sum_g step_jg (q_g . c_jg) + sum_g mid_jg (sum of q_g),
-//   o_g = sum_j (p_j step_jg) c_jg + sum_j p_j mid_jg,      c = code - 8.
-// K's codes are or-ed into the mantissa of 16, and the accumulators (one per group of dims) start
-// at -24 times the rows' group sums of q, which takes the 16 and the 8 away without an
-// instruction per operand; V's are or-ed into that of 128 and 136 is subtracted (its sums run
-// over thousands of keys, where the offset would cost digits).  The scores' mid term is one MMA
-// whose A operand is the group sums of q, split in three bf16 parts (24 bits).  For the output
-// p_j step_jg is formed in fp32 and rounded once to bf16, as the 16-bit cache's kernel rounds
-// p_j; the mid term is an MMA with the mids as four more columns.
+//   o_g = sum_j (p_j step_jg) c_jg + sum_j p_j mid_jg.
+// Scores: q is brought to fp16 by a power of two per row (exact but for values below 2^-14 of
+// the row's largest, whose error is 2^-25 of that); the accumulators, one per group of dims, are
+// scaled by the steps in fp32; the mid term is one bf16 MMA whose A operand is the group sums
+// of q, split in three parts (24 bits).
+// Outputs: p and the steps are fp16 (steps relative to the largest of their group that the warp
+// has met, times 2^10), and so is their product: roundings of 2^-11, an eighth of what bf16 would
+// cost; products below 2^-24 of the largest step lose digits.  The mid term is a bf16 MMA with
+// the mids as four more columns.
 //
-// CTA = one split of a (sequence, KV head), two groups of four warps that take its blocks in
+// CTA = one split of a (sequence, KV head), three groups of four warps that take its blocks in
 // turn, 32 keys a warp, each warp with a softmax base of its own that moves only when a row's
-// maximum passes it by more than 8 (log2 units).  Whole records (K and V of a block, 160 D
+// maximum passes it by more than 4 (log2 units).  Whole records (K and V of a block, 160 D
 // contiguous bytes) come through a ring, one bulk copy each; a group's first warp refills a
-// stage in the middle of its next block, when the other warps have left the stage.  Q's
-// operands stay in shared memory: at 128 registers a thread two CTAs fit an SM.
+// stage in the middle of its next block, when the other warps have left the stage.  Twelve
+// warps leave a thread 168 registers, which hold Q's operands and the outputs.
+//
+// The CTAs of a cluster end by writing their partial outputs, maxima and sums into each
+// other's shared memory (each owns a share of the rows), so after one cluster barrier
+// everything is local.
 
-constexpr int kMmaGroups = 4;                              // groups of warps
+constexpr int kMmaGroups = 3;                              // groups of warps
 constexpr int kGroupWarps = 4;
 constexpr int kMmaWarps = kMmaGroups * kGroupWarps;
 constexpr int kMmaThreads = kMmaWarps * 32;
+constexpr int kMaxSplits = 8;          // CTAs of a cluster
 constexpr int kMaxList = 1024;         // blocks of a split
 constexpr int kMaxMassList = 128;      // blocks of a split whose weights are kept
-constexpr float kSlack = 8.f;
+constexpr float kSlack = 4.f;          // p <= 2^4
+constexpr int kStepShift = 10;         // steps below 2^11: p * step < 2^15 in fp16
+constexpr uint32_t kMinStepExp = 27;   // biased exponent of the smallest step, 2^-100
 
 struct Entry {
   int phys, seen, blk;
@@ -245,29 +255,39 @@ struct MmaSmem {
     __align__(128) uint8_t ring[kStages][PackedRecord<D>::kPairBytes];
     float part[kMmaWarps][kRows][D + 4];                   // the warps' outputs, after the ring
   };
-  float o[kRows][D];                   // the CTA's outputs, relative to m
-  uint4 qf[kGroups][2][32];            // Q as A operands, per lane
-  float qsum[kGroups][kRows];          // sums of q over a group of dims
-  float m[kRows], l[kRows], norm[kRows];
+  // from every CTA of the cluster: its outputs of this CTA's rows, its rows' maxima and sums
+  float o[kRows][D];                   // [split][row of this CTA][D]
+  float m[kMaxSplits][kRows], l[kMaxSplits][kRows];
+  float norm[kRows];
+  __half vstep[kMmaWarps][kGroups][32];                    // V's steps of a warp's keys
   float wm[kMmaWarps][kRows], wl[kMmaWarps][kRows];
   uint64_t full[kStages], empty[kStages];
   int last[kStages];                   // a stage's last copy
   int abort, count;
 };
 
-// d = a b + c
-__device__ __forceinline__ void mma_16816(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1,
-                                          float c0, float c1, float c2, float c3) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
-      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2),
-        "f"(c3));
+template <bool kBf16>
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1, float c0, float c1, float c2, float c3) {
+  if (kBf16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2),
+          "f"(c3));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2),
+          "f"(c3));
 }
-__device__ __forceinline__ void mma_16816(float (&d)[4], const uint4& a, uint32_t b0,
+template <bool kBf16>
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                           uint32_t b1) {
-  mma_16816(d, a, b0, b1, d[0], d[1], d[2], d[3]);
+  mma_16816<kBf16>(d, a, b0, b1, d[0], d[1], d[2], d[3]);
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -290,42 +310,38 @@ __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
-__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 
-// Codes in bits 3-6 and 19-22 of x as a pair of bf16 integers 16 + code.
-__device__ __forceinline__ uint32_t code_pair_16(uint32_t x) {
-  return (x & 0x00780078u) | 0x41804180u;
-}
-
-// Codes in bits 0-3 and 16-19 of x as a pair of bf16 integers -8 .. 7.
-__device__ __forceinline__ uint32_t code_pair(uint32_t x) {
-  const uint32_t v = (x & 0x000f000fu) | 0x43004300u;     // 128 + code
+// Pairs of fp16.
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x43084308u));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Codes in bits 0-3 and 16-19 (low) or 4-7 and 20-23 (high) of x as integers -8 .. 7.
+__device__ __forceinline__ uint32_t low_codes(uint32_t x) {
+  return sub_f16x2((x & 0x000f000fu) | 0x64006400u, 0x64086408u);    // 1024 + code - 1032
+}
+__device__ __forceinline__ uint32_t high_codes(uint32_t x) {
+  return sub_f16x2((x & 0x00f000f0u) | 0x54005400u, 0x54805480u);    // 64 + code - 72
 }
 
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ uint32_t bf16_pair(uint64_t x) {
-  float lo, hi;
-  split_f32x2(x, lo, hi);
-  return bf16_pair(lo, hi);
+__device__ __forceinline__ uint32_t f16_pair(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
-
 __device__ __forceinline__ float lo_bf16(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float hi_bf16(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
-__device__ __forceinline__ uint64_t widen_bf16(uint32_t x) {
-  return f32x2(lo_bf16(x), hi_bf16(x));
-}
 
-__device__ __forceinline__ uint32_t load_u32(const uint8_t* p) {
+__device__ __forceinline__ uint32_t load_u32(const void* p) {
   return *reinterpret_cast<const uint32_t*>(p);
 }
 
@@ -356,12 +372,15 @@ packed_decode_mma(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict
   float* weights = reinterpret_cast<float*>(list + per);   // [kGroupWarps][kRows][per], kMass only
   cg::cluster_group cluster = cg::this_cluster();
   const int split = (int)cluster.block_rank(), n_split = (int)cluster.num_blocks();
+  const int own = kRows / n_split;                         // rows that a CTA of the cluster ends
   const int bg = blockIdx.y, b = bg / p.Hkv, g = bg % p.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = warp / kGroupWarps, gw = warp % kGroupWarps;
   const int gr = lane >> 2, c = lane & 3;
   const volatile int* abort = &s.abort;
   const float c1 = p.sm_scale * kLog2e;
+  // the other CTAs have started before anything is written into their shared memory
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 
   // Copy number x (block x - first of the list) into its stage, once its last block has left it.
   auto issue = [&](int x, int i) {
@@ -378,6 +397,10 @@ packed_decode_mma(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict
   };
 
   if (warp == kMmaWarps - 1) {
+    // the split's blocks, in order, without entries that are no block of the sequence
+    const int i0 = min(p.k, split * per), i1 = min(p.k, i0 + per);
+    int blk = i0 + lane < i1 ? sel[(size_t)bg * p.k + i0 + lane] : -1;
+    const int L = seq_len_of(p, b), nB_b = (L + kPackedBlock - 1) / kPackedBlock;
     if (lane == 0) {
       for (int i = 0; i < kStages; ++i) {
         ptx::mbar_init(&s.full[i], 1);
@@ -387,18 +410,15 @@ packed_decode_mma(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict
       s.abort = 0;
       ptx::fence_barrier_init();
     }
-    // the split's blocks, in order, without entries that are no block of the sequence
-    const int L = seq_len_of(p, b), nB_b = (L + kPackedBlock - 1) / kPackedBlock;
-    const int i0 = min(p.k, split * per), i1 = min(p.k, i0 + per);
     int n = 0;
     for (int i = i0; i < i1; i += 32) {
-      const int blk = i + lane < i1 ? sel[(size_t)bg * p.k + i + lane] : -1;
       const int phys = blk >= 0 && blk < nB_b ? physical_block(p, b, blk) : -1;
       const uint32_t there = __ballot_sync(0xffffffffu, phys >= 0);
       if (phys >= 0)
         list[n + __popc(there & ((1u << lane) - 1))] =
             Entry{phys, min(kPackedBlock, L - blk * kPackedBlock), blk};
       n += __popc(there);
+      blk = i + 32 + lane < i1 ? sel[(size_t)bg * p.k + i + 32 + lane] : -1;
     }
     if (lane == 0) s.count = n;
     __syncwarp();
@@ -418,58 +438,79 @@ packed_decode_mma(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict
           }
           break;
         }
-    } else if (warp < NG) {
-      // Q as A operands, dims in the order of the codes in K's words: of group x, k-step kk
-      // holds dims 32 x + 8 c + (2 kk, 2 kk + 4) and (2 kk + 1, 2 kk + 5)
+    }
+    // Q as A operands, dims in the order of the codes in K's words: of group x, k-step kk holds
+    // dims 32 x + 8 c + (2 kk, 2 kk + 4) and (2 kk + 1, 2 kk + 5); rows gr and gr + 8
+    uint32_t qa[NG][2][4], qs[4];
+    float cr[2];                                           // score units to log2 units, per row
+    {
       const __nv_bfloat16* q0 = q + ((size_t)b * p.Hq + (size_t)g * p.G + h0) * D;
-      uint4 w[2];
+      float sum[2][NG];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int row = gr + 8 * r;
-        w[r] = row < rows ? *reinterpret_cast<const uint4*>(q0 + (size_t)row * D +
-                                                            warp * kPackedGroup + c * 8)
-                          : make_uint4(0, 0, 0, 0);
-        float t = lo_bf16(w[r].x) + hi_bf16(w[r].x) + lo_bf16(w[r].y) + hi_bf16(w[r].y) +
-                  lo_bf16(w[r].z) + hi_bf16(w[r].z) + lo_bf16(w[r].w) + hi_bf16(w[r].w);
-        t += __shfl_xor_sync(0xffffffffu, t, 1);
-        t += __shfl_xor_sync(0xffffffffu, t, 2);
-        if (c == 0) s.qsum[warp][row] = t;
+        uint4 w[NG];
+        uint32_t top = 0;                                  // largest |q| of the row, bf16 bits
+#pragma unroll
+        for (int x = 0; x < NG; ++x) {
+          w[x] = row < rows ? *reinterpret_cast<const uint4*>(q0 + (size_t)row * D +
+                                                              x * kPackedGroup + c * 8)
+                            : make_uint4(0, 0, 0, 0);
+          const uint32_t v[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) top = max(top, max(v[u] & 0x7fffu, (v[u] >> 16) & 0x7fffu));
+        }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const uint32_t e = min(max(top >> 7, 1u), 253u);
+        const float f = __uint_as_float((254u - e) << 23);
+        cr[r] = c1 * __uint_as_float(e << 23);
+#pragma unroll
+        for (int x = 0; x < NG; ++x) {
+          const float d0 = lo_bf16(w[x].x) * f, d1 = hi_bf16(w[x].x) * f;
+          const float d2 = lo_bf16(w[x].y) * f, d3 = hi_bf16(w[x].y) * f;
+          const float d4 = lo_bf16(w[x].z) * f, d5 = hi_bf16(w[x].z) * f;
+          const float d6 = lo_bf16(w[x].w) * f, d7 = hi_bf16(w[x].w) * f;
+          qa[x][0][r] = f16_pair(d0, d4);
+          qa[x][0][2 + r] = f16_pair(d1, d5);
+          qa[x][1][r] = f16_pair(d2, d6);
+          qa[x][1][2 + r] = f16_pair(d3, d7);
+          float t = ((d0 + d1) + (d2 + d3)) + ((d4 + d5) + (d6 + d7));
+          t += __shfl_xor_sync(0xffffffffu, t, 1);
+          t += __shfl_xor_sync(0xffffffffu, t, 2);
+          sum[r][x] = t;
+        }
       }
-      // dims (0,1) (2,3) (4,5) (6,7) -> (0,4) (1,5) and (2,6) (3,7)
-      s.qf[warp][0][lane] =
-          make_uint4(__byte_perm(w[0].x, w[0].z, 0x5410), __byte_perm(w[1].x, w[1].z, 0x5410),
-                     __byte_perm(w[0].x, w[0].z, 0x7632), __byte_perm(w[1].x, w[1].z, 0x7632));
-      s.qf[warp][1][lane] =
-          make_uint4(__byte_perm(w[0].y, w[0].w, 0x5410), __byte_perm(w[1].y, w[1].w, 0x5410),
-                     __byte_perm(w[0].y, w[0].w, 0x7632), __byte_perm(w[1].y, w[1].w, 0x7632));
+      // the group sums in three bf16 parts: k = part * NG + group
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const bool odd = NG == 4 && (c & 1);
+        const float t0 = odd ? sum[r][2 % NG] : sum[r][0], t1 = odd ? sum[r][3 % NG] : sum[r][1];
+        const float a0 = __bfloat162float(__float2bfloat16_rn(t0));
+        const float a1 = __bfloat162float(__float2bfloat16_rn(t1));
+        const float b0 = __bfloat162float(__float2bfloat16_rn(t0 - a0));
+        const float b1 = __bfloat162float(__float2bfloat16_rn(t1 - a1));
+        const uint32_t hi = bf16_pair(a0, a1), md = bf16_pair(b0, b1);
+        const uint32_t lo = bf16_pair(t0 - a0 - b0, t1 - a1 - b1);
+        if (NG == 4) {
+          qs[r] = c < 2 ? hi : md;
+          qs[2 + r] = c < 2 ? lo : 0u;
+        } else {
+          qs[r] = c == 0 ? hi : c == 1 ? md : c == 2 ? lo : 0u;
+          qs[2 + r] = 0u;
+        }
+      }
     }
     __syncthreads();
     const int n_blocks = s.count;
-    // the group sums of q in three bf16 parts: k = part * NG + group
-    uint4 qs;
-    {
-      uint32_t w[4];
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          float v[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int k = 8 * u + 2 * c + e, part = k / NG;
-            float t = s.qsum[k % NG][gr + 8 * r];
-            for (int y = 0; y < part; ++y) t -= __bfloat162float(__float2bfloat16_rn(t));
-            v[e] = part < 3 ? t : 0.f;
-          }
-          w[2 * u + r] = bf16_pair(v[0], v[1]);
-        }
-      qs = make_uint4(w[0], w[1], w[2], w[3]);
-    }
     float o[4 * NG][4], om[4];
     float base[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+    uint32_t vexp[NG];                                     // exponent of V's largest step so far
 #pragma unroll
     for (int t = 0; t < 4 * NG; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
     om[0] = om[1] = om[2] = om[3] = 0.f;
+#pragma unroll
+    for (int x = 0; x < NG; ++x) vexp[x] = kMinStepExp;
 
     const int key0 = gw * 32;
     bool ok = !*abort;
@@ -491,39 +532,59 @@ packed_decode_mma(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict
         ptx::fence_proxy_async_smem();                     // before the stage's next copy
         __syncwarp();
       }
-      // scores of 16 rows x 32 keys, two n-tiles (16 keys) at a time
-      float sc[4][4];
+      // V's steps of the warp's keys (one a lane) in fp16, relative to the largest of their group
+      {
+        uint32_t t[NG], e[NG];
+        bool grows = false;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t w[2][NG];
+        for (int x = 0; x < NG; ++x) {
+          t[x] = *reinterpret_cast<const uint16_t*>(vr + R::plane(R::kStepOffset, key0 + lane, x));
+          e[x] = __reduce_max_sync(0xffffffffu, t[x]) >> 7;
+          grows |= e[x] > vexp[x];
+        }
+        if (grows) {                                       // the same in all lanes
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int key = key0 + (2 * half + u) * 8 + gr;  // this lane's key as a B column
-          load_words<NG>(kr + R::k_word(key, 0, c), w[u]);
-          const int x = NG == 4 ? 2 * (c & 1) : 0;
-          const uint32_t mids =
-              *reinterpret_cast<const uint16_t*>(kr + R::plane(R::kMidOffset, key, x)) |
-              (uint32_t)*reinterpret_cast<const uint16_t*>(kr + R::plane(R::kMidOffset, key, x + 1))
-                  << 16;
-          mma_16816(sc[2 * half + u], qs, mids, mids, 0.f, 0.f, 0.f, 0.f);
+          for (int x = 0; x < NG; ++x) {
+            const float f = e[x] > vexp[x] ? ex2((float)vexp[x] - (float)e[x]) : 1.f;
+            vexp[x] = max(vexp[x], e[x]);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+              for (int v = 0; v < 4; ++v) o[4 * x + u][v] *= f;
+          }
         }
 #pragma unroll
-        for (int y = 0; y < NG; ++y) {
-          const uint4 a0 = s.qf[y][0][lane], a1 = s.qf[y][1][lane];
-          const float i0 = -24.f * s.qsum[y][gr], i1 = -24.f * s.qsum[y][gr + 8];
+        for (int x = 0; x < NG; ++x)
+          s.vstep[warp][x][lane] = __float2half_rn(
+              lo_bf16(t[x]) * __uint_as_float((254 + kStepShift - vexp[x]) << 23));
+        __syncwarp();
+      }
+      // scores of 16 rows x 32 keys
+      float sc[4][4];
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            float acc[4];
-            mma_16816(acc, a0, code_pair_16(w[u][y] << 3), code_pair_16(w[u][y] >> 1), i0, i0, i1,
-                      i1);
-            mma_16816(acc, a1, code_pair_16(w[u][y] >> 5), code_pair_16(w[u][y] >> 9));
-            // its keys as accumulator columns: 2 c and 2 c + 1
-            const uint64_t step = widen_bf16(load_u32(
-                kr + R::plane(R::kStepOffset, key0 + (2 * half + u) * 8 + 2 * c, y)));
-            float(&t)[4] = sc[2 * half + u];
-            split_f32x2(fma_f32x2(f32x2(acc[0], acc[1]), step, f32x2(t[0], t[1])), t[0], t[1]);
-            split_f32x2(fma_f32x2(f32x2(acc[2], acc[3]), step, f32x2(t[2], t[3])), t[2], t[3]);
-          }
+      for (int nt = 0; nt < 4; ++nt) {
+        const int key = key0 + nt * 8 + gr;                // this lane's key as a B column
+        uint32_t w[NG];
+        load_words<NG>(kr + R::k_word(key, 0, c), w);
+        const int x = NG == 4 ? 2 * (c & 1) : 0;
+        const uint32_t mids =
+            *reinterpret_cast<const uint16_t*>(kr + R::plane(R::kMidOffset, key, x)) |
+            (uint32_t)*reinterpret_cast<const uint16_t*>(kr + R::plane(R::kMidOffset, key, x + 1))
+                << 16;
+        mma_16816<true>(sc[nt], qs, mids, mids, 0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int y = 0; y < NG; ++y) {
+          float acc[4];
+          const uint32_t w8 = w[y] >> 8;
+          mma_16816<false>(acc, qa[y][0], low_codes(w[y]), high_codes(w[y]), 0.f, 0.f, 0.f, 0.f);
+          mma_16816<false>(acc, qa[y][1], low_codes(w8), high_codes(w8));
+          // its keys as accumulator columns: 2 c and 2 c + 1
+          const uint32_t st2 =
+              load_u32(kr + R::plane(R::kStepOffset, key0 + nt * 8 + 2 * c, y));
+          const uint64_t step = f32x2(lo_bf16(st2), hi_bf16(st2));
+          float(&t)[4] = sc[nt];
+          split_f32x2(fma_f32x2(f32x2(acc[0], acc[1]), step, f32x2(t[0], t[1])), t[0], t[1]);
+          split_f32x2(fma_f32x2(f32x2(acc[2], acc[3]), step, f32x2(t[2], t[3])), t[2], t[3]);
         }
       }
       // the stage of this group's block before: its other warps have most likely left it
@@ -548,7 +609,7 @@ packed_decode_mma(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2)) * c1;
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2)) * cr[r];
       }
       if (__any_sync(0xffffffffu, mx[0] > base[0] + kSlack || mx[1] > base[1] + kSlack)) {
         float alpha[2];
@@ -575,11 +636,12 @@ packed_decode_mma(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict
       {
         const float b0 = base[0] == -INFINITY ? 0.f : base[0];
         const float b1 = base[1] == -INFINITY ? 0.f : base[1];
-        const uint64_t c2 = f32x2(c1, c1), n0 = f32x2(-b0, -b0), n1 = f32x2(-b1, -b1);
+        const uint64_t r0 = f32x2(cr[0], cr[0]), r1 = f32x2(cr[1], cr[1]);
+        const uint64_t n0 = f32x2(-b0, -b0), n1 = f32x2(-b1, -b1);
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
-          split_f32x2(fma_f32x2(f32x2(sc[nt][0], sc[nt][1]), c2, n0), sc[nt][0], sc[nt][1]);
-          split_f32x2(fma_f32x2(f32x2(sc[nt][2], sc[nt][3]), c2, n1), sc[nt][2], sc[nt][3]);
+          split_f32x2(fma_f32x2(f32x2(sc[nt][0], sc[nt][1]), r0, n0), sc[nt][0], sc[nt][1]);
+          split_f32x2(fma_f32x2(f32x2(sc[nt][2], sc[nt][3]), r1, n1), sc[nt][2], sc[nt][3]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) sc[nt][e] = ex2(sc[nt][e]);
           sum[0] += sc[nt][0] + sc[nt][1];
@@ -609,23 +671,24 @@ packed_decode_mma(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict
         load_words<NG>(vr + R::v_half(2 * (pair + 4), 0, gr), vb);
         const float* p0 = sc[2 * ks];
         const float* p1 = sc[2 * ks + 1];
-        const uint64_t p00 = f32x2(p0[0], p0[1]), p01 = f32x2(p0[2], p0[3]);
-        const uint64_t p10 = f32x2(p1[0], p1[1]), p11 = f32x2(p1[2], p1[3]);
         {
           uint32_t m0 = 0, m1 = 0;                         // mids of group gr as column gr
           if (gr < NG) {
             m0 = load_u32(vr + R::plane(R::kMidOffset, key, gr));
             m1 = load_u32(vr + R::plane(R::kMidOffset, key + 8, gr));
           }
-          mma_16816(om, make_uint4(bf16_pair(p00), bf16_pair(p01), bf16_pair(p10), bf16_pair(p11)),
-                    m0, m1);
+          const uint32_t pb[4] = {bf16_pair(p0[0], p0[1]), bf16_pair(p0[2], p0[3]),
+                                  bf16_pair(p1[0], p1[1]), bf16_pair(p1[2], p1[3])};
+          mma_16816<true>(om, pb, m0, m1);
         }
+        const uint32_t ph[4] = {f16_pair(p0[0], p0[1]), f16_pair(p0[2], p0[3]),
+                                f16_pair(p1[0], p1[1]), f16_pair(p1[2], p1[3])};
 #pragma unroll
         for (int x = 0; x < NG; ++x) {
-          const uint64_t s0 = widen_bf16(load_u32(vr + R::plane(R::kStepOffset, key, x)));
-          const uint64_t s1 = widen_bf16(load_u32(vr + R::plane(R::kStepOffset, key + 8, x)));
-          const uint4 pa = make_uint4(bf16_pair(mul_f32x2(p00, s0)), bf16_pair(mul_f32x2(p01, s0)),
-                                      bf16_pair(mul_f32x2(p10, s1)), bf16_pair(mul_f32x2(p11, s1)));
+          const uint32_t s0 = load_u32(&s.vstep[warp][x][ks * 16 + 2 * c]);
+          const uint32_t s1 = load_u32(&s.vstep[warp][x][ks * 16 + 8 + 2 * c]);
+          const uint32_t pa[4] = {mul_f16x2(ph[0], s0), mul_f16x2(ph[1], s0),
+                                  mul_f16x2(ph[2], s1), mul_f16x2(ph[3], s1)};
           // the group's 16 bits of the two keys of each pair, a byte (two dims) at a time
           const int word = x / 2, byte = 2 * (x & 1);
 #pragma unroll
@@ -633,8 +696,8 @@ packed_decode_mma(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict
             const uint32_t pick = (uint32_t)(byte + y) * 0x0011u | (uint32_t)(4 + byte + y) * 0x1100u;
             const uint32_t a = __byte_perm(va[word], va[NG / 2 + word], pick);
             const uint32_t e = __byte_perm(vb[word], vb[NG / 2 + word], pick);
-            mma_16816(o[4 * x + 2 * y], pa, code_pair(a), code_pair(e));
-            mma_16816(o[4 * x + 2 * y + 1], pa, code_pair(a >> 4), code_pair(e >> 4));
+            mma_16816<false>(o[4 * x + 2 * y], pa, low_codes(a), low_codes(e));
+            mma_16816<false>(o[4 * x + 2 * y + 1], pa, high_codes(a), high_codes(e));
           }
         }
       }
@@ -648,10 +711,12 @@ packed_decode_mma(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict
     // Every warp has left its loop.  Without an abort every copy has been consumed; after one,
     // a warp waits for the last copy of every stage before the memory is used again.
     __syncthreads();
-    if (*abort && warp == 0)
-      for (int x = 0; x < kStages; ++x)
-        if (s.last[x] >= 0) ptx::mbar_wait_timed(&s.full[x], (s.last[x] / kStages) & 1);
-    __syncthreads();
+    if (*abort) {
+      if (warp == 0)
+        for (int x = 0; x < kStages; ++x)
+          if (s.last[x] >= 0) ptx::mbar_wait_timed(&s.full[x], (s.last[x] / kStages) & 1);
+      __syncthreads();
+    }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 1);
@@ -666,29 +731,34 @@ packed_decode_mma(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict
     // columns 2 c, 2 c + 1 of n-tile 4 x + i are dims 32 x + 4 column + i; the mid term of
     // group x is in lane x / 2 of the quad, element x % 2
 #pragma unroll
-    for (int x = 0; x < NG; ++x)
+    for (int x = 0; x < NG; ++x) {
+      const float f = __uint_as_float((vexp[x] - kStepShift) << 23);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const float mid = __shfl_sync(0xffffffffu, om[2 * r + (x & 1)], (lane & ~3) | (x >> 1));
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float4 v = make_float4(o[4 * x][2 * r + e] + mid, o[4 * x + 1][2 * r + e] + mid,
-                                       o[4 * x + 2][2 * r + e] + mid,
-                                       o[4 * x + 3][2 * r + e] + mid);
+          const float4 v = make_float4(
+              fmaf(o[4 * x][2 * r + e], f, mid), fmaf(o[4 * x + 1][2 * r + e], f, mid),
+              fmaf(o[4 * x + 2][2 * r + e], f, mid), fmaf(o[4 * x + 3][2 * r + e], f, mid));
           *reinterpret_cast<float4*>(
               &s.part[warp][gr + 8 * r][x * kPackedGroup + 4 * (2 * c + e)]) = v;
         }
       }
+    }
+    if (h0 == 0) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     __syncthreads();
-    // the CTA's outputs, sums and maxima
-    if (threadIdx.x < kRows) {
+    // the CTA's maxima and sums to every CTA of the cluster, its outputs to the rows' owners
+    if (threadIdx.x < kRows * n_split) {
+      const int r = threadIdx.x % kRows, to = threadIdx.x / kRows;
       float top = -INFINITY, sum = 0.f;
-      for (int w = 0; w < kMmaWarps; ++w) top = fmaxf(top, s.wm[w][threadIdx.x]);
+#pragma unroll
+      for (int w = 0; w < kMmaWarps; ++w) top = fmaxf(top, s.wm[w][r]);
       if (top != -INFINITY)
-        for (int w = 0; w < kMmaWarps; ++w)
-          sum += ex2(s.wm[w][threadIdx.x] - top) * s.wl[w][threadIdx.x];
-      s.m[threadIdx.x] = top;
-      s.l[threadIdx.x] = sum;
+#pragma unroll
+        for (int w = 0; w < kMmaWarps; ++w) sum += ex2(s.wm[w][r] - top) * s.wl[w][r];
+      *cluster.map_shared_rank(&s.m[split][r], to) = top;
+      *cluster.map_shared_rank(&s.l[split][r], to) = sum;
     }
     for (int e = threadIdx.x; e < kRows * D / 4; e += kMmaThreads) {
       const int r = e / (D / 4), d0 = e % (D / 4) * 4;
@@ -706,29 +776,28 @@ packed_decode_mma(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict
           v.z = fmaf(f, u.z, v.z);
           v.w = fmaf(f, u.w, v.w);
         }
-      *reinterpret_cast<float4*>(&s.o[r][d0]) = v;
+      *reinterpret_cast<float4*>(
+          cluster.map_shared_rank(&s.o[split * own + r % own][d0], r / own)) = v;
     }
     cluster.sync();
-    // every CTA forms the normalisers; each writes its share of the heads' outputs
     if (threadIdx.x < kRows) {
       const int r = threadIdx.x;
       float top = -INFINITY, sum = 0.f;
-      for (int x = 0; x < n_split; ++x) top = fmaxf(top, *cluster.map_shared_rank(&s.m[r], x));
+      for (int x = 0; x < n_split; ++x) top = fmaxf(top, s.m[x][r]);
       if (top != -INFINITY)
-        for (int x = 0; x < n_split; ++x)
-          sum += ex2(*cluster.map_shared_rank(&s.m[r], x) - top) *
-                 *cluster.map_shared_rank(&s.l[r], x);
+        for (int x = 0; x < n_split; ++x) sum += ex2(s.m[x][r] - top) * s.l[x][r];
       s.norm[r] = top == -INFINITY ? -INFINITY : top + __log2f(sum);
       if (lse && split == 0 && r < rows) lse[(size_t)b * p.Hq + g * p.G + h0 + r] = s.norm[r] * kLn2;
     }
     __syncthreads();
-    for (int e = split * kMmaThreads + threadIdx.x; e < rows * D / 2; e += n_split * kMmaThreads) {
-      const int r = e / (D / 2), d0 = e % (D / 2) * 2;
+    for (int e = threadIdx.x; e < own * D / 2; e += kMmaThreads) {
+      const int ro = e / (D / 2), r = split * own + ro, d0 = e % (D / 2) * 2;
+      if (r >= rows) break;
       float2 v = make_float2(0.f, 0.f);
       if (s.norm[r] != -INFINITY)
         for (int x = 0; x < n_split; ++x) {
-          const float f = ex2(*cluster.map_shared_rank(&s.m[r], x) - s.norm[r]);
-          const float2 u = *reinterpret_cast<const float2*>(cluster.map_shared_rank(&s.o[r][d0], x));
+          const float f = ex2(s.m[x][r] - s.norm[r]);
+          const float2 u = *reinterpret_cast<const float2*>(&s.o[x * own + ro][d0]);
           v.x = fmaf(f, u.x, v.x);
           v.y = fmaf(f, u.y, v.y);
         }
@@ -744,10 +813,13 @@ packed_decode_mma(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict
               sum += ex2(weights[(w * kRows + r) * per + i] - s.norm[r]);
         if (!*abort) atomicAdd(mass + (size_t)bg * p.nB + list[i].blk, sum);
       }
-    // the next pass copies into the memory that held the warps' outputs
-    if (h0 + kRows < p.G) ptx::fence_proxy_async_smem();
     first += n_blocks;
-    cluster.sync();                                        // the others have read this CTA's part
+    if (h0 + kRows < p.G) {
+      // the next pass copies into the memory that held the warps' outputs, and the others
+      // write into this CTA's
+      ptx::fence_proxy_async_smem();
+      cluster.sync();
+    }
   }
 }
 
@@ -782,8 +854,8 @@ cudaError_t decode_mma(const Dims& p, int n_split, const void* q, const void* ca
 // and have a block each; with weights, as many as their lists need.
 int packed_splits(const Dims& p, bool mass) {
   int n = 1;
-  while (n < 8 && 2 * n <= p.k && 2 * n * p.B * p.Hkv <= 152) n *= 2;
-  while (n < 8 && (p.k + n - 1) / n > (mass ? kMaxMassList : kMaxList)) n *= 2;
+  while (n < kMaxSplits && 2 * n <= p.k && 2 * n * p.B * p.Hkv <= 152) n *= 2;
+  while (n < kMaxSplits && (p.k + n - 1) / n > (mass ? kMaxMassList : kMaxList)) n *= 2;
   return n;
 }
 
