@@ -266,28 +266,34 @@ struct MmaSmem {
   int abort, count;
 };
 
+// d = a b, d += a b
 template <bool kBf16>
-__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                          uint32_t b1, float c0, float c1, float c2, float c3) {
+__device__ __forceinline__ void mma_new(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
   if (kBf16)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
-        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2),
-          "f"(c3));
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
   else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
-        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2),
-          "f"(c3));
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 template <bool kBf16>
-__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                          uint32_t b1) {
-  mma_16816<kBf16>(d, a, b0, b1, d[0], d[1], d[2], d[3]);
+__device__ __forceinline__ void mma_add(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+  if (kBf16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -322,13 +328,30 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// Codes in bits 0-3 and 16-19 (low) or 4-7 and 20-23 (high) of x as integers -8 .. 7.
-__device__ __forceinline__ uint32_t low_codes(uint32_t x) {
-  return sub_f16x2((x & 0x000f000fu) | 0x64006400u, 0x64086408u);    // 1024 + code - 1032
+// (x & mask) | magic in one instruction: the magic comes in a register that the compiler does not
+// know, as it would split the pair of constants into two instructions.
+template <uint32_t kMask>
+__device__ __forceinline__ uint32_t mask_or(uint32_t x, uint32_t magic) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "n"(kMask), "r"(magic));
+  return r;
 }
-__device__ __forceinline__ uint32_t high_codes(uint32_t x) {
-  return sub_f16x2((x & 0x00f000f0u) | 0x54005400u, 0x54805480u);    // 64 + code - 72
+__device__ __forceinline__ uint32_t opaque(uint32_t x) {
+  uint32_t r;
+  asm volatile("mov.b32 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
+// Codes in bits 0-3 and 16-19 (low) or 4-7 and 20-23 (high) of x as integers -8 .. 7; the magics
+// are the fp16 pairs 1024 and 64.
+struct CodeMagic {
+  uint32_t low = opaque(0x64006400u), high = opaque(0x54005400u);
+  __device__ __forceinline__ uint32_t lows(uint32_t x) const {
+    return sub_f16x2(mask_or<0x000f000fu>(x, low), 0x64086408u);     // 1024 + code - 1032
+  }
+  __device__ __forceinline__ uint32_t highs(uint32_t x) const {
+    return sub_f16x2(mask_or<0x00f000f0u>(x, high), 0x54805480u);    // 64 + code - 72
+  }
+};
 
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -513,6 +536,7 @@ packed_decode_mma(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict
     for (int x = 0; x < NG; ++x) vexp[x] = kMinStepExp;
 
     const int key0 = gw * 32;
+    const CodeMagic codes;
     bool ok = !*abort;
     for (int i = group; ok && i < n_blocks; i += kMmaGroups) {
       const int st = (first + i) % kStages;
@@ -571,13 +595,13 @@ packed_decode_mma(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict
             *reinterpret_cast<const uint16_t*>(kr + R::plane(R::kMidOffset, key, x)) |
             (uint32_t)*reinterpret_cast<const uint16_t*>(kr + R::plane(R::kMidOffset, key, x + 1))
                 << 16;
-        mma_16816<true>(sc[nt], qs, mids, mids, 0.f, 0.f, 0.f, 0.f);
+        mma_new<true>(sc[nt], qs, mids, mids);
 #pragma unroll
         for (int y = 0; y < NG; ++y) {
           float acc[4];
           const uint32_t w8 = w[y] >> 8;
-          mma_16816<false>(acc, qa[y][0], low_codes(w[y]), high_codes(w[y]), 0.f, 0.f, 0.f, 0.f);
-          mma_16816<false>(acc, qa[y][1], low_codes(w8), high_codes(w8));
+          mma_new<false>(acc, qa[y][0], codes.lows(w[y]), codes.highs(w[y]));
+          mma_add<false>(acc, qa[y][1], codes.lows(w8), codes.highs(w8));
           // its keys as accumulator columns: 2 c and 2 c + 1
           const uint32_t st2 =
               load_u32(kr + R::plane(R::kStepOffset, key0 + nt * 8 + 2 * c, y));
@@ -679,7 +703,7 @@ packed_decode_mma(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict
           }
           const uint32_t pb[4] = {bf16_pair(p0[0], p0[1]), bf16_pair(p0[2], p0[3]),
                                   bf16_pair(p1[0], p1[1]), bf16_pair(p1[2], p1[3])};
-          mma_16816<true>(om, pb, m0, m1);
+          mma_add<true>(om, pb, m0, m1);
         }
         const uint32_t ph[4] = {f16_pair(p0[0], p0[1]), f16_pair(p0[2], p0[3]),
                                 f16_pair(p1[0], p1[1]), f16_pair(p1[2], p1[3])};
@@ -696,8 +720,8 @@ packed_decode_mma(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict
             const uint32_t pick = (uint32_t)(byte + y) * 0x0011u | (uint32_t)(4 + byte + y) * 0x1100u;
             const uint32_t a = __byte_perm(va[word], va[NG / 2 + word], pick);
             const uint32_t e = __byte_perm(vb[word], vb[NG / 2 + word], pick);
-            mma_16816<false>(o[4 * x + 2 * y], pa, low_codes(a), low_codes(e));
-            mma_16816<false>(o[4 * x + 2 * y + 1], pa, high_codes(a), high_codes(e));
+            mma_add<false>(o[4 * x + 2 * y], pa, codes.lows(a), codes.lows(e));
+            mma_add<false>(o[4 * x + 2 * y + 1], pa, codes.highs(a), codes.highs(e));
           }
         }
       }
