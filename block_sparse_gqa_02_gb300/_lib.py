@@ -117,6 +117,8 @@ def load(build_if_missing: bool = True, variant: str | None = None):
     """The loaded library of `variant` (default: the process's variant, see
     MSA_LIBRARY_VARIANT), built in-tree with nvcc on first use if needed."""
     variant = _active if variant is None else variant
+    if variant in _libs:
+        return _libs[variant]
     if variant not in ("release", "debug"):
         raise ValueError(f"unknown MSA library variant {variant!r}")
     with _lock:
@@ -152,8 +154,7 @@ def _ptr(x):
 
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return (_torch or _get_torch()).cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -278,32 +279,51 @@ def msa_sparse_decode_paged(shape: MsaShape, seq_lens, block_table, n_phys, q, k
 
 # ----------------------------- rotary positions, the 4-bit cache, eviction by weight
 
-def _arg(x, name, dtype=None, numel=None):
-    """Device pointer of a tensor that must be contiguous, of `dtype` and (at least) `numel`
-    elements, and on the current CUDA device (the one the kernels run on); of an int (a raw
-    pointer) or None as they are."""
-    if x is None or isinstance(x, int):
-        return x
-    import torch
-    if not x.is_cuda or x.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {x.device}, not on the current CUDA device")
-    if dtype is not None and x.dtype is not _torch_dtype(dtype):
-        raise ValueError(f"{name} is {x.dtype}, expected {_torch_dtype(dtype)}")
-    if numel is not None and x.numel() < numel:
-        raise ValueError(f"{name} has {x.numel()} elements, expected {numel}")
-    return _ptr(x)
-
-
+_torch = None
 _TORCH_DTYPES = {}
 
 
-def _torch_dtype(code):
-    if not _TORCH_DTYPES:
+def _get_torch():
+    global _torch
+    if _torch is None:
         import torch
         _TORCH_DTYPES.update({MSA_F32: torch.float32, MSA_BF16: torch.bfloat16,
                               "f32": torch.float32, "i32": torch.int32, "i64": torch.int64,
                               "u8": torch.uint8})
+        _torch = torch
+    return _torch
+
+
+def _torch_dtype(code):
+    _get_torch()
     return _TORCH_DTYPES[code]
+
+
+def _arg(x, name, dtype=None, numel=0, device=None):
+    """Device pointer of a tensor that must be contiguous, of `dtype` and at least `numel`
+    elements, and on `device` (default: the current CUDA device, the one kernels run on); of an
+    int (a raw pointer) or None as they are."""
+    if x is None or isinstance(x, int):
+        return x
+    torch = _torch or _get_torch()
+    if device is None:
+        device = _device()
+    if x.get_device() != device:
+        raise ValueError(f"{name} is on {x.device}, not on the current CUDA device {device}")
+    if dtype is not None and x.dtype is not _TORCH_DTYPES[dtype]:
+        raise ValueError(f"{name} is {x.dtype}, expected {_TORCH_DTYPES[dtype]}")
+    if x.numel() < numel:
+        raise ValueError(f"{name} has {x.numel()} elements, expected {numel}")
+    if not x.is_contiguous():
+        raise ValueError("MSA tensors must be contiguous")
+    return x.data_ptr()
+
+
+def _device():
+    """The current CUDA device, or -2 (no tensor's) on a machine without one."""
+    torch = _torch or _get_torch()
+    return torch.cuda.current_device() if torch.cuda.is_initialized() or \
+        torch.cuda.is_available() else -2
 
 
 def make_rope(batch, seq, dtype="bf16", pos_offset=0, scale=0.0, interleaved=False,
@@ -354,45 +374,52 @@ def msa_rope(desc: MsaRope, tensors: RopeTensors, positions=None, stream=None):
                            _stream(stream)), "msa_rope")
 
 
-def _cache_args(shape, seq_lens, block_table, n_phys, cache):
-    return (_arg(seq_lens, "seq_lens", "i32", shape.batch),
-            _arg(block_table, "block_table", "i32", shape.batch * shape.n_blocks), int(n_phys),
-            _arg(cache, "cache", "u8", int(n_phys) * shape.n_heads_kv * 160 * shape.head_dim))
+def _cache_args(shape, seq_lens, block_table, n_phys, cache, dev):
+    n_phys = int(n_phys)
+    return (_arg(seq_lens, "seq_lens", "i32", shape.batch, dev),
+            block_table if block_table is None else
+            _arg(block_table, "block_table", "i32", shape.batch * shape.n_blocks, dev), n_phys,
+            _arg(cache, "cache", "u8", n_phys * shape.n_heads_kv * 160 * shape.head_dim, dev))
 
 
 def msa_cache_pack(shape: MsaShape, n_new, starts, seq_lens, block_table, n_phys, k, v, cache,
                    stream=None):
-    sl, bt, n_phys, c = _cache_args(shape, seq_lens, block_table, n_phys, cache)
+    dev = _device()
+    sl, bt, n_phys, c = _cache_args(shape, seq_lens, block_table, n_phys, cache, dev)
     n = shape.batch * shape.n_heads_kv * int(n_new) * shape.head_dim
     _check(load().msa_cache_pack(ctypes.byref(shape), int(n_new),
-                                 _arg(starts, "starts", "i32", shape.batch), sl, bt, n_phys,
-                                 _arg(k, "k", shape.dtype, n), _arg(v, "v", shape.dtype, n), c,
-                                 _stream(stream)), "msa_cache_pack")
+                                 _arg(starts, "starts", "i32", shape.batch, dev), sl, bt, n_phys,
+                                 _arg(k, "k", shape.dtype, n, dev),
+                                 _arg(v, "v", shape.dtype, n, dev), c, _stream(stream)),
+           "msa_cache_pack")
 
 
 def msa_cache_unpack(shape: MsaShape, n_out, starts, seq_lens, block_table, n_phys, cache, k, v,
                      stream=None):
-    sl, bt, n_phys, c = _cache_args(shape, seq_lens, block_table, n_phys, cache)
+    dev = _device()
+    sl, bt, n_phys, c = _cache_args(shape, seq_lens, block_table, n_phys, cache, dev)
     n = shape.batch * shape.n_heads_kv * int(n_out) * shape.head_dim
     _check(load().msa_cache_unpack(ctypes.byref(shape), int(n_out),
-                                   _arg(starts, "starts", "i32", shape.batch), sl, bt, n_phys, c,
-                                   _arg(k, "k", shape.dtype, n), _arg(v, "v", shape.dtype, n),
-                                   _stream(stream)), "msa_cache_unpack")
+                                   _arg(starts, "starts", "i32", shape.batch, dev), sl, bt, n_phys,
+                                   c, _arg(k, "k", shape.dtype, n, dev),
+                                   _arg(v, "v", shape.dtype, n, dev), _stream(stream)),
+           "msa_cache_unpack")
 
 
-def _decode_args(shape, q, sel, out, lse, mass):
+def _decode_args(shape, q, sel, out, lse, mass, dev):
     n = shape.batch * shape.n_heads_q * shape.head_dim
     rows = shape.batch * shape.n_heads_kv
-    return (_arg(q, "q", shape.dtype, n), _arg(sel, "sel", "i32", rows * shape.top_k),
-            _arg(out, "out", shape.dtype, n),
-            _arg(lse, "lse", "f32", shape.batch * shape.n_heads_q),
-            _arg(mass, "mass", "f32", rows * shape.n_blocks))
+    return (_arg(q, "q", shape.dtype, n, dev), _arg(sel, "sel", "i32", rows * shape.top_k, dev),
+            _arg(out, "out", shape.dtype, n, dev),
+            _arg(lse, "lse", "f32", shape.batch * shape.n_heads_q, dev),
+            mass if mass is None else _arg(mass, "mass", "f32", rows * shape.n_blocks, dev))
 
 
 def msa_sparse_decode_packed(shape: MsaShape, seq_lens, block_table, n_phys, q, cache, sel, out,
                              lse=None, mass=None, stream=None):
-    sl, bt, n_phys, c = _cache_args(shape, seq_lens, block_table, n_phys, cache)
-    q, sel, out, lse, mass = _decode_args(shape, q, sel, out, lse, mass)
+    dev = _device()
+    sl, bt, n_phys, c = _cache_args(shape, seq_lens, block_table, n_phys, cache, dev)
+    q, sel, out, lse, mass = _decode_args(shape, q, sel, out, lse, mass, dev)
     _check(load().msa_sparse_decode_packed(ctypes.byref(shape), sl, bt, n_phys, q, c, sel, out,
                                            lse, mass, _stream(stream)),
            "msa_sparse_decode_packed")
@@ -400,28 +427,33 @@ def msa_sparse_decode_packed(shape: MsaShape, seq_lens, block_table, n_phys, q, 
 
 def msa_sparse_decode_mass(shape: MsaShape, seq_lens, block_table, n_phys, q, k, v, sel, out, lse,
                            mass, workspace, ws_bytes=None, stream=None):
+    dev = _device()
     if ws_bytes is None:
         ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     n = (int(n_phys) * shape.block_size if block_table is not None
          else shape.batch * shape.seq_k) * shape.n_heads_kv * shape.head_dim
-    q, sel, out, lse, mass = _decode_args(shape, q, sel, out, lse, mass)
+    q, sel, out, lse, mass = _decode_args(shape, q, sel, out, lse, mass, dev)
     _check(load().msa_sparse_decode_mass(
-        ctypes.byref(shape), _arg(seq_lens, "seq_lens", "i32", shape.batch),
-        _arg(block_table, "block_table", "i32", shape.batch * shape.n_blocks), int(n_phys), q,
-        _arg(k, "k", shape.dtype, n), _arg(v, "v", shape.dtype, n), sel, out, lse, mass,
-        _arg(workspace, "workspace"), ws_bytes, _stream(stream)), "msa_sparse_decode_mass")
+        ctypes.byref(shape), _arg(seq_lens, "seq_lens", "i32", shape.batch, dev),
+        block_table if block_table is None else
+        _arg(block_table, "block_table", "i32", shape.batch * shape.n_blocks, dev), int(n_phys), q,
+        _arg(k, "k", shape.dtype, n, dev), _arg(v, "v", shape.dtype, n, dev), sel, out, lse, mass,
+        _arg(workspace, "workspace", None, 0, dev), ws_bytes, _stream(stream)),
+        "msa_sparse_decode_mass")
 
 
 def msa_cache_evict(shape: MsaShape, keep, n_first, n_recent, seq_lens, mass, block_table, kept,
                     new_lens, mass_out, table_out=None, stream=None):
+    dev = _device()
     B, n = shape.batch, shape.batch * shape.n_blocks
     _check(load().msa_cache_evict(
         ctypes.byref(shape), int(keep), int(n_first), int(n_recent),
-        _arg(seq_lens, "seq_lens", "i32", B), _arg(mass, "mass", "f32", n * shape.n_heads_kv),
-        _arg(block_table, "block_table", "i32", n), _arg(kept, "kept", "i32", B * int(keep)),
-        _arg(new_lens, "new_lens", "i32", B),
-        _arg(mass_out, "mass_out", "f32", n * shape.n_heads_kv),
-        _arg(table_out, "table_out", "i32", n), _stream(stream)), "msa_cache_evict")
+        _arg(seq_lens, "seq_lens", "i32", B, dev),
+        _arg(mass, "mass", "f32", n * shape.n_heads_kv, dev),
+        _arg(block_table, "block_table", "i32", n, dev),
+        _arg(kept, "kept", "i32", B * int(keep), dev), _arg(new_lens, "new_lens", "i32", B, dev),
+        _arg(mass_out, "mass_out", "f32", n * shape.n_heads_kv, dev),
+        _arg(table_out, "table_out", "i32", n, dev), _stream(stream)), "msa_cache_evict")
 
 
 class GatherTensors:

@@ -1,11 +1,15 @@
 // Eviction of cache blocks by accumulated attention weight: which blocks of each sequence stay
 // (cache_evict_kernel), and moving them in contiguous caches (cache_gather_kernel).
 //
-// cache_evict_kernel, one CTA per sequence: block scores (the heads' weights summed in head
-// order) become order-preserving 32-bit keys in shared memory, an 8-bit radix select finds the
-// threshold, and a scan over the blocks turns "stays" and "goes" into a stable partition of
-// the block indices.  Rows are read whole before they are written, so outputs may be the
-// inputs.
+// cache_evict_kernel, one CTA per sequence, is a chain of short steps and bound by their
+// latency.  Block scores (the heads' weights summed in head order) become order-preserving
+// 32-bit keys that stay in registers, a contiguous run of blocks a thread; the threshold, the
+// largest key that at least the wanted number reach, is found bit by bit, each bit one count
+// over the CTA with a single barrier (histograms in shared memory took longer: weights share
+// few exponents, so their atomics collide).  A scan then turns "stays" and "goes" into a stable
+// partition of the block indices.  Outputs may be the inputs: kept weights move towards the
+// front, in chunks that are read whole before they are written, and the table's row goes
+// through shared memory.
 //
 // cache_gather_kernel streams bytes: one CTA per kept block of one head of one cache.
 #include "common.cuh"
@@ -24,8 +28,8 @@ __device__ __forceinline__ uint32_t score_key(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Exclusive prefix sum over the CTA of one value per thread; total receives the sum.
-__device__ __forceinline__ int scan(int v, int* warp_sums, int& total) {
+// Exclusive prefix sum over the CTA of one value per thread.
+__device__ __forceinline__ int scan(int v, int* warp_sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int x = v;
 #pragma unroll
@@ -35,33 +39,21 @@ __device__ __forceinline__ int scan(int v, int* warp_sums, int& total) {
   }
   if (lane == 31) warp_sums[warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    int w = warp_sums[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += y;
-    }
-    warp_sums[lane] = w;
-  }
-  __syncthreads();
-  const int before = (warp > 0 ? warp_sums[warp - 1] : 0) + x - v;
-  total = warp_sums[kWarps - 1];
-  __syncthreads();
-  return before;
+  // every warp adds up the warps before it
+  const int before = __reduce_add_sync(0xffffffffu, lane < warp ? warp_sums[lane] : 0);
+  return before + x - v;
 }
 
+// kPer: blocks a thread owns, thread t those from t kPer on; kPer * kThreads >= nB.
+template <int kPer>
 __global__ void __launch_bounds__(kThreads)
-cache_evict_kernel(const float* mass, const int32_t* table, int32_t* __restrict__ kept,
-                   int32_t* new_lens, float* mass_out, int32_t* table_out, Dims p, int keep,
-                   int n_first, int n_recent) {
-  extern __shared__ uint32_t keys[];                       // [nB]: keys, then a row being moved
-  uint16_t* order = reinterpret_cast<uint16_t*>(keys + p.nB);   // [nB]: kept, then dropped
-  __shared__ uint32_t hist[256];
-  __shared__ int warp_sums[kWarps];
-  __shared__ uint32_t s_digit;
-  __shared__ int s_remaining;
-  const int b = blockIdx.x, tid = threadIdx.x;
+cache_evict_kernel(const float* mass, const int32_t* table,
+                   int32_t* __restrict__ kept, int32_t* new_lens, float* mass_out,
+                   int32_t* table_out, Dims p, int keep, int n_first, int n_recent) {
+  extern __shared__ uint32_t row[];                        // [nB]: keys, then the table's row
+  uint16_t* order = reinterpret_cast<uint16_t*>(row + p.nB);    // [nB]: kept, then dropped
+  __shared__ int counts[2][kWarps], sums[2][kWarps];
+  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int L = seq_len_of(p, b), n = (L + p.Bk - 1) / p.Bk;
   const int nk = min(n, keep);
   const float* m0 = mass + (size_t)b * p.Hkv * p.nB;
@@ -70,93 +62,114 @@ cache_evict_kernel(const float* mass, const int32_t* table, int32_t* __restrict_
     for (int i = tid; i < n; i += kThreads) order[i] = (uint16_t)i;
   } else {
     const int lo = n_first, hi = n - n_recent;             // candidates [lo, hi)
-    for (int i = lo + tid; i < hi; i += kThreads) {
-      float x = m0[i];
-      for (int h = 1; h < p.Hkv; ++h) x = __fadd_rn(x, m0[(size_t)h * p.nB + i]);
-      keys[i] = score_key(x);
-    }
-    const int want = keep - n_first - n_recent;
-    uint32_t tau = 0xffffffffu;
-    int take_eq = 0;
-    if (want > 0) {
-      uint32_t prefix = 0, mask = 0;
-      int remaining = want;
-      for (int shift = 24; shift >= 0; shift -= 8) {
-        for (int i = tid; i < 256; i += kThreads) hist[i] = 0;
-        __syncthreads();
-        for (int i = lo + tid; i < hi; i += kThreads)
-          if ((keys[i] & mask) == prefix) atomicAdd(&hist[(keys[i] >> shift) & 255u], 1u);
-        __syncthreads();
-        if (tid < 32) {                                    // lane 0 holds bins 255..248
-          int c[8], sum = 0;
+    constexpr int kBatch = kPer < 8 ? kPer : 8;
+    for (int i0 = tid; i0 < n; i0 += kThreads * kBatch) {
+      float x[kBatch];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) sum += c[e] = (int)hist[255 - 8 * tid - e];
-          int incl = sum;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (tid >= o) incl += y;
-          }
-          int cum = incl - sum;
-          if (cum < remaining && remaining <= incl) {      // exactly one lane
-            int e = 0;
-            while (cum + c[e] < remaining) cum += c[e++];
-            s_digit = 255u - 8u * tid - e;
-            s_remaining = remaining - cum;
-          }
-        }
-        __syncthreads();
-        prefix |= s_digit << shift;
-        mask |= 255u << shift;
-        remaining = s_remaining;
-        __syncthreads();
+      for (int u = 0; u < kBatch; ++u) {
+        const int i = i0 + u * kThreads;
+        x[u] = i < n ? m0[i] : 0.f;
       }
-      tau = prefix;
-      take_eq = remaining;
+      for (int h = 1; h < p.Hkv; h += 3) {                 // three heads' loads in flight
+        float y[3][kBatch];
+#pragma unroll
+        for (int v = 0; v < 3; ++v)
+#pragma unroll
+          for (int u = 0; u < kBatch; ++u) {
+            const int i = i0 + u * kThreads;
+            y[v][u] = i < n && h + v < p.Hkv ? m0[(size_t)(h + v) * p.nB + i] : 0.f;
+          }
+#pragma unroll
+        for (int v = 0; v < 3; ++v)
+          if (h + v < p.Hkv) {
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) x[u] = __fadd_rn(x[u], y[v][u]);
+          }
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int i = i0 + u * kThreads;
+        if (i < n) row[i] = score_key(x[u]);
+      }
     }
-    // thread t owns the contiguous blocks [t c, t c + c)
-    const int c = (n + kThreads - 1) / kThreads;
-    const int i0 = min(n, tid * c), i1 = min(n, i0 + c);
     __syncthreads();
-    auto candidate = [&](int i) { return i >= lo && i < hi; };
-    int n_eq = 0, total;
-    if (want > 0)
-      for (int i = i0; i < i1; ++i) n_eq += candidate(i) && keys[i] == tau;
-    int rank = scan(n_eq, warp_sums, total);
-    auto stays = [&](int i, int& r) {
-      if (!candidate(i)) return true;
-      if (want <= 0) return false;
-      return keys[i] > tau || (keys[i] == tau && r++ < take_eq);
-    };
-    int n_stay = 0;
-    {
-      int r = rank;
-      for (int i = i0; i < i1; ++i) n_stay += stays(i, r);
+    // blocks outside [lo, hi) hold key 0 and never count: the thresholds below are above 0
+    uint32_t key[kPer];
+    const int i0 = tid * kPer;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) key[u] = i0 + u >= lo && i0 + u < hi ? row[i0 + u] : 0;
+    const int want = keep - n_first - n_recent;
+    // the largest threshold that at least `want` keys reach, and how many lie above it
+    uint32_t tau = 0;
+    int above = 0;
+    for (int bit = 31; bit >= 0; --bit) {
+      const uint32_t t = tau | 1u << bit;
+      int cnt = 0;
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) cnt += key[u] >= t;
+      cnt = __reduce_add_sync(0xffffffffu, cnt);
+      if (lane == 0) counts[bit & 1][warp] = cnt;
+      __syncthreads();
+      cnt = __reduce_add_sync(0xffffffffu, counts[bit & 1][lane]);
+      if (cnt >= want)
+        tau = t;
+      else
+        above = cnt;                                       // keys above the final threshold
     }
-    const int before = scan(n_stay, warp_sums, total);
-    int stay = before, go = nk + i0 - before;
-    for (int i = i0; i < i1; ++i) order[stays(i, rank) ? stay++ : go++] = (uint16_t)i;
+    // keys equal to it: the first want - above of them stay
+    int n_eq = 0;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) n_eq += i0 + u >= lo && i0 + u < hi && key[u] == tau;
+    int rank = scan(n_eq, sums[0]);
+    uint32_t stays = 0;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      const int i = i0 + u;
+      const bool candidate = i >= lo && i < hi;
+      const bool s = !candidate || (want > 0 && (key[u] > tau ||
+                                                 (key[u] == tau && rank < want - above)));
+      rank += candidate && key[u] == tau;
+      stays |= (uint32_t)(s && i < n) << u;
+    }
+    const int before = scan(__popc(stays), sums[1]);
+    int stay = before, go = nk + min(i0, n) - before;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u)
+      if (i0 + u < n) order[(stays >> u & 1) ? stay++ : go++] = (uint16_t)(i0 + u);
   }
   __syncthreads();
   for (int i = tid; i < keep; i += kThreads)
     kept[(size_t)b * keep + i] = i < nk ? (int)order[i] : -1;
   if (tid == 0) new_lens[b] = L - (n - nk) * p.Bk;
-  // rows go through shared memory whole: outputs may be the inputs
-  for (int h = 0; h < p.Hkv; ++h) {
-    const size_t row = ((size_t)b * p.Hkv + h) * p.nB;
-    float* buf = reinterpret_cast<float*>(keys);
-    __syncthreads();
-    for (int i = tid; i < n; i += kThreads) buf[i] = mass[row + i];
-    __syncthreads();
-    for (int i = tid; i < p.nB; i += kThreads) mass_out[row + i] = i < nk ? buf[order[i]] : 0.f;
-  }
-  if (table) {
-    const size_t row = (size_t)b * p.nB;
-    int32_t* buf = reinterpret_cast<int32_t*>(keys);
-    __syncthreads();
-    for (int i = tid; i < p.nB; i += kThreads) buf[i] = table[row + i];
-    __syncthreads();
-    for (int i = tid; i < p.nB; i += kThreads) table_out[row + i] = i < n ? buf[order[i]] : buf[i];
+  if (table)
+    for (int i = tid; i < p.nB; i += kThreads) row[i] = (uint32_t)table[(size_t)b * p.nB + i];
+  // weights: entry i comes from order[i] >= i, so a chunk that has been read may be written
+  // before the next is read; four entries a thread and head in flight
+  constexpr int kMove = 4;
+  for (int h = 0; h < p.Hkv; h += 4)
+    for (int c0 = 0; c0 < p.nB; c0 += kThreads * kMove) {
+      const size_t at = ((size_t)b * p.Hkv + h) * p.nB;
+      float x[4][kMove];
+#pragma unroll
+      for (int u = 0; u < kMove; ++u) {
+        const int i = c0 + u * kThreads + tid;
+        const int from = i < nk ? (int)order[i] : -1;
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          x[v][u] = from >= 0 && h + v < p.Hkv ? mass[at + (size_t)v * p.nB + from] : 0.f;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < kMove; ++u) {
+        const int i = c0 + u * kThreads + tid;
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          if (i < p.nB && h + v < p.Hkv) mass_out[at + (size_t)v * p.nB + i] = x[v][u];
+      }
+    }
+  if (table) {                                             // the row was read before the barriers
+    for (int i = tid; i < p.nB; i += kThreads)
+      table_out[(size_t)b * p.nB + i] = (int32_t)(i < n ? row[order[i]] : row[i]);
   }
 }
 
@@ -188,7 +201,16 @@ cache_gather_kernel(const __grid_constant__ GatherArgs a, const int32_t* __restr
   uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(t.dst) +
                                         (bh * t.dst_rows + d0) * t.row_bytes);
   const int64_t n = rows * (t.row_bytes / 16);
-  for (int64_t x = threadIdx.x; x < n; x += kGatherThreads) dst[x] = src[x];
+  constexpr int kFlight = 8;                               // 16-byte loads in flight per thread
+  for (int64_t x0 = threadIdx.x; x0 < n; x0 += kFlight * kGatherThreads) {
+    uint4 v[kFlight];
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u)
+      if (x0 + u * kGatherThreads < n) v[u] = __ldcs(src + x0 + u * kGatherThreads);
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u)
+      if (x0 + u * kGatherThreads < n) __stcs(dst + x0 + u * kGatherThreads, v[u]);
+  }
 }
 
 }  // namespace
@@ -198,11 +220,14 @@ cudaError_t launch_cache_evict(const Dims& p, int keep, int n_first, int n_recen
                                int32_t* new_lens, float* mass_out, int32_t* table_out,
                                cudaStream_t st) {
   const size_t smem = (size_t)p.nB * 6;
-  cudaError_t e = cudaFuncSetAttribute(cache_evict_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  auto kern = p.nB <= 1024   ? cache_evict_kernel<1>
+              : p.nB <= 8192 ? cache_evict_kernel<8>
+                             : cache_evict_kernel<32>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)smem);
   if (e != cudaSuccess) return e;
-  cache_evict_kernel<<<p.B, kThreads, smem, st>>>(mass, table, kept, new_lens, mass_out,
-                                                  table_out, p, keep, n_first, n_recent);
+  kern<<<p.B, kThreads, smem, st>>>(mass, table, kept, new_lens, mass_out, table_out, p, keep,
+                                    n_first, n_recent);
   return cudaGetLastError();
 }
 

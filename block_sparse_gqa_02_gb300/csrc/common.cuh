@@ -137,6 +137,13 @@ cudaError_t launch_index_kl(const Dims& p, const void* q, const void* k, const f
 // Workspace bytes of the index KL (0 on the CUDA-core path).
 size_t index_kl_workspace_bytes(const Dims& p);
 
+// Decode with the blocks' attention weights on the tensor-core kernel (sparse_attn.cu); ws as
+// for launch_sparse_decode, ws_b [B, Hq, k, 4] floats.
+cudaError_t launch_sparse_decode_mma_mass(const Dims& p, const void* q, const void* k,
+                                          const void* v, const int32_t* sel, void* out, float* lse,
+                                          float* mass, float* ws, float* ws_b, cudaStream_t st,
+                                          int* dev_status);
+
 // Decode split-KV: number of block groups each (sequence, KV head) is split into, and
 // the scratch it needs (partial outputs and partial log-sum-exps, fp32).
 int decode_num_splits(const Dims& p);

@@ -1,11 +1,16 @@
 // The attention weight that every selected block of a decode step receives, added up per KV
 // head: mass[b, g, blk] += sum over the group's heads h and the block's keys j of
-// exp(z_hj - lse_h), from the step's log-sum-exps.
+// exp(z_hj - lse_h).
 //
-// CTA = one selection entry of one (sequence, KV head): its keys' logits are formed in fp32
-// from K in shared memory, a thread per key, and the block's weight is one atomic addition, the
-// only one to its address in a call, so results repeat bit for bit.
+// Where decode runs on the tensor cores, its kernel writes each row's log-sum per block (k
+// floats a warp, nothing beside the keys it reads) and the merge forms the weights, so they
+// cost next to nothing.  Other shapes (fp32, head_dim 64, other blocks, wide groups) take
+// mass_kernel after the step: CTA = one selection entry of one (sequence, KV head), its keys'
+// logits formed again in fp32 from K in shared memory, a thread per key, and weighed by the
+// step's log-sum-exps.  Either way a block's weight is one atomic addition, the only one to its
+// address in a call, so results repeat bit for bit.
 #include "common.cuh"
+#include "sparse_decode_mma.cuh"
 
 namespace msa {
 
@@ -29,15 +34,7 @@ mass_kernel(const T* __restrict__ q, const T* __restrict__ k, const int32_t* __r
   const int L = seq_len_of(p, b), nB_b = (L + p.Bk - 1) / p.Bk;
   const int blk = sel[(size_t)bg * p.k + blockIdx.x];
   if (blk < 0 || blk >= nB_b) return;
-  const T* kb;
-  if (p.block_table) {
-    const int phys = p.block_table[(size_t)b * p.nB + blk];
-    // the paged attention reads zeros there; an entry that is no block gets no weight
-    if (phys < 0 || phys >= p.n_phys) return;
-    kb = k + ((size_t)phys * p.Hkv + g) * p.Bk * D;
-  } else {
-    kb = k + ((size_t)bg * p.Sk + (size_t)blk * p.Bk) * D;
-  }
+  const T* kb = k + ((size_t)bg * p.Sk + (size_t)blk * p.Bk) * D;
   const int seen = min(p.Bk, L - blk * p.Bk);
   for (int e = threadIdx.x; e < p.G * D; e += kThreads)
     qs[e] = to_f32(q[((size_t)b * p.Hq + g * p.G) * D + e]) * (p.sm_scale * kLog2e);
@@ -92,14 +89,19 @@ cudaError_t run_mass(const Dims& p, const void* q, const void* k, const int32_t*
 }  // namespace
 
 size_t decode_mass_workspace_bytes(const Dims& p) {
-  // the decode's scratch, and the log-sum-exps when the caller takes none
-  return (decode_workspace_bytes(p) + 15) / 16 * 16 + sizeof(float) * (size_t)p.B * p.Hq;
+  // the decode's scratch, and the blocks' log-sums or (should the caller take none) the
+  // log-sum-exps
+  const size_t more = sparse_decode_mma_supported(p) ? (size_t)p.k * kDecodeWarps : 1;
+  return (decode_workspace_bytes(p) + 15) / 16 * 16 + sizeof(float) * (size_t)p.B * p.Hq * more;
 }
 
 cudaError_t launch_sparse_decode_mass(const Dims& p, const void* q, const void* k, const void* v,
                                       const int32_t* sel, void* out, float* lse, float* mass,
                                       float* ws, cudaStream_t st, int* dev_status) {
-  if (!lse) lse = ws + (decode_workspace_bytes(p) + 15) / 16 * 4;
+  float* more = ws + (decode_workspace_bytes(p) + 15) / 16 * 4;
+  if (sparse_decode_mma_supported(p))
+    return launch_sparse_decode_mma_mass(p, q, k, v, sel, out, lse, mass, ws, more, st, dev_status);
+  if (!lse) lse = more;
   cudaError_t e = launch_sparse_decode(p, q, k, v, sel, out, lse, ws, st, dev_status);
   if (e != cudaSuccess) return e;
   if (p.dtype == 1)

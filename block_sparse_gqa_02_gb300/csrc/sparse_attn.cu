@@ -191,13 +191,11 @@ __global__ void __launch_bounds__(kThreads) sparse_decode_partial_simt(
   if (sub == 0) ws_l[slot] = ra.lse();
 }
 
-// o = sum_s exp(lse_s - lse) o_s with lse = log sum_s exp(lse_s).  One CTA per (b, h).
+// o = sum_s exp(lse_s - lse) o_s with lse = log sum_s exp(lse_s), for one (b, h).
 template <typename T, int D>
-__global__ void __launch_bounds__(D) decode_combine(const float* __restrict__ ws_o,
-                                                   const float* __restrict__ ws_l,
-                                                   T* __restrict__ out, float* __restrict__ lse,
-                                                   Dims p, int n_split) {
-  const int bh = blockIdx.x;
+__device__ __forceinline__ void combine_head(const float* __restrict__ ws_o,
+                                             const float* __restrict__ ws_l, T* __restrict__ out,
+                                             float* __restrict__ lse, int bh, int n_split) {
   const float* l = ws_l + (size_t)bh * n_split;
   float mx = -INFINITY;
   for (int s = 0; s < n_split; ++s) mx = fmaxf(mx, l[s]);
@@ -211,6 +209,69 @@ __global__ void __launch_bounds__(D) decode_combine(const float* __restrict__ ws
   }
   out[(size_t)bh * D + threadIdx.x] = from_f32<T>(den > 0.f ? acc / den : 0.f);
   if (lse && threadIdx.x == 0) lse[bh] = den > 0.f ? mx + logf(den) : -INFINITY;
+}
+
+// One CTA per (b, h).
+template <typename T, int D>
+__global__ void __launch_bounds__(D) decode_combine(const float* __restrict__ ws_o,
+                                                   const float* __restrict__ ws_l,
+                                                   T* __restrict__ out, float* __restrict__ lse,
+                                                   Dims p, int n_split) {
+  combine_head<T, D>(ws_o, ws_l, out, lse, blockIdx.x, n_split);
+}
+
+// The same, and after the B * Hq CTAs that do it one per (b, KV head) that adds the selected
+// blocks' attention weights to mass: sum over heads h and warps w of
+// exp2(ws_b[b, h, i, w] - log2 of head h's normaliser), heads in order. 
+template <typename T, int D>
+__global__ void __launch_bounds__(D) decode_combine_mass(
+    const float* __restrict__ ws_o, const float* __restrict__ ws_l, const float* __restrict__ ws_b,
+    const int32_t* __restrict__ sel, T* __restrict__ out, float* __restrict__ lse,
+    float* __restrict__ mass, Dims p, int n_split) {
+  constexpr int kChunk = 64;                               // selection entries at a time
+  constexpr int kMaxG = 16;
+  if ((int)blockIdx.x < p.B * p.Hq) {
+    combine_head<T, D>(ws_o, ws_l, out, lse, blockIdx.x, n_split);
+    return;
+  }
+  __shared__ float norm[kMaxG], part[kMaxG][kChunk];
+  const int bg = blockIdx.x - p.B * p.Hq, b = bg / p.Hkv, g = bg % p.Hkv;
+  const int L = seq_len_of(p, b), nB_b = (L + p.Bk - 1) / p.Bk;
+  const size_t head0 = (size_t)b * p.Hq + (size_t)g * p.G;
+  if ((int)threadIdx.x < p.G) {
+    const float* l = ws_l + (head0 + threadIdx.x) * n_split;
+    float mx = -INFINITY, den = 0.f;
+    for (int s = 0; s < n_split; ++s) mx = fmaxf(mx, l[s]);
+    if (mx != -INFINITY)
+      for (int s = 0; s < n_split; ++s) den += expf(l[s] - mx);
+    norm[threadIdx.x] = den > 0.f ? (mx + logf(den)) * kLog2e : -INFINITY;
+  }
+  __syncthreads();
+  for (int i0 = 0; i0 < p.k; i0 += kChunk) {
+    const int n = min(kChunk, p.k - i0);
+    for (int e = threadIdx.x; e < p.G * kChunk; e += D) {
+      const int h = e / kChunk, i = e % kChunk;
+      if (i >= n) continue;
+      const int blk = sel[(size_t)bg * p.k + i0 + i];
+      float sum = 0.f;
+      if (blk >= 0 && blk < nB_b && norm[h] != -INFINITY) {
+        static_assert(kDecodeWarps == 4, "one 16-byte load per entry");
+        const float4 v = *reinterpret_cast<const float4*>(
+            ws_b + ((head0 + h) * p.k + i0 + i) * kDecodeWarps);
+        sum = (exp2f(v.x - norm[h]) + exp2f(v.y - norm[h])) +
+              (exp2f(v.z - norm[h]) + exp2f(v.w - norm[h]));
+      }
+      part[h][i] = sum;
+    }
+    __syncthreads();
+    if ((int)threadIdx.x < n) {
+      const int blk = sel[(size_t)bg * p.k + i0 + threadIdx.x];
+      float sum = 0.f;
+      for (int h = 0; h < p.G; ++h) sum += part[h][threadIdx.x];
+      if (blk >= 0 && blk < nB_b) atomicAdd(mass + (size_t)bg * p.nB + blk, sum);
+    }
+    __syncthreads();
+  }
 }
 
 template <typename T, int D>
@@ -236,7 +297,8 @@ cudaError_t decode_split(const Dims& p, const void* q, const void* k, const void
   float* ws_l = ws + (size_t)p.B * p.Hq * n_split * D;
   cudaError_t e;
   if (sparse_decode_mma_supported(p)) {
-    e = launch_sparse_decode_mma(p, q, k, v, sel, ws_o, ws_l, n_split, per, st, dev_status);
+    e = launch_sparse_decode_mma(p, q, k, v, sel, ws_o, ws_l, nullptr, n_split, per, st,
+                                 dev_status);
   } else {
     const size_t smem = 2 * (size_t)kKC * D * sizeof(float);
     auto kern = sparse_decode_partial_simt<T, D>;
@@ -268,6 +330,22 @@ int decode_num_splits(const Dims& p) {
 size_t decode_workspace_bytes(const Dims& p) {
   const size_t slots = (size_t)p.B * p.Hq * decode_num_splits(p);
   return slots * ((size_t)p.d + 1) * sizeof(float);
+}
+
+cudaError_t launch_sparse_decode_mma_mass(const Dims& p, const void* q, const void* k,
+                                          const void* v, const int32_t* sel, void* out, float* lse,
+                                          float* mass, float* ws, float* ws_b, cudaStream_t st,
+                                          int* dev_status) {
+  const int n_split = decode_num_splits(p);
+  const int per = (p.k + n_split - 1) / n_split;
+  float* ws_o = ws;
+  float* ws_l = ws + (size_t)p.B * p.Hq * n_split * p.d;
+  cudaError_t e = launch_sparse_decode_mma(p, q, k, v, sel, ws_o, ws_l, ws_b, n_split, per, st,
+                                           dev_status);
+  if (e != cudaSuccess) return e;
+  decode_combine_mass<__nv_bfloat16, 128><<<p.B * (p.Hq + p.Hkv), 128, 0, st>>>(
+      ws_o, ws_l, ws_b, sel, (__nv_bfloat16*)out, lse, mass, p, n_split);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_sparse_prefill(const Dims& p, const void* q, const void* k, const void* v,

@@ -26,7 +26,7 @@ constexpr int kBk = 128;
 constexpr int kRowBytes = 128;
 constexpr int kBlockBytes = 2 * kBk * kRowBytes;   // one K or V block: [chunk][128][128 B]
 constexpr int kStages = 2;
-constexpr int kComputeWarps = 4;
+constexpr int kComputeWarps = kDecodeWarps;
 constexpr int kThreads = (kComputeWarps + 1) * 32;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -84,12 +84,15 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
+// kMass: also writes, for every row, selection entry and warp, log2 of the sum of exp2 of the
+// warp's scores in that block (ws_b [B, Hq, k, kDecodeWarps]); entries that are skipped are left.
+template <bool kMass>
 __global__ void __launch_bounds__(kThreads)
 sparse_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v,
                          const __nv_bfloat16* __restrict__ q, const int32_t* __restrict__ sel,
-                         float* __restrict__ ws_o, float* __restrict__ ws_l, Dims p, int n_split,
-                         int per, int* status) {
+                         float* __restrict__ ws_o, float* __restrict__ ws_l,
+                         float* __restrict__ ws_b, Dims p, int n_split, int per, int* status) {
   extern __shared__ uint8_t smem_raw[];
   Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                      ~uintptr_t(1023));
@@ -219,14 +222,30 @@ sparse_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k,
       }
       // P = exp2(S - m), bf16 A fragments for P.V (k = keys)
       uint32_t pa[2][4];
+      float blk_sum[2] = {0.f, 0.f};
 #pragma unroll
       for (int nt = 0; nt < 4; ++nt) {
         const float p0 = ex2(sc[nt][0] - mx[0]), p1 = ex2(sc[nt][1] - mx[0]);
         const float p2 = ex2(sc[nt][2] - mx[1]), p3 = ex2(sc[nt][3] - mx[1]);
         l_run[0] += p0 + p1;
         l_run[1] += p2 + p3;
+        if (kMass) {
+          blk_sum[0] += p0 + p1;
+          blk_sum[1] += p2 + p3;
+        }
         pa[nt >> 1][(nt & 1) * 2 + 0] = pack_bf16x2(p0, p1);
         pa[nt >> 1][(nt & 1) * 2 + 1] = pack_bf16x2(p2, p3);
+      }
+      if (kMass) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          blk_sum[r] += __shfl_xor_sync(0xffffffffu, blk_sum[r], 1);
+          blk_sum[r] += __shfl_xor_sync(0xffffffffu, blk_sum[r], 2);
+        }
+        const int row = gr + 8 * c;                          // lanes c = 0 and 1 write
+        if (c < 2 && row < G)
+          ws_b[(((size_t)b * p.Hq + (size_t)g * G + row) * p.k + i) * kDecodeWarps + warp] =
+              c ? mx[1] + __log2f(blk_sum[1]) : mx[0] + __log2f(blk_sum[0]);
       }
 #pragma unroll
       for (int nt = 0; nt < 16; ++nt) {
@@ -326,8 +345,8 @@ bool sparse_decode_mma_supported(const Dims& p) {
 }
 
 cudaError_t launch_sparse_decode_mma(const Dims& p, const void* q, const void* k, const void* v,
-                                     const int32_t* sel, float* ws_o, float* ws_l, int n_split,
-                                     int per, cudaStream_t st, int* status) {
+                                     const int32_t* sel, float* ws_o, float* ws_l, float* ws_b,
+                                     int n_split, int per, cudaStream_t st, int* status) {
   CUtensorMap tk, tv;
   // contiguous caches [B, Hkv, L, d] as (d, L, B*Hkv); paged pools [P, Hkv, 128, d] as
   // (d, 128, P*Hkv)
@@ -340,12 +359,12 @@ cudaError_t launch_sparse_decode_mma(const Dims& p, const void* q, const void* k
   if (e == cudaSuccess) e = make_tensor_map_bf16(&tv, v, 3, kd, ks, kbx);
   if (e != cudaSuccess) return e;
   const size_t smem = sizeof(Smem) + 1024;
-  e = cudaFuncSetAttribute(sparse_decode_mma_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)smem);
+  auto kern = ws_b ? sparse_decode_mma_kernel<true> : sparse_decode_mma_kernel<false>;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   dim3 grid(n_split, p.B * p.Hkv);
-  sparse_decode_mma_kernel<<<grid, kThreads, smem, st>>>(tk, tv, (const __nv_bfloat16*)q, sel,
-                                                         ws_o, ws_l, p, n_split, per, status);
+  kern<<<grid, kThreads, smem, st>>>(tk, tv, (const __nv_bfloat16*)q, sel, ws_o, ws_l, ws_b, p,
+                                     n_split, per, status);
   return cudaGetLastError();
 }
 
