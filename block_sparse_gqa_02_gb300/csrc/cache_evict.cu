@@ -1,18 +1,21 @@
 // Eviction of cache blocks by accumulated attention weight: which blocks of each sequence stay
 // (cache_evict_kernel), and moving them in contiguous caches (cache_gather_kernel).
 //
-// cache_evict_kernel, one CTA per sequence, is a chain of short steps and bound by their
-// latency.  Block scores (the heads' weights summed in head order) become order-preserving
-// 32-bit keys that stay in registers, a contiguous run of blocks a thread; the threshold, the
-// largest key that at least the wanted number reach, is found bit by bit, each bit one count
-// over the CTA with a single barrier (histograms in shared memory took longer: weights share
-// few exponents, so their atomics collide).  A scan then turns "stays" and "goes" into a stable
-// partition of the block indices.  Outputs may be the inputs: kept weights move towards the
-// front, in chunks that are read whole before they are written, and the table's row goes
-// through shared memory.
+// cache_evict_kernel is a chain of short steps and bound by their latency.  A cluster of CTAs
+// takes one sequence.  Each CTA makes the whole choice for itself (no exchange, and the weights
+// it reads are in L2 for the others): block scores (the heads' weights summed in head order)
+// become order-preserving 32-bit keys, a contiguous run of blocks a thread; a radix select over
+// 11, 11 and 10 bits finds the threshold; a scan turns "stays" and "goes" into a stable
+// partition of the block indices.  Then the CTAs share the rows to be moved.  Outputs may be
+// the inputs: all that a sequence's CTAs read lies before a cluster barrier, and what they
+// write after it.
 //
 // cache_gather_kernel streams bytes: one CTA per kept block of one head of one cache.
+#include <cooperative_groups.h>
+
 #include "common.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace msa {
 
@@ -20,6 +23,9 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
+constexpr int kMove = 4;               // entries of a row that a thread moves: 4096 a CTA
+constexpr int kMaxParts = 8;           // CTAs of a sequence
+static_assert(kMaxParts * kThreads * kMove >= kMaxBlocks, "a row is moved in one go");
 
 // Larger float -> larger key; -0 as +0; NaN below everything.
 __device__ __forceinline__ uint32_t score_key(float x) {
@@ -52,8 +58,10 @@ cache_evict_kernel(const float* mass, const int32_t* table,
                    int32_t* table_out, Dims p, int keep, int n_first, int n_recent) {
   extern __shared__ uint32_t row[];                        // [nB]: keys, then the table's row
   uint16_t* order = reinterpret_cast<uint16_t*>(row + p.nB);    // [nB]: kept, then dropped
-  __shared__ int counts[2][kWarps], sums[2][kWarps];
-  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ int hist[2048], sums[2][kWarps], found[2];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int part = (int)cluster.block_rank(), parts = (int)cluster.num_blocks();
+  const int b = blockIdx.x / parts, tid = threadIdx.x;
   const int L = seq_len_of(p, b), n = (L + p.Bk - 1) / p.Bk;
   const int nk = min(n, keep);
   const float* m0 = mass + (size_t)b * p.Hkv * p.nB;
@@ -93,34 +101,46 @@ cache_evict_kernel(const float* mass, const int32_t* table,
       }
     }
     __syncthreads();
-    // blocks outside [lo, hi) hold key 0 and never count: the thresholds below are above 0
     uint32_t key[kPer];
     const int i0 = tid * kPer;
 #pragma unroll
     for (int u = 0; u < kPer; ++u) key[u] = i0 + u >= lo && i0 + u < hi ? row[i0 + u] : 0;
     const int want = keep - n_first - n_recent;
-    // the largest threshold that at least `want` keys reach, and how many lie above it
-    uint32_t tau = 0;
+    // the want-th largest key (keys outside [lo, hi) are not counted), and how many are above it
+    uint32_t tau = 0xffffffffu;
     int above = 0;
-    for (int bit = 31; bit >= 0; --bit) {
-      const uint32_t t = tau | 1u << bit;
-      int cnt = 0;
+    if (want > 0) {
+      uint32_t prefix = 0, mask = 0;
+      for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+        const uint32_t digits = pass == 2 ? 1023u : 2047u;
+        for (int i = tid; i < 2048; i += kThreads) hist[i] = 0;
+        __syncthreads();
 #pragma unroll
-      for (int u = 0; u < kPer; ++u) cnt += key[u] >= t;
-      cnt = __reduce_add_sync(0xffffffffu, cnt);
-      if (lane == 0) counts[bit & 1][warp] = cnt;
-      __syncthreads();
-      cnt = __reduce_add_sync(0xffffffffu, counts[bit & 1][lane]);
-      if (cnt >= want)
-        tau = t;
-      else
-        above = cnt;                                       // keys above the final threshold
+        for (int u = 0; u < kPer; ++u)
+          if (i0 + u >= lo && i0 + u < hi && (key[u] & mask) == prefix)
+            atomicAdd(&hist[(key[u] >> shift) & digits], 1);
+        __syncthreads();
+        // thread t: digits 2047 - 2 t and 2046 - 2 t
+        const int a0 = hist[2047 - 2 * tid], a1 = hist[2046 - 2 * tid];
+        const int before = above + scan(a0 + a1, sums[pass & 1]);
+        if (before < want && want <= before + a0 + a1) {   // one thread
+          const bool second = want > before + a0;
+          found[0] = 2047 - 2 * tid - second;
+          found[1] = before + (second ? a0 : 0);
+        }
+        __syncthreads();
+        prefix |= (uint32_t)found[0] << shift;
+        mask |= digits << shift;
+        above = found[1];
+      }
+      tau = prefix;
     }
     // keys equal to it: the first want - above of them stay
     int n_eq = 0;
 #pragma unroll
     for (int u = 0; u < kPer; ++u) n_eq += i0 + u >= lo && i0 + u < hi && key[u] == tau;
-    int rank = scan(n_eq, sums[0]);
+    int rank = scan(n_eq, sums[1]);
     uint32_t stays = 0;
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
@@ -131,46 +151,45 @@ cache_evict_kernel(const float* mass, const int32_t* table,
       rank += candidate && key[u] == tau;
       stays |= (uint32_t)(s && i < n) << u;
     }
-    const int before = scan(__popc(stays), sums[1]);
+    const int before = scan(__popc(stays), sums[0]);
     int stay = before, go = nk + min(i0, n) - before;
 #pragma unroll
     for (int u = 0; u < kPer; ++u)
       if (i0 + u < n) order[(stays >> u & 1) ? stay++ : go++] = (uint16_t)(i0 + u);
   }
   __syncthreads();
-  for (int i = tid; i < keep; i += kThreads)
+  // the CTA's share of the rows, four entries of four heads a thread at a time; entry i comes
+  // from order[i]
+  const int share = (p.nB + parts - 1) / parts, e0 = part * share, e1 = min(p.nB, e0 + share);
+  const size_t trow = (size_t)b * p.nB;
+  for (int i = part * kThreads + tid; i < keep; i += parts * kThreads)
     kept[(size_t)b * keep + i] = i < nk ? (int)order[i] : -1;
-  if (tid == 0) new_lens[b] = L - (n - nk) * p.Bk;
   if (table)
-    for (int i = tid; i < p.nB; i += kThreads) row[i] = (uint32_t)table[(size_t)b * p.nB + i];
-  // weights: entry i comes from order[i] >= i, so a chunk that has been read may be written
-  // before the next is read; four entries a thread and head in flight
-  constexpr int kMove = 4;
-  for (int h = 0; h < p.Hkv; h += 4)
-    for (int c0 = 0; c0 < p.nB; c0 += kThreads * kMove) {
-      const size_t at = ((size_t)b * p.Hkv + h) * p.nB;
-      float x[4][kMove];
+    for (int i = e0 + tid; i < e1; i += kThreads)
+      row[i] = (uint32_t)table[trow + (i < n ? (int)order[i] : i)];
+  for (int h = 0; h < p.Hkv; h += 4) {
+    const size_t at = ((size_t)b * p.Hkv + h) * p.nB;
+    float x[4][kMove];
 #pragma unroll
-      for (int u = 0; u < kMove; ++u) {
-        const int i = c0 + u * kThreads + tid;
-        const int from = i < nk ? (int)order[i] : -1;
+    for (int u = 0; u < kMove; ++u) {
+      const int i = e0 + u * kThreads + tid;
+      const int from = i < e1 && i < nk ? (int)order[i] : -1;
 #pragma unroll
-        for (int v = 0; v < 4; ++v)
-          x[v][u] = from >= 0 && h + v < p.Hkv ? mass[at + (size_t)v * p.nB + from] : 0.f;
-      }
-      __syncthreads();
-#pragma unroll
-      for (int u = 0; u < kMove; ++u) {
-        const int i = c0 + u * kThreads + tid;
-#pragma unroll
-        for (int v = 0; v < 4; ++v)
-          if (i < p.nB && h + v < p.Hkv) mass_out[at + (size_t)v * p.nB + i] = x[v][u];
-      }
+      for (int v = 0; v < 4; ++v)
+        x[v][u] = from >= 0 && h + v < p.Hkv ? mass[at + (size_t)v * p.nB + from] : 0.f;
     }
-  if (table) {                                             // the row was read before the barriers
-    for (int i = tid; i < p.nB; i += kThreads)
-      table_out[(size_t)b * p.nB + i] = (int32_t)(i < n ? row[order[i]] : row[i]);
+    cluster.sync();
+#pragma unroll
+    for (int u = 0; u < kMove; ++u) {
+      const int i = e0 + u * kThreads + tid;
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        if (i < e1 && h + v < p.Hkv) mass_out[at + (size_t)v * p.nB + i] = x[v][u];
+    }
   }
+  if (part == 0 && tid == 0) new_lens[b] = L - (n - nk) * p.Bk;
+  if (table)
+    for (int i = e0 + tid; i < e1; i += kThreads) table_out[trow + i] = (int32_t)row[i];
 }
 
 constexpr int kGatherThreads = 256;
@@ -226,9 +245,22 @@ cudaError_t launch_cache_evict(const Dims& p, int keep, int n_first, int n_recen
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)smem);
   if (e != cudaSuccess) return e;
-  kern<<<p.B, kThreads, smem, st>>>(mass, table, kept, new_lens, mass_out, table_out, p, keep,
-                                    n_first, n_recent);
-  return cudaGetLastError();
+  int parts = (p.nB + kThreads - 1) / kThreads;            // at most an entry a thread, or all
+  if (parts > kMaxParts) parts = kMaxParts;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.B * parts);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = parts;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, mass, table, kept, new_lens, mass_out, table_out, p, keep,
+                            n_first, n_recent);
 }
 
 cudaError_t launch_cache_gather(int batch, const msa_gather_tensor* tensors, int n,

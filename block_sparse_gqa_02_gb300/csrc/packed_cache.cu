@@ -1,9 +1,9 @@
 // Tokens into the 4-bit KV cache and back (format: include/msa.h, packed_cache.cuh).
 //
-// CTA = the tokens of one call that fall into K's or V's record of one block and head.  Four
-// lanes hold a group of 32 dims, eight dims each: the group's range is two shuffles, and a
-// lane's eight codes are one 32-bit word of K's record or two 16-bit halves of V's.  Both
-// kernels stream, so HBM bounds them; V's halves lie 8 D bytes apart, so the record goes
+// CTA = the tokens of one call that fall into K's or V's record of one block and head.  Both
+// kernels stream, so HBM should bound them; what they cost is instructions, so packing gives a
+// thread a whole group of 32 dims (its range needs no shuffles, its scales are formed once) and
+// unpacking works on pairs of bf16.  V's 16-bit halves lie 16 D bytes apart, so the record goes
 // through shared memory: a block that is filled whole leaves it in 16-byte stores, of any other
 // only the stored tokens' bytes are written.  Unpacking stages the record when it needs a
 // quarter of it or more, and reads a few tokens' bytes where they are.
@@ -51,6 +51,69 @@ __device__ __forceinline__ Part part_of(const Dims& p, const int32_t* starts, in
   return r;
 }
 
+// The 32 values of a group, and its largest and smallest (NaN if there is one).
+template <typename T> struct GroupLoad;
+template <> struct GroupLoad<__nv_bfloat16> {
+  uint4 w[4];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+  __device__ __forceinline__ static __nv_bfloat162 pair(uint32_t x) {
+    return *reinterpret_cast<const __nv_bfloat162*>(&x);
+  }
+  __device__ __forceinline__ void range(float& hi, float& lo) const {
+    __nv_bfloat162 h = pair(w[0].x), l = h;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      h = __hmax2_nan(__hmax2_nan(h, pair(w[i].x)), __hmax2_nan(pair(w[i].y), pair(w[i].z)));
+      l = __hmin2_nan(__hmin2_nan(l, pair(w[i].x)), __hmin2_nan(pair(w[i].y), pair(w[i].z)));
+      h = __hmax2_nan(h, pair(w[i].w));
+      l = __hmin2_nan(l, pair(w[i].w));
+    }
+    hi = __bfloat162float(__hmax_nan(h.x, h.y));
+    lo = __bfloat162float(__hmin_nan(l.x, l.y));
+  }
+  // values 8 c .. 8 c + 7
+  __device__ __forceinline__ void eight(int c, float* x) const {
+    const uint32_t v[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(v[i] << 16);
+      x[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
+    }
+  }
+};
+template <> struct GroupLoad<float> {
+  float4 w[8];
+  __device__ __forceinline__ void load(const float* p) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = reinterpret_cast<const float4*>(p)[i];
+  }
+  __device__ __forceinline__ static float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+  }
+  __device__ __forceinline__ static float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+  }
+  __device__ __forceinline__ void range(float& hi, float& lo) const {
+    hi = lo = w[0].x;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      hi = max_nan(max_nan(hi, w[i].x), max_nan(max_nan(w[i].y, w[i].z), w[i].w));
+      lo = min_nan(min_nan(lo, w[i].x), min_nan(min_nan(w[i].y, w[i].z), w[i].w));
+    }
+  }
+  __device__ __forceinline__ void eight(int c, float* x) const {
+    reinterpret_cast<float4*>(x)[0] = w[2 * c];
+    reinterpret_cast<float4*>(x)[1] = w[2 * c + 1];
+  }
+};
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) pack_kernel(const T* __restrict__ k,
                                                         const T* __restrict__ v,
@@ -58,56 +121,58 @@ __global__ void __launch_bounds__(kThreads) pack_kernel(const T* __restrict__ k,
                                                         const int32_t* __restrict__ starts, int n,
                                                         int per_seq, Dims p) {
   using R = PackedRecord<D>;
-  constexpr int kLanes = D / 8;                            // lanes of one row
-  constexpr int kRowsAtOnce = kThreads / kLanes;
+  constexpr int NG = R::kGroups;
   __shared__ __align__(16) uint8_t image[R::kBytes];
   bool is_v;
   const Part part = part_of<D>(p, starts, n, per_seq, cache, is_v);
   if (!part.record) return;
-  const int lane = threadIdx.x % kLanes, grp = lane / 4, c = lane % 4;
-  const T* src = is_v ? v : k;
-  // whole warps go round together: the shuffles need all lanes
-  for (int r0 = part.lo; r0 < part.hi; r0 += kRowsAtOnce) {
-    const int row = r0 + (int)threadIdx.x / kLanes;
-    const bool there = row < part.hi;
-    float x[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) x[u] = 0.f;
-    if (there) {
-      const T* s = src + (size_t)(part.token + row - part.lo) * D + lane * 8;
-#pragma unroll
-      for (int u = 0; u < 8; u += Vec16<T>::N) Vec16<T>::load(s + u, x + u);
-    }
-    float hi = x[0], lo = x[0];
-    int bad = 0;
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      hi = fmaxf(hi, x[u]);
-      lo = fminf(lo, x[u]);
-      bad |= !(fabsf(x[u]) <= 3.402823466e38f);
-    }
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-      bad |= __shfl_xor_sync(0xffffffffu, bad, o);
-    }
-    if (!there) continue;
+  const T* src = (is_v ? v : k) + (size_t)part.token * D;
+  const int items = (part.hi - part.lo) * NG;              // a thread a group of 32 dims
+  for (int e = threadIdx.x; e < items; e += kThreads) {
+    const int row = part.lo + e / NG, g = e % NG;
+    GroupLoad<T> x;
+    x.load(src + (size_t)e * kPackedGroup);
+    float hi, lo;
+    x.range(hi, lo);
+    const bool bad = !(fabsf(hi) <= 3.402823466e38f && fabsf(lo) <= 3.402823466e38f);
     float step, mid, inv;
-    packed_scales(hi, lo, bad != 0, step, mid, inv);
-    uint32_t w = 0;
+    packed_scales(hi, lo, bad, step, mid, inv);
+    // codes are monotone in x: unless the ends of the range need it, nothing is clamped
+    const float top = __fmul_rn(__fsub_rn(hi, mid), inv), end = __fmul_rn(__fsub_rn(lo, mid), inv);
+    const bool clamp = !(top <= 7.25f && end >= -8.25f);
+    uint32_t word[4];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) w |= packed_code(x[u], mid, inv) << (4 * u);
-    if (is_v) {
-      *reinterpret_cast<uint16_t*>(image + R::v_half(row, grp, 2 * c)) = (uint16_t)w;
-      *reinterpret_cast<uint16_t*>(image + R::v_half(row, grp, 2 * c + 1)) = (uint16_t)(w >> 16);
-    } else {
-      *reinterpret_cast<uint32_t*>(image + R::k_word(row, grp, c)) = w;
+    for (int c = 0; c < 4; ++c) {
+      float y[8];
+      x.eight(c, y);
+      // rint(t) + 8 in the low bits of t + (3 * 2^22 + 8); the constant's own bits, shifted like
+      // the codes, are taken off beforehand
+      constexpr uint32_t kMagic = 0x4B400000u;
+      uint32_t w = 0;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) w -= kMagic << (4 * u);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        float t = __fmul_rn(__fsub_rn(y[u], mid), inv);
+        if (clamp) t = fminf(fmaxf(t, -8.f), 7.f);
+        w += __float_as_uint(__fadd_rn(t, 12582920.f)) << (4 * u);
+      }
+      word[c] = inv > 0.f ? w : 0x88888888u;
     }
-    if (c < 2)
-      *reinterpret_cast<__nv_bfloat16*>(
-          image + R::plane(c ? R::kMidOffset : R::kStepOffset, row, grp)) =
-          __float2bfloat16_rn(c ? mid : step);
+    if (is_v) {
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        *reinterpret_cast<uint16_t*>(image + R::v_half(row, g, r)) =
+            (uint16_t)(word[r / 2] >> (16 * (r & 1)));
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        *reinterpret_cast<uint32_t*>(image + R::k_word(row, g, c)) = word[c];
+    }
+    *reinterpret_cast<__nv_bfloat16*>(image + R::plane(R::kStepOffset, row, g)) =
+        __float2bfloat16_rn(step);
+    *reinterpret_cast<__nv_bfloat16*>(image + R::plane(R::kMidOffset, row, g)) =
+        __float2bfloat16_rn(mid);
   }
   __syncthreads();
   if (part.hi - part.lo == kPackedBlock) {
@@ -139,22 +204,32 @@ __global__ void __launch_bounds__(kThreads) pack_kernel(const T* __restrict__ k,
   }
 }
 
-template <typename T>
-__device__ __forceinline__ void store8(T* dst, const float* x);
-template <>
-__device__ __forceinline__ void store8<float>(float* dst, const float* x) {
+// The eight values of a word of codes, lowest nibble first.
+__device__ __forceinline__ void store_values(float* dst, uint32_t w, uint32_t step, uint32_t mid) {
+  const float s = __uint_as_float(step << 16), m = __uint_as_float(mid << 16);
+  float x[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) x[u] = packed_value((w >> (4 * u)) & 15u, s, m);
   reinterpret_cast<float4*>(dst)[0] = make_float4(x[0], x[1], x[2], x[3]);
   reinterpret_cast<float4*>(dst)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
-template <>
-__device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* dst, const float* x) {
-  uint32_t w[4];
+// In bf16: codes as exact integers (or-ed into the mantissa of 128, 136 subtracted), pairs of
+// nibbles i and i + 4, one fused multiply-add (one rounding, the product is exact), and the
+// pairs put in order.
+__device__ __forceinline__ void store_values(__nv_bfloat16* dst, uint32_t w, uint32_t step,
+                                             uint32_t mid) {
+  const uint32_t s2 = step * 0x10001u, m2 = mid * 0x10001u;
+  uint32_t x[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&v);
+  for (int u = 0; u < 4; ++u) {
+    uint32_t c;
+    asm("sub.rn.bf16x2 %0, %1, %2;"
+        : "=r"(c) : "r"(((w >> (4 * u)) & 0x000f000fu) | 0x43004300u), "r"(0x43084308u));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(x[u]) : "r"(c), "r"(s2), "r"(m2));
   }
-  *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+  *reinterpret_cast<uint4*>(dst) =
+      make_uint4(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410),
+                 __byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x7632));
 }
 
 template <typename T, int D>
@@ -184,12 +259,9 @@ __global__ void __launch_bounds__(kThreads) unpack_kernel(T* __restrict__ k, T* 
           (uint32_t)*reinterpret_cast<const uint16_t*>(rec + R::v_half(row, grp, 2 * c + 1)) << 16;
     else
       w = *reinterpret_cast<const uint32_t*>(rec + R::k_word(row, grp, c));
-    const float step = load_bf16(rec + R::plane(R::kStepOffset, row, grp));
-    const float mid = load_bf16(rec + R::plane(R::kMidOffset, row, grp));
-    float x[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) x[u] = packed_value((w >> (4 * u)) & 15u, step, mid);
-    store8<T>((is_v ? v : k) + (size_t)(part.token + row - part.lo) * D + lane * 8, x);
+    const uint32_t step = *reinterpret_cast<const uint16_t*>(rec + R::plane(R::kStepOffset, row, grp));
+    const uint32_t mid = *reinterpret_cast<const uint16_t*>(rec + R::plane(R::kMidOffset, row, grp));
+    store_values((is_v ? v : k) + (size_t)(part.token + row - part.lo) * D + lane * 8, w, step, mid);
   }
 }
 

@@ -54,11 +54,6 @@ __device__ __forceinline__ void packed_scales(float hi, float lo, bool bad, floa
   }
 }
 
-__device__ __forceinline__ uint32_t packed_code(float x, float mid, float inv) {
-  const float c = rintf(__fmul_rn(__fsub_rn(x, mid), inv)) + 8.f;
-  return inv > 0.f ? (uint32_t)fminf(fmaxf(c, 0.f), 15.f) : 8u;
-}
-
 __device__ __forceinline__ float packed_value(uint32_t code, float step, float mid) {
   return fmaf((float)((int)code - 8), step, mid);
 }
