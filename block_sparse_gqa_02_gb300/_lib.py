@@ -279,51 +279,60 @@ def msa_sparse_decode_paged(shape: MsaShape, seq_lens, block_table, n_phys, q, k
 
 # ----------------------------- rotary positions, the 4-bit cache, eviction by weight
 
-_torch = None
-_TORCH_DTYPES = {}
+_torch = _I32 = _I64 = _U8 = _F32 = None
+_FLOATS = {}               # msa_dtype -> torch dtype
 
 
 def _get_torch():
-    global _torch
+    global _torch, _I32, _I64, _U8, _F32
     if _torch is None:
         import torch
-        _TORCH_DTYPES.update({MSA_F32: torch.float32, MSA_BF16: torch.bfloat16,
-                              "f32": torch.float32, "i32": torch.int32, "i64": torch.int64,
-                              "u8": torch.uint8})
+        _FLOATS.update({MSA_F32: torch.float32, MSA_BF16: torch.bfloat16})
+        _I32, _I64, _U8, _F32 = torch.int32, torch.int64, torch.uint8, torch.float32
         _torch = torch
     return _torch
 
 
-def _torch_dtype(code):
-    _get_torch()
-    return _TORCH_DTYPES[code]
-
-
-def _arg(x, name, dtype=None, numel=0, device=None):
-    """Device pointer of a tensor that must be contiguous, of `dtype` and at least `numel`
-    elements, and on `device` (default: the current CUDA device, the one kernels run on); of an
-    int (a raw pointer) or None as they are."""
-    if x is None or isinstance(x, int):
-        return x
+def _device():
+    """The current CUDA device (initialising CUDA), or -2, no tensor's, on a machine without."""
     torch = _torch or _get_torch()
-    if device is None:
-        device = _device()
-    if x.get_device() != device:
-        raise ValueError(f"{name} is on {x.device}, not on the current CUDA device {device}")
-    if dtype is not None and x.dtype is not _TORCH_DTYPES[dtype]:
-        raise ValueError(f"{name} is {x.dtype}, expected {_TORCH_DTYPES[dtype]}")
+    return torch.cuda.current_device() if torch.cuda.is_available() else -2
+
+
+_fast = []                 # torch's raw device and stream getters, once CUDA is in use
+
+
+def _place(stream):
+    """The current device, and the raw stream: the given one or torch's current one."""
+    if _fast:
+        dev = _fast[0]()
+        if stream is None:
+            return dev, _fast[1](dev)
+    else:
+        dev = _device()
+        if dev >= 0:
+            c = _torch._C
+            if hasattr(c, "_cuda_getDevice") and hasattr(c, "_cuda_getCurrentRawStream"):
+                _fast.extend((c._cuda_getDevice, c._cuda_getCurrentRawStream))
+        elif stream is None:
+            return dev, 0
+    return dev, _stream(stream)
+
+
+def _arg(x, name, dtype, numel, dev):
+    """Device pointer of a tensor that must be contiguous, of `dtype` (None: any) and at least
+    `numel` elements, and on device `dev`; of an int (a raw pointer) or None as they are."""
+    if x is None or type(x) is int:
+        return x
+    if x.get_device() != dev:
+        raise ValueError(f"{name} is on {x.device}, not on the current CUDA device")
+    if dtype is not None and x.dtype is not dtype:
+        raise ValueError(f"{name} is {x.dtype}, expected {dtype}")
     if x.numel() < numel:
         raise ValueError(f"{name} has {x.numel()} elements, expected {numel}")
     if not x.is_contiguous():
-        raise ValueError("MSA tensors must be contiguous")
+        raise ValueError(f"{name}: MSA tensors must be contiguous")
     return x.data_ptr()
-
-
-def _device():
-    """The current CUDA device, or -2 (no tensor's) on a machine without one."""
-    torch = _torch or _get_torch()
-    return torch.cuda.current_device() if torch.cuda.is_initialized() or \
-        torch.cuda.is_available() else -2
 
 
 def make_rope(batch, seq, dtype="bf16", pos_offset=0, scale=0.0, interleaved=False,
@@ -341,20 +350,26 @@ class RopeTensors:
 
     def __init__(self, rows):
         rows = list(rows)
+        dev = _device()
         self.rows = rows
         self.array = (MsaRopeTensor * max(1, len(rows)))()
-        self.sizes = []
+        self.batch = self.seq = self.dtype = None
         for i, (x, y, freqs, head_major) in enumerate(rows):
-            heads = 1 if x.dim() == 3 else x.shape[1 if head_major else 2]
             if x.dim() not in (3, 4) or y.shape != x.shape or y.dtype != x.dtype:
                 raise ValueError(f"rope tensor {i}: x and y need the same [batch, seq, (heads,) d] "
                                  f"shape and type, got {tuple(x.shape)} and {tuple(y.shape)}")
+            head_major = bool(head_major) and x.dim() == 4
+            heads = 1 if x.dim() == 3 else x.shape[1 if head_major else 2]
+            this = x.shape[0], x.shape[2 if head_major else 1], x.dtype
+            if i and this != (self.batch, self.seq, self.dtype):
+                raise ValueError(f"rope tensor {i} has (batch, seq, dtype) {this}, the others "
+                                 f"{(self.batch, self.seq, self.dtype)}")
+            self.batch, self.seq, self.dtype = this
             self.array[i] = MsaRopeTensor(
-                _arg(x, f"x of rope tensor {i}"), _arg(y, f"y of rope tensor {i}"),
-                _arg(freqs, f"freqs of rope tensor {i}", "i64"), heads, x.shape[-1],
-                2 * freqs.numel(), int(bool(head_major)))
-            seq = x.shape[2] if head_major and x.dim() == 4 else x.shape[1]
-            self.sizes.append((x.shape[0], seq, x.dtype))
+                _arg(x, f"x of rope tensor {i}", None, 0, dev),
+                _arg(y, f"y of rope tensor {i}", None, 0, dev),
+                _arg(freqs, f"freqs of rope tensor {i}", _I64, 0, dev), heads, x.shape[-1],
+                2 * freqs.numel(), int(head_major))
 
     def __len__(self):
         return len(self.rows)
@@ -365,95 +380,99 @@ def make_rope_tensors(rows) -> RopeTensors:
 
 
 def msa_rope(desc: MsaRope, tensors: RopeTensors, positions=None, stream=None):
-    want = (desc.batch, desc.seq, _torch_dtype(desc.dtype))
-    for i, size in enumerate(tensors.sizes):
-        if size != want:
-            raise ValueError(f"rope tensor {i} has (batch, seq, dtype) {size}, the call {want}")
-    _check(load().msa_rope(ctypes.byref(desc), tensors.array, len(tensors),
-                           _arg(positions, "positions", "i32", desc.batch * desc.seq),
-                           _stream(stream)), "msa_rope")
+    dev, st = _place(stream)
+    batch, seq = desc.batch, desc.seq
+    if tensors.rows and (tensors.batch != batch or tensors.seq != seq or
+                         tensors.dtype is not _FLOATS.get(desc.dtype)):
+        raise ValueError(f"the rope tensors have (batch, seq, dtype) "
+                         f"{(tensors.batch, tensors.seq, tensors.dtype)}, the call "
+                         f"{(batch, seq, _FLOATS.get(desc.dtype))}")
+    _check(load().msa_rope(ctypes.byref(desc), tensors.array, len(tensors.rows),
+                           _arg(positions, "positions", _I32, batch * seq, dev), st), "msa_rope")
 
 
-def _cache_args(shape, seq_lens, block_table, n_phys, cache, dev):
-    n_phys = int(n_phys)
-    return (_arg(seq_lens, "seq_lens", "i32", shape.batch, dev),
+def _cache_args(shape, batch, hkv, d, seq_lens, block_table, n_phys, cache, dev):
+    return (_arg(seq_lens, "seq_lens", _I32, batch, dev),
             block_table if block_table is None else
-            _arg(block_table, "block_table", "i32", shape.batch * shape.n_blocks, dev), n_phys,
-            _arg(cache, "cache", "u8", n_phys * shape.n_heads_kv * 160 * shape.head_dim, dev))
+            _arg(block_table, "block_table", _I32, batch * shape.n_blocks, dev), n_phys,
+            _arg(cache, "cache", _U8, n_phys * hkv * 160 * d, dev))
+
+
+def _cache_rows(call, where, shape, n, starts, seq_lens, block_table, n_phys, cache, k, v, stream):
+    """The arguments of pack (cache last) and unpack (cache before k and v)."""
+    dev, st = _place(stream)
+    n, n_phys = int(n), int(n_phys)
+    batch, hkv, d, dt = shape.batch, shape.n_heads_kv, shape.head_dim, _FLOATS.get(shape.dtype)
+    rows = batch * hkv * n * d
+    args = _cache_args(shape, batch, hkv, d, seq_lens, block_table, n_phys, cache, dev)
+    kv = _arg(k, "k", dt, rows, dev), _arg(v, "v", dt, rows, dev)
+    tail = kv + args[3:] if where == "msa_cache_pack" else args[3:] + kv
+    _check(call(ctypes.byref(shape), n, _arg(starts, "starts", _I32, batch, dev), *args[:3], *tail,
+                st), where)
 
 
 def msa_cache_pack(shape: MsaShape, n_new, starts, seq_lens, block_table, n_phys, k, v, cache,
                    stream=None):
-    dev = _device()
-    sl, bt, n_phys, c = _cache_args(shape, seq_lens, block_table, n_phys, cache, dev)
-    n = shape.batch * shape.n_heads_kv * int(n_new) * shape.head_dim
-    _check(load().msa_cache_pack(ctypes.byref(shape), int(n_new),
-                                 _arg(starts, "starts", "i32", shape.batch, dev), sl, bt, n_phys,
-                                 _arg(k, "k", shape.dtype, n, dev),
-                                 _arg(v, "v", shape.dtype, n, dev), c, _stream(stream)),
-           "msa_cache_pack")
+    _cache_rows(load().msa_cache_pack, "msa_cache_pack", shape, n_new, starts, seq_lens,
+                block_table, n_phys, cache, k, v, stream)
 
 
 def msa_cache_unpack(shape: MsaShape, n_out, starts, seq_lens, block_table, n_phys, cache, k, v,
                      stream=None):
-    dev = _device()
-    sl, bt, n_phys, c = _cache_args(shape, seq_lens, block_table, n_phys, cache, dev)
-    n = shape.batch * shape.n_heads_kv * int(n_out) * shape.head_dim
-    _check(load().msa_cache_unpack(ctypes.byref(shape), int(n_out),
-                                   _arg(starts, "starts", "i32", shape.batch, dev), sl, bt, n_phys,
-                                   c, _arg(k, "k", shape.dtype, n, dev),
-                                   _arg(v, "v", shape.dtype, n, dev), _stream(stream)),
-           "msa_cache_unpack")
+    _cache_rows(load().msa_cache_unpack, "msa_cache_unpack", shape, n_out, starts, seq_lens,
+                block_table, n_phys, cache, k, v, stream)
 
 
-def _decode_args(shape, q, sel, out, lse, mass, dev):
-    n = shape.batch * shape.n_heads_q * shape.head_dim
-    rows = shape.batch * shape.n_heads_kv
-    return (_arg(q, "q", shape.dtype, n, dev), _arg(sel, "sel", "i32", rows * shape.top_k, dev),
-            _arg(out, "out", shape.dtype, n, dev),
-            _arg(lse, "lse", "f32", shape.batch * shape.n_heads_q, dev),
-            mass if mass is None else _arg(mass, "mass", "f32", rows * shape.n_blocks, dev))
+def _decode_args(shape, batch, hkv, d, dt, q, sel, out, lse, mass, dev):
+    hq = shape.n_heads_q
+    n = batch * hq * d
+    return (_arg(q, "q", dt, n, dev), _arg(sel, "sel", _I32, batch * hkv * shape.top_k, dev),
+            _arg(out, "out", dt, n, dev), _arg(lse, "lse", _F32, batch * hq, dev),
+            mass if mass is None else _arg(mass, "mass", _F32, batch * hkv * shape.n_blocks, dev))
 
 
 def msa_sparse_decode_packed(shape: MsaShape, seq_lens, block_table, n_phys, q, cache, sel, out,
                              lse=None, mass=None, stream=None):
-    dev = _device()
-    sl, bt, n_phys, c = _cache_args(shape, seq_lens, block_table, n_phys, cache, dev)
-    q, sel, out, lse, mass = _decode_args(shape, q, sel, out, lse, mass, dev)
+    dev, st = _place(stream)
+    batch, hkv, d = shape.batch, shape.n_heads_kv, shape.head_dim
+    sl, bt, n_phys, c = _cache_args(shape, batch, hkv, d, seq_lens, block_table, int(n_phys), cache,
+                                    dev)
+    q, sel, out, lse, mass = _decode_args(shape, batch, hkv, d, _FLOATS.get(shape.dtype), q, sel,
+                                          out, lse, mass, dev)
     _check(load().msa_sparse_decode_packed(ctypes.byref(shape), sl, bt, n_phys, q, c, sel, out,
-                                           lse, mass, _stream(stream)),
-           "msa_sparse_decode_packed")
+                                           lse, mass, st), "msa_sparse_decode_packed")
 
 
 def msa_sparse_decode_mass(shape: MsaShape, seq_lens, block_table, n_phys, q, k, v, sel, out, lse,
                            mass, workspace, ws_bytes=None, stream=None):
-    dev = _device()
+    dev, st = _place(stream)
     if ws_bytes is None:
         ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    n = (int(n_phys) * shape.block_size if block_table is not None
-         else shape.batch * shape.seq_k) * shape.n_heads_kv * shape.head_dim
-    q, sel, out, lse, mass = _decode_args(shape, q, sel, out, lse, mass, dev)
+    n_phys = int(n_phys)
+    batch, hkv, d, dt = shape.batch, shape.n_heads_kv, shape.head_dim, _FLOATS.get(shape.dtype)
+    n = (n_phys * shape.block_size if block_table is not None else batch * shape.seq_k) * hkv * d
+    q, sel, out, lse, mass = _decode_args(shape, batch, hkv, d, dt, q, sel, out, lse, mass, dev)
     _check(load().msa_sparse_decode_mass(
-        ctypes.byref(shape), _arg(seq_lens, "seq_lens", "i32", shape.batch, dev),
+        ctypes.byref(shape), _arg(seq_lens, "seq_lens", _I32, batch, dev),
         block_table if block_table is None else
-        _arg(block_table, "block_table", "i32", shape.batch * shape.n_blocks, dev), int(n_phys), q,
-        _arg(k, "k", shape.dtype, n, dev), _arg(v, "v", shape.dtype, n, dev), sel, out, lse, mass,
-        _arg(workspace, "workspace", None, 0, dev), ws_bytes, _stream(stream)),
-        "msa_sparse_decode_mass")
+        _arg(block_table, "block_table", _I32, batch * shape.n_blocks, dev), n_phys, q,
+        _arg(k, "k", dt, n, dev), _arg(v, "v", dt, n, dev), sel, out, lse, mass,
+        _arg(workspace, "workspace", None, 0, dev), ws_bytes, st), "msa_sparse_decode_mass")
 
 
 def msa_cache_evict(shape: MsaShape, keep, n_first, n_recent, seq_lens, mass, block_table, kept,
                     new_lens, mass_out, table_out=None, stream=None):
-    dev = _device()
-    B, n = shape.batch, shape.batch * shape.n_blocks
+    dev, st = _place(stream)
+    keep, batch = int(keep), shape.batch
+    n = batch * shape.n_blocks
+    m = n * shape.n_heads_kv
     _check(load().msa_cache_evict(
-        ctypes.byref(shape), int(keep), int(n_first), int(n_recent),
-        _arg(seq_lens, "seq_lens", "i32", B, dev),
-        _arg(mass, "mass", "f32", n * shape.n_heads_kv, dev),
-        _arg(block_table, "block_table", "i32", n, dev),
-        _arg(kept, "kept", "i32", B * int(keep), dev), _arg(new_lens, "new_lens", "i32", B, dev),
-        _arg(mass_out, "mass_out", "f32", n * shape.n_heads_kv, dev),
-        _arg(table_out, "table_out", "i32", n, dev), _stream(stream)), "msa_cache_evict")
+        ctypes.byref(shape), keep, int(n_first), int(n_recent),
+        _arg(seq_lens, "seq_lens", _I32, batch, dev), _arg(mass, "mass", _F32, m, dev),
+        _arg(block_table, "block_table", _I32, n, dev),
+        _arg(kept, "kept", _I32, batch * keep, dev), _arg(new_lens, "new_lens", _I32, batch, dev),
+        _arg(mass_out, "mass_out", _F32, m, dev), _arg(table_out, "table_out", _I32, n, dev), st),
+        "msa_cache_evict")
 
 
 class GatherTensors:
@@ -463,6 +482,7 @@ class GatherTensors:
 
     def __init__(self, rows):
         rows = list(rows)
+        dev = _device()
         self.rows = rows
         self.array = (MsaGatherTensor * max(1, len(rows)))()
         self.batches = []
@@ -473,7 +493,8 @@ class GatherTensors:
                 raise ValueError(f"gather tensor {i}: src and dst differ in more than their rows: "
                                  f"{tuple(src.shape)} and {tuple(dst.shape)}")
             self.array[i] = MsaGatherTensor(
-                _arg(src, f"src of gather tensor {i}"), _arg(dst, f"dst of gather tensor {i}"),
+                _arg(src, f"src of gather tensor {i}", None, 0, dev),
+                _arg(dst, f"dst of gather tensor {i}", None, 0, dev),
                 src.shape[lead], dst.shape[lead], 1 if lead == 1 else src.shape[1],
                 src.shape[-1] * src.element_size())
             self.batches.append(src.shape[0])
@@ -487,14 +508,15 @@ def make_gather_tensors(rows) -> GatherTensors:
 
 
 def msa_cache_gather(batch, tensors: GatherTensors, kept, block_size=128, stream=None):
+    dev, st = _place(stream)
     for i, n in enumerate(tensors.batches):
         if n != batch:
             raise ValueError(f"gather tensor {i} has batch {n}, the call {batch}")
     if kept.dim() != 2 or kept.shape[0] != batch:
         raise ValueError(f"kept is {tuple(kept.shape)}, expected [{batch}, keep]")
     _check(load().msa_cache_gather(int(batch), tensors.array, len(tensors),
-                                   _arg(kept, "kept", "i32"), kept.shape[1], int(block_size),
-                                   _stream(stream)), "msa_cache_gather")
+                                   _arg(kept, "kept", _I32, 0, dev), kept.shape[1], int(block_size),
+                                   st), "msa_cache_gather")
 
 
 def msa_workspace_bytes(shape: MsaShape, which: int) -> int:
