@@ -205,8 +205,11 @@ cudaError_t launch_rope(const msa_rope_desc& desc, const msa_rope_tensor* tensor
   long long all = 0;                                       // units of the whole call
   for (int i = 0; i < n; ++i)
     all += (long long)desc.batch * desc.seq * tensors[i].n_heads * (tensors[i].head_dim / (2 * vp));
-  // a tile is eight units a thread, or one where that would leave SMs without a tile
-  const int target = all >= 152ll * 8 * kThreads * 8 ? 8 * kThreads : kThreads;
+  // A tile is up to sixteen units a thread (a CTA's start costs the more the smaller the tile:
+  // 16, 8, 4, 2 units took 767, 785, 824, 841 us on 4.9 GB), halved until there are five waves
+  // of tiles (on 420 MB 16, 8, 4 and 2 units took 73, 71, 67 and 68 us).
+  int target = 16 * kThreads;
+  while (target > kThreads && all < 5ll * 152 * 8 * target) target /= 2;
   long long tiles = 0;
   int table = 0;
   for (int i = 0; i < n; ++i) {
