@@ -251,6 +251,7 @@ template <int D>
 struct MmaSmem {
   static constexpr int kStages = D == 128 ? 8 : 16;
   static constexpr int kGroups = PackedRecord<D>::kGroups;
+  static_assert(kStages <= 32, "the first copies are issued a lane each");
   union {
     __align__(128) uint8_t ring[kStages][PackedRecord<D>::kPairBytes];
     float part[kMmaWarps][kRows][D + 4];                   // the warps' outputs, after the ring
@@ -259,6 +260,9 @@ struct MmaSmem {
   float o[kRows][D];                   // [split][row of this CTA][D]
   float m[kMaxSplits][kRows], l[kMaxSplits][kRows];
   float norm[kRows];
+  uint4 qf[kGroups][2][32];            // Q as A operands, per lane
+  float qsum[kGroups][kRows];          // sums of q over a group of dims
+  float cr[kRows];                     // score units to log2 units
   __half vstep[kMmaWarps][kGroups][32];                    // V's steps of a warp's keys
   float wm[kMmaWarps][kRows], wl[kMmaWarps][kRows];
   uint64_t full[kStages], empty[kStages];
@@ -403,7 +407,7 @@ packed_decode_mma(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict
   const volatile int* abort = &s.abort;
   const float c1 = p.sm_scale * kLog2e;
   // the other CTAs have started before anything is written into their shared memory
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 
   // Copy number x (block x - first of the list) into its stage, once its last block has left it.
   auto issue = [&](int x, int i) {
@@ -451,34 +455,31 @@ packed_decode_mma(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict
   int first = 0;                                           // copies of the passes before
   for (int h0 = 0; h0 < p.G; h0 += kRows) {
     const int rows = min(kRows, p.G - h0);
-    if (warp == kMmaWarps - 1) {
-      const int n = s.count;
-      for (int i = 0; i < min(n, kStages) && !*abort; ++i)
-        if (!issue(first + i, i)) {
-          if (lane == 0) {
-            s.abort = 1;
-            if (status) atomicExch(status, 0x411);
-          }
-          break;
-        }
+    if (warp == kMmaWarps - 1 && lane < min(s.count, kStages) && !*abort) {
+      // the first copies, a lane each; every stage is empty here
+      const int x = first + lane, st = x % kStages;
+      s.last[st] = x;
+      ptx::mbar_arrive_expect_tx(&s.full[st], R::kPairBytes);
+      ptx::bulk_load(s.ring[st], cache + ((size_t)list[lane].phys * p.Hkv + g) * R::kPairBytes,
+                     R::kPairBytes, &s.full[st]);
     }
     // Q as A operands, dims in the order of the codes in K's words: of group x, k-step kk holds
     // dims 32 x + 8 c + (2 kk, 2 kk + 4) and (2 kk + 1, 2 kk + 5); rows gr and gr + 8
-    uint32_t qa[NG][2][4], qs[4];
-    float cr[2];                                           // score units to log2 units, per row
-    {
+    if (warp < NG) {
       const __nv_bfloat16* q0 = q + ((size_t)b * p.Hq + (size_t)g * p.G + h0) * D;
-      float sum[2][NG];
+      uint32_t f0[4], f1[4];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int row = gr + 8 * r;
         uint4 w[NG];
-        uint32_t top = 0;                                  // largest |q| of the row, bf16 bits
 #pragma unroll
-        for (int x = 0; x < NG; ++x) {
+        for (int x = 0; x < NG; ++x)
           w[x] = row < rows ? *reinterpret_cast<const uint4*>(q0 + (size_t)row * D +
                                                               x * kPackedGroup + c * 8)
                             : make_uint4(0, 0, 0, 0);
+        uint32_t top = 0;                                  // largest |q| of the row, bf16 bits
+#pragma unroll
+        for (int x = 0; x < NG; ++x) {
           const uint32_t v[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
 #pragma unroll
           for (int u = 0; u < 4; ++u) top = max(top, max(v[u] & 0x7fffu, (v[u] >> 16) & 0x7fffu));
@@ -487,45 +488,50 @@ packed_decode_mma(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const uint32_t e = min(max(top >> 7, 1u), 253u);
         const float f = __uint_as_float((254u - e) << 23);
-        cr[r] = c1 * __uint_as_float(e << 23);
+        uint4 own = w[0];
 #pragma unroll
-        for (int x = 0; x < NG; ++x) {
-          const float d0 = lo_bf16(w[x].x) * f, d1 = hi_bf16(w[x].x) * f;
-          const float d2 = lo_bf16(w[x].y) * f, d3 = hi_bf16(w[x].y) * f;
-          const float d4 = lo_bf16(w[x].z) * f, d5 = hi_bf16(w[x].z) * f;
-          const float d6 = lo_bf16(w[x].w) * f, d7 = hi_bf16(w[x].w) * f;
-          qa[x][0][r] = f16_pair(d0, d4);
-          qa[x][0][2 + r] = f16_pair(d1, d5);
-          qa[x][1][r] = f16_pair(d2, d6);
-          qa[x][1][2 + r] = f16_pair(d3, d7);
-          float t = ((d0 + d1) + (d2 + d3)) + ((d4 + d5) + (d6 + d7));
-          t += __shfl_xor_sync(0xffffffffu, t, 1);
-          t += __shfl_xor_sync(0xffffffffu, t, 2);
-          sum[r][x] = t;
-        }
+        for (int x = 1; x < NG; ++x)
+          if (warp == x) own = w[x];
+        const float d0 = lo_bf16(own.x) * f, d1 = hi_bf16(own.x) * f;
+        const float d2 = lo_bf16(own.y) * f, d3 = hi_bf16(own.y) * f;
+        const float d4 = lo_bf16(own.z) * f, d5 = hi_bf16(own.z) * f;
+        const float d6 = lo_bf16(own.w) * f, d7 = hi_bf16(own.w) * f;
+        f0[r] = f16_pair(d0, d4);
+        f0[2 + r] = f16_pair(d1, d5);
+        f1[r] = f16_pair(d2, d6);
+        f1[2 + r] = f16_pair(d3, d7);
+        float t = ((d0 + d1) + (d2 + d3)) + ((d4 + d5) + (d6 + d7));
+        t += __shfl_xor_sync(0xffffffffu, t, 1);
+        t += __shfl_xor_sync(0xffffffffu, t, 2);
+        if (c == 0) s.qsum[warp][row] = t;
+        if (warp == 0 && c == 0) s.cr[row] = c1 * __uint_as_float(e << 23);
       }
-      // the group sums in three bf16 parts: k = part * NG + group
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const bool odd = NG == 4 && (c & 1);
-        const float t0 = odd ? sum[r][2 % NG] : sum[r][0], t1 = odd ? sum[r][3 % NG] : sum[r][1];
-        const float a0 = __bfloat162float(__float2bfloat16_rn(t0));
-        const float a1 = __bfloat162float(__float2bfloat16_rn(t1));
-        const float b0 = __bfloat162float(__float2bfloat16_rn(t0 - a0));
-        const float b1 = __bfloat162float(__float2bfloat16_rn(t1 - a1));
-        const uint32_t hi = bf16_pair(a0, a1), md = bf16_pair(b0, b1);
-        const uint32_t lo = bf16_pair(t0 - a0 - b0, t1 - a1 - b1);
-        if (NG == 4) {
-          qs[r] = c < 2 ? hi : md;
-          qs[2 + r] = c < 2 ? lo : 0u;
-        } else {
-          qs[r] = c == 0 ? hi : c == 1 ? md : c == 2 ? lo : 0u;
-          qs[2 + r] = 0u;
-        }
-      }
+      s.qf[warp][0][lane] = make_uint4(f0[0], f0[1], f0[2], f0[3]);
+      s.qf[warp][1][lane] = make_uint4(f1[0], f1[1], f1[2], f1[3]);
     }
     __syncthreads();
     const int n_blocks = s.count;
+    const float cr[2] = {s.cr[gr], s.cr[gr + 8]};
+    // the group sums of q in three bf16 parts: k = part * NG + group
+    uint32_t qs[4];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int x = NG == 4 ? 2 * (c & 1) : 0;
+      const float t0 = s.qsum[x][gr + 8 * r], t1 = s.qsum[x + 1][gr + 8 * r];
+      const float a0 = __bfloat162float(__float2bfloat16_rn(t0));
+      const float a1 = __bfloat162float(__float2bfloat16_rn(t1));
+      const float b0 = __bfloat162float(__float2bfloat16_rn(t0 - a0));
+      const float b1 = __bfloat162float(__float2bfloat16_rn(t1 - a1));
+      const uint32_t hi = bf16_pair(a0, a1), md = bf16_pair(b0, b1);
+      const uint32_t lo = bf16_pair(t0 - a0 - b0, t1 - a1 - b1);
+      if (NG == 4) {
+        qs[r] = c < 2 ? hi : md;
+        qs[2 + r] = c < 2 ? lo : 0u;
+      } else {
+        qs[r] = c == 0 ? hi : c == 1 ? md : c == 2 ? lo : 0u;
+        qs[2 + r] = 0u;
+      }
+    }
     float o[4 * NG][4], om[4];
     float base[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
     uint32_t vexp[NG];                                     // exponent of V's largest step so far
@@ -583,32 +589,40 @@ packed_decode_mma(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict
               lo_bf16(t[x]) * __uint_as_float((254 + kStepShift - vexp[x]) << 23));
         __syncwarp();
       }
-      // scores of 16 rows x 32 keys
+      // scores of 16 rows x 32 keys, two n-tiles (16 keys) at a time
       float sc[4][4];
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {
-        const int key = key0 + nt * 8 + gr;                // this lane's key as a B column
-        uint32_t w[NG];
-        load_words<NG>(kr + R::k_word(key, 0, c), w);
-        const int x = NG == 4 ? 2 * (c & 1) : 0;
-        const uint32_t mids =
-            *reinterpret_cast<const uint16_t*>(kr + R::plane(R::kMidOffset, key, x)) |
-            (uint32_t)*reinterpret_cast<const uint16_t*>(kr + R::plane(R::kMidOffset, key, x + 1))
-                << 16;
-        mma_new<true>(sc[nt], qs, mids, mids);
+      for (int half = 0; half < 2; ++half) {
+        uint32_t w[2][NG];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int key = key0 + (2 * half + u) * 8 + gr;  // this lane's key as a B column
+          load_words<NG>(kr + R::k_word(key, 0, c), w[u]);
+          const int x = NG == 4 ? 2 * (c & 1) : 0;
+          const uint32_t mids =
+              *reinterpret_cast<const uint16_t*>(kr + R::plane(R::kMidOffset, key, x)) |
+              (uint32_t)*reinterpret_cast<const uint16_t*>(kr + R::plane(R::kMidOffset, key, x + 1))
+                  << 16;
+          mma_new<true>(sc[2 * half + u], qs, mids, mids);
+        }
 #pragma unroll
         for (int y = 0; y < NG; ++y) {
-          float acc[4];
-          const uint32_t w8 = w[y] >> 8;
-          mma_new<false>(acc, qa[y][0], codes.lows(w[y]), codes.highs(w[y]));
-          mma_add<false>(acc, qa[y][1], codes.lows(w8), codes.highs(w8));
-          // its keys as accumulator columns: 2 c and 2 c + 1
-          const uint32_t st2 =
-              load_u32(kr + R::plane(R::kStepOffset, key0 + nt * 8 + 2 * c, y));
-          const uint64_t step = f32x2(lo_bf16(st2), hi_bf16(st2));
-          float(&t)[4] = sc[nt];
-          split_f32x2(fma_f32x2(f32x2(acc[0], acc[1]), step, f32x2(t[0], t[1])), t[0], t[1]);
-          split_f32x2(fma_f32x2(f32x2(acc[2], acc[3]), step, f32x2(t[2], t[3])), t[2], t[3]);
+          const uint4 v0 = s.qf[y][0][lane], v1 = s.qf[y][1][lane];
+          const uint32_t a0[4] = {v0.x, v0.y, v0.z, v0.w}, a1[4] = {v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            float acc[4];
+            const uint32_t w8 = w[u][y] >> 8;
+            mma_new<false>(acc, a0, codes.lows(w[u][y]), codes.highs(w[u][y]));
+            mma_add<false>(acc, a1, codes.lows(w8), codes.highs(w8));
+            // its keys as accumulator columns: 2 c and 2 c + 1
+            const uint32_t st2 = load_u32(
+                kr + R::plane(R::kStepOffset, key0 + (2 * half + u) * 8 + 2 * c, y));
+            const uint64_t step = f32x2(lo_bf16(st2), hi_bf16(st2));
+            float(&t)[4] = sc[2 * half + u];
+            split_f32x2(fma_f32x2(f32x2(acc[0], acc[1]), step, f32x2(t[0], t[1])), t[0], t[1]);
+            split_f32x2(fma_f32x2(f32x2(acc[2], acc[3]), step, f32x2(t[2], t[3])), t[2], t[3]);
+          }
         }
       }
       // the stage of this group's block before: its other warps have most likely left it
@@ -732,15 +746,6 @@ packed_decode_mma(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict
       s.abort = 1;
       if (status) atomicExch(status, 0x412);
     }
-    // Every warp has left its loop.  Without an abort every copy has been consumed; after one,
-    // a warp waits for the last copy of every stage before the memory is used again.
-    __syncthreads();
-    if (*abort) {
-      if (warp == 0)
-        for (int x = 0; x < kStages; ++x)
-          if (s.last[x] >= 0) ptx::mbar_wait_timed(&s.full[x], (s.last[x] / kStages) & 1);
-      __syncthreads();
-    }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 1);
@@ -752,19 +757,39 @@ packed_decode_mma(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict
       s.wl[warp][gr] = l_run[0];
       s.wl[warp][gr + 8] = l_run[1];
     }
-    // columns 2 c, 2 c + 1 of n-tile 4 x + i are dims 32 x + 4 column + i; the mid term of
-    // group x is in lane x / 2 of the quad, element x % 2
+    // Every warp has left its loop.  Without an abort every copy has been consumed; after one,
+    // a warp waits for the last copy of every stage before the memory is used again.
+    __syncthreads();
+    if (*abort) {
+      if (warp == 0)
+        for (int x = 0; x < kStages; ++x)
+          if (s.last[x] >= 0) ptx::mbar_wait_timed(&s.full[x], (s.last[x] / kStages) & 1);
+      __syncthreads();
+    }
+    // the warp's outputs relative to the CTA's maxima.  Columns 2 c, 2 c + 1 of n-tile 4 x + i
+    // are dims 32 x + 4 column + i; the mid term of group x is in lane x / 2 of the quad,
+    // element x % 2
+    float rel[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kMmaWarps; ++w) top = fmaxf(top, s.wm[w][gr + 8 * r]);
+      rel[r] = base[r] == -INFINITY ? 0.f : ex2(base[r] - top);
+    }
 #pragma unroll
     for (int x = 0; x < NG; ++x) {
       const float f = __uint_as_float((vexp[x] - kStepShift) << 23);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float mid = __shfl_sync(0xffffffffu, om[2 * r + (x & 1)], (lane & ~3) | (x >> 1));
+        const float mid = rel[r] * __shfl_sync(0xffffffffu, om[2 * r + (x & 1)],
+                                               (lane & ~3) | (x >> 1));
+        const float fr = f * rel[r];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float4 v = make_float4(
-              fmaf(o[4 * x][2 * r + e], f, mid), fmaf(o[4 * x + 1][2 * r + e], f, mid),
-              fmaf(o[4 * x + 2][2 * r + e], f, mid), fmaf(o[4 * x + 3][2 * r + e], f, mid));
+              fmaf(o[4 * x][2 * r + e], fr, mid), fmaf(o[4 * x + 1][2 * r + e], fr, mid),
+              fmaf(o[4 * x + 2][2 * r + e], fr, mid), fmaf(o[4 * x + 3][2 * r + e], fr, mid));
           *reinterpret_cast<float4*>(
               &s.part[warp][gr + 8 * r][x * kPackedGroup + 4 * (2 * c + e)]) = v;
         }
@@ -786,20 +811,15 @@ packed_decode_mma(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict
     }
     for (int e = threadIdx.x; e < kRows * D / 4; e += kMmaThreads) {
       const int r = e / (D / 4), d0 = e % (D / 4) * 4;
-      float top = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kMmaWarps; ++w) top = fmaxf(top, s.wm[w][r]);
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (top != -INFINITY)
 #pragma unroll
-        for (int w = 0; w < kMmaWarps; ++w) {
-          const float f = ex2(s.wm[w][r] - top);
-          const float4 u = *reinterpret_cast<const float4*>(&s.part[w][r][d0]);
-          v.x = fmaf(f, u.x, v.x);
-          v.y = fmaf(f, u.y, v.y);
-          v.z = fmaf(f, u.z, v.z);
-          v.w = fmaf(f, u.w, v.w);
-        }
+      for (int w = 0; w < kMmaWarps; ++w) {
+        const float4 u = *reinterpret_cast<const float4*>(&s.part[w][r][d0]);
+        v.x += u.x;
+        v.y += u.y;
+        v.z += u.z;
+        v.w += u.w;
+      }
       *reinterpret_cast<float4*>(
           cluster.map_shared_rank(&s.o[split * own + r % own][d0], r / own)) = v;
     }
