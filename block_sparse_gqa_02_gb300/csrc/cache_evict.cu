@@ -14,6 +14,8 @@
 #include <cooperative_groups.h>
 
 #include "common.cuh"
+#include "launch.cuh"
+#include "ptx.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -62,6 +64,7 @@ cache_evict_kernel(const float* mass, const int32_t* table,
   cg::cluster_group cluster = cg::this_cluster();
   const int part = (int)cluster.block_rank(), parts = (int)cluster.num_blocks();
   const int b = blockIdx.x / parts, tid = threadIdx.x;
+  ptx::grid_wait();
   const int L = seq_len_of(p, b), n = (L + p.Bk - 1) / p.Bk;
   const int nk = min(n, keep);
   const float* m0 = mass + (size_t)b * p.Hkv * p.nB;
@@ -207,6 +210,7 @@ cache_gather_kernel(const __grid_constant__ GatherArgs a, const int32_t* __restr
   const msa_gather_tensor& t = a.t[ti];
   const long long e = (long long)blockIdx.x - a.first[ti];
   const int i = (int)(e % a.keep);
+  ptx::grid_wait();
   const long long bh = e / a.keep, b = bh / t.n_heads;
   const int blk = kept[b * a.keep + i];
   if (blk < 0) return;
@@ -247,20 +251,7 @@ cudaError_t launch_cache_evict(const Dims& p, int keep, int n_first, int n_recen
   if (e != cudaSuccess) return e;
   int parts = (p.nB + kThreads - 1) / kThreads;            // at most an entry a thread, or all
   if (parts > kMaxParts) parts = kMaxParts;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)p.B * parts);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = parts;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, mass, table, kept, new_lens, mass_out, table_out, p, keep,
-                            n_first, n_recent);
+  return launch_after(kern, dim3((unsigned)p.B * parts), kThreads, smem, parts, st, mass, table, kept, new_lens, mass_out, table_out, p, keep, n_first, n_recent);
 }
 
 cudaError_t launch_cache_gather(int batch, const msa_gather_tensor* tensors, int n,
@@ -276,8 +267,7 @@ cudaError_t launch_cache_gather(int batch, const msa_gather_tensor* tensors, int
     ctas += (long long)batch * tensors[i].n_heads * keep;
   }
   if (ctas > 2147483647ll) return cudaErrorInvalidConfiguration;
-  cache_gather_kernel<<<(unsigned)ctas, kGatherThreads, 0, st>>>(a, kept);
-  return cudaGetLastError();
+  return launch_after(cache_gather_kernel, dim3((unsigned)ctas), kGatherThreads, 0, 0, st, a, kept);
 }
 
 }  // namespace msa

@@ -7,7 +7,9 @@
 // through shared memory: a block that is filled whole leaves it in 16-byte stores, of any other
 // only the stored tokens' bytes are written.  Unpacking stages the record when it needs a
 // quarter of it or more, and reads a few tokens' bytes where they are.
+#include "launch.cuh"
 #include "packed_cache.cuh"
+#include "ptx.cuh"
 
 namespace msa {
 
@@ -28,6 +30,7 @@ template <int D>
 __device__ __forceinline__ Part part_of(const Dims& p, const int32_t* starts, int n, int per_seq,
                                         uint8_t* cache, bool& is_v) {
   Part r = {nullptr, 0, 0, 0};
+  ptx::grid_wait();
   int e = blockIdx.x;
   const int x = e % per_seq;
   e /= per_seq;
@@ -278,9 +281,8 @@ cudaError_t pack(const Dims& p, int n, const int32_t* starts, const void* k, con
   int per_seq;
   const long long grid = grid_of(p, n, per_seq);
   if (grid > 2147483647ll) return cudaErrorInvalidConfiguration;
-  pack_kernel<T, D><<<(unsigned)grid, kThreads, 0, st>>>((const T*)k, (const T*)v,
-                                                         (uint8_t*)cache, starts, n, per_seq, p);
-  return cudaGetLastError();
+  return launch_after(pack_kernel<T, D>, dim3((unsigned)grid), kThreads, 0, 0, st, (const T*)k,
+                      (const T*)v, (uint8_t*)cache, starts, n, per_seq, p);
 }
 
 template <typename T, int D>
@@ -289,9 +291,8 @@ cudaError_t unpack(const Dims& p, int n, const int32_t* starts, const void* cach
   int per_seq;
   const long long grid = grid_of(p, n, per_seq);
   if (grid > 2147483647ll) return cudaErrorInvalidConfiguration;
-  unpack_kernel<T, D><<<(unsigned)grid, kThreads, 0, st>>>((T*)k, (T*)v, (const uint8_t*)cache,
-                                                           starts, n, per_seq, p);
-  return cudaGetLastError();
+  return launch_after(unpack_kernel<T, D>, dim3((unsigned)grid), kThreads, 0, 0, st, (T*)k, (T*)v,
+                      (const uint8_t*)cache, starts, n, per_seq, p);
 }
 
 }  // namespace

@@ -11,6 +11,7 @@
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
+#include "launch.cuh"
 #include "packed_cache.cuh"
 #include "ptx.cuh"
 
@@ -48,6 +49,7 @@ packed_decode_simt(const T* __restrict__ q, const uint8_t* __restrict__ cache,
   S& s = *reinterpret_cast<S*>(smem_raw);
   float* weights = reinterpret_cast<float*>(smem_raw + sizeof(S));   // [kRows][per], mass only
   cg::cluster_group cluster = cg::this_cluster();
+  ptx::grid_wait();
   const int split = (int)cluster.block_rank(), n_split = (int)cluster.num_blocks();
   const int bg = blockIdx.y, b = bg / p.Hkv, g = bg % p.Hkv;
   const int L = seq_len_of(p, b), nB_b = (L + kPackedBlock - 1) / kPackedBlock;
@@ -408,6 +410,7 @@ packed_decode_mma(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict
   const float c1 = p.sm_scale * kLog2e;
   // the other CTAs have started before anything is written into their shared memory
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  ptx::grid_wait();
 
   // Copy number x (block x - first of the list) into its stage, once its last block has left it.
   auto issue = [&](int x, int i) {
@@ -878,20 +881,7 @@ cudaError_t decode_mma(const Dims& p, int n_split, const void* q, const void* ca
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)smem);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(n_split, p.B * p.Hkv);
-  cfg.blockDim = dim3(kMmaThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = n_split;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, (const __nv_bfloat16*)q, (const uint8_t*)cache, sel,
-                            (__nv_bfloat16*)out, lse, mass, p, per, status);
+  return launch_after(kern, dim3(n_split, p.B * p.Hkv), kMmaThreads, smem, n_split, st, (const __nv_bfloat16*)q, (const uint8_t*)cache, sel, (__nv_bfloat16*)out, lse, mass, p, per, status);
 }
 
 // CTAs that share a (sequence, KV head): doubled while they fit on the SMs two at a time
@@ -914,20 +904,7 @@ cudaError_t decode_simt(const Dims& p, const void* q, const void* cache, const i
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)smem);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(n_split, p.B * p.Hkv);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = n_split;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, (const T*)q, (const uint8_t*)cache, sel, (T*)out, lse,
-                            mass, p, per);
+  return launch_after(kern, dim3(n_split, p.B * p.Hkv), kThreads, smem, n_split, st, (const T*)q, (const uint8_t*)cache, sel, (T*)out, lse, mass, p, per);
 }
 
 }  // namespace

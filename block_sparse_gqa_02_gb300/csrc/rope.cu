@@ -13,6 +13,8 @@
 // loads and stores a unit.  All tensors of a call share one launch: their tiles are numbered
 // one after the other.
 #include "common.cuh"
+#include "launch.cuh"
+#include "ptx.cuh"
 
 namespace msa {
 
@@ -112,6 +114,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   const bool in_place = tn.x == tn.y;
   const T* x = static_cast<const T*>(tn.x);                // may be y itself
   T* y = static_cast<T*>(tn.y);
+  ptx::grid_wait();
 
   for (int e0 = 0; e0 < total; e0 += kThreads * kBatch) {
     uint4 lo[kBatch], hi[kBatch];
@@ -245,8 +248,7 @@ cudaError_t launch_rope(const msa_rope_desc& desc, const msa_rope_tensor* tensor
   auto kern = desc.dtype == MSA_BF16
       ? (desc.interleaved ? rope_kernel<__nv_bfloat16, true> : rope_kernel<__nv_bfloat16, false>)
       : (desc.interleaved ? rope_kernel<float, true> : rope_kernel<float, false>);
-  kern<<<(unsigned)tiles, kThreads, smem, st>>>(a);
-  return cudaGetLastError();
+  return launch_after(kern, dim3((unsigned)tiles), kThreads, smem, 0, st, a);
 }
 
 }  // namespace msa

@@ -7,6 +7,8 @@
 // This file holds the CUDA-core kernels: prefill for fp32 and for shapes the tensor-core
 // kernel does not cover, and the split-KV decode with its log-sum-exp merge.
 #include "common.cuh"
+#include "launch.cuh"
+#include "ptx.cuh"
 #include "sparse_decode_mma.cuh"
 #include "sparse_prefill_tc.cuh"
 
@@ -230,6 +232,7 @@ __global__ void __launch_bounds__(D) decode_combine_mass(
     float* __restrict__ mass, Dims p, int n_split) {
   constexpr int kChunk = 64;                               // selection entries at a time
   constexpr int kMaxG = 16;
+  ptx::grid_wait();
   if ((int)blockIdx.x < p.B * p.Hq) {
     combine_head<T, D>(ws_o, ws_l, out, lse, blockIdx.x, n_split);
     return;
@@ -343,9 +346,8 @@ cudaError_t launch_sparse_decode_mma_mass(const Dims& p, const void* q, const vo
   cudaError_t e = launch_sparse_decode_mma(p, q, k, v, sel, ws_o, ws_l, ws_b, n_split, per, st,
                                            dev_status);
   if (e != cudaSuccess) return e;
-  decode_combine_mass<__nv_bfloat16, 128><<<p.B * (p.Hq + p.Hkv), 128, 0, st>>>(
-      ws_o, ws_l, ws_b, sel, (__nv_bfloat16*)out, lse, mass, p, n_split);
-  return cudaGetLastError();
+  return launch_after(decode_combine_mass<__nv_bfloat16, 128>, dim3(p.B * (p.Hq + p.Hkv)), 128, 0,
+                      0, st, ws_o, ws_l, ws_b, sel, (__nv_bfloat16*)out, lse, mass, p, n_split);
 }
 
 cudaError_t launch_sparse_prefill(const Dims& p, const void* q, const void* k, const void* v,

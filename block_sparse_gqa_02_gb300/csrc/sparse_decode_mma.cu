@@ -13,6 +13,7 @@
 // softmax, log2 domain), then merge their partial (max, sum, O) through shared memory and
 // write the split's normalised partial output and natural-log lse for the log-sum-exp merge.
 #include "common.cuh"
+#include "launch.cuh"
 #include "ptx.cuh"
 #include "sparse_decode_mma.cuh"
 #include "tma_host.cuh"
@@ -96,6 +97,7 @@ sparse_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k,
   extern __shared__ uint8_t smem_raw[];
   Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                      ~uintptr_t(1023));
+  if (kMass) ptx::grid_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = blockIdx.x, bg = blockIdx.y, b = bg / p.Hkv, g = bg % p.Hkv;
   const int G = p.G;
@@ -359,10 +361,13 @@ cudaError_t launch_sparse_decode_mma(const Dims& p, const void* q, const void* k
   if (e == cudaSuccess) e = make_tensor_map_bf16(&tv, v, 3, kd, ks, kbx);
   if (e != cudaSuccess) return e;
   const size_t smem = sizeof(Smem) + 1024;
+  dim3 grid(n_split, p.B * p.Hkv);
   auto kern = ws_b ? sparse_decode_mma_kernel<true> : sparse_decode_mma_kernel<false>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  dim3 grid(n_split, p.B * p.Hkv);
+  if (ws_b)
+    return launch_after(kern, grid, kThreads, smem, 0, st, tk, tv, (const __nv_bfloat16*)q, sel,
+                        ws_o, ws_l, ws_b, p, n_split, per, status);
   kern<<<grid, kThreads, smem, st>>>(tk, tv, (const __nv_bfloat16*)q, sel, ws_o, ws_l, ws_b, p,
                                      n_split, per, status);
   return cudaGetLastError();
