@@ -249,31 +249,36 @@ __global__ void __launch_bounds__(D) decode_combine_mass(
       for (int s = 0; s < n_split; ++s) den += expf(l[s] - mx);
     norm[threadIdx.x] = den > 0.f ? (mx + logf(den)) * kLog2e : -INFINITY;
   }
-  __syncthreads();
+  // thread: entry i of a chunk, every other head; a head's four warps are one 16-byte load, and
+  // all of a thread's loads are in flight together
+  static_assert(kDecodeWarps == 4 && D == 2 * kChunk, "layout of the loads");
+  const int i = threadIdx.x % kChunk, h0 = threadIdx.x / kChunk;
   for (int i0 = 0; i0 < p.k; i0 += kChunk) {
-    const int n = min(kChunk, p.k - i0);
-    for (int e = threadIdx.x; e < p.G * kChunk; e += D) {
-      const int h = e / kChunk, i = e % kChunk;
-      if (i >= n) continue;
-      const int blk = sel[(size_t)bg * p.k + i0 + i];
+    const int blk = i0 + i < p.k ? sel[(size_t)bg * p.k + i0 + i] : -1;
+    const bool there = blk >= 0 && blk < nB_b;
+    float4 v[kMaxG / 2];
+#pragma unroll
+    for (int u = 0; u < kMaxG / 2; ++u)
+      if (there && h0 + 2 * u < p.G)
+        v[u] = *reinterpret_cast<const float4*>(
+            ws_b + ((head0 + h0 + 2 * u) * p.k + i0 + i) * kDecodeWarps);
+    __syncthreads();                                       // norm; part of the chunk before
+#pragma unroll
+    for (int u = 0; u < kMaxG / 2; ++u) {
+      const int h = h0 + 2 * u;
+      if (h >= p.G) continue;
       float sum = 0.f;
-      if (blk >= 0 && blk < nB_b && norm[h] != -INFINITY) {
-        static_assert(kDecodeWarps == 4, "one 16-byte load per entry");
-        const float4 v = *reinterpret_cast<const float4*>(
-            ws_b + ((head0 + h) * p.k + i0 + i) * kDecodeWarps);
-        sum = (exp2f(v.x - norm[h]) + exp2f(v.y - norm[h])) +
-              (exp2f(v.z - norm[h]) + exp2f(v.w - norm[h]));
-      }
+      if (there && norm[h] != -INFINITY)
+        sum = (exp2f(v[u].x - norm[h]) + exp2f(v[u].y - norm[h])) +
+              (exp2f(v[u].z - norm[h]) + exp2f(v[u].w - norm[h]));
       part[h][i] = sum;
     }
     __syncthreads();
-    if ((int)threadIdx.x < n) {
-      const int blk = sel[(size_t)bg * p.k + i0 + threadIdx.x];
+    if (h0 == 0 && there) {
       float sum = 0.f;
-      for (int h = 0; h < p.G; ++h) sum += part[h][threadIdx.x];
-      if (blk >= 0 && blk < nB_b) atomicAdd(mass + (size_t)bg * p.nB + blk, sum);
+      for (int h = 0; h < p.G; ++h) sum += part[h][i];
+      atomicAdd(mass + (size_t)bg * p.nB + blk, sum);
     }
-    __syncthreads();
   }
 }
 

@@ -109,6 +109,10 @@ EVICT = {
     "max_blocks": (1, 32768, 2, None, 20000, 7, 9, 1),
     "keep_past_blocks": (2, 700, 2, [700, 300], 50, 0, 1, 128),
     "one_goes": (1, 1281, 3, None, 10, 1, 1, 128),
+    # 3, 5 and 7 CTAs a sequence; rows of lengths that are no multiple of anything
+    "three_parts": (2, 2501, 5, [2501, 2048], 777, 3, 5, 1),
+    "five_parts": (1, 4999, 1, None, 2500, 0, 1, 1),
+    "seven_parts": (2, 7001 * 128, 3, None, 6999, 1, 1, 128),
 }
 
 
