@@ -251,7 +251,8 @@ cudaError_t launch_cache_evict(const Dims& p, int keep, int n_first, int n_recen
   if (e != cudaSuccess) return e;
   int parts = (p.nB + kThreads - 1) / kThreads;            // at most an entry a thread, or all
   if (parts > kMaxParts) parts = kMaxParts;
-  return launch_after(kern, dim3((unsigned)p.B * parts), kThreads, smem, parts, st, mass, table, kept, new_lens, mass_out, table_out, p, keep, n_first, n_recent);
+  return launch_after(kern, dim3((unsigned)p.B * parts), kThreads, smem, parts, st, mass, table, kept,
+                      new_lens, mass_out, table_out, p, keep, n_first, n_recent);
 }
 
 cudaError_t launch_cache_gather(int batch, const msa_gather_tensor* tensors, int n,

@@ -206,6 +206,30 @@ def test_packed_decode(name):
     check_lse(l2, l, dtype, name)
 
 
+def test_packed_decode_thousands_of_entries():
+    """More entries than a split lists at once, the blocks anywhere among them; the same with
+    weights' limit."""
+    B, cap, Hkv, d = 1, 9 * 128, 2, 128
+    for dtype, topk in (("bf16", 8300), ("f32", 17000), ("bf16", 1024)):
+        cache, table, P, kv, vv = _filled(B, cap, Hkv, d, [cap], dtype, True, 7)
+        shape = _shape(B, cap, 8, Hkv, d, topk, dtype)
+        rng = np.random.default_rng(topk)
+        sel_np = np.full((B, Hkv, 1, topk), -1, dtype=np.int32)
+        for g in range(Hkv):
+            sel_np[0, g, 0, np.sort(rng.choice(topk, 8, replace=False))] = rng.permutation(9)[:8]
+        sel, q = torch.from_numpy(sel_np).cuda(), _rows((B, 1, 8, d), DT[dtype], 1)
+        out, lse = torch.empty_like(q), torch.empty((B, 8, 1), device="cuda")
+        mass = torch.zeros((B, Hkv, 9), device="cuda") if topk <= 1024 else None
+        _lib.msa_sparse_decode_packed(shape, None, table, P, q, cache, sel, out, lse, mass)
+        _lib.msa_get_device_status()
+        o, l, m = co.decode_mass(q, list(kv), list(vv), sel_np, [cap])
+        check_out(out, o, dtype)
+        check_lse(lse, l, dtype)
+        if mass is not None:
+            tol = _weight_tol(to_np(q), kv, d ** -0.5, d) + 2.0 ** -24
+            assert np.all(np.abs(to_np(mass) - m) <= tol * m)
+
+
 def test_packed_decode_bad_entries():
     """Selection entries that are no block of the sequence and table entries that are no physical
     block are skipped: the output of the row without them."""
