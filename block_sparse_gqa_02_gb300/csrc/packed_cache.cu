@@ -208,7 +208,8 @@ __global__ void __launch_bounds__(kThreads) pack_kernel(const T* __restrict__ k,
 }
 
 // The eight values of a word of codes, lowest nibble first.
-__device__ __forceinline__ void store_values(float* dst, uint32_t w, uint32_t step, uint32_t mid) {
+__device__ __forceinline__ void store_values(float* dst, uint32_t w, uint32_t step, uint32_t mid,
+                                             uint32_t) {
   const float s = __uint_as_float(step << 16), m = __uint_as_float(mid << 16);
   float x[8];
 #pragma unroll
@@ -220,14 +221,15 @@ __device__ __forceinline__ void store_values(float* dst, uint32_t w, uint32_t st
 // nibbles i and i + 4, one fused multiply-add (one rounding, the product is exact), and the
 // pairs put in order.
 __device__ __forceinline__ void store_values(__nv_bfloat16* dst, uint32_t w, uint32_t step,
-                                             uint32_t mid) {
+                                             uint32_t mid, uint32_t magic) {
   const uint32_t s2 = step * 0x10001u, m2 = mid * 0x10001u;
   uint32_t x[4];
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     uint32_t c;
-    asm("sub.rn.bf16x2 %0, %1, %2;"
-        : "=r"(c) : "r"(((w >> (4 * u)) & 0x000f000fu) | 0x43004300u), "r"(0x43084308u));
+    // (x & mask) | magic is one instruction when the magic is in a register
+    asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xEA;" : "=r"(c) : "r"(w >> (4 * u)), "r"(magic));
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(c), "r"(0x43084308u));
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(x[u]) : "r"(c), "r"(s2), "r"(m2));
   }
   *reinterpret_cast<uint4*>(dst) =
@@ -255,16 +257,30 @@ __global__ void __launch_bounds__(kThreads) unpack_kernel(T* __restrict__ k, T* 
     rec = image;
   }
   const int lane = threadIdx.x % kLanes, grp = lane / 4, c = lane % 4;
-  for (int row = part.lo + (int)threadIdx.x / kLanes; row < part.hi; row += kRowsAtOnce) {
+  const int row0 = part.lo + (int)threadIdx.x / kLanes;
+  uint32_t magic;                                          // the bf16 pair 128
+  asm volatile("mov.b32 %0, 0x43004300;" : "=r"(magic));
+  T* dst = (is_v ? v : k) + (size_t)(part.token + row0 - part.lo) * D + lane * 8;
+  // rows go in steps that leave the exchange of V's key pairs alone, so offsets grow evenly
+  static_assert(kRowsAtOnce % 16 == 0 && (D == 128 || kRowsAtOnce % 32 == 0), "exchanged pairs");
+  int at = is_v ? R::v_half(row0, grp, 2 * c) : R::k_word(row0, grp, c);
+  const int more = R::v_half(row0, grp, 2 * c + 1) - R::v_half(row0, grp, 2 * c);
+  int plane = R::plane(R::kStepOffset, row0, grp);
+#pragma unroll 2
+  for (int row = row0; row < part.hi; row += kRowsAtOnce) {
     uint32_t w;
     if (is_v)
-      w = *reinterpret_cast<const uint16_t*>(rec + R::v_half(row, grp, 2 * c)) |
-          (uint32_t)*reinterpret_cast<const uint16_t*>(rec + R::v_half(row, grp, 2 * c + 1)) << 16;
+      w = *reinterpret_cast<const uint16_t*>(rec + at) |
+          (uint32_t)*reinterpret_cast<const uint16_t*>(rec + at + more) << 16;
     else
-      w = *reinterpret_cast<const uint32_t*>(rec + R::k_word(row, grp, c));
-    const uint32_t step = *reinterpret_cast<const uint16_t*>(rec + R::plane(R::kStepOffset, row, grp));
-    const uint32_t mid = *reinterpret_cast<const uint16_t*>(rec + R::plane(R::kMidOffset, row, grp));
-    store_values((is_v ? v : k) + (size_t)(part.token + row - part.lo) * D + lane * 8, w, step, mid);
+      w = *reinterpret_cast<const uint32_t*>(rec + at);
+    const uint32_t step = *reinterpret_cast<const uint16_t*>(rec + plane);
+    const uint32_t mid = *reinterpret_cast<const uint16_t*>(rec + plane + R::kMidOffset -
+                                                            R::kStepOffset);
+    store_values(dst, w, step, mid, magic);
+    at += is_v ? kRowsAtOnce * 2 * R::kGroups : kRowsAtOnce * (D / 2);
+    plane += kRowsAtOnce * 2;
+    dst += (size_t)kRowsAtOnce * D;
   }
 }
 
