@@ -350,7 +350,7 @@ class RopeTensors:
 
     def __init__(self, rows):
         rows = list(rows)
-        dev = _device()
+        self.device = dev = _device()
         self.rows = rows
         self.array = (MsaRopeTensor * max(1, len(rows)))()
         self.batch = self.seq = self.dtype = None
@@ -382,6 +382,9 @@ def make_rope_tensors(rows) -> RopeTensors:
 def msa_rope(desc: MsaRope, tensors: RopeTensors, positions=None, stream=None):
     dev, st = _place(stream)
     batch, seq = desc.batch, desc.seq
+    if tensors.device != dev:
+        raise ValueError(f"the rope tensors are on CUDA device {tensors.device}, the current one "
+                         f"is {dev}")
     if tensors.rows and (tensors.batch != batch or tensors.seq != seq or
                          tensors.dtype is not _FLOATS.get(desc.dtype)):
         raise ValueError(f"the rope tensors have (batch, seq, dtype) "
@@ -482,7 +485,7 @@ class GatherTensors:
 
     def __init__(self, rows):
         rows = list(rows)
-        dev = _device()
+        self.device = dev = _device()
         self.rows = rows
         self.array = (MsaGatherTensor * max(1, len(rows)))()
         self.batches = []
@@ -509,6 +512,9 @@ def make_gather_tensors(rows) -> GatherTensors:
 
 def msa_cache_gather(batch, tensors: GatherTensors, kept, block_size=128, stream=None):
     dev, st = _place(stream)
+    if tensors.device != dev:
+        raise ValueError(f"the gather tensors are on CUDA device {tensors.device}, the current one "
+                         f"is {dev}")
     for i, n in enumerate(tensors.batches):
         if n != batch:
             raise ValueError(f"gather tensor {i} has batch {n}, the call {batch}")

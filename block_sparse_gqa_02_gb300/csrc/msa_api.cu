@@ -119,6 +119,12 @@ msa_status check_ptr(const void* p, const char* name, bool nullable = false) {
   return MSA_OK;
 }
 
+// Whether two buffers of `bytes` bytes share memory (a null one shares none).
+bool overlap(const void* a, const void* b, size_t bytes) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return a && b && (x < y ? y - x < bytes : x - y < bytes);
+}
+
 #define MSA_TRY(expr)                    \
   do {                                   \
     msa_status st_ = (expr);             \
@@ -611,6 +617,14 @@ msa_status msa_cache_evict(const msa_shape* shape, int32_t keep, int32_t n_first
   if ((block_table == nullptr) != (table_out == nullptr))
     return fail(MSA_ERR_INVALID_ARG, "block_table and table_out are given together or not at all");
   MSA_TRY(check_ptr(table_out, "table_out", true));
+  // an output is its input's buffer or clear of it
+  const size_t mass_bytes = (size_t)d.B * d.Hkv * d.nB * 4, table_bytes = (size_t)d.B * d.nB * 4;
+  if (mass_out != mass && overlap(mass_out, mass, mass_bytes))
+    return fail(MSA_ERR_INVALID_ARG, "mass_out overlaps mass without being it");
+  if (table_out != block_table && overlap(table_out, block_table, table_bytes))
+    return fail(MSA_ERR_INVALID_ARG, "table_out overlaps block_table without being it");
+  if (new_lens != seq_lens && overlap(new_lens, seq_lens, (size_t)d.B * 4))
+    return fail(MSA_ERR_INVALID_ARG, "new_lens overlaps seq_lens without being it");
   d.seq_lens = seq_lens;
   {
     const cudaError_t ve = launch_debug_validate(d, nullptr, (cudaStream_t)stream, status_ptr());

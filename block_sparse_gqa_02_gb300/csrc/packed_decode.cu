@@ -3,8 +3,8 @@
 // sparse_decode does over a 16- or 32-bit cache.
 //
 // A thread-block cluster takes one (sequence, KV head); its CTAs share the selected blocks out
-// and meet through distributed shared memory: each reads the others' running maxima, sums and
-// outputs of its slice of the heads, so one launch does the whole step without a workspace.
+// and meet through distributed shared memory, so one launch does the whole step without a
+// workspace.
 //
 // The G <= 16 heads of a group (16 of them a pass) are the M rows of mma.sync.m16n8k16.  The
 // codes become exact fp16 integers c = code - 8: a code or-ed into the mantissa of 1024 (or, four
@@ -15,7 +15,8 @@
 // Scores: q is brought to fp16 by a power of two per row (exact but for values below 2^-14 of
 // the row's largest, whose error is 2^-25 of that); the accumulators, one per group of dims, are
 // scaled by the steps in fp32; the mid term is one bf16 MMA whose A operand is the group sums
-// of q, split in three parts (24 bits).
+// of q, split in three parts (24 bits).  The row's power of two joins the softmax scale, so a
+// score is formed at up to 2^9 times a step and steps above 2^118 would overflow.
 // Outputs: p and the steps are fp16 (steps relative to the largest of their group that the warp
 // has met, times 2^10), and so is their product: roundings of 2^-11, an eighth of what bf16 would
 // cost; products below 2^-24 of the largest step lose digits.  The mid term is a bf16 MMA with
@@ -28,8 +29,15 @@
 // turn, 32 keys a warp, each warp with a softmax base of its own that moves only when a row's
 // maximum passes it by more than 4 (log2 units).  Whole records (K and V of a block, 160 D
 // contiguous bytes) come through a ring, one bulk copy each; a group's first warp refills a
-// stage in the middle of its next block, when the other warps have left the stage.  Twelve
-// warps leave a thread 168 registers, which hold Q's operands and the outputs.
+// stage in the middle of its next block, when the other warps have left the stage.  Q's
+// operands are read from shared memory for every 16 keys; the outputs stay in registers, which
+// twelve warps leave enough of (168 a thread; sixteen warps of 128 spilled and gained nothing).
+//
+// What bounds it (8 x 1M, 64 blocks a head, 18.7 us, 42 MB, 2.3 TB/s): of a CTA's 17 us, with
+// sixteen blocks each, 2.5 pass before its first block has arrived, 11.5 in the loop and 3 in
+// the merge.  The loop issues some 900 instructions a warp and block; 62 % of the issue slots
+// are used, the tensor pipe (mma.sync) 38 % and the ALUs 44 %: without the second product the
+// call takes 14.9 us, without the first 14.3, so about 10.5 are the memory's and the ends'.
 //
 // The CTAs of a cluster end by writing their partial outputs, maxima and sums into each
 // other's shared memory (each owns a share of the rows), so after one cluster barrier
@@ -824,6 +832,10 @@ cudaError_t decode_mma(const Dims& p, const void* q, const void* cache, const in
   const int per = (p.k - 1) / n_split + 1, listed = per < kMaxList ? per : kMaxList;
   const size_t smem = sizeof(MmaSmem<D, sizeof(T) == 4 ? 2 : 1>) + sizeof(Entry) * listed +
                       (kMass ? sizeof(float) * kGroupWarps * kRows * per : 0);
+  static_assert(sizeof(MmaSmem<D, sizeof(T) == 4 ? 2 : 1>) +
+                        (kMass ? kMaxMassList * (sizeof(Entry) + 4 * kGroupWarps * kRows)
+                               : kMaxList * sizeof(Entry)) <= 227 * 1024,
+                "shared memory of a CTA");
   auto kern = packed_decode_mma<T, D, kMass>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)smem);

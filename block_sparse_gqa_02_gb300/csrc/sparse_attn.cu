@@ -200,9 +200,11 @@ __device__ __forceinline__ void combine_head(const float* __restrict__ ws_o,
                                              float* __restrict__ lse, int bh, int n_split) {
   const float* l = ws_l + (size_t)bh * n_split;
   float mx = -INFINITY;
+#pragma unroll 4
   for (int s = 0; s < n_split; ++s) mx = fmaxf(mx, l[s]);
   float acc = 0.f, den = 0.f;
   if (mx != -INFINITY) {
+#pragma unroll 4
     for (int s = 0; s < n_split; ++s) {
       const float w = expf(l[s] - mx);
       den += w;
@@ -244,8 +246,10 @@ __global__ void __launch_bounds__(D) decode_combine_mass(
   if ((int)threadIdx.x < p.G) {
     const float* l = ws_l + (head0 + threadIdx.x) * n_split;
     float mx = -INFINITY, den = 0.f;
+#pragma unroll 4
     for (int s = 0; s < n_split; ++s) mx = fmaxf(mx, l[s]);
     if (mx != -INFINITY)
+#pragma unroll 4
       for (int s = 0; s < n_split; ++s) den += expf(l[s] - mx);
     norm[threadIdx.x] = den > 0.f ? (mx + logf(den)) * kLog2e : -INFINITY;
   }

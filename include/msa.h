@@ -279,8 +279,8 @@ msa_status msa_rope(const msa_rope_desc* desc, const msa_rope_tensor* tensors, i
  *   mid  = bf16(lo + 8 * step)
  *   code = clamp(rint((x - mid) * fp32(1 / step)) + 8, 0, 15), 8 when step is 0
  *   value = mid + (code - 8) * step                   (what the cache holds)
- * |value - x| <= step / 2 + 2^-8 |mid| + 2^-8 * 8 step; a group holding a NaN or an infinity
- * is stored as NaN values.
+ * |value - x| <= step / 2 + 2^-8 |mid| + 2^-8 * 8 step (for |x| within bf16's range); a group
+ * holding a NaN or an infinity is stored as NaN values.
  *
  * cache   uint8 [n_phys, n_heads_kv, 160 * head_dim], 16-byte aligned: K's record of the
  *         block, then V's.  With a block_table (int32 [batch, n_blocks]) logical block j of
@@ -319,9 +319,10 @@ msa_status msa_cache_unpack(const msa_shape* shape, int32_t n_out, const int32_t
                             const void* cache, void* k, void* v, void* stream);
 
 /* msa_sparse_decode over the 4-bit cache: attention of q [batch, 1, n_heads_q, head_dim] over
- * the values that the selected blocks hold.  out, lse as there (lse may be NULL); bytes of
- * the last block past the sequence's length are never used, whatever they hold.  No
- * workspace.  At most 64 query heads per KV head.
+ * the values that the selected blocks hold (below 2^118 in magnitude; V's steps within 2^24 of
+ * the largest of their group of dims keep all their digits).  out, lse as there (lse may be
+ * NULL); bytes of the last block past the sequence's length are never used, whatever they hold.
+ * No workspace.  At most 64 query heads per KV head.
  * mass: NULL, or the accumulated attention weights below (then top_k is at most 1024). */
 msa_status msa_sparse_decode_packed(const msa_shape* shape, const int32_t* seq_lens,
                                     const int32_t* block_table, int32_t n_phys, const void* q,
@@ -334,9 +335,9 @@ msa_status msa_sparse_decode_packed(const msa_shape* shape, const int32_t* seq_l
  *   block of exp(z_hj - lse_h)                   (the weights of one head sum to 1)
  * mass: float32 [batch, n_heads_kv, n_blocks], the caller's, zeroed when a sequence starts.
  * out and lse (may be NULL) are bit for bit those of msa_sparse_decode, or, with seq_lens and
- * block_table (both given), of msa_sparse_decode_paged on its shapes.  Each entry of mass
- * gets one addition a call, so results repeat bit for bit (a block listed twice is counted
- * twice).  workspace: msa_workspace_bytes(shape, 4) bytes, as for msa_sparse_decode. */
+ * block_table (both given), of msa_sparse_decode_paged on its shapes.  A selected block's entry
+ * gets one addition a call, so results repeat bit for bit.  (A block listed twice is counted
+ * twice, in either order.)  workspace: msa_workspace_bytes(shape, 4) bytes, as for msa_sparse_decode. */
 msa_status msa_sparse_decode_mass(const msa_shape* shape, const int32_t* seq_lens,
                                   const int32_t* block_table, int32_t n_phys, const void* q,
                                   const void* k, const void* v, const int32_t* sel, void* out,
@@ -356,7 +357,8 @@ msa_status msa_sparse_decode_mass(const msa_shape* shape, const int32_t* seq_len
  *             with the kept blocks first and the dropped ones after them (both ascending),
  *             entries past the sequence's last block as they were.  A sequence grows into
  *             the blocks it dropped, or the caller takes them back.
- * new_lens, mass_out and table_out may be the inputs themselves (in place).  shape: a decode
+ * new_lens, mass_out and table_out may be the inputs themselves (in place), but may not
+ * overlap them otherwise.  shape: a decode
  * shape (n_blocks at most 32768); seq_lens NULL: every length is seq_k.
  * keep >= n_first + n_recent, n_first >= 0, n_recent >= 1. */
 msa_status msa_cache_evict(const msa_shape* shape, int32_t keep, int32_t n_first, int32_t n_recent,

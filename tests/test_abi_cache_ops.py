@@ -139,6 +139,8 @@ def test_evict_arguments(lib):
     assert call(s, kept=FAKE + 4) == MSA_ERR_INVALID_ARG
     assert call(s, t_out=None) == MSA_ERR_INVALID_ARG
     assert call(s, table=None) == MSA_ERR_INVALID_ARG
+    assert call(s, out=FAKE + 16) == MSA_ERR_INVALID_ARG and b"mass_out" in lib.msa_last_error()
+    assert call(s, t_out=FAKE - 16) == MSA_ERR_INVALID_ARG and b"table_out" in lib.msa_last_error()
     assert call(_shape(seq_q=1000, q_tile=64)) == MSA_ERR_INVALID_ARG
     assert call(_shape(seq_k=(1 << 22) + 1)) == MSA_ERR_UNSUPPORTED  # 32769 blocks
 

@@ -189,6 +189,31 @@ def test_gather(dtype):
             assert np.array_equal(res[b], want), b
 
 
+def test_gather_of_the_4_bit_cache():
+    """A table-less 4-bit cache cut by whole blocks: the decode over the kept blocks' new places is
+    the decode over their old ones, bit for bit."""
+    B, Hkv, d, cap, keep = 2, 4, 128, 1100, 5
+    shape = _lib.make_shape(B, 1, cap, 16, Hkv, d, 128, 128, keep, 1)
+    nB = shape.n_blocks
+    cache = api.alloc_packed_cache(B * nB, Hkv, d)
+    k, v = _rows((B, Hkv, cap, d), DT["bf16"], 1), _rows((B, Hkv, cap, d), DT["bf16"], 2)
+    _lib.msa_cache_pack(shape, cap, None, None, None, B * nB, k, v, cache)
+    kept = _i32([[0, 2, 3, 7, 8], [1, 4, 5, 6, 8]])
+    small = api.alloc_packed_cache(B * keep, Hkv, d)
+    pair = (cache.view(B, 1, nB * 128, -1), small.view(B, 1, keep * 128, -1))
+    _lib.msa_cache_gather(B, _lib.make_gather_tensors([pair]), kept)
+    q = _rows((B, 1, 16, d), DT["bf16"], 3)
+    outs = []
+    for c, n, sel in ((cache, cap, kept), (small, cap - (nB - keep) * 128,
+                                           torch.arange(keep, device="cuda", dtype=torch.int32).expand(B, keep))):
+        s = _lib.make_shape(B, 1, n, 16, Hkv, d, 128, 128, keep, 1)
+        out = torch.empty_like(q)
+        _lib.msa_sparse_decode_packed(s, None, None, c.shape[0], q, c,
+                                      sel[:, None, None].expand(B, Hkv, 1, keep).contiguous(), out)
+        outs.append(out)
+    assert torch.equal(*outs)
+
+
 def test_gather_past_32_bit_offsets():
     """Sources and destinations of more than 4 GiB a tensor."""
     rows, d = 9_000_000, 256

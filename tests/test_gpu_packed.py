@@ -291,6 +291,66 @@ def test_packed_decode_large_logits_and_outlier_scales():
     assert np.all(np.abs(to_np(lse) - l) <= 2e-3 + (d + 8) * 2.0 ** -24 * np.abs(l) * 8)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_packed_decode_small_value_under_all_the_weight(dtype):
+    """One key of values 2^-20 of the others' takes (almost) all the weight: its digits stay."""
+    B, cap, Hkv, d = 1, 400, 1, 64
+    shape = _shape(B, cap, 4, Hkv, d, 4, dtype)
+    k, v = _rows((B, Hkv, cap, d), DT[dtype], 1) * 0.1, _rows((B, Hkv, cap, d), DT[dtype], 2)
+    q = torch.ones((B, 1, 4, d), device="cuda").to(DT[dtype])
+    k[0, 0, 7] = 10.0                                       # a logit of 80, the others' about 0
+    v[0, 0, 7] *= 2.0 ** -20
+    cache = torch.zeros((4, Hkv, 160 * d), dtype=torch.uint8, device="cuda")
+    _lib.msa_cache_pack(shape, cap, None, None, None, 4, k, v, cache)
+    sel = _i32([3, 2, 1, 0]).expand(B, Hkv, 1, 4).contiguous()   # the key comes last
+    out = torch.empty_like(q)
+    _lib.msa_sparse_decode_packed(shape, None, None, 4, q, cache, sel, out)
+    o, _, _ = co.decode_mass(q, co.pack_values(to_np(k))[0], co.pack_values(to_np(v))[0],
+                             sel.cpu().numpy(), [cap])
+    # the key's p * step is 2^-10 of fp16's unit here: normal, so 2^-11 of it (fp32: its rest too)
+    assert np.abs(o).max() < 1e-5
+    check_out(out.double() * 2.0 ** 20, o * 2.0 ** 20, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_packed_decode_extreme_magnitudes(dtype):
+    """Queries, keys and values far from one, the logits in the ordinary range; a query row of
+    zeros; fp32 and bf16."""
+    B, cap, Hkv, d = 1, 500, 2, 128
+    shape = _shape(B, cap, 8, Hkv, d, 4, dtype)
+    sel = _i32([0, 1, 2, 3]).expand(B, Hkv, 1, 4).contiguous()
+    for qs, vs in ((2.0 ** 80, 2.0 ** 100), (2.0 ** -80, 2.0 ** -80), (2.0 ** 40, 1.0)):
+        k, v = _rows((B, Hkv, cap, d), DT[dtype], 1) / qs, _rows((B, Hkv, cap, d), DT[dtype], 2) * vs
+        q = _rows((B, 1, 8, d), DT[dtype], 3) * qs
+        q[0, 0, 3] = 0
+        cache = torch.zeros((4, Hkv, 160 * d), dtype=torch.uint8, device="cuda")
+        _lib.msa_cache_pack(shape, cap, None, None, None, 4, k, v, cache)
+        out, lse = torch.empty_like(q), torch.empty((B, 8, 1), device="cuda")
+        _lib.msa_sparse_decode_packed(shape, None, None, 4, q, cache, sel, out, lse)
+        o, l, _ = co.decode_mass(q, co.pack_values(to_np(k))[0], co.pack_values(to_np(v))[0],
+                                 sel.cpu().numpy(), [cap])
+        check_out(out.double() / vs, o / vs, dtype)
+        check_lse(lse, l, dtype)
+
+
+def test_packed_decode_many_sequences():
+    """More (sequence, KV head) pairs than SMs: one CTA each, several waves."""
+    B, cap, Hkv, d = 90, 260, 4, 64
+    lens = [1 + (37 * i) % cap for i in range(B)]
+    cache, table, P, kv, vv = _filled(B, cap, Hkv, d, lens, "bf16", True, 3)
+    shape = _shape(B, cap, 8, Hkv, d, 3)
+    sel = _i32([0, 1, 2]).expand(B, Hkv, 1, 3).contiguous()
+    q = _rows((B, 1, 8, d), DT["bf16"], 1)
+    out, lse, mass = torch.empty_like(q), torch.empty((B, 8, 1), device="cuda"), \
+        torch.zeros((B, Hkv, 3), device="cuda")
+    _lib.msa_sparse_decode_packed(shape, _i32(lens), table, P, q, cache, sel, out, lse, mass)
+    o, l, m = co.decode_mass(q, list(kv), list(vv), sel.cpu().numpy(), lens)
+    check_out(out, o, "bf16")
+    check_lse(lse, l, "bf16")
+    tol = _weight_tol(to_np(q), kv, d ** -0.5, d) + 2.0 ** -24
+    assert np.all(np.abs(to_np(mass) - m) <= tol * m)
+
+
 def test_packed_cache_past_32_bit_offsets():
     """A pool of more than 4 GiB: the last physical blocks hold the sequence."""
     Hkv, d = 8, 128
