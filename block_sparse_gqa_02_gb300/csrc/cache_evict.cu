@@ -8,9 +8,12 @@
 // 11, 11 and 10 bits finds the threshold; a scan turns "stays" and "goes" into a stable
 // partition of the block indices.  Then the CTAs share the rows to be moved.  Outputs may be
 // the inputs: all that a sequence's CTAs read lies before a cluster barrier, and what they
-// write after it.
+// write after it.  Measured: 11.2 us for 8 sequences of 8192 blocks and 4 heads (the choice takes
+// about 7000 of 30000 clocks; finding the threshold bit by bit took 16700, one CTA a sequence
+// with loads one after the other 24.6 us).
 //
-// cache_gather_kernel streams bytes: one CTA per kept block of one head of one cache.
+// cache_gather_kernel streams bytes: one CTA per kept block of one head of one cache, eight
+// 16-byte loads in flight a thread (301 MB in 41 us, 7.3 TB/s with the writes still in L2).
 #include <cooperative_groups.h>
 
 #include "common.cuh"

@@ -3,8 +3,9 @@
 // exp(z_hj - lse_h).
 //
 // Where decode runs on the tensor cores, its kernel writes each row's log-sum per block (k
-// floats a warp, nothing beside the keys it reads) and the merge forms the weights, so they
-// cost next to nothing.  Other shapes (fp32, head_dim 64, other blocks, wide groups) take
+// floats a warp, nothing beside the keys it reads) and the merge forms the weights in CTAs of its
+// own: 30.7 us for 134 MB (8 ragged sequences, 64 blocks a head) against 32.7 for the same step
+// without them, whose two launches do not overlap.  Other shapes (fp32, head_dim 64, other blocks, wide groups) take
 // mass_kernel after the step: CTA = one selection entry of one (sequence, KV head), its keys'
 // logits formed again in fp32 from K in shared memory, a thread per key, and weighed by the
 // step's log-sum-exps.  Either way a block's weight is one atomic addition, the only one to its

@@ -296,7 +296,7 @@ packed_decode_mma(const T* __restrict__ q, const uint8_t* __restrict__ cache,
   extern __shared__ __align__(128) uint8_t smem_raw[];
   S& s = *reinterpret_cast<S*>(smem_raw);
   Entry* list = reinterpret_cast<Entry*>(smem_raw + sizeof(S));   // [min(per, kMaxList)]
-  float* weights = reinterpret_cast<float*>(list + per);   // [kGroupWarps][kRows][per], kMass only
+  float* weights = reinterpret_cast<float*>(list + per);   // [kGroupWarps][per][kRows], kMass only
   cg::cluster_group cluster = cg::this_cluster();
   const int split = (int)cluster.block_rank(), n_split = (int)cluster.num_blocks();
   const int own = kRows / n_split;                         // rows that a CTA of the cluster ends
@@ -607,7 +607,7 @@ packed_decode_mma(const T* __restrict__ q, const uint8_t* __restrict__ cache,
           }
           const float bs = c ? base[1] : base[0], sm = c ? sum[1] : sum[0];
           if (c < 2)
-            weights[(gw * kRows + gr + 8 * c) * per + i] =
+            weights[(gw * per + i) * kRows + gr + 8 * c] =
                 bs == -INFINITY ? -INFINITY : bs + __log2f(sm);
         }
         // outputs: 16 keys a step
@@ -797,14 +797,18 @@ packed_decode_mma(const T* __restrict__ q, const uint8_t* __restrict__ cache,
         }
       store_pair(out + ((size_t)b * p.Hq + g * p.G + h0 + r) * D + d0, v);
     }
-    if (kMass)
-      for (int i = threadIdx.x; i < n_blocks; i += kMmaThreads) {
+    if (kMass)                                             // sixteen lanes a block, one a row
+      for (int e0 = 0; e0 < n_blocks * kRows; e0 += kMmaThreads) {
+        const int e = e0 + (int)threadIdx.x, i = e / kRows, r = e % kRows;
         float sum = 0.f;
-        for (int r = 0; r < rows; ++r)
-          if (s.norm[r] != -INFINITY)
-            for (int w = 0; w < kGroupWarps; ++w)
-              sum += ex2(weights[(w * kRows + r) * per + i] - s.norm[r]);
-        if (!*abort) atomicAdd(mass + (size_t)bg * p.nB + list[i].blk, sum);
+        if (i < n_blocks && r < rows && s.norm[r] != -INFINITY)
+#pragma unroll
+          for (int w = 0; w < kGroupWarps; ++w)
+            sum += ex2(weights[(w * per + i) * kRows + r] - s.norm[r]);
+#pragma unroll
+        for (int x = kRows / 2; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        if (r == 0 && i < n_blocks && !*abort)
+          atomicAdd(mass + (size_t)bg * p.nB + list[i].blk, sum);
       }
     if (h0 + kRows < p.G) {
       // the next pass copies into the memory that held the warps' outputs, and the others
