@@ -752,9 +752,10 @@ packed_decode_mma(const T* __restrict__ q, const uint8_t* __restrict__ cache,
       float top = -INFINITY, sum = 0.f;
 #pragma unroll
       for (int w = 0; w < kMmaWarps; ++w) top = fmaxf(top, s.wm[w][r]);
-      if (top != -INFINITY)
+      // a warp without a base has a sum of 0, or NaN when all its scores are no numbers
+      const float ref = top == -INFINITY ? 0.f : top;
 #pragma unroll
-        for (int w = 0; w < kMmaWarps; ++w) sum += ex2(s.wm[w][r] - top) * s.wl[w][r];
+      for (int w = 0; w < kMmaWarps; ++w) sum += ex2(s.wm[w][r] - ref) * s.wl[w][r];
       *cluster.map_shared_rank(&s.m[split][r], to) = top;
       *cluster.map_shared_rank(&s.l[split][r], to) = sum;
     }
@@ -777,9 +778,9 @@ packed_decode_mma(const T* __restrict__ q, const uint8_t* __restrict__ cache,
       const int r = threadIdx.x;
       float top = -INFINITY, sum = 0.f;
       for (int x = 0; x < n_split; ++x) top = fmaxf(top, s.m[x][r]);
-      if (top != -INFINITY)
-        for (int x = 0; x < n_split; ++x) sum += ex2(s.m[x][r] - top) * s.l[x][r];
-      s.norm[r] = top == -INFINITY ? -INFINITY : top + __log2f(sum);
+      const float ref = top == -INFINITY ? 0.f : top;
+      for (int x = 0; x < n_split; ++x) sum += ex2(s.m[x][r] - ref) * s.l[x][r];
+      s.norm[r] = sum == 0.f ? -INFINITY : ref + __log2f(sum);
       if (lse && split == 0 && r < rows)
         lse[(size_t)b * p.Hq + g * p.G + h0 + r] = s.norm[r] * kLn2;
     }

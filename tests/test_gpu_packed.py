@@ -333,6 +333,30 @@ def test_packed_decode_extreme_magnitudes(dtype):
         check_lse(lse, l, dtype)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_packed_decode_not_a_number(dtype):
+    """A NaN in a key that is seen shows in every output of its head, alone or among others; one in
+    a value in its group's dims; none of another sequence's or head's."""
+    B, cap, Hkv, d = 2, 300, 2, 64
+    shape = _shape(B, cap, 4, Hkv, d, 3, dtype)
+    for where, lens in (("alone", [1, 300]), ("among", [290, 300])):
+        k, v = _rows((B, Hkv, cap, d), DT[dtype], 1), _rows((B, Hkv, cap, d), DT[dtype], 2)
+        k[0, 0, 0, 5] = float("nan")
+        v[1, 1, 200, 40] = float("nan")
+        cache = torch.full((6, Hkv, 160 * d), 0xFF, dtype=torch.uint8, device="cuda")
+        _lib.msa_cache_pack(shape, cap, _i32([0, 0]), _i32(lens), None, 6, k, v, cache)
+        sel = _i32([0, 1, 2]).expand(B, Hkv, 1, 3).contiguous()
+        q = _rows((B, 1, 4, d), DT[dtype], 3)
+        out, lse = torch.empty_like(q), torch.empty((B, 4, 1), device="cuda")
+        _lib.msa_sparse_decode_packed(shape, _i32(lens), None, 6, q, cache, sel, out, lse)
+        bad = torch.isnan(out)
+        want = torch.zeros_like(bad)
+        want[0, 0, :2] = True
+        want[1, 0, 2:, 32:] = True
+        assert torch.equal(bad, want), where
+        assert torch.equal(torch.isnan(lse[..., 0]), want[:, 0, :, 0]), where
+
+
 def test_packed_decode_many_sequences():
     """More (sequence, KV head) pairs than SMs: one CTA each, several waves."""
     B, cap, Hkv, d = 90, 260, 4, 64
