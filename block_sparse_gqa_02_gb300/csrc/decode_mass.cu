@@ -5,11 +5,14 @@
 // Where decode runs on the tensor cores, its kernel writes each row's log-sum per block (k
 // floats a warp, nothing beside the keys it reads) and the merge forms the weights in CTAs of its
 // own: 30.7 us for 134 MB (8 ragged sequences, 64 blocks a head) against 32.7 for the same step
-// without them, whose two launches do not overlap.  Other shapes (fp32, head_dim 64, other blocks, wide groups) take
-// mass_kernel after the step: CTA = one selection entry of one (sequence, KV head), its keys'
-// logits formed again in fp32 from K in shared memory, a thread per key, and weighed by the
-// step's log-sum-exps.  Either way a block's weight is one atomic addition, the only one to its
-// address in a call, so results repeat bit for bit.
+// without them, whose two launches do not overlap.  Other shapes (fp32, head_dim 64, other blocks,
+// wide groups) take mass_kernel after the step: CTA = one selection entry of one (sequence, KV
+// head), its keys' logits formed again in fp32 from K in shared memory, a thread per key, and
+// weighed by the step's log-sum-exps.  A key read from shared memory serves eight heads: 4 x 50000
+// keys, 48 blocks a head take 29 us more than the step's 277 (fp32, head_dim 128, 16 heads a KV
+// head; 51 with a read per head) and 19 more than its 124 (bf16, head_dim 64; 31).  Either way a
+// block's weight is one atomic addition, the only one to its address in a call, so results repeat
+// bit for bit.
 #include "common.cuh"
 #include "sparse_decode_mma.cuh"
 
@@ -21,15 +24,17 @@ constexpr int kThreads = 128;
 constexpr int kKeys = 128;             // keys of a pass, one thread each
 constexpr float kLog2e = 1.4426950408889634f;
 
-template <typename T, int D>
+// kHeads: heads that share a read of a key from shared memory, 8 or 2.
+template <typename T, int D, int kHeads>
 __global__ void __launch_bounds__(kThreads)
 mass_kernel(const T* __restrict__ q, const T* __restrict__ k, const int32_t* __restrict__ sel,
             const float* __restrict__ lse, float* __restrict__ mass, Dims p) {
   constexpr int kRow = D + 4;                              // floats of a staged key
   extern __shared__ float smem[];
   float* ks = smem;                                        // [kKeys][kRow]
-  float* qs = smem + kKeys * kRow;                         // [G][D]
-  float* ls = qs + p.G * D;                                // [G] lse in log2 units
+  const int heads = (p.G + kHeads - 1) / kHeads * kHeads;  // rows past the last head stay zero
+  float* qs = smem + kKeys * kRow;                         // [heads][D]
+  float* ls = qs + heads * D;                              // [heads] lse in log2 units
   __shared__ float part[kThreads / 32];
   const int bg = blockIdx.y, b = bg / p.Hkv, g = bg % p.Hkv;
   const int L = seq_len_of(p, b), nB_b = (L + p.Bk - 1) / p.Bk;
@@ -37,10 +42,11 @@ mass_kernel(const T* __restrict__ q, const T* __restrict__ k, const int32_t* __r
   if (blk < 0 || blk >= nB_b) return;
   const T* kb = k + ((size_t)bg * p.Sk + (size_t)blk * p.Bk) * D;
   const int seen = min(p.Bk, L - blk * p.Bk);
-  for (int e = threadIdx.x; e < p.G * D; e += kThreads)
-    qs[e] = to_f32(q[((size_t)b * p.Hq + g * p.G) * D + e]) * (p.sm_scale * kLog2e);
-  for (int h = threadIdx.x; h < p.G; h += kThreads)
-    ls[h] = lse[(size_t)b * p.Hq + g * p.G + h] * kLog2e;
+  for (int e = threadIdx.x; e < heads * D; e += kThreads)
+    qs[e] = e < p.G * D ? to_f32(q[((size_t)b * p.Hq + g * p.G) * D + e]) * (p.sm_scale * kLog2e)
+                        : 0.f;
+  for (int h = threadIdx.x; h < heads; h += kThreads)      // a head without keys adds nothing
+    ls[h] = h < p.G ? lse[(size_t)b * p.Hq + g * p.G + h] * kLog2e : -INFINITY;
   float sum = 0.f;
   for (int j0 = 0; j0 < seen; j0 += kKeys) {
     const int n = min(kKeys, seen - j0);
@@ -50,18 +56,25 @@ mass_kernel(const T* __restrict__ q, const T* __restrict__ k, const int32_t* __r
     __syncthreads();
     const int j = threadIdx.x;
     if (j < n)
-      for (int h = 0; h < p.G; ++h) {
-        float dot = 0.f;
-#pragma unroll 8
+      for (int h0 = 0; h0 < p.G; h0 += kHeads) {           // a key's values serve kHeads heads
+        float dot[kHeads];
+#pragma unroll
+        for (int h = 0; h < kHeads; ++h) dot[h] = 0.f;
+#pragma unroll 4
         for (int d0 = 0; d0 < D; d0 += 4) {
           const float4 kx = *reinterpret_cast<const float4*>(ks + j * kRow + d0);
-          const float4 qx = *reinterpret_cast<const float4*>(qs + h * D + d0);
-          dot = fmaf(qx.x, kx.x, dot);
-          dot = fmaf(qx.y, kx.y, dot);
-          dot = fmaf(qx.z, kx.z, dot);
-          dot = fmaf(qx.w, kx.w, dot);
+#pragma unroll
+          for (int h = 0; h < kHeads; ++h) {
+            const float4 qx = *reinterpret_cast<const float4*>(qs + (h0 + h) * D + d0);
+            dot[h] = fmaf(qx.x, kx.x, dot[h]);
+            dot[h] = fmaf(qx.y, kx.y, dot[h]);
+            dot[h] = fmaf(qx.z, kx.z, dot[h]);
+            dot[h] = fmaf(qx.w, kx.w, dot[h]);
+          }
         }
-        if (ls[h] != -INFINITY) sum += exp2f(dot - ls[h]);
+#pragma unroll
+        for (int h = 0; h < kHeads; ++h)
+          if (ls[h0 + h] != -INFINITY) sum += exp2f(dot[h] - ls[h0 + h]);
       }
   }
 #pragma unroll
@@ -74,17 +87,26 @@ mass_kernel(const T* __restrict__ q, const T* __restrict__ k, const int32_t* __r
   }
 }
 
-template <typename T, int D>
-cudaError_t run_mass(const Dims& p, const void* q, const void* k, const int32_t* sel,
+template <typename T, int D, int kHeads>
+cudaError_t run_heads(const Dims& p, const void* q, const void* k, const int32_t* sel,
                      const float* lse, float* mass, cudaStream_t st) {
-  auto kern = mass_kernel<T, D>;
-  const size_t smem = sizeof(float) * (kKeys * (D + 4) + (size_t)p.G * (D + 1));
+  auto kern = mass_kernel<T, D, kHeads>;
+  const size_t heads = (size_t)(p.G + kHeads - 1) / kHeads * kHeads;
+  const size_t smem = sizeof(float) * (kKeys * (D + 4) + heads * (D + 1));
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)smem);
   if (e != cudaSuccess) return e;
   kern<<<dim3(p.k, p.B * p.Hkv), kThreads, smem, st>>>((const T*)q, (const T*)k, sel, lse, mass,
                                                        p);
   return cudaGetLastError();
+}
+
+// Groups of up to two heads do no work for six that are not there.
+template <typename T, int D>
+cudaError_t run_mass(const Dims& p, const void* q, const void* k, const int32_t* sel,
+                     const float* lse, float* mass, cudaStream_t st) {
+  return p.G > 2 ? run_heads<T, D, 8>(p, q, k, sel, lse, mass, st)
+                 : run_heads<T, D, 2>(p, q, k, sel, lse, mass, st);
 }
 
 }  // namespace

@@ -32,6 +32,9 @@ MASS = {
     "block_200": (1, 1000, 8, 4, 64, 200, 3, "f32"),
     "f32": (2, 1100, 16, 4, 128, 128, 5, "f32"),
     "block_1": (1, 50, 4, 1, 64, 1, 7, "f32"),
+    "group_1": (2, 500, 4, 4, 128, 128, 3, "f32"),
+    "group_9": (1, 400, 18, 2, 64, 128, 4, "f32"),
+    "group_64": (1, 300, 64, 1, 64, 128, 3, "bf16"),
 }
 
 
