@@ -5,133 +5,421 @@
 // Where decode runs on the tensor cores, its kernel writes each row's log-sum per block (k
 // floats a warp, nothing beside the keys it reads) and the merge forms the weights in CTAs of its
 // own: 30.7 us for 134 MB (8 ragged sequences, 64 blocks a head) against 32.7 for the same step
-// without them, whose two launches do not overlap.  Other shapes (fp32, head_dim 64, other blocks,
-// wide groups) take mass_kernel after the step: CTA = one selection entry of one (sequence, KV
-// head), its keys' logits formed again in fp32 from K in shared memory, a thread per key, and
-// weighed by the step's log-sum-exps.  A key read from shared memory serves eight heads: 4 x 50000
-// keys, 48 blocks a head take 29 us more than the step's 277 (fp32, head_dim 128, 16 heads a KV
-// head; 51 with a read per head) and 19 more than its 124 (bf16, head_dim 64; 31).  Either way a
-// block's weight is one atomic addition, the only one to its address in a call, so results repeat
-// bit for bit.
+// without them, whose two launches do not overlap.  A block's weight is one atomic addition, the
+// only one to its address in a call, so results repeat bit for bit.
+//
+// Other shapes (fp32, head_dim 64, other blocks, wide groups) are computed here, on the CUDA
+// cores: fp32 products have no tensor-core form that keeps their 24 bits.  4 x 50000 keys, 48
+// blocks a head: 44 us for 200 MB (fp32, head_dim 128, 8 KV heads of 2), 77 for 100 MB (fp32, 4 KV
+// heads of 16), 30 for 25 MB (bf16, head_dim 64, 4 KV heads of 16).
 #include "common.cuh"
+#include "launch.cuh"
+#include "ptx.cuh"
 #include "sparse_decode_mma.cuh"
 
 namespace msa {
 
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kKeys = 128;             // keys of a pass, one thread each
+constexpr int kWarps = kDecodeWarps;   // of a CTA; a tile of 32 keys each
+constexpr int kThreads = 32 * kWarps;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
-// kHeads: heads that share a read of a key from shared memory, 8 or 2.
-template <typename T, int D, int kHeads>
-__global__ void __launch_bounds__(kThreads)
-mass_kernel(const T* __restrict__ q, const T* __restrict__ k, const int32_t* __restrict__ sel,
-            const float* __restrict__ lse, float* __restrict__ mass, Dims p) {
-  constexpr int kRow = D + 4;                              // floats of a staged key
-  extern __shared__ float smem[];
-  float* ks = smem;                                        // [kKeys][kRow]
-  const int heads = (p.G + kHeads - 1) / kHeads * kHeads;  // rows past the last head stay zero
-  float* qs = smem + kKeys * kRow;                         // [heads][D]
-  float* ls = qs + heads * D;                              // [heads] lse in log2 units
-  __shared__ float part[kThreads / 32];
-  const int bg = blockIdx.y, b = bg / p.Hkv, g = bg % p.Hkv;
-  const int L = seq_len_of(p, b), nB_b = (L + p.Bk - 1) / p.Bk;
-  const int blk = sel[(size_t)bg * p.k + blockIdx.x];
-  if (blk < 0 || blk >= nB_b) return;
-  const T* kb = k + ((size_t)bg * p.Sk + (size_t)blk * p.Bk) * D;
-  const int seen = min(p.Bk, L - blk * p.Bk);
-  for (int e = threadIdx.x; e < heads * D; e += kThreads)
-    qs[e] = e < p.G * D ? to_f32(q[((size_t)b * p.Hq + g * p.G) * D + e]) * (p.sm_scale * kLog2e)
-                        : 0.f;
-  for (int h = threadIdx.x; h < heads; h += kThreads)      // a head without keys adds nothing
-    ls[h] = h < p.G ? lse[(size_t)b * p.Hq + g * p.G + h] * kLog2e : -INFINITY;
-  float sum = 0.f;
-  for (int j0 = 0; j0 < seen; j0 += kKeys) {
-    const int n = min(kKeys, seen - j0);
-    __syncthreads();
-    for (int e = threadIdx.x * Vec16<T>::N; e < n * D; e += kThreads * Vec16<T>::N)
-      Vec16<T>::load(kb + (size_t)j0 * D + e, ks + e / D * kRow + e % D);
-    __syncthreads();
-    const int j = threadIdx.x;
-    if (j < n)
-      for (int h0 = 0; h0 < p.G; h0 += kHeads) {           // a key's values serve kHeads heads
-        float dot[kHeads];
+template <int kH> __device__ __forceinline__ void load_row(const float* s, float (&o)[kH]) {
+  if constexpr (kH == 2) {
+    const float2 x = *reinterpret_cast<const float2*>(s);
+    o[0] = x.x; o[1] = x.y;
+  } else {
 #pragma unroll
-        for (int h = 0; h < kHeads; ++h) dot[h] = 0.f;
-#pragma unroll 4
-        for (int d0 = 0; d0 < D; d0 += 4) {
-          const float4 kx = *reinterpret_cast<const float4*>(ks + j * kRow + d0);
+    for (int i = 0; i < kH; i += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(s + i);
+      o[i] = x.x; o[i + 1] = x.y; o[i + 2] = x.z; o[i + 3] = x.w;
+    }
+  }
+}
+
+// kH values a lane -> the warp's maximum or sum of value `lane / (32 / kH)`: halves of the values
+// change lanes until each lane holds one, kH + log2(32 / kH) - 1 shuffles where a reduction per
+// value takes 5 kH.
+template <int kH, bool kMax>
+__device__ __forceinline__ float reduce_heads(const float (&in)[kH], int lane) {
+  float v[kH];
 #pragma unroll
-          for (int h = 0; h < kHeads; ++h) {
-            const float4 qx = *reinterpret_cast<const float4*>(qs + (h0 + h) * D + d0);
-            dot[h] = fmaf(qx.x, kx.x, dot[h]);
-            dot[h] = fmaf(qx.y, kx.y, dot[h]);
-            dot[h] = fmaf(qx.z, kx.z, dot[h]);
-            dot[h] = fmaf(qx.w, kx.w, dot[h]);
-          }
-        }
+  for (int i = 0; i < kH; ++i) v[i] = in[i];
+  int o = 16;
 #pragma unroll
-        for (int h = 0; h < kHeads; ++h)
-          if (ls[h0 + h] != -INFINITY) sum += exp2f(dot[h] - ls[h0 + h]);
-      }
+  for (int n = kH / 2; n >= 1; n /= 2, o /= 2) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float mine = up ? v[i + n] : v[i], other = up ? v[i] : v[i + n];
+      const float got = __shfl_xor_sync(0xffffffffu, other, o);
+      v[i] = kMax ? fmaxf(mine, got) : mine + got;
+    }
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
+  for (; o > 0; o /= 2) {
+    const float got = __shfl_xor_sync(0xffffffffu, v[0], o);
+    v[0] = kMax ? fmaxf(v[0], got) : v[0] + got;
+  }
+  return v[0];
+}
+
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(dst)), "l"(src)
+               : "memory");
+}
+
+// Elements of V that a lane holds, converted: 4 or 2.
+template <typename T, int N> __device__ __forceinline__ void unpack_v(const void* raw, float* o);
+template <> __device__ __forceinline__ void unpack_v<float, 4>(const void* raw, float* o) {
+  const float4 x = *static_cast<const float4*>(raw);
+  o[0] = x.x; o[1] = x.y; o[2] = x.z; o[3] = x.w;
+}
+template <> __device__ __forceinline__ void unpack_v<float, 2>(const void* raw, float* o) {
+  const float2 x = *static_cast<const float2*>(raw);
+  o[0] = x.x; o[1] = x.y;
+}
+template <> __device__ __forceinline__ void unpack_v<__nv_bfloat16, 4>(const void* raw, float* o) {
+  const uint2 x = *static_cast<const uint2*>(raw);
+  o[0] = __uint_as_float(x.x << 16); o[1] = __uint_as_float(x.x & 0xffff0000u);
+  o[2] = __uint_as_float(x.y << 16); o[3] = __uint_as_float(x.y & 0xffff0000u);
+}
+template <> __device__ __forceinline__ void unpack_v<__nv_bfloat16, 2>(const void* raw, float* o) {
+  const uint32_t x = *static_cast<const uint32_t*>(raw);
+  o[0] = __uint_as_float(x << 16); o[1] = __uint_as_float(x & 0xffff0000u);
+}
+template <int kBytes> struct Raw;
+template <> struct Raw<4> { using type = uint32_t; };
+template <> struct Raw<8> { using type = uint2; };
+template <> struct Raw<16> { using type = uint4; };
+
+template <typename T, int D, int kH> struct Layout {
+  static constexpr int kKRow = D * (int)sizeof(T) + 16;    // bytes of a staged key: 16 mod 128
+  static constexpr int kPRow = kH == 2 ? 2 : kH + 4;       // floats of a key's weights
+  static constexpr int kTileBytes = 32 * kKRow;            // K of a warp; its output at the end
+  static constexpr int kQ = kWarps * kTileBytes;
+  static constexpr int kP = kQ + kH * D * 4;
+  static constexpr int kStat = kP + kWarps * 32 * kPRow * 4;
+  static constexpr int kBytes = kStat + kWarps * 2 * kH * 4;
+  static_assert(kH * D * 4 <= kTileBytes, "a warp's output fits its K tile");
+};
+
+// Grid (splits, B * Hkv, chunks of kH heads).  A warp takes 32 keys of every block of its split
+// (again 128 further on, in longer blocks) for kH heads and keeps their running maximum, sum and
+// output by itself; the CTA's four are joined at its end.
+//   scores: a lane per key, K from shared memory (one read serves kH heads), Q broadcast;
+//   output: a lane per D / 32 dims, V from memory to registers, the weights broadcast.
+// The copy of the next tile of K runs under the second part.
+template <typename T, int D, int kH>
+__global__ void __launch_bounds__(kThreads, 3)
+decode_mass_partial(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
+                    const int32_t* __restrict__ sel, float* __restrict__ ws_o,
+                    float* __restrict__ ws_l, float* __restrict__ ws_b, Dims p, int n_split,
+                    int per) {
+  using L = Layout<T, D, kH>;
+  constexpr int kVec = D / 32;                             // dims of a lane
+  constexpr int kChunk = 16 / (int)sizeof(T);              // dims of a 16-byte load
+  constexpr int kOwn = 32 / kH;                            // lanes that share a head's statistics
+  constexpr int kUnroll = kH == 16 ? 1 : 2;
+  constexpr int kAhead = 4;                                // loads of V in flight
+  using RawV = typename Raw<kVec * (int)sizeof(T)>::type;
+  extern __shared__ __align__(16) unsigned char smem[];
+  ptx::grid_wait();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int bg = blockIdx.y, b = bg / p.Hkv, g = bg % p.Hkv, h0 = blockIdx.z * kH;
+  const size_t head0 = (size_t)b * p.Hq + (size_t)g * p.G + h0;
+  const int heads = min(kH, p.G - h0);
+  unsigned char* ks = smem + warp * L::kTileBytes;
+  float* qs = reinterpret_cast<float*>(smem + L::kQ);
+  float* ps = reinterpret_cast<float*>(smem + L::kP) + warp * 32 * L::kPRow;
+  float* stat = reinterpret_cast<float*>(smem + L::kStat) + warp * 2 * kH;
+  const int32_t* srow = sel + (size_t)bg * p.k;
+  const T* kb = k + (size_t)bg * p.Sk * D;
+  const T* vb = v + (size_t)bg * p.Sk * D;
+  const int e0 = blockIdx.x * per, e1 = min(p.k, e0 + per);
+
+  // the warp's tiles in order: entry e, its block's keys [j, j + n) of the cache
+  struct Tile { int e, off, j, n; };
+  auto settle = [&](Tile& t) {                             // the first tile from (e, off) on
+    for (; t.e < e1; ++t.e, t.off = 32 * warp) {
+      const int blk = srow[t.e];
+      if (blk < 0 || blk >= p.nB) continue;
+      const int seen = min(p.Bk, p.Sk - blk * p.Bk);
+      if (t.off >= seen) continue;
+      t.j = blk * p.Bk + t.off;
+      t.n = min(32, seen - t.off);
+      return;
+    }
+    t.n = 0;
+  };
+  auto copy_k = [&](const Tile& t) {
+    const T* src = kb + (size_t)t.j * D;
+    for (int c = lane; c < t.n * (D / kChunk); c += 32)
+      copy16(ks + c / (D / kChunk) * L::kKRow + c % (D / kChunk) * 16, src + c * kChunk);
+  };
+  Tile t{e0, 32 * warp, 0, 0};
+  settle(t);
+  copy_k(t);
+  for (int x = threadIdx.x; x < kH * D; x += kThreads)     // rows past the last head are zero
+    qs[x] = x / D < heads ? to_f32(q[head0 * D + x]) * (p.sm_scale * kLog2e) : 0.f;
+  const int own = lane / kOwn;                             // the head of this lane's statistics
+  const bool writer = lane % kOwn == 0 && own < heads;
+  float* wb = ws_b + (head0 + own) * p.k * kWarps + warp;
+  if (writer)
+    for (int e = e0; e < e1; ++e) wb[(size_t)e * kWarps] = -INFINITY;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < kThreads / 32; ++w) sum += part[w];
+
+  float acc[kH][kVec];
+#pragma unroll
+  for (int h = 0; h < kH; ++h)
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) acc[h][i] = 0.f;
+  float m = -INFINITY, l = 0.f, le = 0.f;                  // maximum, sum, sum of this entry
+  while (t.n > 0) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+    float s[kH];
+#pragma unroll
+    for (int h = 0; h < kH; ++h) s[h] = 0.f;
+#pragma unroll kUnroll
+    for (int c = 0; c < D / kChunk; ++c) {
+      float kx[kChunk];
+      Vec16<T>::load(reinterpret_cast<const T*>(ks + lane * L::kKRow + c * 16), kx);
+#pragma unroll
+      for (int h = 0; h < kH; ++h)
+#pragma unroll
+        for (int i = 0; i < kChunk; i += 4) {
+          const float4 qx = *reinterpret_cast<const float4*>(qs + h * D + c * kChunk + i);
+          s[h] = fmaf(qx.x, kx[i], s[h]);
+          s[h] = fmaf(qx.y, kx[i + 1], s[h]);
+          s[h] = fmaf(qx.z, kx[i + 2], s[h]);
+          s[h] = fmaf(qx.w, kx[i + 3], s[h]);
+        }
+    }
+    if (lane >= t.n) {
+#pragma unroll
+      for (int h = 0; h < kH; ++h) s[h] = -INFINITY;
+    }
+    __syncwarp();                                          // K is read
+    const Tile now = t;
+    t.off += 32 * kWarps;
+    settle(t);
+    copy_k(t);
+
+    // a maximum of -inf (nothing but -inf so far) is subtracted as 0; NaN passes the maximum and
+    // stays in the sums
+    const float mx = fmaxf(m, reduce_heads<kH, true>(s, lane));
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    const float scale = exp2f(m - ref);
+    m = mx;
+    if (lane % kOwn == 0) {
+      stat[own] = ref;
+      stat[kH + own] = scale;
+    }
+    __syncwarp();
+    float r[kH];
+    load_row<kH>(stat, r);
+#pragma unroll
+    for (int h = 0; h < kH; ++h) s[h] = exp2f(s[h] - r[h]);
+    load_row<kH>(stat + kH, r);
+#pragma unroll
+    for (int h = 0; h < kH; ++h)
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) acc[h][i] *= r[h];
+    float* pw = ps + lane * L::kPRow;
+    if constexpr (kH == 2) {
+      *reinterpret_cast<float2*>(pw) = make_float2(s[0], s[1]);
+    } else {
+#pragma unroll
+      for (int h = 0; h < kH; h += 4)
+        *reinterpret_cast<float4*>(pw + h) = make_float4(s[h], s[h + 1], s[h + 2], s[h + 3]);
+    }
+    const float sum = reduce_heads<kH, false>(s, lane);
+    l = l * scale + sum;
+    le = le * scale + sum;
+    if (t.e != now.e) {                                    // the entry's last tile of this warp
+      if (writer) wb[(size_t)now.e * kWarps] = ref + log2f(le);
+      le = 0.f;
+    }
+    __syncwarp();                                          // the weights are there
+    const RawV* vr = reinterpret_cast<const RawV*>(vb + (size_t)now.j * D) + lane;
+    for (int j0 = 0; j0 < now.n; j0 += kAhead) {
+      RawV raw[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+        if (j0 + j < now.n) raw[j] = vr[(j0 + j) * 32];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (j0 + j >= now.n) break;
+        float vx[kVec];
+        unpack_v<T, kVec>(&raw[j], vx);
+        load_row<kH>(ps + (j0 + j) * L::kPRow, r);
+#pragma unroll
+        for (int h = 0; h < kH; ++h)
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) acc[h][i] = fmaf(r[h], vx[i], acc[h][i]);
+      }
+    }
+  }
+
+  // the four warps' maxima, sums and outputs
+  __syncwarp();                                            // stat of the last tile is read
+  if (lane % kOwn == 0) {
+    stat[own] = m;
+    stat[kH + own] = l;
+  }
+  float* os = reinterpret_cast<float*>(ks);                // no copy is in flight
+#pragma unroll
+  for (int h = 0; h < kH; ++h)
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) os[h * D + lane * kVec + i] = acc[h][i];
+  __syncthreads();
+  const float* st = reinterpret_cast<const float*>(smem + L::kStat);
+  for (int x = threadIdx.x; x < heads * D; x += kThreads) {
+    const int h = x / D;
+    float mx = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, st[w * 2 * kH + h]);
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    float o = 0.f, sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = exp2f(st[w * 2 * kH + h] - ref);
+      sum = fmaf(f, st[w * 2 * kH + kH + h], sum);
+      o = fmaf(f, reinterpret_cast<const float*>(smem + w * L::kTileBytes)[x], o);
+    }
+    const size_t slot = (head0 + h) * n_split + blockIdx.x;
+    ws_o[slot * D + x % D] = sum == 0.f ? 0.f : o / sum;
+    if (x % D == 0) ws_l[slot] = ref + log2f(sum);
+  }
+}
+
+// log2 of the sum of 2^l over a head's splits; -inf for none.
+__device__ __forceinline__ float log_sum(const float* l, int n) {
+  float mx = -INFINITY, sum = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < n; ++s) mx = fmaxf(mx, l[s]);
+  const float ref = mx == -INFINITY ? 0.f : mx;
+#pragma unroll 4
+  for (int s = 0; s < n; ++s) sum += exp2f(l[s] - ref);
+  return ref + log2f(sum);
+}
+
+// CTA = one (b, head): the output and its log-sum-exp; after those, one per (b, KV head): the
+// blocks' weights, sum over heads and warps of 2^(ws_b - log_sum), heads in order.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads)
+decode_mass_merge(const float* __restrict__ ws_o, const float* __restrict__ ws_l,
+                  const float* __restrict__ ws_b, const int32_t* __restrict__ sel,
+                  T* __restrict__ out, float* __restrict__ lse, float* __restrict__ mass, Dims p,
+                  int n_split) {
+  constexpr int kMaxG = 64;
+  __shared__ float norm[kMaxG];
+  ptx::grid_wait();
+  if ((int)blockIdx.x < p.B * p.Hq) {
+    const size_t bh = blockIdx.x;
+    const float* l = ws_l + bh * n_split;
+    const float all = log_sum(l, n_split);
+    if (threadIdx.x < D) {
+      float o = 0.f;
+      if (all != -INFINITY)
+#pragma unroll 4
+        for (int s = 0; s < n_split; ++s)
+          o = fmaf(exp2f(l[s] - all), ws_o[(bh * n_split + s) * D + threadIdx.x], o);
+      out[bh * D + threadIdx.x] = from_f32<T>(o);
+    }
+    if (lse && threadIdx.x == 0) lse[bh] = all * kLn2;
+    return;
+  }
+  const int bg = blockIdx.x - p.B * p.Hq;
+  const size_t head0 = (size_t)(bg / p.Hkv) * p.Hq + (size_t)(bg % p.Hkv) * p.G;
+  if ((int)threadIdx.x < p.G) norm[threadIdx.x] = log_sum(ws_l + (head0 + threadIdx.x) * n_split, n_split);
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.k; i += kThreads) {
+    const int blk = sel[(size_t)bg * p.k + i];
+    if (blk < 0 || blk >= p.nB) continue;
+    float sum = 0.f;
+#pragma unroll 8
+    for (int h = 0; h < p.G; ++h) {
+      const float4 x = *reinterpret_cast<const float4*>(ws_b + ((head0 + h) * p.k + i) * kWarps);
+      if (norm[h] != -INFINITY)
+        sum += (exp2f(x.x - norm[h]) + exp2f(x.y - norm[h])) +
+               (exp2f(x.z - norm[h]) + exp2f(x.w - norm[h]));
+    }
     atomicAdd(mass + (size_t)bg * p.nB + blk, sum);
   }
 }
 
-template <typename T, int D, int kHeads>
-cudaError_t run_heads(const Dims& p, const void* q, const void* k, const int32_t* sel,
-                     const float* lse, float* mass, cudaStream_t st) {
-  auto kern = mass_kernel<T, D, kHeads>;
-  const size_t heads = (size_t)(p.G + kHeads - 1) / kHeads * kHeads;
-  const size_t smem = sizeof(float) * (kKeys * (D + 4) + heads * (D + 1));
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
-  if (e != cudaSuccess) return e;
-  kern<<<dim3(p.k, p.B * p.Hkv), kThreads, smem, st>>>((const T*)q, (const T*)k, sel, lse, mass,
-                                                       p);
-  return cudaGetLastError();
+// Heads of a CTA: as many as the group has, up to 16 (64 accumulators a thread).
+int chunk_heads(const Dims& p) { return p.G > 8 ? 16 : (p.G > 2 ? 8 : 2); }
+
+// Splits: three CTAs an SM at once, of whole entries.
+int mass_splits(const Dims& p, int* per) {
+  const int h = chunk_heads(p), units = p.B * p.Hkv * ((p.G + h - 1) / h);
+  const int want = max(1, min(p.k, 3 * 152 / units));
+  *per = (p.k + want - 1) / want;
+  return (p.k + *per - 1) / *per;
 }
 
-// Groups of up to two heads do no work for six that are not there.
-template <typename T, int D>
-cudaError_t run_mass(const Dims& p, const void* q, const void* k, const int32_t* sel,
-                     const float* lse, float* mass, cudaStream_t st) {
-  return p.G > 2 ? run_heads<T, D, 8>(p, q, k, sel, lse, mass, st)
-                 : run_heads<T, D, 2>(p, q, k, sel, lse, mass, st);
+size_t out_floats(const Dims& p, int n_split) {
+  return (size_t)p.B * p.Hq * n_split * p.d;
+}
+size_t sum_floats(const Dims& p, int n_split) {
+  return ((size_t)p.B * p.Hq * n_split + 3) / 4 * 4;
+}
+
+template <typename T, int D, int kH>
+cudaError_t run_heads(const Dims& p, const void* q, const void* k, const void* v,
+                      const int32_t* sel, void* out, float* lse, float* mass, float* ws,
+                      cudaStream_t st) {
+  int per;
+  const int n_split = mass_splits(p, &per);
+  float* ws_l = ws + out_floats(p, n_split);
+  float* ws_b = ws_l + sum_floats(p, n_split);
+  auto kern = decode_mass_partial<T, D, kH>;
+  constexpr int smem = Layout<T, D, kH>::kBytes;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  e = launch_after(kern, dim3(n_split, p.B * p.Hkv, (p.G + kH - 1) / kH), kThreads, smem, 0, st,
+                   (const T*)q, (const T*)k, (const T*)v, sel, ws, ws_l, ws_b, p, n_split, per);
+  if (e != cudaSuccess) return e;
+  return launch_after(decode_mass_merge<T, D>, dim3(p.B * (p.Hq + p.Hkv)), kThreads, 0, 0, st, ws,
+                      ws_l, ws_b, sel, (T*)out, lse, mass, p, n_split);
+}
+
+template <typename T, int D, typename... A>
+cudaError_t run_mass(const Dims& p, A... a) {
+  const int h = chunk_heads(p);
+  return h == 16 ? run_heads<T, D, 16>(p, a...)
+                 : (h == 8 ? run_heads<T, D, 8>(p, a...) : run_heads<T, D, 2>(p, a...));
 }
 
 }  // namespace
 
 size_t decode_mass_workspace_bytes(const Dims& p) {
-  // the decode's scratch, and the blocks' log-sums or (should the caller take none) the
-  // log-sum-exps
-  const size_t more = sparse_decode_mma_supported(p) ? (size_t)p.k * kDecodeWarps : 1;
-  return (decode_workspace_bytes(p) + 15) / 16 * 16 + sizeof(float) * (size_t)p.B * p.Hq * more;
+  // partial outputs, their log-sums and the selection entries' log-sums by warp
+  const size_t entries = (size_t)p.B * p.Hq * p.k * kDecodeWarps;
+  if (sparse_decode_mma_supported(p))
+    return (decode_workspace_bytes(p) + 15) / 16 * 16 + sizeof(float) * entries;
+  int per;
+  const int n_split = mass_splits(p, &per);
+  return sizeof(float) * (out_floats(p, n_split) + sum_floats(p, n_split) + entries);
 }
 
 cudaError_t launch_sparse_decode_mass(const Dims& p, const void* q, const void* k, const void* v,
                                       const int32_t* sel, void* out, float* lse, float* mass,
                                       float* ws, cudaStream_t st, int* dev_status) {
-  float* more = ws + (decode_workspace_bytes(p) + 15) / 16 * 4;
   if (sparse_decode_mma_supported(p))
-    return launch_sparse_decode_mma_mass(p, q, k, v, sel, out, lse, mass, ws, more, st, dev_status);
-  if (!lse) lse = more;
-  cudaError_t e = launch_sparse_decode(p, q, k, v, sel, out, lse, ws, st, dev_status);
-  if (e != cudaSuccess) return e;
+    return launch_sparse_decode_mma_mass(p, q, k, v, sel, out, lse, mass, ws,
+                                         ws + (decode_workspace_bytes(p) + 15) / 16 * 4, st,
+                                         dev_status);
   if (p.dtype == 1)
-    return p.d == 128 ? run_mass<__nv_bfloat16, 128>(p, q, k, sel, lse, mass, st)
-                      : run_mass<__nv_bfloat16, 64>(p, q, k, sel, lse, mass, st);
-  return p.d == 128 ? run_mass<float, 128>(p, q, k, sel, lse, mass, st)
-                    : run_mass<float, 64>(p, q, k, sel, lse, mass, st);
+    return p.d == 128 ? run_mass<__nv_bfloat16, 128>(p, q, k, v, sel, out, lse, mass, ws, st)
+                      : run_mass<__nv_bfloat16, 64>(p, q, k, v, sel, out, lse, mass, ws, st);
+  return p.d == 128 ? run_mass<float, 128>(p, q, k, v, sel, out, lse, mass, ws, st)
+                    : run_mass<float, 64>(p, q, k, v, sel, out, lse, mass, ws, st);
 }
 
 }  // namespace msa

@@ -334,9 +334,11 @@ msa_status msa_sparse_decode_packed(const msa_shape* shape, const int32_t* seq_l
  *   mass[b, g, sel[b, g, i]] += sum over the group's query heads h and the keys j of that
  *   block of exp(z_hj - lse_h)                   (the weights of one head sum to 1)
  * mass: float32 [batch, n_heads_kv, n_blocks], the caller's, zeroed when a sequence starts.
- * out and lse (may be NULL) are bit for bit those of msa_sparse_decode, or, with seq_lens and
- * block_table (both given), of msa_sparse_decode_paged on its shapes.  A selected block's entry
- * gets one addition a call, so results repeat bit for bit.  (A block listed twice is counted
+ * out and lse (may be NULL) are bit for bit those of msa_sparse_decode where that runs on the
+ * tensor cores (bf16, head_dim 128, block 128, at most 16 query heads per KV head), or, with
+ * seq_lens and block_table (both given), of msa_sparse_decode_paged on its shapes; on other
+ * shapes the sums run in another order.  A selected block's entry gets one addition a call, so
+ * results repeat bit for bit.  (A block listed twice is counted
  * twice, in either order.)  workspace: msa_workspace_bytes(shape, 4) bytes, as for msa_sparse_decode. */
 msa_status msa_sparse_decode_mass(const msa_shape* shape, const int32_t* seq_lens,
                                   const int32_t* block_table, int32_t n_phys, const void* q,
