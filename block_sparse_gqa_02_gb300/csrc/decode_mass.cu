@@ -10,8 +10,11 @@
 //
 // Other shapes (fp32, head_dim 64, other blocks, wide groups) are computed here, on the CUDA
 // cores: fp32 products have no tensor-core form that keeps their 24 bits.  4 x 50000 keys, 48
-// blocks a head: 44 us for 200 MB (fp32, head_dim 128, 8 KV heads of 2), 77 for 100 MB (fp32, 4 KV
-// heads of 16), 30 for 25 MB (bf16, head_dim 64, 4 KV heads of 16).
+// blocks a head: 41 us for 200 MB (fp32, head_dim 128, 8 KV heads of 2), 17 for 100 MB (fp32,
+// head_dim 64, 8 of 1: memory), 46 for 100 MB (fp32, head_dim 128, 4 of 16: the latency of a
+// tile's 4096 products a lane at two warps a scheduler), 25 for 25 MB (bf16, head_dim 64, 4 of 16).
+#include <type_traits>
+
 #include "common.cuh"
 #include "launch.cuh"
 #include "ptx.cuh"
@@ -103,6 +106,7 @@ template <typename T, int D, int kH> struct Layout {
   static constexpr int kP = kQ + kH * D * 4;
   static constexpr int kStat = kP + kWarps * 32 * kPRow * 4;
   static constexpr int kBytes = kStat + kWarps * 2 * kH * 4;
+  static constexpr int kResident = 232448 / (kBytes + 1024) < 3 ? 232448 / (kBytes + 1024) : 3;
   static_assert(kH * D * 4 <= kTileBytes, "a warp's output fits its K tile");
 };
 
@@ -113,7 +117,7 @@ template <typename T, int D, int kH> struct Layout {
 //   output: a lane per D / 32 dims, V from memory to registers, the weights broadcast.
 // The copy of the next tile of K runs under the second part.
 template <typename T, int D, int kH>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, Layout<T, D, kH>::kResident)
 decode_mass_partial(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
                     const int32_t* __restrict__ sel, float* __restrict__ ws_o,
                     float* __restrict__ ws_l, float* __restrict__ ws_b, Dims p, int n_split,
@@ -122,8 +126,7 @@ decode_mass_partial(const T* __restrict__ q, const T* __restrict__ k, const T* _
   constexpr int kVec = D / 32;                             // dims of a lane
   constexpr int kChunk = 16 / (int)sizeof(T);              // dims of a 16-byte load
   constexpr int kOwn = 32 / kH;                            // lanes that share a head's statistics
-  constexpr int kUnroll = kH == 16 ? 1 : 2;
-  constexpr int kAhead = 4;                                // loads of V in flight
+  constexpr int kAhead = kH == 2 ? 16 : 8;                 // loads of V in flight
   using RawV = typename Raw<kVec * (int)sizeof(T)>::type;
   extern __shared__ __align__(16) unsigned char smem[];
   ptx::grid_wait();
@@ -180,10 +183,10 @@ decode_mass_partial(const T* __restrict__ q, const T* __restrict__ k, const T* _
   while (t.n > 0) {
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
-    float s[kH];
+    float2 s2[kH];
 #pragma unroll
-    for (int h = 0; h < kH; ++h) s[h] = 0.f;
-#pragma unroll kUnroll
+    for (int h = 0; h < kH; ++h) s2[h] = make_float2(0.f, 0.f);
+#pragma unroll 4
     for (int c = 0; c < D / kChunk; ++c) {
       float kx[kChunk];
       Vec16<T>::load(reinterpret_cast<const T*>(ks + lane * L::kKRow + c * 16), kx);
@@ -192,12 +195,13 @@ decode_mass_partial(const T* __restrict__ q, const T* __restrict__ k, const T* _
 #pragma unroll
         for (int i = 0; i < kChunk; i += 4) {
           const float4 qx = *reinterpret_cast<const float4*>(qs + h * D + c * kChunk + i);
-          s[h] = fmaf(qx.x, kx[i], s[h]);
-          s[h] = fmaf(qx.y, kx[i + 1], s[h]);
-          s[h] = fmaf(qx.z, kx[i + 2], s[h]);
-          s[h] = fmaf(qx.w, kx[i + 3], s[h]);
+          s2[h] = __ffma2_rn(make_float2(qx.x, qx.y), make_float2(kx[i], kx[i + 1]), s2[h]);
+          s2[h] = __ffma2_rn(make_float2(qx.z, qx.w), make_float2(kx[i + 2], kx[i + 3]), s2[h]);
         }
     }
+    float s[kH];
+#pragma unroll
+    for (int h = 0; h < kH; ++h) s[h] = s2[h].x + s2[h].y;
     if (lane >= t.n) {
 #pragma unroll
       for (int h = 0; h < kH; ++h) s[h] = -INFINITY;
@@ -245,23 +249,29 @@ decode_mass_partial(const T* __restrict__ q, const T* __restrict__ k, const T* _
     }
     __syncwarp();                                          // the weights are there
     const RawV* vr = reinterpret_cast<const RawV*>(vb + (size_t)now.j * D) + lane;
-    for (int j0 = 0; j0 < now.n; j0 += kAhead) {
-      RawV raw[kAhead];
+    auto add_v = [&](auto whole) {
+      constexpr bool kWhole = decltype(whole)::value;      // 32 keys: nothing to check
+#pragma unroll 2
+      for (int j0 = 0; j0 < (kWhole ? 32 : now.n); j0 += kAhead) {
+        RawV raw[kAhead];
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j)
-        if (j0 + j < now.n) raw[j] = vr[(j0 + j) * 32];
+        for (int j = 0; j < kAhead; ++j)
+          if (kWhole || j0 + j < now.n) raw[j] = vr[(j0 + j) * 32];
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        if (j0 + j >= now.n) break;
-        float vx[kVec];
-        unpack_v<T, kVec>(&raw[j], vx);
-        load_row<kH>(ps + (j0 + j) * L::kPRow, r);
+        for (int j = 0; j < kAhead; ++j) {
+          if (!kWhole && j0 + j >= now.n) break;
+          float vx[kVec];
+          unpack_v<T, kVec>(&raw[j], vx);
+          load_row<kH>(ps + (j0 + j) * L::kPRow, r);
 #pragma unroll
-        for (int h = 0; h < kH; ++h)
+          for (int h = 0; h < kH; ++h)
 #pragma unroll
-          for (int i = 0; i < kVec; ++i) acc[h][i] = fmaf(r[h], vx[i], acc[h][i]);
+            for (int i = 0; i < kVec; ++i) acc[h][i] = fmaf(r[h], vx[i], acc[h][i]);
+        }
       }
-    }
+    };
+    if (now.n == 32) add_v(std::true_type{});
+    else add_v(std::false_type{});
   }
 
   // the four warps' maxima, sums and outputs
@@ -296,69 +306,131 @@ decode_mass_partial(const T* __restrict__ q, const T* __restrict__ k, const T* _
   }
 }
 
-// log2 of the sum of 2^l over a head's splits; -inf for none.
-__device__ __forceinline__ float log_sum(const float* l, int n) {
+// log2 of the sum of 2^l over a head's splits, by a warp; -inf for none.
+__device__ __forceinline__ float log_sum(const float* l, int n, int lane) {
   float mx = -INFINITY, sum = 0.f;
-#pragma unroll 4
-  for (int s = 0; s < n; ++s) mx = fmaxf(mx, l[s]);
+  for (int s = lane; s < n; s += 32) mx = fmaxf(mx, l[s]);
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   const float ref = mx == -INFINITY ? 0.f : mx;
-#pragma unroll 4
-  for (int s = 0; s < n; ++s) sum += exp2f(l[s] - ref);
+  for (int s = lane; s < n; s += 32) sum += exp2f(l[s] - ref);
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   return ref + log2f(sum);
 }
 
-// CTA = one (b, head): the output and its log-sum-exp; after those, one per (b, KV head): the
-// blocks' weights, sum over heads and warps of 2^(ws_b - log_sum), heads in order.
+constexpr int kMergeEntries = 32;      // selection entries of a CTA that adds weights
+
+// CTA = one (b, head): the output and its log-sum-exp, a warp taking every fourth split.  After
+// those, CTA = 32 selection entries of one (b, KV head): their weights, the sum over heads and
+// warps of 2^(ws_b - log_sum), a warp taking every fourth head.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
 decode_mass_merge(const float* __restrict__ ws_o, const float* __restrict__ ws_l,
                   const float* __restrict__ ws_b, const int32_t* __restrict__ sel,
                   T* __restrict__ out, float* __restrict__ lse, float* __restrict__ mass, Dims p,
                   int n_split) {
-  constexpr int kMaxG = 64;
-  __shared__ float norm[kMaxG];
+  constexpr int kMaxG = 64, kVec = D / 32, kAhead = 8;
+  __shared__ float norm[kMaxG], part[kWarps][D];
   ptx::grid_wait();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if ((int)blockIdx.x < p.B * p.Hq) {
     const size_t bh = blockIdx.x;
     const float* l = ws_l + bh * n_split;
-    const float all = log_sum(l, n_split);
+    const float* o = ws_o + bh * n_split * D + lane * kVec;
+    const float all = log_sum(l, n_split, lane);
+    float acc[kVec] = {};
+    if (all != -INFINITY)
+      for (int s0 = warp; s0 < n_split; s0 += kWarps * kAhead) {
+        float x[kAhead][kVec], f[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          const int s = s0 + u * kWarps;
+          if (s >= n_split) break;
+          unpack_v<float, kVec>(o + (size_t)s * D, x[u]);
+          f[u] = l[s];
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          if (s0 + u * kWarps >= n_split) break;
+          f[u] = exp2f(f[u] - all);
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) acc[i] = fmaf(f[u], x[u][i], acc[i]);
+        }
+      }
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) part[warp][lane * kVec + i] = acc[i];
+    __syncthreads();
     if (threadIdx.x < D) {
-      float o = 0.f;
-      if (all != -INFINITY)
-#pragma unroll 4
-        for (int s = 0; s < n_split; ++s)
-          o = fmaf(exp2f(l[s] - all), ws_o[(bh * n_split + s) * D + threadIdx.x], o);
-      out[bh * D + threadIdx.x] = from_f32<T>(o);
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) sum += part[w][threadIdx.x];
+      out[bh * D + threadIdx.x] = from_f32<T>(sum);
     }
     if (lse && threadIdx.x == 0) lse[bh] = all * kLn2;
     return;
   }
-  const int bg = blockIdx.x - p.B * p.Hq;
+  const int chunks = (p.k + kMergeEntries - 1) / kMergeEntries;
+  const int bg = (blockIdx.x - p.B * p.Hq) / chunks;
+  const int i = (blockIdx.x - p.B * p.Hq) % chunks * kMergeEntries + lane;
   const size_t head0 = (size_t)(bg / p.Hkv) * p.Hq + (size_t)(bg % p.Hkv) * p.G;
-  if ((int)threadIdx.x < p.G) norm[threadIdx.x] = log_sum(ws_l + (head0 + threadIdx.x) * n_split, n_split);
-  __syncthreads();
-  for (int i = threadIdx.x; i < p.k; i += kThreads) {
-    const int blk = sel[(size_t)bg * p.k + i];
-    if (blk < 0 || blk >= p.nB) continue;
-    float sum = 0.f;
-#pragma unroll 8
-    for (int h = 0; h < p.G; ++h) {
-      const float4 x = *reinterpret_cast<const float4*>(ws_b + ((head0 + h) * p.k + i) * kWarps);
-      if (norm[h] != -INFINITY)
-        sum += (exp2f(x.x - norm[h]) + exp2f(x.y - norm[h])) +
-               (exp2f(x.z - norm[h]) + exp2f(x.w - norm[h]));
+  const int blk = i < p.k ? sel[(size_t)bg * p.k + i] : -1;
+  const bool there = blk >= 0 && blk < p.nB;
+  float sum = 0.f;
+  for (int h0 = warp; h0 - warp < p.G; h0 += 4 * kWarps) {
+    float4 x[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (there && h0 + u * kWarps < p.G)
+        x[u] = *reinterpret_cast<const float4*>(
+            ws_b + ((head0 + h0 + u * kWarps) * p.k + i) * kWarps);
+    if (h0 == warp) {                                      // the first loads are in flight
+      for (int h = warp; h < p.G; h += kWarps) {
+        const float n = log_sum(ws_l + (head0 + h) * n_split, n_split, lane);
+        if (lane == 0) norm[h] = n;
+      }
+      __syncwarp();                                        // read by the warp that wrote it
     }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int h = h0 + u * kWarps;
+      if (there && h < p.G && norm[h] != -INFINITY)
+        sum += (exp2f(x[u].x - norm[h]) + exp2f(x[u].y - norm[h])) +
+               (exp2f(x[u].z - norm[h]) + exp2f(x[u].w - norm[h]));
+    }
+  }
+  part[warp][lane] = sum;
+  __syncthreads();
+  if (warp == 0 && there) {
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) sum += part[w][lane];
     atomicAdd(mass + (size_t)bg * p.nB + blk, sum);
   }
 }
 
-// Heads of a CTA: as many as the group has, up to 16 (64 accumulators a thread).
-int chunk_heads(const Dims& p) { return p.G > 8 ? 16 : (p.G > 2 ? 8 : 2); }
+// Heads of a CTA.  Few heads leave more CTAs and shorter tiles, many read the keys fewer times:
+// 2 where that makes at most two CTAs an SM, 8 up to four, else 16.  Measured at 16 heads a KV
+// head, fp32, head_dim 128, with 2, 8 and 16: 1 x 128 keys 10.3, 13.1 and 18.4 us, 4 x 8000 31.1,
+// 21.9 and 24.0, 8 x 8000 53.8, 33.9 and 31.9.
+int chunk_heads(const Dims& p) {
+  const long long tiles = (long long)p.B * p.Hkv * min(p.k, p.nB);
+  if (tiles * ((p.G + 1) / 2) <= 2 * 152 || p.G <= 2) return 2;
+  return tiles * ((p.G + 7) / 8) <= 4 * 152 || p.G <= 8 ? 8 : 16;
+}
 
-// Splits: three CTAs an SM at once, of whole entries.
+template <typename T> int resident(const Dims& p) {
+  const int h = chunk_heads(p);
+  return p.d == 128 ? (h == 16 ? Layout<T, 128, 16>::kResident
+                               : (h == 8 ? Layout<T, 128, 8>::kResident : Layout<T, 128, 2>::kResident))
+                    : (h == 16 ? Layout<T, 64, 16>::kResident
+                               : (h == 8 ? Layout<T, 64, 8>::kResident : Layout<T, 64, 2>::kResident));
+}
+
+// Splits of whole entries: the CTAs that run at once.
 int mass_splits(const Dims& p, int* per) {
   const int h = chunk_heads(p), units = p.B * p.Hkv * ((p.G + h - 1) / h);
-  const int want = max(1, min(p.k, 3 * 152 / units));
+  const int slots = 152 * (p.dtype == 1 ? resident<__nv_bfloat16>(p) : resident<float>(p));
+  const int want = max(1, min(p.k, slots / units));
   *per = (p.k + want - 1) / want;
   return (p.k + *per - 1) / *per;
 }
@@ -385,8 +457,9 @@ cudaError_t run_heads(const Dims& p, const void* q, const void* k, const void* v
   e = launch_after(kern, dim3(n_split, p.B * p.Hkv, (p.G + kH - 1) / kH), kThreads, smem, 0, st,
                    (const T*)q, (const T*)k, (const T*)v, sel, ws, ws_l, ws_b, p, n_split, per);
   if (e != cudaSuccess) return e;
-  return launch_after(decode_mass_merge<T, D>, dim3(p.B * (p.Hq + p.Hkv)), kThreads, 0, 0, st, ws,
-                      ws_l, ws_b, sel, (T*)out, lse, mass, p, n_split);
+  const unsigned chunks = (p.k + kMergeEntries - 1) / kMergeEntries;
+  return launch_after(decode_mass_merge<T, D>, dim3(p.B * (p.Hq + p.Hkv * chunks)), kThreads, 0, 0,
+                      st, ws, ws_l, ws_b, sel, (T*)out, lse, mass, p, n_split);
 }
 
 template <typename T, int D, typename... A>

@@ -37,6 +37,11 @@ MASS = {
     "block_1000": (2, 3001, 8, 2, 64, 1000, 3, "bf16"),
     "block_129": (1, 1500, 12, 1, 128, 129, 6, "f32"),
     "block_32": (2, 999, 10, 2, 128, 32, 20, "bf16"),
+    "heads_8_of_5": (2, 5200, 10, 2, 128, 128, 40, "f32"),
+    "heads_16": (4, 5200, 32, 2, 128, 128, 40, "f32"),
+    "heads_16_of_12": (4, 5200, 24, 2, 64, 128, 40, "f32"),
+    "heads_16_d64": (4, 5200, 32, 2, 64, 128, 40, "bf16"),
+    "heads_16_of_20": (4, 5200, 40, 2, 128, 64, 60, "bf16"),
     "batch_300": (300, 130, 2, 2, 64, 128, 2, "bf16"),
     "k_past_blocks": (2, 300, 8, 4, 64, 128, 70, "f32"),
     "group_1": (2, 500, 4, 4, 128, 128, 3, "f32"),
@@ -76,6 +81,40 @@ def test_decode_mass(name):
     m2 = torch.full((B, Hkv, nB), 0.25, device="cuda")
     _lib.msa_sparse_decode_mass(shape, None, None, 0, q, k, v, sel, o2, None, m2, _ws(shape, 4))
     assert torch.equal(m2, mass.tensor) and torch.equal(o2, out.tensor)
+
+
+@pytest.mark.parametrize("d,dtype", [(128, "bf16"), (64, "bf16"), (128, "f32")])
+def test_decode_mass_specials(d, dtype):
+    """NaN in a key that nobody selected changes nothing; in a selected one it shows in that KV
+    head's rows only; keys whose scores are all -inf, and rows without a selection, add nothing."""
+    B, L, Hq, Hkv = 2, 700, 8, 4
+    shape = _lib.make_shape(B, 1, L, Hq, Hkv, d, 128, 128, 3, 1, dtype)
+    q, k, v = (_rows(s, DT[dtype], i) for i, s in enumerate(
+        ((B, 1, Hq, d), (B, Hkv, L, d), (B, Hkv, L, d))))
+    sel = torch.tensor([0, 2, 5], dtype=torch.int32, device="cuda").repeat(B, Hkv, 1, 1).contiguous()
+    sel[0, 1] = -1
+
+    def run():
+        out, lse = torch.empty_like(q), torch.empty((B, Hq, 1), device="cuda")
+        mass = torch.zeros((B, Hkv, 6), device="cuda")
+        _lib.msa_sparse_decode_mass(shape, None, None, 0, q, k, v, sel, out, lse, mass, _ws(shape, 4))
+        return out, lse, mass
+
+    want = run()
+    assert not want[0][0, 0, 2:4].any() and torch.isneginf(want[1][0, 2:4]).all()
+    assert not want[2][0, 1].any() and not want[2][:, :, [1, 3, 4]].any()
+    k[0, 0, 128], v[0, 0, 511] = float("nan"), float("inf")    # blocks 1 and 3
+    assert all(torch.equal(x, y) for x, y in zip(run(), want))
+    k[1, 3, 300, 0] = float("nan")                             # block 2, selected
+    out, lse, mass = run()
+    assert torch.isnan(out[1, 0, 6:]).all() and not torch.isnan(out[1, 0, :6]).any()
+    assert torch.equal(out[0], want[0][0]) and torch.equal(mass[1, :3], want[2][1, :3])
+    # one head pair's q against keys that leave only -inf
+    q[1, 0, :2] = 1.0
+    k[1, 0] = 0.0
+    k[1, 0, :, 0] = float("-inf")
+    out, lse, mass = run()
+    assert not out[1, 0, :2].any() and torch.isneginf(lse[1, :2]).all() and not mass[1, 0].any()
 
 
 @pytest.mark.parametrize("lens", [[1, 127, 129, 4097, 0], [3000, 2999, 64]])
