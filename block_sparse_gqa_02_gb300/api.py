@@ -114,6 +114,12 @@ def _rotate(rope_, q, k, idx_q, idx_k, pos_offset=0):
     return [None if r[0] is None else next(got) for r in rows]
 
 
+def _check_shape(x, name, want):
+    """A per-block array is indexed by its shape, so a larger one is not a longer one."""
+    if x is not None and tuple(x.shape) != want:
+        raise ValueError(f"{name} is {tuple(x.shape)}, expected {want}")
+
+
 def prefill(q, k, v, idx_q, idx_k, block_size=128, top_k=16, q_tile=64, sm_scale=0.0,
             index_scale=0.0, rope=None):
     """MSA prefill.  q [B,T,Hq,d], k/v [B,Hkv,T,d], idx_q [B,T,Hkv,dI], idx_k [B,T,dI].
@@ -145,6 +151,7 @@ def decode(q, k_cache, v_cache, idx_q, idx_k, block_size=128, top_k=64, sm_scale
     q and idx_q are rotated to that position (the caches hold rotated keys).  With mass
     (float32 [B,Hkv,blocks]) the attention weight of every selected block is added to it."""
     shape = _shape_of(q, k_cache, idx_q, block_size, top_k, 1, sm_scale, index_scale)
+    _check_shape(mass, "mass", (shape.batch, shape.n_heads_kv, shape.n_blocks))
     bufs = alloc_decode_outputs(shape, q.device, q.dtype, mass is not None)
     if rope is not None:
         q, _, idx_q, _ = _rotate(rope, q, None, idx_q, None, shape.seq_k - 1)
@@ -175,6 +182,9 @@ def decode_packed(q, k, v, cache, idx_q, idx_k_pool, seq_lens, block_table, capa
     Hkv, n_phys = cache.shape[1], cache.shape[0]
     shape = make_shape(B, 1, capacity, Hq, Hkv, d, idx_q.shape[-1], 128, top_k, 1, _DT[q.dtype],
                        sm_scale, index_scale)
+    _check_shape(block_table, "block_table", (B, shape.n_blocks))
+    _check_shape(idx_k_pool, "idx_k_pool", (n_phys, 128, idx_q.shape[-1]))
+    _check_shape(mass, "mass", (B, Hkv, shape.n_blocks))
     bufs = alloc_prefill_outputs(shape, q.device, q.dtype)
     if rope is not None:
         index = rope.freqs if rope.index_freqs is None else rope.index_freqs
@@ -197,6 +207,8 @@ def evict_paged(seq_lens, mass, block_table, capacity, keep, n_first=1, n_recent
     ones in the table).  Returns kept int32 [B, keep], the old indices of what stays."""
     B, Hkv, _ = mass.shape
     shape = make_shape(B, 1, capacity, Hkv, Hkv, 128, 128, block_size, 1, 1)
+    _check_shape(mass, "mass", (B, Hkv, shape.n_blocks))
+    _check_shape(block_table, "block_table", (B, shape.n_blocks))
     kept = torch.empty((B, keep), dtype=torch.int32, device=mass.device)
     msa_cache_evict(shape, keep, n_first, n_recent, seq_lens, mass, block_table, kept, seq_lens,
                     mass, block_table)
@@ -209,6 +221,7 @@ def evict(k_cache, v_cache, idx_k, mass, keep, n_first=1, n_recent=2, block_size
     B, Hkv, L, d = k_cache.shape
     shape = make_shape(B, 1, L, Hkv, Hkv, d, 128, block_size, 1, 1)
     n = shape.n_blocks
+    _check_shape(mass, "mass", (B, Hkv, n))
     rows = L - (n - min(n, keep)) * block_size
     new = lambda x: torch.empty((*x.shape[:-2], rows, x.shape[-1]), dtype=x.dtype, device=x.device)  # noqa: E731
     kept = torch.empty((B, keep), dtype=torch.int32, device=mass.device)

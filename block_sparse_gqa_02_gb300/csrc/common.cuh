@@ -164,6 +164,10 @@ cudaError_t launch_sparse_decode_packed(const Dims& p, const void* q, const void
 // Selected blocks per row that decode can accumulate weights for over the 4-bit cache.
 constexpr int kMaxPackedMassBlocks = 1024;
 
+// The same over 16- and 32-bit caches, and the entries of an eviction's list: far more than
+// there can be blocks, few enough for 32-bit loops over them.
+constexpr int kMaxMassBlocks = 1 << 20, kMaxKeep = 1 << 20;
+
 // Decode with accumulated attention weights, and eviction by them (decode_mass.cu,
 // cache_evict.cu).
 cudaError_t launch_sparse_decode_mass(const Dims& p, const void* q, const void* k, const void* v,

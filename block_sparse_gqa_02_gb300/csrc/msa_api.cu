@@ -581,6 +581,8 @@ msa_status msa_sparse_decode_mass(const msa_shape* shape, const int32_t* seq_len
   MSA_TRY(check_ptr(lse, "lse", true));
   MSA_TRY(check_ptr(mass, "mass"));
   MSA_TRY(check_ptr(workspace, "workspace"));
+  if (d.k > kMaxMassBlocks)
+    return fail(MSA_ERR_UNSUPPORTED, "mass needs top_k <= %d (got %d)", kMaxMassBlocks, d.k);
   const size_t need = decode_mass_workspace_bytes(d);
   if (ws_bytes < need)
     return fail(MSA_ERR_INVALID_ARG, "workspace of %zu bytes is too small: need %zu", ws_bytes,
@@ -608,6 +610,8 @@ msa_status msa_cache_evict(const msa_shape* shape, int32_t keep, int32_t n_first
     return fail(MSA_ERR_INVALID_ARG,
                 "keep (%d) must hold the first n_first (%d, >= 0) and last n_recent (%d, >= 1) "
                 "blocks", keep, n_first, n_recent);
+  if (keep > kMaxKeep)
+    return fail(MSA_ERR_UNSUPPORTED, "keep %d: at most %d", keep, kMaxKeep);
   MSA_TRY(check_ptr(seq_lens, "seq_lens", true));
   MSA_TRY(check_ptr(mass, "mass"));
   MSA_TRY(check_ptr(block_table, "block_table", true));

@@ -11,9 +11,10 @@
 // A CTA takes a tile of tokens and heads of one tensor: it forms the tile's sines and cosines
 // once in shared memory (each is shared by the heads), then streams the tile with two 16-byte
 // loads and stores a unit (the table lies so that neighbouring units read neighbouring banks: in
-// the order of the dims its reads took 78 % of shared memory's cycles).  All tensors of a call share one launch: their tiles are numbered
-// one after the other.  Measured: 743 us for the tensors of a 128K prefill (4.9 GB, 6.6 TB/s), 64.5
-// us for 420 MB of fp32 gradients (6.5 TB/s); 3.7 us on the device for a decode step's four.
+// the order of the dims its reads took 78 % of shared memory's cycles).  All tensors of a call
+// share one launch: their tiles are numbered one after the other.  Measured: 743 us for the
+// tensors of a 128K prefill (4.9 GB, 6.6 TB/s), 64.5 us for 420 MB of fp32 gradients (6.5 TB/s);
+// 3.7 us on the device for a decode step's four.
 #include "common.cuh"
 #include "launch.cuh"
 #include "ptx.cuh"

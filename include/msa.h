@@ -273,8 +273,9 @@ msa_status msa_rope(const msa_rope_desc* desc, const msa_rope_tensor* tensors, i
 
 /* ---------------------------------------------------------------- the 4-bit KV cache
  * K and V in 4 bits: 5 bits a value with their scales, 160 * head_dim bytes for the 128 keys
- * of one KV head's block against 512 * head_dim in bf16.  A group is 32 consecutive dims of one token and head.  With hi, lo its
- * largest and smallest value (fp32 arithmetic, each operation rounded to nearest even):
+ * of one KV head's block against 512 * head_dim in bf16.  A group is 32 consecutive dims of one
+ * token and head.  With hi, lo its largest and smallest value (fp32 arithmetic, each operation
+ * rounded to nearest even):
  *   step = bf16(hi * f - lo * f), f = fp32(1 / 15)    (steps below 2^-100 become 0)
  *   mid  = bf16(lo + 8 * step)
  *   code = clamp(rint((x - mid) * fp32(1 / step)) + 8, 0, 15), 8 when step is 0
@@ -338,8 +339,9 @@ msa_status msa_sparse_decode_packed(const msa_shape* shape, const int32_t* seq_l
  * tensor cores (bf16, head_dim 128, block 128, at most 16 query heads per KV head), or, with
  * seq_lens and block_table (both given), of msa_sparse_decode_paged on its shapes; on other
  * shapes the sums run in another order.  A selected block's entry gets one addition a call, so
- * results repeat bit for bit.  (A block listed twice is counted
- * twice, in either order.)  workspace: msa_workspace_bytes(shape, 4) bytes, as for msa_sparse_decode. */
+ * results repeat bit for bit.  (A block listed twice is counted twice, in either order.)
+ * top_k is at most 2^20.  workspace: msa_workspace_bytes(shape, 4) bytes, as for
+ * msa_sparse_decode. */
 msa_status msa_sparse_decode_mass(const msa_shape* shape, const int32_t* seq_lens,
                                   const int32_t* block_table, int32_t n_phys, const void* q,
                                   const void* k, const void* v, const int32_t* sel, void* out,
@@ -360,9 +362,9 @@ msa_status msa_sparse_decode_mass(const msa_shape* shape, const int32_t* seq_len
  *             entries past the sequence's last block as they were.  A sequence grows into
  *             the blocks it dropped, or the caller takes them back.
  * new_lens, mass_out and table_out may be the inputs themselves (in place), but may not
- * overlap them otherwise.  shape: a decode
- * shape (n_blocks at most 32768); seq_lens NULL: every length is seq_k.
- * keep >= n_first + n_recent, n_first >= 0, n_recent >= 1. */
+ * overlap them otherwise, nor one another or kept.  shape: a decode shape (n_blocks at most
+ * 32768); seq_lens NULL: every length is seq_k.
+ * n_first + n_recent <= keep <= 2^20, n_first >= 0, n_recent >= 1. */
 msa_status msa_cache_evict(const msa_shape* shape, int32_t keep, int32_t n_first, int32_t n_recent,
                            const int32_t* seq_lens, const float* mass, const int32_t* block_table,
                            int32_t* kept, int32_t* new_lens, float* mass_out, int32_t* table_out,
@@ -387,7 +389,8 @@ msa_status msa_cache_gather(int32_t batch, const msa_gather_tensor* tensors, int
 
 /* Scratch bytes msa_sparse_prefill (which = 0), msa_sparse_decode (which = 1),
  * msa_sparse_prefill_backward (which = 2), msa_index_kl_loss (which = 3) or
- * msa_sparse_decode_mass (which = 4) needs for this shape; 0 when none.  Returns 0 for an invalid shape. */
+ * msa_sparse_decode_mass (which = 4) needs for this shape; 0 when none.  Returns 0 for an
+ * invalid shape. */
 size_t msa_workspace_bytes(const msa_shape* shape, int which);
 
 /* Synchronises `stream`, then reports (and clears) the device status word and any pending

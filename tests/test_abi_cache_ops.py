@@ -124,6 +124,8 @@ def test_decode_mass_arguments(lib):
     assert call(_shape(seq_q=1000, q_tile=64)) == MSA_ERR_INVALID_ARG
     assert call(_shape(n_heads_q=4 * 65)) == MSA_ERR_UNSUPPORTED
     assert lib.msa_workspace_bytes(ctypes.byref(_shape(seq_q=1000, q_tile=64)), 4) == 0
+    for kw in (dict(), dict(dtype="f32"), dict(head_dim=64)):
+        assert call(_shape(top_k=(1 << 20) + 1, **kw), ws_bytes=1 << 50) == MSA_ERR_UNSUPPORTED
 
 
 def test_evict_arguments(lib):
@@ -143,6 +145,7 @@ def test_evict_arguments(lib):
     assert call(s, t_out=FAKE - 16) == MSA_ERR_INVALID_ARG and b"table_out" in lib.msa_last_error()
     assert call(_shape(seq_q=1000, q_tile=64)) == MSA_ERR_INVALID_ARG
     assert call(_shape(seq_k=(1 << 22) + 1)) == MSA_ERR_UNSUPPORTED  # 32769 blocks
+    assert call(s, keep=(1 << 20) + 1) == MSA_ERR_UNSUPPORTED
 
 
 @pytest.mark.parametrize("row,status", [
@@ -173,3 +176,31 @@ def test_binding_refuses_tensors_off_the_device(lib):
     q = torch.zeros(2, 1, 16, 128, dtype=torch.bfloat16)             # on the host
     with pytest.raises(ValueError, match="current CUDA device"):
         _lib.msa_sparse_decode_packed(s, None, None, 16, q, FAKE, FAKE, FAKE, stream=0)
+
+
+def test_api_refuses_arrays_of_another_stride():
+    """Arrays with an entry per block are indexed by the call's number of blocks: one with room
+    for more would be read in the wrong rows."""
+    import torch
+    from block_sparse_gqa_02_gb300 import api
+    B, H, L, d, bf = 2, 4, 1000, 128, torch.bfloat16
+    z = lambda *s, dt=bf: torch.zeros(s, dtype=dt)  # noqa: E731
+    q, k, iq, ik = z(B, 1, 16, d), z(B, H, L, d), z(B, 1, H, d), z(B, L, d)
+    lens, mass, table = z(B, dt=torch.int32), z(B, H, 8, dt=torch.float32), z(B, 8, dt=torch.int32)
+    cache, pool = z(20, H, 160 * d, dt=torch.uint8), z(20, 128, d)
+    wide, long = z(B, H, 9, dt=torch.float32), z(B, 9, dt=torch.int32)
+    with pytest.raises(ValueError, match="mass is"):
+        api.decode(q, k, k, iq, ik, mass=wide)
+    with pytest.raises(ValueError, match="mass is"):
+        api.evict(k, k, ik, wide, 4)
+    with pytest.raises(ValueError, match="mass is"):
+        api.evict_paged(lens, wide, table, L, 4)
+    with pytest.raises(ValueError, match="block_table is"):
+        api.evict_paged(lens, mass, long, L, 4)
+    new = z(B, H, 1, d)
+    with pytest.raises(ValueError, match="mass is"):
+        api.decode_packed(q, new, new, cache, iq, pool, lens, table, L, mass=wide)
+    with pytest.raises(ValueError, match="block_table is"):
+        api.decode_packed(q, new, new, cache, iq, pool, lens, long, L)
+    with pytest.raises(ValueError, match="idx_k_pool is"):
+        api.decode_packed(q, new, new, cache, iq, pool[:19], lens, table, L)
