@@ -117,6 +117,54 @@ def test_decode_mass_specials(d, dtype):
     assert not out[1, 0, :2].any() and torch.isneginf(lse[1, :2]).all() and not mass[1, 0].any()
 
 
+@pytest.mark.parametrize("d,dtype", [(128, "bf16"), (64, "bf16"), (128, "f32")])
+def test_decode_mass_graphs_and_streams(d, dtype):
+    """Two captured steps, each with a workspace of its own, replayed at once on two streams, and
+    two that share one replayed in turn: the bits of the eager calls."""
+    B, L, Hq, Hkv = 2, 3000, 16, 4
+    shape = _lib.make_shape(B, 1, L, Hq, Hkv, d, 128, 128, 6, 1, dtype)
+    nB = shape.n_blocks
+    steps = []
+    for i in range(2):
+        q, k, v = (_rows(s, DT[dtype], 10 * i + j) for j, s in enumerate(
+            ((B, 1, Hq, d), (B, Hkv, L, d), (B, Hkv, L, d))))
+        sel = torch.from_numpy(random_selection(np.full((B, Hkv, 1), nB), 6, i)).cuda()
+        steps.append((q, k, v, sel, torch.empty_like(q), torch.empty((B, Hq, 1), device="cuda"),
+                      torch.zeros((B, Hkv, nB), device="cuda")))
+
+    def call(step, ws):
+        q, k, v, sel, out, lse, mass = step
+        _lib.msa_sparse_decode_mass(shape, None, None, 0, q, k, v, sel, out, lse, mass, ws)
+
+    own = [_ws(shape, 4), _ws(shape, 4)]
+    for step in steps:
+        call(step, own[0])
+    torch.cuda.synchronize()
+    want = [[x.clone() for x in step[4:]] for step in steps]
+
+    def graphs(spaces):
+        out = []
+        for step, ws in zip(steps, spaces):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                call(step, ws)
+            out.append(g)
+        return out
+
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for captured, at_once in ((graphs(own), True), (graphs([own[0]] * 2), False)):
+        for step in steps:
+            for x in step[4:]:
+                x.zero_()
+        torch.cuda.synchronize()
+        for g, stream in zip(captured, streams):
+            with torch.cuda.stream(stream if at_once else streams[0]):
+                g.replay()
+        torch.cuda.synchronize()
+        for step, w in zip(steps, want):
+            assert all(torch.equal(x, y) for x, y in zip(step[4:], w))
+
+
 @pytest.mark.parametrize("lens", [[1, 127, 129, 4097, 0], [3000, 2999, 64]])
 def test_decode_mass_paged(lens):
     cfg = CONFIGS["d1m"].with_(seq=5000, top_k=8, n_plants=0)
