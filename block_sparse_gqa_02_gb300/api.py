@@ -104,14 +104,23 @@ def rope(tensors, positions=None, pos_offset=0, scale=1.0, interleaved=False, in
     return [y for _, y, _, _ in rows]
 
 
-def _rotate(rope_, q, k, idx_q, idx_k, pos_offset=0):
-    """The given tensors (None: left out) at positions pos_offset, pos_offset + 1, ..."""
+def _rotate(rope_, q, k, idx_q, idx_k, pos_offset=0, positions=None):
+    """The given tensors (None: left out) at positions pos_offset, pos_offset + 1, ..., or, one
+    token a sequence, at pos_offset + positions [B]."""
     index = rope_.freqs if rope_.index_freqs is None else rope_.index_freqs
     rows = [(q, rope_.freqs, False), (k, rope_.freqs, True), (idx_q, index, False),
             (idx_k, index, False)]
-    got = iter(rope([r for r in rows if r[0] is not None], None, pos_offset, rope_.scale,
+    got = iter(rope([r for r in rows if r[0] is not None], positions, pos_offset, rope_.scale,
                     rope_.interleaved))
     return [None if r[0] is None else next(got) for r in rows]
+
+
+def _check_positions(positions, rope_, batch):
+    if positions is None:
+        return
+    if rope_ is None:
+        raise ValueError("positions are those of a Rope, and rope is None")
+    _check_shape(positions, "positions", (batch,))
 
 
 def _check_shape(x, name, want):
@@ -145,16 +154,21 @@ def alloc_decode_outputs(shape, device, dtype, mass=False):
 
 
 def decode(q, k_cache, v_cache, idx_q, idx_k, block_size=128, top_k=64, sm_scale=0.0,
-           index_scale=0.0, rope=None, mass=None):
+           index_scale=0.0, rope=None, mass=None, positions=None):
     """One MSA decode step.  q [B,1,Hq,d], caches [B,Hkv,L,d], idx_q [B,1,Hkv,dI],
-    idx_k [B,L,dI]; the new token is at position L-1 and already in the caches.  With a Rope,
-    q and idx_q are rotated to that position (the caches hold rotated keys).  With mass
-    (float32 [B,Hkv,blocks]) the attention weight of every selected block is added to it."""
+    idx_k [B,L,dI]; the new token is the last of the caches' L and already in them.  With a
+    Rope, q and idx_q are rotated (the caches hold rotated keys) to positions (int32 [B]: the
+    new tokens' absolute positions), or without them to L-1.  That is right while nothing has
+    been evicted: the keys that evict leaves stay rotated to the positions they had, so after it
+    the positions go on counting from where they were, past L.  With mass (float32
+    [B,Hkv,blocks]) the attention weight of every selected block is added to it."""
     shape = _shape_of(q, k_cache, idx_q, block_size, top_k, 1, sm_scale, index_scale)
     _check_shape(mass, "mass", (shape.batch, shape.n_heads_kv, shape.n_blocks))
+    _check_positions(positions, rope, shape.batch)
     bufs = alloc_decode_outputs(shape, q.device, q.dtype, mass is not None)
     if rope is not None:
-        q, _, idx_q, _ = _rotate(rope, q, None, idx_q, None, shape.seq_k - 1)
+        q, _, idx_q, _ = _rotate(rope, q, None, idx_q, None,
+                                 shape.seq_k - 1 if positions is None else 0, positions)
     if mass is None:
         run_decode(shape, q, k_cache, v_cache, idx_q, idx_k, bufs)
     else:
@@ -171,13 +185,17 @@ def alloc_packed_cache(n_phys, n_heads_kv, head_dim, device="cuda"):
 
 
 def decode_packed(q, k, v, cache, idx_q, idx_k_pool, seq_lens, block_table, capacity, top_k=64,
-                  sm_scale=0.0, index_scale=0.0, rope=None, mass=None):
+                  sm_scale=0.0, index_scale=0.0, rope=None, mass=None, positions=None):
     """One MSA decode step over a paged cache whose K and V are held in 4 bits.  q [B,1,Hq,d];
-    k, v [B,Hkv,1,d]: the new token's rows, packed into the cache at position seq_lens - 1;
+    k, v [B,Hkv,1,d]: the new token's rows, packed into the cache as its row seq_lens - 1;
     cache from alloc_packed_cache; idx_q [B,1,Hkv,128]; idx_k_pool [P,128,128] 16-bit index keys
     (rotated, the new token's among them); seq_lens int32 [B] (the new token counted);
-    block_table int32 [B, ceil(capacity / 128)].  With a Rope, q, k and idx_q are rotated to
-    position seq_lens - 1 first.  With mass, the blocks' attention weights are added to it."""
+    block_table int32 [B, ceil(capacity / 128)].  With a Rope, q, k and idx_q are rotated first,
+    to positions (int32 [B]: the new tokens' absolute positions), or without them to
+    seq_lens - 1.  That is right while nothing has been evicted: evict_paged shortens seq_lens,
+    but the keys that stay are rotated to the positions they had, so positions are then a count
+    of its own that evictions leave alone.  With mass, the blocks' attention weights are added
+    to it."""
     B, _, Hq, d = q.shape
     Hkv, n_phys = cache.shape[1], cache.shape[0]
     shape = make_shape(B, 1, capacity, Hq, Hkv, d, idx_q.shape[-1], 128, top_k, 1, _DT[q.dtype],
@@ -185,14 +203,11 @@ def decode_packed(q, k, v, cache, idx_q, idx_k_pool, seq_lens, block_table, capa
     _check_shape(block_table, "block_table", (B, shape.n_blocks))
     _check_shape(idx_k_pool, "idx_k_pool", (n_phys, 128, idx_q.shape[-1]))
     _check_shape(mass, "mass", (B, Hkv, shape.n_blocks))
+    _check_positions(positions, rope, B)
     bufs = alloc_prefill_outputs(shape, q.device, q.dtype)
     if rope is not None:
-        index = rope.freqs if rope.index_freqs is None else rope.index_freqs
-        rows = [(x, torch.empty_like(x), f, h)
-                for x, f, h in ((q, rope.freqs, False), (k, rope.freqs, True), (idx_q, index, False))]
-        msa_rope(make_rope(B, 1, _DT[q.dtype], -1, rope.scale, rope.interleaved),
-                 make_rope_tensors(rows), seq_lens)
-        q, k, idx_q = (y for _, y, _, _ in rows)
+        q, k, idx_q, _ = _rotate(rope, q, k, idx_q, None,
+                                 *((-1, seq_lens) if positions is None else (0, positions)))
     msa_cache_pack(shape, 1, None, seq_lens, block_table, n_phys, k, v, cache)
     msa_index_scores_paged(shape, seq_lens, block_table, n_phys, idx_q, idx_k_pool, bufs["scores"])
     msa_block_topk_ragged(shape, seq_lens, bufs["scores"], bufs["sel"])
@@ -204,7 +219,8 @@ def decode_packed(q, k, v, cache, idx_q, idx_k_pool, seq_lens, block_table, capa
 def evict_paged(seq_lens, mass, block_table, capacity, keep, n_first=1, n_recent=2, block_size=128):
     """Cuts every sequence of a paged cache to at most `keep` blocks, in place: seq_lens, mass
     [B,Hkv,blocks] and block_table are updated (the dropped physical blocks follow the kept
-    ones in the table).  Returns kept int32 [B, keep], the old indices of what stays."""
+    ones in the table).  Returns kept int32 [B, keep], the old indices of what stays.  Keys keep
+    their rotation: later steps with a Rope need positions that did not shrink with seq_lens."""
     B, Hkv, _ = mass.shape
     shape = make_shape(B, 1, capacity, Hkv, Hkv, 128, 128, block_size, 1, 1)
     _check_shape(mass, "mass", (B, Hkv, shape.n_blocks))
@@ -217,7 +233,8 @@ def evict_paged(seq_lens, mass, block_table, capacity, keep, n_first=1, n_recent
 
 def evict(k_cache, v_cache, idx_k, mass, keep, n_first=1, n_recent=2, block_size=128):
     """Cuts contiguous caches (k, v [B,Hkv,L,d], idx_k [B,L,dI]) to at most `keep` blocks.
-    Returns a dict with the shorter caches k, v, idx_k, their mass, and kept int32 [B, keep]."""
+    Returns a dict with the shorter caches k, v, idx_k, their mass, and kept int32 [B, keep].
+    Keys keep their rotation: later steps with a Rope need positions that go on from L."""
     B, Hkv, L, d = k_cache.shape
     shape = make_shape(B, 1, L, Hkv, Hkv, d, 128, block_size, 1, 1)
     n = shape.n_blocks

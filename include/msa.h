@@ -246,7 +246,9 @@ msa_status msa_sparse_decode_paged(const msa_shape* shape, const int32_t* seq_le
  * the result is rounded once to the dtype.
  *   positions   int32 [batch, seq], device; NULL: 0, 1, ..., seq - 1 in every sequence.
  *               With the cache lengths of a decode batch (seq = 1) and pos_offset = -1 the
- *               new tokens sit at the end of their caches.  Sums wrap as 32-bit integers.
+ *               new tokens sit at the end of their caches, as long as nothing was evicted
+ *               (msa_cache_evict shortens the lengths, but not the positions).  Sums wrap as
+ *               32-bit integers.
  * Up to MSA_ROPE_MAX_TENSORS tensors sharing these positions go in one launch; each is
  * [batch, seq, n_heads, head_dim], or [batch, n_heads, seq, head_dim] with head_major = 1.
  * y may be x itself (in place); otherwise no y may overlap another tensor.
@@ -354,6 +356,8 @@ msa_status msa_sparse_decode_mass(const msa_shape* shape, const int32_t* seq_len
  * of its mass over the KV heads in head order (NaN counts as the lowest).  Whole blocks go
  * and the rest keep their keys together, so the index scores of those that stay do not
  * change; all heads of a sequence drop the same ones, as they share index keys and table.
+ * Keys that were rotated stay rotated to the positions they had, so the new tokens' positions
+ * (msa_rope) go on counting past the shortened lengths.
  *   kept      int32 [batch, keep]: the old indices of the blocks that stay, ascending, -1 padded
  *   new_lens  int32 [batch]: the lengths without the dropped blocks
  *   mass_out  [batch, n_heads_kv, n_blocks]: mass of the kept blocks, in their order, then 0
