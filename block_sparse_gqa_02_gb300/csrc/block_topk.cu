@@ -212,8 +212,10 @@ static cudaError_t launch_rows(const Dims& p, const float* scores, int32_t* sel,
   const int rows = shared ? p.B * p.nR : p.B * p.Hkv * p.nR;
   const size_t smem = (size_t)p.nB * sizeof(uint32_t);
   if (smem > 48 * 1024) {
+    // the kernel's limit, the same in every call: host threads with other sizes share it
     cudaError_t e = cudaFuncSetAttribute(block_topk_kernel<kThreads>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)(kMaxBlocks * sizeof(uint32_t)));
     if (e != cudaSuccess) return e;
   }
   block_topk_kernel<kThreads><<<rows, kThreads, smem, st>>>(scores, sel, p, shared);

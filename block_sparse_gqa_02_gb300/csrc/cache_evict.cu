@@ -246,11 +246,12 @@ cudaError_t launch_cache_evict(const Dims& p, int keep, int n_first, int n_recen
                                int32_t* new_lens, float* mass_out, int32_t* table_out,
                                cudaStream_t st) {
   const size_t smem = (size_t)p.nB * 6;
-  auto kern = p.nB <= 1024   ? cache_evict_kernel<1>
-              : p.nB <= 8192 ? cache_evict_kernel<8>
-                             : cache_evict_kernel<32>;
+  const int per = p.nB <= 1024 ? 1 : p.nB <= 8192 ? 8 : 32;
+  auto kern = per == 1 ? cache_evict_kernel<1> : per == 8 ? cache_evict_kernel<8>
+                                                          : cache_evict_kernel<32>;
+  // the kernel's limit, the same in every call: host threads with other sizes share it
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+                                       per * kThreads * 6);
   if (e != cudaSuccess) return e;
   int parts = (p.nB + kThreads - 1) / kThreads;            // at most an entry a thread, or all
   if (parts > kMaxParts) parts = kMaxParts;

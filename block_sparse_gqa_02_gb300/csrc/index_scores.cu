@@ -141,8 +141,11 @@ static cudaError_t launch_prefill_simt(const Dims& p, const void* iq, const void
   const int threads = ((rows + 31) / 32) * 32;
   const size_t smem = ((size_t)p.Bk * DI + (size_t)threads) * sizeof(float);
   auto kern = index_scores_prefill_simt<T, DI>;
+  // the kernel's limit, the same in every call: host threads with other sizes share it.  A key
+  // block of at most 200 KiB (validated) and a float for each of at most 256 rows
+  constexpr int kLargest = 200 * 1024 + 256 * (int)sizeof(float);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+                                       kLargest);
   if (e != cudaSuccess) return e;
   dim3 grid(p.nR, p.B);
   kern<<<grid, threads, smem, st>>>((const T*)iq, (const T*)ik, scores, p);

@@ -837,13 +837,15 @@ cudaError_t decode_mma(const Dims& p, const void* q, const void* cache, const in
   const int per = (p.k - 1) / n_split + 1, listed = per < kMaxList ? per : kMaxList;
   const size_t smem = sizeof(MmaSmem<D, sizeof(T) == 4 ? 2 : 1>) + sizeof(Entry) * listed +
                       (kMass ? sizeof(float) * kGroupWarps * kRows * per : 0);
-  static_assert(sizeof(MmaSmem<D, sizeof(T) == 4 ? 2 : 1>) +
-                        (kMass ? kMaxMassList * (sizeof(Entry) + 4 * kGroupWarps * kRows)
-                               : kMaxList * sizeof(Entry)) <= 227 * 1024,
-                "shared memory of a CTA");
+  // the kernel's limit is set to the same value by every call: host threads share it, and one with
+  // short lists must not lower it between another's setting and its launch
+  constexpr size_t kLargest = sizeof(MmaSmem<D, sizeof(T) == 4 ? 2 : 1>) +
+                              (kMass ? kMaxMassList * (sizeof(Entry) + 4 * kGroupWarps * kRows)
+                                     : kMaxList * sizeof(Entry));
+  static_assert(kLargest <= 227 * 1024, "shared memory of a CTA");
   auto kern = packed_decode_mma<T, D, kMass>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+                                       (int)kLargest);
   if (e == cudaSuccess && n_split > 8)
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
