@@ -211,7 +211,7 @@ static cudaError_t launch_rows(const Dims& p, const float* scores, int32_t* sel,
                                int shared) {
   const int rows = shared ? p.B * p.nR : p.B * p.Hkv * p.nR;
   const size_t smem = (size_t)p.nB * sizeof(uint32_t);
-  if (smem > 48 * 1024) {
+  if (smem > 40 * 1024) {                                  // 48 KiB less the kernel's own arrays
     // the kernel's limit, the same in every call: host threads with other sizes share it
     cudaError_t e = cudaFuncSetAttribute(block_topk_kernel<kThreads>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
