@@ -19,7 +19,8 @@ struct Dims {
   int decode;    // 1 when Sq == 1 and Qt == 1
   int dtype;     // 0 f32, 1 bf16
   float sm_scale, index_scale;
-  int inject;    // test hook: 1 = the tensor-core prefill producer issues no copies
+  int inject;    // test hook: 1 = the tensor-core prefill producer issues no copies, 2 = a decode
+                 // row's first split copies no block after its first
   // paged decode (all null / 0 for contiguous caches): per-sequence cache lengths [B],
   // block table [B, nB] of physical block ids, and the number of physical blocks
   const int32_t* seq_lens;

@@ -722,7 +722,7 @@ const char* msa_status_string(msa_status status) {
 const char* msa_last_error(void) { return g_last_error; }
 
 msa_status msa_debug_set_fault(int32_t mode) {
-  if (mode != 0 && mode != 1) return fail(MSA_ERR_INVALID_ARG, "fault mode must be 0 or 1");
+  if (mode < 0 || mode > 2) return fail(MSA_ERR_INVALID_ARG, "fault mode must be 0, 1 or 2");
   g_fault_mode = mode;
   return MSA_OK;
 }

@@ -226,7 +226,8 @@ __global__ void __launch_bounds__(D) decode_combine(const float* __restrict__ ws
 
 // The same, and after the B * Hq CTAs that do it one per (b, KV head) that adds the selected
 // blocks' attention weights to mass: sum over heads h and warps w of
-// exp2(ws_b[b, h, i, w] - log2 of head h's normaliser), heads in order. 
+// exp2(ws_b[b, h, i, w] - log2 of head h's normaliser), heads in order.  A split that gave up has
+// a log-sum of NaN; its head's output is then 0, its lse -inf, and no weight is added.
 template <typename T, int D>
 __global__ void __launch_bounds__(D) decode_combine_mass(
     const float* __restrict__ ws_o, const float* __restrict__ ws_l, const float* __restrict__ ws_b,

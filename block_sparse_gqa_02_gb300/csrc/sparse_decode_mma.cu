@@ -135,6 +135,7 @@ sparse_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k,
     for (int i = i0; i < i1; ++i) {
       const int blk = block_at(i);
       if (!valid(blk)) continue;
+      if (p.inject == 2 && split == 0 && j > 0) break;       // test hook: no copies any more
       const int st = j % kStages;
       if (!ptx::mbar_wait(&s.empty[st], ((j / kStages) & 1) ^ 1, abort)) { ok = false; break; }
       if (lane == 0) {
@@ -335,7 +336,12 @@ sparse_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k,
         for (int w = 0; w < kComputeWarps; ++w) acc = fmaf(wgt[w], s.o[w][r][d0 + dd], acc);
         ws_o[slot * kD + d0 + dd] = acc * inv;
       }
-      if (d0 == 0) ws_l[slot] = lt > 0.f ? (mt + __log2f(lt)) * kLn2 : -INFINITY;
+      if (d0 == 0) {
+        ws_l[slot] = lt > 0.f ? (mt + __log2f(lt)) * kLn2 : -INFINITY;
+        // After a wait that was given up ws_b lacks entries: a normaliser of NaN makes the merge
+        // leave the rows' weights out, all of them, as the other splits' lack this one's share
+        if (kMass && *abort) ws_l[slot] = __int_as_float(0x7fffffff);
+      }
     }
   }
 }

@@ -342,6 +342,8 @@ msa_status msa_sparse_decode_packed(const msa_shape* shape, const int32_t* seq_l
  * seq_lens and block_table (both given), of msa_sparse_decode_paged on its shapes; on other
  * shapes the sums run in another order.  A selected block's entry gets one addition a call, so
  * results repeat bit for bit.  (A block listed twice is counted twice, in either order.)
+ * Where a kernel gives up a bounded wait (MSA_ERR_TIMEOUT), nothing is added for that sequence
+ * and KV head, and its out is 0 and its lse -inf.
  * top_k is at most 2^20.  workspace: msa_workspace_bytes(shape, 4) bytes, as for
  * msa_sparse_decode. */
 msa_status msa_sparse_decode_mass(const msa_shape* shape, const int32_t* seq_lens,
@@ -411,8 +413,10 @@ const char* msa_last_error(void);
  * afterwards (from any thread) has its copy-issuing warp issue nothing, so the warps that
  * wait for the copies give up after their one-second bound, the kernel writes zeros and
  * -inf, and the next msa_get_device_status() reports MSA_ERR_TIMEOUT.  No copy or MMA is
- * ever in flight in this mode, and the CUDA context stays usable.  mode 0 (default):
- * normal operation.  Any other mode: MSA_ERR_INVALID_ARG. */
+ * ever in flight in this mode, and the CUDA context stays usable.  mode 2: in every tensor-core
+ * decode launch, the CTA of a row's first split issues only the copy of its first block, so it
+ * gives up in the same way if it has another.  mode 0 (default): normal operation.  Any other
+ * mode: MSA_ERR_INVALID_ARG. */
 msa_status msa_debug_set_fault(int32_t mode);
 
 /* MSA_ABI_VERSION of the loaded library. */
