@@ -373,7 +373,8 @@ packed_decode_mma(const T* __restrict__ q, const uint8_t* __restrict__ cache,
         }
         if (lane == 0) s.count = n;
         __syncwarp();
-        if (lane < min(n, kStages) && !*abort) {
+        const int now = p.inject == 2 && split == 0 ? min(n, 1) : n;   // test hook: one copy
+        if (lane < min(now, kStages) && !*abort) {
           // the first copies, a lane each; every stage is empty here
           const int x = first + lane, st = x % kStages;
           s.last[st] = x;
@@ -757,7 +758,8 @@ packed_decode_mma(const T* __restrict__ q, const uint8_t* __restrict__ cache,
 #pragma unroll
       for (int w = 0; w < kMmaWarps; ++w) sum += ex2(s.wm[w][r] - ref) * s.wl[w][r];
       *cluster.map_shared_rank(&s.m[split][r], to) = top;
-      *cluster.map_shared_rank(&s.l[split][r], to) = sum;
+      // a sum below zero: this CTA gave up a wait
+      *cluster.map_shared_rank(&s.l[split][r], to) = *abort ? -1.f : sum;
     }
     for (int e = threadIdx.x; e < kRows * D / 4; e += kMmaThreads) {
       const int r = e / (D / 4), d0 = e % (D / 4) * 4;
@@ -777,10 +779,15 @@ packed_decode_mma(const T* __restrict__ q, const uint8_t* __restrict__ cache,
     if (threadIdx.x < kRows) {
       const int r = threadIdx.x;
       float top = -INFINITY, sum = 0.f;
-      for (int x = 0; x < n_split; ++x) top = fmaxf(top, s.m[x][r]);
+      bool gave_up = false;
+      for (int x = 0; x < n_split; ++x) {
+        top = fmaxf(top, s.m[x][r]);
+        gave_up |= s.l[x][r] < 0.f;
+      }
       const float ref = top == -INFINITY ? 0.f : top;
       for (int x = 0; x < n_split; ++x) sum += ex2(s.m[x][r] - ref) * s.l[x][r];
-      s.norm[r] = sum == 0.f ? -INFINITY : ref + __log2f(sum);
+      // without all of the row's blocks: output 0, lse -inf, no weights
+      s.norm[r] = sum == 0.f || gave_up ? -INFINITY : ref + __log2f(sum);
       if (lse && split == 0 && r < rows)
         lse[(size_t)b * p.Hq + g * p.G + h0 + r] = s.norm[r] * kLn2;
     }
@@ -808,7 +815,7 @@ packed_decode_mma(const T* __restrict__ q, const uint8_t* __restrict__ cache,
             sum += ex2(weights[(w * per + i) * kRows + r] - s.norm[r]);
 #pragma unroll
         for (int x = kRows / 2; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-        if (r == 0 && i < n_blocks && !*abort)
+        if (r == 0 && i < n_blocks)
           atomicAdd(mass + (size_t)bg * p.nB + list[i].blk, sum);
       }
     if (h0 + kRows < p.G) {

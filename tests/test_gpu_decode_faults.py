@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 import torch
 
-from block_sparse_gqa_02_gb300 import _lib
+from block_sparse_gqa_02_gb300 import _lib, api
 from oracle import cache_ops as co
 from tests.parity import check_lse, check_out, to_np
 from tests.test_gpu_packed import _i32, _rows, _weight_tol
@@ -43,8 +43,8 @@ def _check(call, out, lse, mass, o, l, w, tol):
     _faulty(call)
     assert bool((mass[0] == 3).all())                  # nothing added for the rows that failed
     assert bool((out[0] == 0).all()) and bool(torch.isneginf(lse[0]).all())
-    # an addition to 3 rounds once more
-    bound = tol * w + 2.0 ** -24 * (3 + w)
+    # an addition to 3 rounds once more; a wide group makes two
+    bound = tol * w + 2 * 2.0 ** -24 * (3 + w)
     assert np.all(np.abs(to_np(mass) - 3 - w)[1] <= bound[1])
     check_out(out[1:], o[1:], "bf16")
     check_lse(lse[1:], l[1:], "bf16")
@@ -79,3 +79,21 @@ def test_16_bit_cache(paged):
     o, l, w = co.decode_mass(q, list(to_np(k)), list(to_np(v)), sel_np, [L] * B)
     _check(lambda: _lib.msa_sparse_decode_mass(shape, *pool[:3], q, *pool[3:], sel, out, lse, mass, ws),
            out, lse, mass, o, l, w, _weight_tol(to_np(q), to_np(k), d ** -0.5, d))
+
+
+@pytest.mark.parametrize("heads", [8, 20])             # a group in one pass, and in two
+def test_4_bit_cache(heads):
+    B, Hkv, d, L, topk = 2, 2, 128, 64 * 128, 60
+    Hq = heads * Hkv
+    shape = _lib.make_shape(B, 1, L, Hq, Hkv, d, 128, 128, topk, 1)
+    q, k, v = (_rows(s, BF, i) for i, s in enumerate(((B, 1, Hq, d), (B, Hkv, L, d), (B, Hkv, L, d))))
+    cache = api.alloc_packed_cache(B * 64, Hkv, d)
+    _lib.msa_cache_pack(shape, L, None, None, None, B * 64, k, v, cache)
+    sel_np = _sel(B, Hkv, topk, 64)
+    sel = torch.from_numpy(sel_np).cuda()
+    out, lse = torch.empty_like(q), torch.empty((B, Hq, 1), device="cuda")
+    mass = torch.full((B, Hkv, 64), 3.0, device="cuda")
+    kv = [list(co.pack_values(to_np(x))[0]) for x in (k, v)]
+    o, l, w = co.decode_mass(q, *kv, sel_np, [L] * B)
+    _check(lambda: _lib.msa_sparse_decode_packed(shape, None, None, B * 64, q, cache, sel, out, lse, mass),
+           out, lse, mass, o, l, w, _weight_tol(to_np(q), np.stack(kv[0]), d ** -0.5, d))
