@@ -95,7 +95,7 @@ struct MmaSmem {
   float wm[kMmaWarps][kRows], wl[kMmaWarps][kRows];
   uint64_t full[kStages], empty[kStages];
   int last[kStages];                   // a stage's last copy
-  int abort, count;
+  int abort, count, lost;              // lost: some CTA of the cluster gave up a wait
 };
 
 // d = a b, d += a b
@@ -296,7 +296,9 @@ packed_decode_mma(const T* __restrict__ q, const uint8_t* __restrict__ cache,
   extern __shared__ __align__(128) uint8_t smem_raw[];
   S& s = *reinterpret_cast<S*>(smem_raw);
   Entry* list = reinterpret_cast<Entry*>(smem_raw + sizeof(S));   // [min(per, kMaxList)]
-  float* weights = reinterpret_cast<float*>(list + per);   // [kGroupWarps][per][kRows], kMass only
+  // kMass only: log-sums [kGroupWarps][per][kRows], and the blocks' weights so far [per]
+  float* weights = reinterpret_cast<float*>(list + per);
+  float* total = weights + kGroupWarps * per * kRows;
   cg::cluster_group cluster = cg::this_cluster();
   const int split = (int)cluster.block_rank(), n_split = (int)cluster.num_blocks();
   const int own = kRows / n_split;                         // rows that a CTA of the cluster ends
@@ -324,7 +326,8 @@ packed_decode_mma(const T* __restrict__ q, const uint8_t* __restrict__ cache,
     return true;
   };
 
-  // more than 16 heads of a group: one pass after the other, weights added up in order
+  // more than 16 heads of a group: one pass after the other, weights added up in order and to mass
+  // in the last
   int first = 0;                                           // copies made so far
   for (int h0 = 0; h0 < p.G; h0 += kRows) {
     const int rows = min(kRows, p.G - h0);
@@ -358,7 +361,7 @@ packed_decode_mma(const T* __restrict__ q, const uint8_t* __restrict__ cache,
             ptx::mbar_init(&s.empty[i], kGroupWarps);
             s.last[i] = -1;
           }
-          s.abort = 0;
+          s.abort = s.lost = 0;
           ptx::fence_barrier_init();
         }
         int n = 0;
@@ -788,6 +791,7 @@ packed_decode_mma(const T* __restrict__ q, const uint8_t* __restrict__ cache,
       for (int x = 0; x < n_split; ++x) sum += ex2(s.m[x][r] - ref) * s.l[x][r];
       // without all of the row's blocks: output 0, lse -inf, no weights
       s.norm[r] = sum == 0.f || gave_up ? -INFINITY : ref + __log2f(sum);
+      if (gave_up) s.lost = 1;
       if (lse && split == 0 && r < rows)
         lse[(size_t)b * p.Hq + g * p.G + h0 + r] = s.norm[r] * kLn2;
     }
@@ -805,7 +809,8 @@ packed_decode_mma(const T* __restrict__ q, const uint8_t* __restrict__ cache,
         }
       store_pair(out + ((size_t)b * p.Hq + g * p.G + h0 + r) * D + d0, v);
     }
-    if (kMass)                                             // sixteen lanes a block, one a row
+    if (kMass)                                             // sixteen lanes a block, one a row; a
+                                                           // lane meets its block in every pass
       for (int e0 = 0; e0 < n_blocks * kRows; e0 += kMmaThreads) {
         const int e = e0 + (int)threadIdx.x, i = e / kRows, r = e % kRows;
         float sum = 0.f;
@@ -815,8 +820,11 @@ packed_decode_mma(const T* __restrict__ q, const uint8_t* __restrict__ cache,
             sum += ex2(weights[(w * per + i) * kRows + r] - s.norm[r]);
 #pragma unroll
         for (int x = kRows / 2; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-        if (r == 0 && i < n_blocks)
-          atomicAdd(mass + (size_t)bg * p.nB + list[i].blk, sum);
+        if (r == 0 && i < n_blocks) {
+          if (h0 > 0) sum += total[i];
+          if (h0 + kRows < p.G) total[i] = sum;
+          else if (!s.lost) atomicAdd(mass + (size_t)bg * p.nB + list[i].blk, sum);
+        }
       }
     if (h0 + kRows < p.G) {
       // the next pass copies into the memory that held the warps' outputs, and the others
@@ -843,11 +851,11 @@ cudaError_t decode_mma(const Dims& p, const void* q, const void* cache, const in
   static_assert(kMaxPackedMassBlocks <= kMaxSplits * kMaxMassList, "lists of weights");
   const int per = (p.k - 1) / n_split + 1, listed = per < kMaxList ? per : kMaxList;
   const size_t smem = sizeof(MmaSmem<D, sizeof(T) == 4 ? 2 : 1>) + sizeof(Entry) * listed +
-                      (kMass ? sizeof(float) * kGroupWarps * kRows * per : 0);
+                      (kMass ? sizeof(float) * (kGroupWarps * kRows + 1) * per : 0);
   // the kernel's limit is set to the same value by every call: host threads share it, and one with
   // short lists must not lower it between another's setting and its launch
   constexpr size_t kLargest = sizeof(MmaSmem<D, sizeof(T) == 4 ? 2 : 1>) +
-                              (kMass ? kMaxMassList * (sizeof(Entry) + 4 * kGroupWarps * kRows)
+                              (kMass ? kMaxMassList * (sizeof(Entry) + 4 * kGroupWarps * kRows + 4)
                                      : kMaxList * sizeof(Entry));
   static_assert(kLargest <= 227 * 1024, "shared memory of a CTA");
   auto kern = packed_decode_mma<T, D, kMass>;

@@ -343,7 +343,7 @@ msa_status msa_sparse_decode_packed(const msa_shape* shape, const int32_t* seq_l
  * shapes the sums run in another order.  A selected block's entry gets one addition a call, so
  * results repeat bit for bit.  (A block listed twice is counted twice, in either order.)
  * Where a kernel gives up a bounded wait (MSA_ERR_TIMEOUT), nothing is added for that sequence
- * and KV head, and its out is 0 and its lse -inf.
+ * and KV head, and the heads concerned have out 0 and lse -inf.
  * top_k is at most 2^20.  workspace: msa_workspace_bytes(shape, 4) bytes, as for
  * msa_sparse_decode. */
 msa_status msa_sparse_decode_mass(const msa_shape* shape, const int32_t* seq_lens,
