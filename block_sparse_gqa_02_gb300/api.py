@@ -179,6 +179,13 @@ def decode(q, k_cache, v_cache, idx_q, idx_k, block_size=128, top_k=64, sm_scale
     return bufs
 
 
+def _check_step(x, name, numel, dtype, dev):
+    """All that a call would refuse a tensor for, ahead of the step's first launch."""
+    _lib._arg(x, name, dtype, numel, dev)
+    if x.data_ptr() % 16:
+        raise ValueError(f"{name} is not 16-byte aligned")
+
+
 def alloc_packed_cache(n_phys, n_heads_kv, head_dim, device="cuda"):
     """A 4-bit cache of n_phys blocks of 128 keys (layout in include/msa.h)."""
     return torch.zeros((n_phys, n_heads_kv, 160 * head_dim), dtype=torch.uint8, device=device)
@@ -195,15 +202,35 @@ def decode_packed(q, k, v, cache, idx_q, idx_k_pool, seq_lens, block_table, capa
     seq_lens - 1.  That is right while nothing has been evicted: evict_paged shortens seq_lens,
     but the keys that stay are rotated to the positions they had, so positions are then a count
     of its own that evictions leave alone.  With mass, the blocks' attention weights are added
-    to it."""
+    to it (top_k at most 1024).
+
+    The paged index scores set the step's limits: bf16, head_dim 128, 4 KV heads, at most 16
+    query heads per KV head.  (msa_cache_pack and msa_sparse_decode_packed take more, with a
+    selection from elsewhere.)  A step that is refused has not changed the cache."""
     B, _, Hq, d = q.shape
     Hkv, n_phys = cache.shape[1], cache.shape[0]
     shape = make_shape(B, 1, capacity, Hq, Hkv, d, idx_q.shape[-1], 128, top_k, 1, _DT[q.dtype],
                        sm_scale, index_scale)
+    if q.dtype is not torch.bfloat16 or d != 128 or idx_q.shape[-1] != 128 or Hkv != 4 or Hq > 64:
+        raise _lib.MsaError(_lib.MSA_ERR_UNSUPPORTED, "decode_packed",
+                            "a step over the 4-bit cache runs bf16, head_dim = index_dim = 128, 4 KV "
+                            "heads, at most 16 query heads per KV head")
+    if mass is not None and top_k > 1024:
+        raise _lib.MsaError(_lib.MSA_ERR_UNSUPPORTED, "decode_packed", "mass needs top_k <= 1024")
     _check_shape(block_table, "block_table", (B, shape.n_blocks))
     _check_shape(idx_k_pool, "idx_k_pool", (n_phys, 128, idx_q.shape[-1]))
     _check_shape(mass, "mass", (B, Hkv, shape.n_blocks))
     _check_positions(positions, rope, B)
+    dev = _lib._place(None)[0]
+    for x, name, n, dt in ((q, "q", B * Hq * d, q.dtype), (idx_q, "idx_q", B * Hkv * d, q.dtype),
+                           (idx_k_pool, "idx_k_pool", n_phys * 128 * d, q.dtype),
+                           (k, "k", B * Hkv * d, q.dtype), (v, "v", B * Hkv * d, q.dtype),
+                           (cache, "cache", n_phys * Hkv * 160 * d, torch.uint8),
+                           (seq_lens, "seq_lens", B, torch.int32),
+                           (block_table, "block_table", 0, torch.int32)):
+        _check_step(x, name, n, dt, dev)
+    if mass is not None:
+        _check_step(mass, "mass", 0, torch.float32, dev)
     bufs = alloc_prefill_outputs(shape, q.device, q.dtype)
     if rope is not None:
         q, k, idx_q, _ = _rotate(rope, q, k, idx_q, None,
