@@ -319,17 +319,23 @@ def _place(stream):
     return dev, _stream(stream)
 
 
-def _arg(x, name, dtype, numel, dev):
+def _arg(x, name, dtype, numel, dev, rows=0):
     """Device pointer of a tensor that must be contiguous, of `dtype` (None: any) and at least
-    `numel` elements, and on device `dev`; of an int (a raw pointer) or None as they are."""
+    `numel` elements, and on device `dev`; of an int (a raw pointer) or None as they are.
+    rows: the entries of the first axis that the call indexes.  A longer first axis (or a flat
+    buffer) has the call's elements at its start; with any other axis longer every row but the
+    first would be read in the wrong place."""
     if x is None or type(x) is int:
         return x
+    n = x.numel()
+    if n != numel and rows and x.dim() > 1 and n * rows != numel * x.shape[0]:
+        raise ValueError(f"{name} is {tuple(x.shape)}: {n} elements, expected {numel} in {rows} rows")
     if x.get_device() != dev:
         raise ValueError(f"{name} is on {x.device}, not on the current CUDA device")
     if dtype is not None and x.dtype is not dtype:
         raise ValueError(f"{name} is {x.dtype}, expected {dtype}")
-    if x.numel() < numel:
-        raise ValueError(f"{name} has {x.numel()} elements, expected {numel}")
+    if n < numel:
+        raise ValueError(f"{name} has {n} elements, expected {numel}")
     if not x.is_contiguous():
         raise ValueError(f"{name}: MSA tensors must be contiguous")
     return x.data_ptr()
@@ -391,14 +397,14 @@ def msa_rope(desc: MsaRope, tensors: RopeTensors, positions=None, stream=None):
                          f"{(tensors.batch, tensors.seq, tensors.dtype)}, the call "
                          f"{(batch, seq, _FLOATS.get(desc.dtype))}")
     _check(load().msa_rope(ctypes.byref(desc), tensors.array, len(tensors.rows),
-                           _arg(positions, "positions", _I32, batch * seq, dev), st), "msa_rope")
+                           _arg(positions, "positions", _I32, batch * seq, dev, batch), st), "msa_rope")
 
 
 def _cache_args(shape, batch, hkv, d, seq_lens, block_table, n_phys, cache, dev):
-    return (_arg(seq_lens, "seq_lens", _I32, batch, dev),
+    return (_arg(seq_lens, "seq_lens", _I32, batch, dev, batch),
             block_table if block_table is None else
-            _arg(block_table, "block_table", _I32, batch * shape.n_blocks, dev), n_phys,
-            _arg(cache, "cache", _U8, n_phys * hkv * 160 * d, dev))
+            _arg(block_table, "block_table", _I32, batch * shape.n_blocks, dev, batch), n_phys,
+            _arg(cache, "cache", _U8, n_phys * hkv * 160 * d, dev, n_phys))
 
 
 def _cache_rows(call, where, shape, n, starts, seq_lens, block_table, n_phys, cache, k, v, stream):
@@ -408,10 +414,10 @@ def _cache_rows(call, where, shape, n, starts, seq_lens, block_table, n_phys, ca
     batch, hkv, d, dt = shape.batch, shape.n_heads_kv, shape.head_dim, _FLOATS.get(shape.dtype)
     rows = batch * hkv * n * d
     args = _cache_args(shape, batch, hkv, d, seq_lens, block_table, n_phys, cache, dev)
-    kv = _arg(k, "k", dt, rows, dev), _arg(v, "v", dt, rows, dev)
+    kv = _arg(k, "k", dt, rows, dev, batch), _arg(v, "v", dt, rows, dev, batch)
     tail = kv + args[3:] if where == "msa_cache_pack" else args[3:] + kv
-    _check(call(ctypes.byref(shape), n, _arg(starts, "starts", _I32, batch, dev), *args[:3], *tail,
-                st), where)
+    _check(call(ctypes.byref(shape), n, _arg(starts, "starts", _I32, batch, dev, batch), *args[:3],
+                *tail, st), where)
 
 
 def msa_cache_pack(shape: MsaShape, n_new, starts, seq_lens, block_table, n_phys, k, v, cache,
@@ -429,9 +435,11 @@ def msa_cache_unpack(shape: MsaShape, n_out, starts, seq_lens, block_table, n_ph
 def _decode_args(shape, batch, hkv, d, dt, q, sel, out, lse, mass, dev):
     hq = shape.n_heads_q
     n = batch * hq * d
-    return (_arg(q, "q", dt, n, dev), _arg(sel, "sel", _I32, batch * hkv * shape.top_k, dev),
-            _arg(out, "out", dt, n, dev), _arg(lse, "lse", _F32, batch * hq, dev),
-            mass if mass is None else _arg(mass, "mass", _F32, batch * hkv * shape.n_blocks, dev))
+    return (_arg(q, "q", dt, n, dev, batch),
+            _arg(sel, "sel", _I32, batch * hkv * shape.top_k, dev, batch),
+            _arg(out, "out", dt, n, dev, batch), _arg(lse, "lse", _F32, batch * hq, dev, batch),
+            mass if mass is None else
+            _arg(mass, "mass", _F32, batch * hkv * shape.n_blocks, dev, batch))
 
 
 def msa_sparse_decode_packed(shape: MsaShape, seq_lens, block_table, n_phys, q, cache, sel, out,
@@ -453,13 +461,14 @@ def msa_sparse_decode_mass(shape: MsaShape, seq_lens, block_table, n_phys, q, k,
         ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     n_phys = int(n_phys)
     batch, hkv, d, dt = shape.batch, shape.n_heads_kv, shape.head_dim, _FLOATS.get(shape.dtype)
-    n = (n_phys * shape.block_size if block_table is not None else batch * shape.seq_k) * hkv * d
+    paged = block_table is not None
+    n = (n_phys * shape.block_size if paged else batch * shape.seq_k) * hkv * d
+    rows = n_phys if paged else batch
     q, sel, out, lse, mass = _decode_args(shape, batch, hkv, d, dt, q, sel, out, lse, mass, dev)
     _check(load().msa_sparse_decode_mass(
-        ctypes.byref(shape), _arg(seq_lens, "seq_lens", _I32, batch, dev),
-        block_table if block_table is None else
-        _arg(block_table, "block_table", _I32, batch * shape.n_blocks, dev), n_phys, q,
-        _arg(k, "k", dt, n, dev), _arg(v, "v", dt, n, dev), sel, out, lse, mass,
+        ctypes.byref(shape), _arg(seq_lens, "seq_lens", _I32, batch, dev, batch),
+        _arg(block_table, "block_table", _I32, batch * shape.n_blocks, dev, batch) if paged else None,
+        n_phys, q, _arg(k, "k", dt, n, dev, rows), _arg(v, "v", dt, n, dev, rows), sel, out, lse, mass,
         _arg(workspace, "workspace", None, 0, dev), ws_bytes, st), "msa_sparse_decode_mass")
 
 
@@ -471,11 +480,12 @@ def msa_cache_evict(shape: MsaShape, keep, n_first, n_recent, seq_lens, mass, bl
     m = n * shape.n_heads_kv
     _check(load().msa_cache_evict(
         ctypes.byref(shape), keep, int(n_first), int(n_recent),
-        _arg(seq_lens, "seq_lens", _I32, batch, dev), _arg(mass, "mass", _F32, m, dev),
-        _arg(block_table, "block_table", _I32, n, dev),
-        _arg(kept, "kept", _I32, batch * keep, dev), _arg(new_lens, "new_lens", _I32, batch, dev),
-        _arg(mass_out, "mass_out", _F32, m, dev), _arg(table_out, "table_out", _I32, n, dev), st),
-        "msa_cache_evict")
+        _arg(seq_lens, "seq_lens", _I32, batch, dev, batch), _arg(mass, "mass", _F32, m, dev, batch),
+        _arg(block_table, "block_table", _I32, n, dev, batch),
+        _arg(kept, "kept", _I32, batch * keep, dev, batch),
+        _arg(new_lens, "new_lens", _I32, batch, dev, batch),
+        _arg(mass_out, "mass_out", _F32, m, dev, batch),
+        _arg(table_out, "table_out", _I32, n, dev, batch), st), "msa_cache_evict")
 
 
 class GatherTensors:

@@ -179,9 +179,9 @@ def decode(q, k_cache, v_cache, idx_q, idx_k, block_size=128, top_k=64, sm_scale
     return bufs
 
 
-def _check_step(x, name, numel, dtype, dev):
+def _check_step(x, name, rows, numel, dtype, dev):
     """All that a call would refuse a tensor for, ahead of the step's first launch."""
-    _lib._arg(x, name, dtype, numel, dev)
+    _lib._arg(x, name, dtype, numel, dev, rows)
     if x.data_ptr() % 16:
         raise ValueError(f"{name} is not 16-byte aligned")
 
@@ -222,15 +222,15 @@ def decode_packed(q, k, v, cache, idx_q, idx_k_pool, seq_lens, block_table, capa
     _check_shape(mass, "mass", (B, Hkv, shape.n_blocks))
     _check_positions(positions, rope, B)
     dev = _lib._place(None)[0]
-    for x, name, n, dt in ((q, "q", B * Hq * d, q.dtype), (idx_q, "idx_q", B * Hkv * d, q.dtype),
-                           (idx_k_pool, "idx_k_pool", n_phys * 128 * d, q.dtype),
-                           (k, "k", B * Hkv * d, q.dtype), (v, "v", B * Hkv * d, q.dtype),
-                           (cache, "cache", n_phys * Hkv * 160 * d, torch.uint8),
-                           (seq_lens, "seq_lens", B, torch.int32),
-                           (block_table, "block_table", 0, torch.int32)):
-        _check_step(x, name, n, dt, dev)
-    if mass is not None:
-        _check_step(mass, "mass", 0, torch.float32, dev)
+    nB = shape.n_blocks
+    for x, name, rows, n, dt in (
+            (q, "q", B, Hq * d, q.dtype), (idx_q, "idx_q", B, Hkv * d, q.dtype),
+            (idx_k_pool, "idx_k_pool", n_phys, 128 * d, q.dtype), (k, "k", B, Hkv * d, q.dtype),
+            (v, "v", B, Hkv * d, q.dtype), (cache, "cache", n_phys, Hkv * 160 * d, torch.uint8),
+            (seq_lens, "seq_lens", B, 1, torch.int32), (block_table, "block_table", B, nB, torch.int32),
+            (mass, "mass", B, Hkv * nB, torch.float32)):
+        if x is not None:
+            _check_step(x, name, rows, rows * n, dt, dev)
     bufs = alloc_prefill_outputs(shape, q.device, q.dtype)
     if rope is not None:
         q, k, idx_q, _ = _rotate(rope, q, k, idx_q, None,
