@@ -629,6 +629,19 @@ msa_status msa_cache_evict(const msa_shape* shape, int32_t keep, int32_t n_first
     return fail(MSA_ERR_INVALID_ARG, "table_out overlaps block_table without being it");
   if (new_lens != seq_lens && overlap(new_lens, seq_lens, (size_t)d.B * 4))
     return fail(MSA_ERR_INVALID_ARG, "new_lens overlaps seq_lens without being it");
+  // ... and clear of everything else
+  const struct { const void* p; size_t n; const char* name; } buf[7] = {
+      {kept, (size_t)d.B * keep * 4, "kept"}, {new_lens, (size_t)d.B * 4, "new_lens"},
+      {mass_out, mass_bytes, "mass_out"}, {table_out, table_bytes, "table_out"},
+      {seq_lens, (size_t)d.B * 4, "seq_lens"}, {mass, mass_bytes, "mass"},
+      {block_table, table_bytes, "block_table"}};
+  for (int i = 0; i < 4; ++i)
+    for (int j = i + 1; j < 7; ++j) {
+      if (i > 0 && j == i + 3) continue;                   // the output's own input: above
+      const uintptr_t a = (uintptr_t)buf[i].p, b = (uintptr_t)buf[j].p;
+      if (a && b && a < b + buf[j].n && b < a + buf[i].n)
+        return fail(MSA_ERR_INVALID_ARG, "%s overlaps %s", buf[i].name, buf[j].name);
+    }
   d.seq_lens = seq_lens;
   {
     const cudaError_t ve = launch_debug_validate(d, nullptr, (cudaStream_t)stream, status_ptr());
