@@ -266,6 +266,10 @@ def evict(k_cache, v_cache, idx_k, mass, keep, n_first=1, n_recent=2, block_size
     shape = make_shape(B, 1, L, Hkv, Hkv, d, 128, block_size, 1, 1)
     n = shape.n_blocks
     _check_shape(mass, "mass", (B, Hkv, n))
+    if tuple(v_cache.shape[:-1]) != (B, Hkv, L):
+        raise ValueError(f"v_cache is {tuple(v_cache.shape)}, expected {(B, Hkv, L, d)}")
+    if idx_k.dim() != 3 or tuple(idx_k.shape[:2]) != (B, L):
+        raise ValueError(f"idx_k is {tuple(idx_k.shape)}, expected {(B, L, 'dI')}")
     rows = L - (n - min(n, keep)) * block_size
     new = lambda x: torch.empty((*x.shape[:-2], rows, x.shape[-1]), dtype=x.dtype, device=x.device)  # noqa: E731
     kept = torch.empty((B, keep), dtype=torch.int32, device=mass.device)
