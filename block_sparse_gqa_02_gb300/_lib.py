@@ -327,18 +327,23 @@ def _arg(x, name, dtype, numel, dev, rows=0):
     first would be read in the wrong place."""
     if x is None or type(x) is int:
         return x
-    n = x.numel()
-    if n != numel and rows and x.dim() > 1 and n * rows != numel * x.shape[0]:
-        raise ValueError(f"{name} is {tuple(x.shape)}: {n} elements, expected {numel} in {rows} rows")
+    if numel and x.numel() != numel:
+        _check_size(x, name, numel, rows)
     if x.get_device() != dev:
         raise ValueError(f"{name} is on {x.device}, not on the current CUDA device")
     if dtype is not None and x.dtype is not dtype:
         raise ValueError(f"{name} is {x.dtype}, expected {dtype}")
-    if n < numel:
-        raise ValueError(f"{name} has {n} elements, expected {numel}")
     if not x.is_contiguous():
         raise ValueError(f"{name}: MSA tensors must be contiguous")
     return x.data_ptr()
+
+
+def _check_size(x, name, numel, rows):
+    n = x.numel()
+    if rows and x.dim() > 1 and n * rows != numel * x.shape[0]:
+        raise ValueError(f"{name} is {tuple(x.shape)}: {n} elements, expected {numel} in {rows} rows")
+    if n < numel:
+        raise ValueError(f"{name} has {n} elements, expected {numel}")
 
 
 def make_rope(batch, seq, dtype="bf16", pos_offset=0, scale=0.0, interleaved=False,
