@@ -180,9 +180,8 @@ def decode(q, k_cache, v_cache, idx_q, idx_k, block_size=128, top_k=64, sm_scale
 
 
 def _check_step(x, name, rows, numel, dtype, dev):
-    """All that a call would refuse a tensor for, ahead of the step's first launch."""
-    _lib._arg(x, name, dtype, numel, dev, rows)
-    if x.data_ptr() % 16:
+    """What a call would refuse a tensor for, ahead of the step's first launch."""
+    if _lib._arg(x, name, dtype, numel, dev, rows) % 16:
         raise ValueError(f"{name} is not 16-byte aligned")
 
 
@@ -221,20 +220,22 @@ def decode_packed(q, k, v, cache, idx_q, idx_k_pool, seq_lens, block_table, capa
     _check_shape(idx_k_pool, "idx_k_pool", (n_phys, 128, idx_q.shape[-1]))
     _check_shape(mass, "mass", (B, Hkv, shape.n_blocks))
     _check_positions(positions, rope, B)
+    # packing checks its own arguments ahead of its launch; these are those of the calls after it
     dev = _lib._place(None)[0]
-    nB = shape.n_blocks
-    for x, name, rows, n, dt in (
-            (q, "q", B, Hq * d, q.dtype), (idx_q, "idx_q", B, Hkv * d, q.dtype),
-            (idx_k_pool, "idx_k_pool", n_phys, 128 * d, q.dtype), (k, "k", B, Hkv * d, q.dtype),
-            (v, "v", B, Hkv * d, q.dtype), (cache, "cache", n_phys, Hkv * 160 * d, torch.uint8),
-            (seq_lens, "seq_lens", B, 1, torch.int32), (block_table, "block_table", B, nB, torch.int32),
-            (mass, "mass", B, Hkv * nB, torch.float32)):
-        if x is not None:
-            _check_step(x, name, rows, rows * n, dt, dev)
+    _check_step(q, "q", B, B * Hq * d, q.dtype, dev)
+    _check_step(idx_q, "idx_q", B, B * Hkv * d, q.dtype, dev)
+    _check_step(idx_k_pool, "idx_k_pool", n_phys, n_phys * 128 * d, q.dtype, dev)
+    if mass is not None:
+        _check_step(mass, "mass", B, B * Hkv * shape.n_blocks, torch.float32, dev)
     bufs = alloc_prefill_outputs(shape, q.device, q.dtype)
     if rope is not None:
-        q, k, idx_q, _ = _rotate(rope, q, k, idx_q, None,
-                                 *((-1, seq_lens) if positions is None else (0, positions)))
+        index = rope.freqs if rope.index_freqs is None else rope.index_freqs
+        rows = [(x, torch.empty_like(x), f, h)
+                for x, f, h in ((q, rope.freqs, False), (k, rope.freqs, True), (idx_q, index, False))]
+        msa_rope(make_rope(B, 1, _DT[q.dtype], -1 if positions is None else 0, rope.scale,
+                           rope.interleaved), make_rope_tensors(rows),
+                 seq_lens if positions is None else positions)
+        q, k, idx_q = (y for _, y, _, _ in rows)
     msa_cache_pack(shape, 1, None, seq_lens, block_table, n_phys, k, v, cache)
     msa_index_scores_paged(shape, seq_lens, block_table, n_phys, idx_q, idx_k_pool, bufs["scores"])
     msa_block_topk_ragged(shape, seq_lens, bufs["scores"], bufs["sel"])
