@@ -9,10 +9,14 @@
 // only one to its address in a call, so results repeat bit for bit.
 //
 // Other shapes (fp32, head_dim 64, other blocks, wide groups) are computed here, on the CUDA
-// cores: fp32 products have no tensor-core form that keeps their 24 bits.  4 x 50000 keys, 48
-// blocks a head: 41 us for 200 MB (fp32, head_dim 128, 8 KV heads of 2), 17 for 100 MB (fp32,
-// head_dim 64, 8 of 1: memory), 46 for 100 MB (fp32, head_dim 128, 4 of 16: the latency of a
-// tile's 4096 products a lane at two warps a scheduler), 25 for 25 MB (bf16, head_dim 64, 4 of 16).
+// cores, in fp32 whatever the caches' type: one kernel for every shape that the call takes.  On the
+// tensor cores fp32 products would need operands split in three bf16 parts and six products for
+// their 24 bits; bf16 ones the decode kernel with head_dim 64, passes of heads and other tiles.
+// Neither is built, and the shapes with many heads a KV head are that far from memory's time.
+// 4 x 50000 keys, 48 blocks a head: 41 us for 200 MB (fp32, head_dim 128, 8 KV heads of 2), 17 for
+// 100 MB (fp32, head_dim 64, 8 of 1: memory), 46 for 100 MB (fp32, head_dim 128, 4 of 16: the
+// latency of a tile's 4096 products a lane at two warps a scheduler), 25 for 25 MB (bf16, head_dim
+// 64, 4 of 16).
 #include <type_traits>
 
 #include "common.cuh"

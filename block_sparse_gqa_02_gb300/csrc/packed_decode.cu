@@ -18,12 +18,17 @@
 // of q, split in three parts (24 bits).  The row's power of two joins the softmax scale, so a
 // score is formed at up to 2^9 times a step and steps above 2^118 would overflow.
 // Outputs: p and the steps are fp16 (steps relative to the largest of their group that the warp
-// has met, times 2^10), and so is their product: roundings of 2^-11, an eighth of what bf16 would
-// cost; products below 2^-24 of the largest step lose digits.  The mid term is a bf16 MMA with
-// the mids as four more columns.
+// has met, times 2^10), and so is their product: two roundings of 2^-11 (a step's 8 bits are exact),
+// each an eighth of what bf16 would cost; products below 2^-24 of the largest step lose digits.  The
+// mid term is a bf16 MMA with the mids, which are bf16, as four more columns, and p rounded to
+// bf16: 2^-8 of each key's share, against a row sum of unrounded p.  Where V has channels with
+// offsets the mids carry most of the value, so this is the largest rounding of the call (fp16 has no
+// room for mids, whose range is bf16's).  The roundings of different keys are independent and add up
+// to less than the output's own to bf16: against fp64 the outputs of the measured cases are off as
+// much as fp32 sums rounded to bf16 are.
 // fp32 queries take the same kernel with q, p and p * step split in two fp16 parts (22 bits) and
-// the mid term's p in three of bf16, a product each: 24.9 us where bf16 takes 17.5 (8 x 128K, 16
-// heads a group); fp32 arithmetic on the CUDA cores took 158.
+// the mid term's p in three of bf16 (24 bits), a product each: 24.9 us where bf16 takes 17.5 (8 x
+// 128K, 16 heads a group); fp32 arithmetic on the CUDA cores took 158.
 //
 // CTA = one split of a (sequence, KV head), three groups of four warps that take its blocks in
 // turn, 32 keys a warp, each warp with a softmax base of its own that moves only when a row's

@@ -5,8 +5,8 @@
 // The angle is kept as a fraction of a turn in 64-bit fixed point: p * freqs[i] wraps modulo
 // one turn in integer arithmetic, exactly, so a position of a million loses nothing and no
 // slow range reduction is needed.  The fraction is reduced to an eighth of a turn around the
-// nearest quarter before it becomes an fp32 number (|x| <= 1/4 half turn, so its rounding is
-// at most 2^-27 half turns), and sine and cosine come from sincospif.
+// nearest quarter, cut to units of 2^-34 turns and becomes an fp32 number (|x| <= 1/4 half turn, so
+// its rounding is at most 2^-28 turns), and sine and cosine come from sincospif.
 //
 // A CTA takes a tile of tokens and heads of one tensor: it forms the tile's sines and cosines
 // once in shared memory (each is shared by the heads), then streams the tile with two 16-byte

@@ -242,8 +242,9 @@ msa_status msa_sparse_decode_paged(const msa_shape* shape, const int32_t* seq_le
  * dims from rotary_dim on are copied.  freqs holds turns per position in units of 2^-64
  * turns, so the product wraps at whole turns exactly and far positions lose nothing; any
  * scheme for long contexts (positions divided, base raised, ramped frequencies) is a choice
- * of freqs and scale.  Angles are exact to 2^-32 turns before the sine, products are fp32,
- * the result is rounded once to the dtype.
+ * of freqs and scale.  The sine takes the angle in fp32, reduced to an eighth of a turn: it is off
+ * by at most 2^-28 + 2^-34 turns (2^-25 radians); products are fp32, the result is rounded once to
+ * the dtype.
  *   positions   int32 [batch, seq], device; NULL: 0, 1, ..., seq - 1 in every sequence.
  *               With the cache lengths of a decode batch (seq = 1) and pos_offset = -1 the
  *               new tokens sit at the end of their caches, as long as nothing was evicted
