@@ -50,6 +50,12 @@ class MsaRopeTensor(ctypes.Structure):
                 ("rotary_dim", _i32), ("head_major", _i32)]
 
 
+class MsaCommitTensor(ctypes.Structure):
+    """Mirror of ``msa_commit_tensor``."""
+    _fields_ = [("src", _vp), ("dst", _vp), ("n_heads", _i32), ("row_bytes", _i32),
+                ("packed", _i32)]
+
+
 class MsaGatherTensor(ctypes.Structure):
     """Mirror of ``msa_gather_tensor``."""
     _fields_ = [("src", _vp), ("dst", _vp), ("src_rows", ctypes.c_int64),
@@ -84,6 +90,16 @@ SIGNATURES = {
                                _vp]),
     "msa_cache_gather": (_i32, [_i32, ctypes.POINTER(MsaGatherTensor), _i32, _vp, _i32, _i32,
                                 _vp]),
+    "msa_tree_mask": (_i32, [_SHAPE_P, _vp, _vp, _vp, _vp, _vp]),
+    "msa_index_pack": (_i32, [_SHAPE_P, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _vp]),
+    "msa_index_unpack": (_i32, [_SHAPE_P, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _vp]),
+    "msa_index_scores_tree": (_i32, [_SHAPE_P, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _vp,
+                                     _vp]),
+    "msa_block_topk_tree": (_i32, [_SHAPE_P, _vp, _vp, _vp, _vp, _vp]),
+    "msa_sparse_decode_tree": (_i32, [_SHAPE_P, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
+                                      _vp, _vp, _vp, _vp, _sz, _vp]),
+    "msa_tree_commit": (_i32, [_SHAPE_P, _vp, _vp, _i32, _vp, _i32,
+                               ctypes.POINTER(MsaCommitTensor), _i32, _vp, _vp]),
     "msa_workspace_bytes": (_sz, [_SHAPE_P, ctypes.c_int]),
     "msa_get_device_status": (_i32, [_vp]),
     "msa_status_string": (ctypes.c_char_p, [_i32]),
@@ -538,6 +554,174 @@ def msa_cache_gather(batch, tensors: GatherTensors, kept, block_size=128, stream
     _check(load().msa_cache_gather(int(batch), tensors.array, len(tensors),
                                    _arg(kept, "kept", _I32, 0, dev), kept.shape[1], int(block_size),
                                    st), "msa_cache_gather")
+
+
+# ------------------------------------------- decode over a tree of drafted tokens
+
+def msa_tree_mask(shape: MsaShape, seq_lens, parents, mask, positions=None, stream=None):
+    """mask: int64 [batch, tokens] (its bits are the library's 64-bit words)."""
+    dev, st = _place(stream)
+    batch = shape.batch
+    n = batch * shape.seq_q
+    _check(load().msa_tree_mask(
+        ctypes.byref(shape), _arg(seq_lens, "seq_lens", _I32, batch, dev, batch),
+        _arg(parents, "parents", _I32, n, dev, batch), _arg(mask, "mask", _I64, n, dev, batch),
+        _arg(positions, "positions", _I32, n, dev, batch), st), "msa_tree_mask")
+
+
+def _index_rows(call, where, shape, n, starts, seq_lens, block_table, n_phys, cache, x, stream):
+    """The arguments of index packing (cache last) and unpacking (cache before the rows)."""
+    dev, st = _place(stream)
+    n, n_phys = int(n), int(n_phys)
+    batch, d = shape.batch, shape.index_dim
+    c = _arg(cache, "cache", _U8, n_phys * 128 * (d + 1), dev, n_phys)
+    rows = _arg(x, "x", _FLOATS.get(shape.dtype), batch * n * d, dev, batch)
+    _check(call(ctypes.byref(shape), n, _arg(starts, "starts", _I32, batch, dev, batch),
+                _arg(seq_lens, "seq_lens", _I32, batch, dev, batch),
+                _arg(block_table, "block_table", _I32, batch * shape.n_blocks, dev, batch), n_phys,
+                *((rows, c) if where == "msa_index_pack" else (c, rows)), st), where)
+
+
+def msa_index_pack(shape: MsaShape, n_new, starts, seq_lens, block_table, n_phys, x, cache,
+                   stream=None):
+    _index_rows(load().msa_index_pack, "msa_index_pack", shape, n_new, starts, seq_lens, block_table,
+                n_phys, cache, x, stream)
+
+
+def msa_index_unpack(shape: MsaShape, n_out, starts, seq_lens, block_table, n_phys, cache, y,
+                     stream=None):
+    _index_rows(load().msa_index_unpack, "msa_index_unpack", shape, n_out, starts, seq_lens,
+                block_table, n_phys, cache, y, stream)
+
+
+def _tree_cache(shape, x, name, lead, d, block_table, n_phys, dtype, dev):
+    """A cache of rows of d: [batch, *lead, seq_k, d], or pools [n_phys, *lead, block, d]."""
+    if block_table is None:
+        return _arg(x, name, dtype, shape.batch * lead * shape.seq_k * d, dev, shape.batch)
+    return _arg(x, name, dtype, n_phys * lead * shape.block_size * d, dev, n_phys)
+
+
+def msa_index_scores_tree(shape: MsaShape, seq_lens, block_table, n_phys, mask, idx_q, idx_k,
+                          idx_draft, block_scores, packed=False, stream=None):
+    dev, st = _place(stream)
+    n_phys, packed = int(n_phys), int(packed)
+    batch, n, hkv, d, dt = (shape.batch, shape.seq_q, shape.n_heads_kv, shape.index_dim,
+                            _FLOATS.get(shape.dtype))
+    if packed:
+        rec = 128 * (d + 1)
+        k = _arg(idx_k, "idx_k", _U8, n_phys * rec, dev, n_phys)
+        kd = _arg(idx_draft, "idx_draft", _U8, batch * rec, dev, batch)
+    else:
+        k = _tree_cache(shape, idx_k, "idx_k", 1, d, block_table, n_phys, dt, dev)
+        kd = _arg(idx_draft, "idx_draft", dt, batch * n * d, dev, batch)
+    _check(load().msa_index_scores_tree(
+        ctypes.byref(shape), _arg(seq_lens, "seq_lens", _I32, batch, dev, batch),
+        _arg(block_table, "block_table", _I32, batch * shape.n_blocks, dev, batch), n_phys,
+        _arg(mask, "mask", _I64, batch * n, dev, batch),
+        _arg(idx_q, "idx_q", dt, batch * n * hkv * d, dev, batch), k, kd, packed,
+        _arg(block_scores, "block_scores", _F32, batch * hkv * n * shape.n_blocks, dev, batch), st),
+        "msa_index_scores_tree")
+
+
+def msa_block_topk_tree(shape: MsaShape, seq_lens, mask, block_scores, sel, stream=None):
+    dev, st = _place(stream)
+    batch, n = shape.batch, shape.seq_q
+    rows = batch * shape.n_heads_kv * n
+    _check(load().msa_block_topk_tree(
+        ctypes.byref(shape), _arg(seq_lens, "seq_lens", _I32, batch, dev, batch),
+        _arg(mask, "mask", _I64, batch * n, dev, batch),
+        _arg(block_scores, "block_scores", _F32, rows * shape.n_blocks, dev, batch),
+        _arg(sel, "sel", _I32, rows * shape.top_k, dev, batch), st), "msa_block_topk_tree")
+
+
+def msa_sparse_decode_tree(shape: MsaShape, seq_lens, block_table, n_phys, mask, q, k, v, k_draft,
+                           v_draft, sel, out, lse, workspace, ws_bytes=None, stream=None):
+    dev, st = _place(stream)
+    if ws_bytes is None:
+        ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    n_phys = int(n_phys)
+    batch, n, hq, hkv, d, dt = (shape.batch, shape.seq_q, shape.n_heads_q, shape.n_heads_kv,
+                                shape.head_dim, _FLOATS.get(shape.dtype))
+    rows = batch * n * hq * d
+    drafts = batch * hkv * n * d
+    _check(load().msa_sparse_decode_tree(
+        ctypes.byref(shape), _arg(seq_lens, "seq_lens", _I32, batch, dev, batch),
+        _arg(block_table, "block_table", _I32, batch * shape.n_blocks, dev, batch), n_phys,
+        _arg(mask, "mask", _I64, batch * n, dev, batch), _arg(q, "q", dt, rows, dev, batch),
+        _tree_cache(shape, k, "k", hkv, d, block_table, n_phys, dt, dev),
+        _tree_cache(shape, v, "v", hkv, d, block_table, n_phys, dt, dev),
+        _arg(k_draft, "k_draft", dt, drafts, dev, batch),
+        _arg(v_draft, "v_draft", dt, drafts, dev, batch),
+        _arg(sel, "sel", _I32, batch * hkv * n * shape.top_k, dev, batch),
+        _arg(out, "out", dt, rows, dev, batch), _arg(lse, "lse", _F32, batch * hq * n, dev, batch),
+        _arg(workspace, "workspace", None, 0, dev), ws_bytes, st), "msa_sparse_decode_tree")
+
+
+class CommitTensors:
+    """The caches of a msa_tree_commit call.  rows: (src, dst), src [batch, heads, tokens, d] or
+    [batch, tokens, d] (one head), dst with the cache's rows in place of the tokens (pools:
+    [n_phys, (heads,) block, d]).  packed: (src, dst) of 8-bit index keys, uint8 [batch, 128 (d + 1)]
+    and [n_phys, 128 (d + 1)].  Holds the tensors, and may be kept and used for every call."""
+
+    def __init__(self, rows, packed=()):
+        rows, packed = list(rows), list(packed)
+        self.device = dev = _device()
+        self.rows, self.packed = rows, packed
+        self.array = (MsaCommitTensor * max(1, len(rows) + len(packed)))()
+        self.shapes = []                     # (batch, tokens or None, first axis and rows of dst)
+        for i, (src, dst) in enumerate(rows):
+            heads = 1 if src.dim() == 3 else src.shape[1]
+            if src.dim() not in (3, 4) or dst.dim() != src.dim() or dst.dtype != src.dtype or \
+                    dst.shape[-1] != src.shape[-1] or (src.dim() == 4 and dst.shape[1] != heads):
+                raise ValueError(f"commit tensor {i}: src and dst differ in more than their rows: "
+                                 f"{tuple(src.shape)} and {tuple(dst.shape)}")
+            self.array[i] = MsaCommitTensor(
+                _arg(src, f"src of commit tensor {i}", None, 0, dev),
+                _arg(dst, f"dst of commit tensor {i}", None, 0, dev), heads,
+                src.shape[-1] * src.element_size(), 0)
+            self.shapes.append((src.shape[0], src.shape[-2], dst.shape[0], dst.shape[-2]))
+        for j, (src, dst) in enumerate(packed):
+            i = len(rows) + j
+            n = src.shape[-1]
+            if src.dim() != 2 or dst.dim() != 2 or dst.shape[1] != n or n % 128 or n < 256:
+                raise ValueError(f"commit tensor {i}: 8-bit index keys are [batch, 128 (d + 1)] and "
+                                 f"[n_phys, 128 (d + 1)], got {tuple(src.shape)} and {tuple(dst.shape)}")
+            self.array[i] = MsaCommitTensor(_arg(src, f"src of commit tensor {i}", _U8, 0, dev),
+                                            _arg(dst, f"dst of commit tensor {i}", _U8, 0, dev), 1,
+                                            n // 128 - 1, 1)
+            self.shapes.append((src.shape[0], None, dst.shape[0], 128))
+
+    def __len__(self):
+        return len(self.shapes)
+
+
+def make_commit_tensors(rows, packed=()) -> CommitTensors:
+    return CommitTensors(rows, packed)
+
+
+def msa_tree_commit(shape: MsaShape, seq_lens, block_table, n_phys, accepted,
+                    tensors: CommitTensors, new_lens, stream=None):
+    dev, st = _place(stream)
+    batch, n_phys = shape.batch, int(n_phys)
+    if tensors.device != dev:
+        raise ValueError(f"the commit tensors are on CUDA device {tensors.device}, the current one "
+                         f"is {dev}")
+    for i, (b, tokens, lead, rows) in enumerate(tensors.shapes):
+        if tokens is None:
+            want, have = (batch, n_phys), (b, lead)
+        elif block_table is None:
+            want, have = (batch, shape.seq_q, batch, shape.seq_k), (b, tokens, lead, rows)
+        else:
+            want, have = (batch, shape.seq_q, n_phys, shape.block_size), (b, tokens, lead, rows)
+        if want != have:
+            raise ValueError(f"commit tensor {i} has (batch, tokens, cache axes) {have}, the call {want}")
+    if accepted.dim() != 2 or accepted.shape[0] != batch:
+        raise ValueError(f"accepted is {tuple(accepted.shape)}, expected [{batch}, tokens]")
+    _check(load().msa_tree_commit(
+        ctypes.byref(shape), _arg(seq_lens, "seq_lens", _I32, batch, dev, batch),
+        _arg(block_table, "block_table", _I32, batch * shape.n_blocks, dev, batch), n_phys,
+        _arg(accepted, "accepted", _I32, 0, dev), accepted.shape[1], tensors.array, len(tensors),
+        _arg(new_lens, "new_lens", _I32, batch, dev, batch), st), "msa_tree_commit")
 
 
 def msa_workspace_bytes(shape: MsaShape, which: int) -> int:

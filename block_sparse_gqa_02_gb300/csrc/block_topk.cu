@@ -11,6 +11,7 @@
 // selected blocks are then compacted in index order, which writes them ascending without
 // a sort.  Bit-exact and deterministic.
 #include "common.cuh"
+#include "tree.cuh"
 
 namespace msa {
 
@@ -71,7 +72,12 @@ __global__ void __launch_bounds__(kThreads) block_topk_kernel(const float* __res
   const int m = row % p.nR;
   const int b = shared ? row / p.nR : row / (p.Hkv * p.nR);
   // ragged decode: the query of sequence b sits at its own cache length - 1
-  const int last = p.seq_lens ? seq_len_of(p, b) - 1 : row_last_pos(p, m);
+  int last = p.seq_lens ? seq_len_of(p, b) - 1 : row_last_pos(p, m);
+  if (p.tree_mask) {                                        // row m: a drafted token, or none
+    const int L = seq_len_of(p, b);
+    const TreeWord path = tree_path(p, b, m, L);
+    last = path ? tree_pos(path, L) : -1;
+  }
   const float* srow = scores + (size_t)row * p.nB;
   int32_t* out = sel + (size_t)row * p.k;
   const size_t head_stride = (size_t)p.nR * p.nB;           // between heads, same (b, m)

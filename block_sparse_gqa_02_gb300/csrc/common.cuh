@@ -26,6 +26,8 @@ struct Dims {
   const int32_t* seq_lens;
   const int32_t* block_table;
   int n_phys;
+  // a tree of nR drafted tokens a sequence (null elsewhere): the tokens' paths [B, nR]
+  const unsigned long long* tree_mask;
 };
 
 // ------------------------------------------------------------ debug checks
@@ -181,6 +183,27 @@ cudaError_t launch_cache_evict(const Dims& p, int keep, int n_first, int n_recen
                                cudaStream_t st);
 cudaError_t launch_cache_gather(int batch, const msa_gather_tensor* tensors, int n,
                                 const int32_t* kept, int keep, int block, cudaStream_t st);
+
+// A decode step over a tree of drafted tokens (tree.cu, index_cache.cu, tree_scores.cu,
+// tree_decode.cu); p.block_table may be null.
+cudaError_t launch_tree_mask(const Dims& p, const int32_t* parents, unsigned long long* mask,
+                             int32_t* positions, cudaStream_t st);
+cudaError_t launch_tree_commit(const Dims& p, const int32_t* accepted, int n_accept,
+                               const msa_commit_tensor* tensors, int n, int32_t* new_lens,
+                               cudaStream_t st);
+cudaError_t launch_index_pack(const Dims& p, int n, const int32_t* starts, const void* x,
+                              void* cache, cudaStream_t st);
+cudaError_t launch_index_unpack(const Dims& p, int n, const int32_t* starts, const void* cache,
+                                void* x, cudaStream_t st);
+// packed: idx_k and idx_draft hold the 8-bit records, else rows of p.dtype
+cudaError_t launch_index_scores_tree(const Dims& p, const void* idx_q, const void* idx_k,
+                                     const void* idx_draft, int packed, float* scores,
+                                     cudaStream_t st, int* dev_status);
+cudaError_t launch_sparse_decode_tree(const Dims& p, const void* q, const void* k, const void* v,
+                                      const void* k_draft, const void* v_draft,
+                                      const int32_t* sel, void* out, float* lse, float* ws,
+                                      cudaStream_t st, int* dev_status);
+size_t tree_workspace_bytes(const Dims& p);
 
 // Largest candidate count the top-k kernel keeps in shared memory.
 constexpr int kMaxBlocks = 32768;

@@ -5,6 +5,7 @@
 // which msa_get_device_status() reports as MSA_ERR_BOUNDS; nothing traps, and the kernels
 // that follow skip out-of-range entries as they always do.
 #include "common.cuh"
+#include "tree.cuh"
 
 namespace msa {
 
@@ -17,7 +18,12 @@ __global__ void validate_sel_kernel(const int32_t* __restrict__ sel, Dims p, int
   for (long long row = blockIdx.x * (long long)blockDim.x + threadIdx.x; row < rows;
        row += (long long)gridDim.x * blockDim.x) {
     const int b = (int)(row / ((long long)p.Hkv * p.nR));
-    const int n_blocks = p.seq_lens ? (seq_len_of(p, b) + p.Bk - 1) / p.Bk : p.nB;
+    int n_blocks = p.seq_lens ? (seq_len_of(p, b) + p.Bk - 1) / p.Bk : p.nB;
+    if (p.tree_mask) {                                     // up to the token's own block
+      const int L = seq_len_of(p, b);
+      const TreeWord path = tree_path(p, b, (int)(row % p.nR), L);
+      n_blocks = path ? tree_pos(path, L) / p.Bk + 1 : 0;
+    }
     const int32_t* r = sel + row * p.k;
     for (int i = 0; i < p.k; ++i) {
       const int e = r[i];

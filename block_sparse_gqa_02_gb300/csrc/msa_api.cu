@@ -6,6 +6,7 @@
 #include <string.h>
 
 #include "common.cuh"
+#include "index_cache.cuh"
 #include "index_tc.cuh"
 #include "msa.h"
 
@@ -110,6 +111,7 @@ msa_status make_dims(const msa_shape* s, Dims* d) {
   d->seq_lens = nullptr;
   d->block_table = nullptr;
   d->n_phys = 0;
+  d->tree_mask = nullptr;
   return MSA_OK;
 }
 
@@ -690,8 +692,270 @@ msa_status msa_cache_gather(int32_t batch, const msa_gather_tensor* tensors, int
   return e == cudaSuccess ? MSA_OK : cuda_fail(e, "msa_cache_gather launch");
 }
 
+// ------------------------------------------------- decode over a tree of drafted tokens
+
+namespace {
+// A tree's shape: that of a decode step but for seq_q = tokens.
+msa_status make_tree_shape(const msa_shape* shape, Dims* d) {
+  if (!shape) return fail(MSA_ERR_INVALID_ARG, "shape is NULL");
+  if (shape->seq_q < 1 || shape->q_tile != 1)
+    return fail(MSA_ERR_INVALID_ARG, "a tree's shape has seq_q >= 1 tokens and q_tile 1 (got %d, %d)",
+                shape->seq_q, shape->q_tile);
+  if (shape->seq_q > MSA_TREE_MAX_TOKENS)
+    return fail(MSA_ERR_UNSUPPORTED, "%d tokens in a tree: at most %d", shape->seq_q,
+                MSA_TREE_MAX_TOKENS);
+  msa_shape one = *shape;
+  one.seq_q = 1;
+  MSA_TRY(make_dims(&one, d));
+  d->Sq = d->nR = shape->seq_q;
+  return MSA_OK;
+}
+
+msa_status make_tree_dims(const msa_shape* shape, const int32_t* seq_lens, const uint64_t* mask,
+                          Dims* d) {
+  MSA_TRY(make_tree_shape(shape, d));
+  MSA_TRY(check_ptr(seq_lens, "seq_lens"));
+  d->seq_lens = seq_lens;
+  if (mask) {
+    MSA_TRY(check_ptr(mask, "mask"));
+    d->tree_mask = reinterpret_cast<const unsigned long long*>(mask);
+  }
+  return MSA_OK;
+}
+
+msa_status set_tree_table(const int32_t* block_table, int32_t n_phys, bool packed, Dims* d) {
+  MSA_TRY(check_ptr(block_table, "block_table", true));
+  if (block_table && n_phys < 1) return fail(MSA_ERR_INVALID_ARG, "n_phys must be >= 1");
+  if (!block_table && packed && (long long)d->B * d->nB != n_phys)
+    return fail(MSA_ERR_INVALID_ARG,
+                "without a block_table n_phys (%d) must be batch * n_blocks = %lld", n_phys,
+                (long long)d->B * d->nB);
+  d->block_table = block_table;
+  d->n_phys = n_phys;
+  return MSA_OK;
+}
+
+msa_status make_index_dims(const msa_shape* shape, const int32_t* seq_lens,
+                           const int32_t* block_table, int32_t n_phys, Dims* d) {
+  if (!shape) return fail(MSA_ERR_INVALID_ARG, "shape is NULL");
+  msa_shape one = *shape;
+  one.seq_q = one.q_tile = 1;
+  MSA_TRY(make_dims(&one, d));
+  if (d->Bk != kIndexBlock)
+    return fail(MSA_ERR_UNSUPPORTED, "the 8-bit index cache holds blocks of 128 keys (got %d)", d->Bk);
+  MSA_TRY(check_ptr(seq_lens, "seq_lens", true));
+  if (n_phys < 1) return fail(MSA_ERR_INVALID_ARG, "n_phys must be >= 1");
+  MSA_TRY(set_tree_table(block_table, n_phys, true, d));
+  d->seq_lens = seq_lens;
+  return MSA_OK;
+}
+}  // namespace
+
+msa_status msa_tree_mask(const msa_shape* shape, const int32_t* seq_lens, const int32_t* parents,
+                         uint64_t* mask, int32_t* positions, void* stream) {
+  g_last_error[0] = 0;
+  Dims d;
+  MSA_TRY(make_tree_dims(shape, seq_lens, nullptr, &d));
+  MSA_TRY(check_ptr(parents, "parents"));
+  MSA_TRY(check_ptr(mask, "mask"));
+  MSA_TRY(check_ptr(positions, "positions", true));
+  {
+    const cudaError_t ve = launch_debug_validate(d, nullptr, (cudaStream_t)stream, status_ptr());
+    if (ve != cudaSuccess) return cuda_fail(ve, "msa_tree_mask debug validation");
+  }
+  cudaError_t e = launch_tree_mask(d, parents, reinterpret_cast<unsigned long long*>(mask),
+                                   positions, (cudaStream_t)stream);
+  return e == cudaSuccess ? MSA_OK : cuda_fail(e, "msa_tree_mask launch");
+}
+
+msa_status msa_index_pack(const msa_shape* shape, int32_t n_new, const int32_t* starts,
+                          const int32_t* seq_lens, const int32_t* block_table, int32_t n_phys,
+                          const void* x, void* cache, void* stream) {
+  g_last_error[0] = 0;
+  Dims d;
+  MSA_TRY(make_index_dims(shape, seq_lens, block_table, n_phys, &d));
+  if (n_new < 1) return fail(MSA_ERR_INVALID_ARG, "n_new must be >= 1 (got %d)", n_new);
+  MSA_TRY(check_ptr(starts, "starts", true));
+  MSA_TRY(check_ptr(x, "x"));
+  MSA_TRY(check_ptr(cache, "cache"));
+  {
+    const cudaError_t ve = launch_debug_validate(d, nullptr, (cudaStream_t)stream, status_ptr());
+    if (ve != cudaSuccess) return cuda_fail(ve, "msa_index_pack debug validation");
+  }
+  cudaError_t e = launch_index_pack(d, n_new, starts, x, cache, (cudaStream_t)stream);
+  return e == cudaSuccess ? MSA_OK : cuda_fail(e, "msa_index_pack launch");
+}
+
+msa_status msa_index_unpack(const msa_shape* shape, int32_t n_out, const int32_t* starts,
+                            const int32_t* seq_lens, const int32_t* block_table, int32_t n_phys,
+                            const void* cache, void* y, void* stream) {
+  g_last_error[0] = 0;
+  Dims d;
+  MSA_TRY(make_index_dims(shape, seq_lens, block_table, n_phys, &d));
+  if (n_out < 1) return fail(MSA_ERR_INVALID_ARG, "n_out must be >= 1 (got %d)", n_out);
+  MSA_TRY(check_ptr(starts, "starts", true));
+  MSA_TRY(check_ptr(cache, "cache"));
+  MSA_TRY(check_ptr(y, "y"));
+  {
+    const cudaError_t ve = launch_debug_validate(d, nullptr, (cudaStream_t)stream, status_ptr());
+    if (ve != cudaSuccess) return cuda_fail(ve, "msa_index_unpack debug validation");
+  }
+  cudaError_t e = launch_index_unpack(d, n_out, starts, cache, y, (cudaStream_t)stream);
+  return e == cudaSuccess ? MSA_OK : cuda_fail(e, "msa_index_unpack launch");
+}
+
+msa_status msa_index_scores_tree(const msa_shape* shape, const int32_t* seq_lens,
+                                 const int32_t* block_table, int32_t n_phys, const uint64_t* mask,
+                                 const void* idx_q, const void* idx_k, const void* idx_draft,
+                                 int32_t packed, float* block_scores, void* stream) {
+  g_last_error[0] = 0;
+  Dims d;
+  if (packed != 0 && packed != 1) return fail(MSA_ERR_INVALID_ARG, "packed must be 0 or 1");
+  MSA_TRY(check_ptr(mask, "mask"));
+  MSA_TRY(make_tree_dims(shape, seq_lens, mask, &d));
+  MSA_TRY(set_tree_table(block_table, n_phys, packed, &d));
+  if (packed && d.Bk != kIndexBlock)
+    return fail(MSA_ERR_UNSUPPORTED, "the 8-bit index cache holds blocks of 128 keys (got %d)", d.Bk);
+  if (d.Hkv > 64) return fail(MSA_ERR_UNSUPPORTED, "%d KV heads: at most 64", d.Hkv);
+  MSA_TRY(check_ptr(idx_q, "idx_q"));
+  MSA_TRY(check_ptr(idx_k, "idx_k"));
+  MSA_TRY(check_ptr(idx_draft, "idx_draft"));
+  MSA_TRY(check_ptr(block_scores, "block_scores"));
+  {
+    const cudaError_t ve = launch_debug_validate(d, nullptr, (cudaStream_t)stream, status_ptr());
+    if (ve != cudaSuccess) return cuda_fail(ve, "msa_index_scores_tree debug validation");
+  }
+  cudaError_t e = launch_index_scores_tree(d, idx_q, idx_k, idx_draft, packed, block_scores,
+                                           (cudaStream_t)stream, status_ptr());
+  return e == cudaSuccess ? MSA_OK : cuda_fail(e, "msa_index_scores_tree launch");
+}
+
+msa_status msa_block_topk_tree(const msa_shape* shape, const int32_t* seq_lens,
+                               const uint64_t* mask, const float* block_scores, int32_t* sel,
+                               void* stream) {
+  g_last_error[0] = 0;
+  Dims d;
+  MSA_TRY(check_ptr(mask, "mask"));
+  MSA_TRY(make_tree_dims(shape, seq_lens, mask, &d));
+  MSA_TRY(check_ptr(block_scores, "block_scores"));
+  MSA_TRY(check_ptr(sel, "sel"));
+  {
+    const cudaError_t ve = launch_debug_validate(d, nullptr, (cudaStream_t)stream, status_ptr());
+    if (ve != cudaSuccess) return cuda_fail(ve, "msa_block_topk_tree debug validation");
+  }
+  cudaError_t e = launch_block_topk(d, block_scores, sel, (cudaStream_t)stream);
+  return e == cudaSuccess ? MSA_OK : cuda_fail(e, "msa_block_topk_tree launch");
+}
+
+msa_status msa_sparse_decode_tree(const msa_shape* shape, const int32_t* seq_lens,
+                                  const int32_t* block_table, int32_t n_phys, const uint64_t* mask,
+                                  const void* q, const void* k, const void* v, const void* k_draft,
+                                  const void* v_draft, const int32_t* sel, void* out, float* lse,
+                                  void* workspace, size_t ws_bytes, void* stream) {
+  g_last_error[0] = 0;
+  Dims d;
+  MSA_TRY(check_ptr(mask, "mask"));
+  MSA_TRY(make_tree_dims(shape, seq_lens, mask, &d));
+  MSA_TRY(set_tree_table(block_table, n_phys, false, &d));
+  if (d.G > 64) return fail(MSA_ERR_UNSUPPORTED, "decode needs n_heads_q / n_heads_kv <= 64");
+  MSA_TRY(check_ptr(q, "q"));
+  MSA_TRY(check_ptr(k, "k"));
+  MSA_TRY(check_ptr(v, "v"));
+  MSA_TRY(check_ptr(k_draft, "k_draft"));
+  MSA_TRY(check_ptr(v_draft, "v_draft"));
+  MSA_TRY(check_ptr(sel, "sel"));
+  MSA_TRY(check_ptr(out, "out"));
+  MSA_TRY(check_ptr(lse, "lse", true));
+  MSA_TRY(check_ptr(workspace, "workspace"));
+  const size_t need = tree_workspace_bytes(d);
+  if (ws_bytes < need)
+    return fail(MSA_ERR_INVALID_ARG, "workspace of %zu bytes is too small: need %zu", ws_bytes,
+                need);
+  {
+    const cudaError_t ve = launch_debug_validate(d, sel, (cudaStream_t)stream, status_ptr());
+    if (ve != cudaSuccess) return cuda_fail(ve, "msa_sparse_decode_tree debug validation");
+  }
+  cudaError_t e = launch_sparse_decode_tree(d, q, k, v, k_draft, v_draft, sel, out, lse,
+                                            static_cast<float*>(workspace), (cudaStream_t)stream,
+                                            status_ptr());
+  return e == cudaSuccess ? MSA_OK : cuda_fail(e, "msa_sparse_decode_tree launch");
+}
+
+msa_status msa_tree_commit(const msa_shape* shape, const int32_t* seq_lens,
+                           const int32_t* block_table, int32_t n_phys, const int32_t* accepted,
+                           int32_t n_accept, const msa_commit_tensor* tensors, int32_t n_tensors,
+                           int32_t* new_lens, void* stream) {
+  g_last_error[0] = 0;
+  Dims d;
+  MSA_TRY(make_tree_dims(shape, seq_lens, nullptr, &d));
+  if (!tensors) return fail(MSA_ERR_INVALID_ARG, "tensors is NULL");
+  if (n_tensors < 1 || n_tensors > MSA_COMMIT_MAX_TENSORS)
+    return fail(MSA_ERR_INVALID_ARG, "n_tensors must be in [1, %d] (got %d)",
+                MSA_COMMIT_MAX_TENSORS, n_tensors);
+  if (n_accept < 1 || n_accept > MSA_TREE_MAX_TOKENS)
+    return fail(MSA_ERR_INVALID_ARG, "n_accept must be in [1, %d] (got %d)", MSA_TREE_MAX_TOKENS,
+                n_accept);
+  MSA_TRY(set_tree_table(block_table, n_phys, true, &d));
+  MSA_TRY(check_ptr(accepted, "accepted"));
+  MSA_TRY(check_ptr(new_lens, "new_lens"));
+  // buffers of the call: [start, bytes) of lengths, list and table, then sources and destinations
+  struct Span { __int128 at, bytes; const char* name; };
+  Span in[3 + MSA_COMMIT_MAX_TENSORS], out[1 + MSA_COMMIT_MAX_TENSORS];
+  int n_in = 0, n_out = 0;
+  auto span = [](const void* ptr, __int128 bytes, const char* name) {
+    return Span{(__int128)(uintptr_t)ptr, bytes, name};
+  };
+  in[n_in++] = span(accepted, (__int128)d.B * n_accept * 4, "accepted");
+  if (new_lens != seq_lens) in[n_in++] = span(seq_lens, (__int128)d.B * 4, "seq_lens");
+  if (block_table) in[n_in++] = span(block_table, (__int128)d.B * d.nB * 4, "block_table");
+  out[n_out++] = span(new_lens, (__int128)d.B * 4, "new_lens");
+  for (int i = 0; i < n_tensors; ++i) {
+    const msa_commit_tensor& t = tensors[i];
+    MSA_TRY(check_ptr(t.src, "src"));
+    MSA_TRY(check_ptr(t.dst, "dst"));
+    if (t.packed != 0 && t.packed != 1)
+      return fail(MSA_ERR_INVALID_ARG, "tensor %d: packed must be 0 or 1", i);
+    if (t.n_heads < 1 || t.row_bytes < 16)
+      return fail(MSA_ERR_INVALID_ARG, "tensor %d: n_heads must be >= 1, row_bytes >= 16", i);
+    if (t.row_bytes % 16 != 0 || (long long)t.n_heads * t.row_bytes > (1 << 24))
+      return fail(MSA_ERR_UNSUPPORTED, "tensor %d: row_bytes %d: a multiple of 16, with %d heads "
+                  "at most 2^24", i, t.row_bytes, t.n_heads);
+    if (t.packed && (t.n_heads != 1 || (t.row_bytes != 64 && t.row_bytes != 128) ||
+                     d.Bk != kIndexBlock))
+      return fail(MSA_ERR_UNSUPPORTED, "tensor %d: 8-bit index keys have one head of 64 or 128 "
+                  "bytes and blocks of 128 keys", i);
+    const __int128 one = (__int128)t.n_heads * t.row_bytes;
+    const __int128 rec = (__int128)kIndexBlock * (t.row_bytes + 1);
+    in[n_in++] = span(t.src, t.packed ? d.B * rec : one * d.B * d.nR, "src");
+    out[n_out++] = span(t.dst, t.packed ? n_phys * rec
+                                        : one * (block_table ? (__int128)n_phys * d.Bk
+                                                             : (__int128)d.B * d.Sk), "dst");
+  }
+  for (int i = 0; i < n_out; ++i) {
+    auto clash = [&](const Span& o) {
+      return out[i].at < o.at + o.bytes && o.at < out[i].at + out[i].bytes;
+    };
+    for (int j = 0; j < n_in; ++j)
+      if (clash(in[j]))
+        return fail(MSA_ERR_INVALID_ARG, "%s (output %d) overlaps %s", out[i].name, i, in[j].name);
+    for (int j = 0; j < i; ++j)
+      if (clash(out[j]))
+        return fail(MSA_ERR_INVALID_ARG, "%s (output %d) overlaps %s", out[i].name, i, out[j].name);
+  }
+  // new_lens in place of seq_lens: still clear of the caches (checked above as an output)
+  {
+    const cudaError_t ve = launch_debug_validate(d, nullptr, (cudaStream_t)stream, status_ptr());
+    if (ve != cudaSuccess) return cuda_fail(ve, "msa_tree_commit debug validation");
+  }
+  cudaError_t e = launch_tree_commit(d, accepted, n_accept, tensors, n_tensors, new_lens,
+                                     (cudaStream_t)stream);
+  return e == cudaSuccess ? MSA_OK : cuda_fail(e, "msa_tree_commit launch");
+}
+
 size_t msa_workspace_bytes(const msa_shape* shape, int which) {
   Dims d;
+  if (which == 5)                                          // a tree's shape is no other call's
+    return make_tree_shape(shape, &d) == MSA_OK && d.G <= 64 ? tree_workspace_bytes(d) : 0;
   if (make_dims(shape, &d) != MSA_OK) return 0;
   if (which == 1 && d.decode) return decode_workspace_bytes(d);
   if (which == 2 && !d.decode) return backward_workspace_bytes(d);

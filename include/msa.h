@@ -394,9 +394,123 @@ typedef struct msa_gather_tensor {
 msa_status msa_cache_gather(int32_t batch, const msa_gather_tensor* tensors, int32_t n_tensors,
                             const int32_t* kept, int32_t keep, int32_t block_size, void* stream);
 
+/* ---------------------------------------------------- decode over a tree of drafted tokens
+ * Checks several drafted tokens of every sequence in one step: the caches are read once for all
+ * of them.  The drafts of a sequence form a forest of up to MSA_TREE_MAX_TOKENS tokens; token i's
+ * parent is an earlier token or, for -1, the last cached token.  mask [batch, n_tokens] is the
+ * tree in bits: bit a of mask[b, i] is set when token a is on the path from the root to i, i
+ * among them; 0 (or any word without bit i) means that the sequence has no token i.  With the
+ * cache length L_b (drafts not counted) and depth = bits of mask[b, i] - 1, token i is at position
+ * L_b + depth.  It sees the cached keys j < L_b and the keys of its path, each in the block of
+ * its position: what a decode step would give it with its path appended to the cache.
+ *
+ * shape: seq_q = n_tokens (1 .. 64), q_tile = 1, seq_k the capacity of the caches (with a block
+ * table: n_blocks = ceil(seq_k / block_size) entries a sequence); a token at a position of seq_k
+ * or more counts as absent.  Arrays over tokens have them as the shape's seq_q:
+ *   q, out [batch, n_tokens, n_heads_q, head_dim], idx_q [batch, n_tokens, n_heads_kv, index_dim],
+ *   k_draft, v_draft [batch, n_heads_kv, n_tokens, head_dim], lse [batch, n_heads_q, n_tokens],
+ *   block_scores [batch, n_heads_kv, n_tokens, n_blocks], sel [batch, n_heads_kv, n_tokens, top_k].
+ * Absent tokens get scores -inf, sel -1, out 0, lse -inf, and nothing of theirs is used, whatever
+ * it holds.  seq_lens int32 [batch] (device) is needed; lengths are clamped to [0, seq_k].
+ * block_table NULL: the caches are contiguous (n_phys is read for 8-bit index keys only); else
+ * pools of n_phys blocks, as in the paged calls.  Table entries outside [0, n_phys) cause no fault
+ * and meaningless output.  Cached keys and values, and those of the tree's tokens, must be finite;
+ * rows past the lengths may hold anything. */
+#define MSA_TREE_MAX_TOKENS 64
+
+/* The tree's masks from parents int32 [batch, n_tokens], and (positions may be NULL) the tokens'
+ * positions int32 [batch, n_tokens], -1 for absent ones.  A token is absent when its parent is not
+ * in [-1, i), or is absent. */
+msa_status msa_tree_mask(const msa_shape* shape, const int32_t* seq_lens, const int32_t* parents,
+                         uint64_t* mask, int32_t* positions, void* stream);
+
+/* Index keys in 8 bits: 128 * (index_dim + 1) bytes for a block of 128 keys against 256 * index_dim
+ * in bf16.  Every key (row) has a power of two of its own: with amax its largest magnitude
+ *   e = the least integer >= -126 with amax <= 448 * 2^e
+ *   code = x * 2^-e rounded to nearest even to the 8-bit float of 4 exponent and 3 fraction bits
+ *   value = code * 2^e                                (what the cache holds; exact in bf16)
+ * |value - x| <= max(2^-4 |x|, 2^(e - 10)).  A row with a NaN or an infinity is stored as NaN; it
+ * gives its block an unspecified score.  Values of 2^128 or more (amax above 1.9375 * 2^127) read
+ * back as infinity.
+ * cache   uint8 [n_phys, 128 * (index_dim + 1)], 16-byte aligned.  One record:
+ *   [0, 128 d)        codes of key j, dim i at j * d + i            (d = index_dim)
+ *   [128 d, 128 d + 128)  e + 127 of key j (255: the NaN row)
+ * With a block_table logical block j of sequence b is physical block block_table[b, j]; without
+ * one it is b * n_blocks + j, and n_phys must be batch * n_blocks.
+ * shape: of any step over this cache (batch, seq_k, index_dim, block_size = 128 and dtype matter).
+ * x, y: [batch, n, index_dim] of the shape's dtype.  Token i of sequence b is at position
+ * starts[b] + i, or, with starts NULL, at seq_lens[b] - n + i; positions outside [0, seq_lens[b])
+ * are not stored, and their rows of y are left as they are.  seq_lens NULL: every length is
+ * seq_k.  Only the stored tokens' bytes change. */
+msa_status msa_index_pack(const msa_shape* shape, int32_t n_new, const int32_t* starts,
+                          const int32_t* seq_lens, const int32_t* block_table, int32_t n_phys,
+                          const void* x, void* cache, void* stream);
+msa_status msa_index_unpack(const msa_shape* shape, int32_t n_out, const int32_t* starts,
+                            const int32_t* seq_lens, const int32_t* block_table, int32_t n_phys,
+                            const void* cache, void* y, void* stream);
+
+/* msa_index_scores for the tokens of a tree, each for itself: the maximum over the keys it sees
+ * of every block, -inf for a block without one.  At most 64 KV heads.
+ *   packed = 1: idx_k is the 8-bit cache above, idx_draft uint8 [batch, 128 * (index_dim + 1)] the
+ *               drafts' keys in one record a sequence, token i its row i (msa_index_pack with
+ *               seq_k = n_tokens, starts and seq_lens NULL); block_size 128;
+ *   packed = 0: idx_k of the shape's dtype, [batch, seq_k, index_dim] or pools [n_phys, block_size,
+ *               index_dim]; idx_draft [batch, n_tokens, index_dim].
+ * Products are exact and accumulated in fp32 (bf16 queries of 128 dims against 8-bit keys take
+ * two 8-bit parts that hold all of a dim's digits unless it is 2^-10 of the query's largest or
+ * less: those are off by at most 2^-18 of the largest). */
+msa_status msa_index_scores_tree(const msa_shape* shape, const int32_t* seq_lens,
+                                 const int32_t* block_table, int32_t n_phys, const uint64_t* mask,
+                                 const void* idx_q, const void* idx_k, const void* idx_draft,
+                                 int32_t packed, float* block_scores, void* stream);
+
+/* msa_block_topk for the tokens of a tree: the block of the token's position, and the best
+ * top_k - 1 of those before it. */
+msa_status msa_block_topk_tree(const msa_shape* shape, const int32_t* seq_lens,
+                               const uint64_t* mask, const float* block_scores, int32_t* sel,
+                               void* stream);
+
+/* Attention of the tree's tokens: msa_sparse_decode for each, over the keys it sees in its selected
+ * blocks.  k, v: [batch, n_heads_kv, seq_k, head_dim], or pools [n_phys, n_heads_kv, block_size,
+ * head_dim].  lse may be NULL.  Entries of sel outside [0, the token's own block] are skipped;
+ * entries must be distinct.  At most 64 query heads per KV head.  bf16 in blocks of 128 runs on
+ * the tensor cores, which read a block once for the tokens (256 query heads of a KV head at a
+ * time) that selected it.  workspace: msa_workspace_bytes(shape, 5) bytes, 16-byte aligned. */
+msa_status msa_sparse_decode_tree(const msa_shape* shape, const int32_t* seq_lens,
+                                  const int32_t* block_table, int32_t n_phys, const uint64_t* mask,
+                                  const void* q, const void* k, const void* v, const void* k_draft,
+                                  const void* v_draft, const int32_t* sel, void* out, float* lse,
+                                  void* workspace, size_t ws_bytes, void* stream);
+
+/* Moves the accepted tokens' rows into the caches: row accepted[b, i] of every source goes to
+ * position seq_lens[b] + i, and new_lens[b] = seq_lens[b] + the number of them.  accepted int32
+ * [batch, n_accept] (n_accept at most 64): a sequence's list ends at its first entry outside [0,
+ * n_tokens), or where the cache is full.  Nothing else in the caches changes.  new_lens may be
+ * seq_lens itself.  Up to MSA_COMMIT_MAX_TENSORS caches a call:
+ *   packed = 0: src [batch, n_heads, n_tokens, row_bytes]; dst [batch, n_heads, seq_k, row_bytes],
+ *               or with a block_table pools [n_phys, n_heads, block_size, row_bytes];
+ *   packed = 1: 8-bit index keys (n_heads 1, row_bytes = index_dim 64 or 128, block_size 128):
+ *               src one record a sequence, dst the cache.
+ * row_bytes: a multiple of 16; n_heads * row_bytes at most 2^24.  Without a block_table n_phys must
+ * be batch * n_blocks.  A position whose table entry is outside [0, n_phys) is not stored.  No dst
+ * may overlap another buffer of the call.  tensors is a host array, read before the call returns. */
+#define MSA_COMMIT_MAX_TENSORS 8
+typedef struct msa_commit_tensor {
+  const void* src;
+  void* dst;
+  int32_t n_heads;
+  int32_t row_bytes;
+  int32_t packed;
+} msa_commit_tensor;
+msa_status msa_tree_commit(const msa_shape* shape, const int32_t* seq_lens,
+                           const int32_t* block_table, int32_t n_phys, const int32_t* accepted,
+                           int32_t n_accept, const msa_commit_tensor* tensors, int32_t n_tensors,
+                           int32_t* new_lens, void* stream);
+
 /* Scratch bytes msa_sparse_prefill (which = 0), msa_sparse_decode (which = 1),
- * msa_sparse_prefill_backward (which = 2), msa_index_kl_loss (which = 3) or
- * msa_sparse_decode_mass (which = 4) needs for this shape; 0 when none.  Returns 0 for an
+ * msa_sparse_prefill_backward (which = 2), msa_index_kl_loss (which = 3),
+ * msa_sparse_decode_mass (which = 4) or msa_sparse_decode_tree (which = 5, a tree's shape) needs
+ * for this shape; 0 when none.  Returns 0 for an
  * invalid shape. */
 size_t msa_workspace_bytes(const msa_shape* shape, int which);
 

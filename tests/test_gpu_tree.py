@@ -1,0 +1,308 @@
+"""Decode over a tree of drafted tokens: every call against the fp64 oracle."""
+import numpy as np
+import pytest
+import torch
+
+from block_sparse_gqa_02_gb300 import _lib
+from oracle import tree_ops
+from tests.canary import guarded_like
+from tests.tree_cases import DTYPES, Tree, random_parents
+
+pytestmark = pytest.mark.gpu
+
+
+def _ok():
+    _lib.msa_get_device_status()
+
+
+# -------------------------------------------------------------------------- paths
+
+@pytest.mark.parametrize("n", [1, 2, 31, 32, 33, 63, 64])
+@pytest.mark.parametrize("kind", ["chain", "tree", "bad", "star"])
+def test_mask(n, kind):
+    rng = np.random.default_rng(n)
+    lens, cap = [0, 5, 970, 1000, 999], 1000
+    parents = random_parents(rng, 5, n, kind)
+    shape = _lib.make_shape(5, n, cap, 4, 4, 128, 128, 128, 1, 1)
+    mask, pos = guarded_like((5, n), torch.int64), guarded_like((5, n), torch.int32)
+    lens_t = torch.tensor(lens, dtype=torch.int32).cuda()
+    _lib.msa_tree_mask(shape, lens_t, torch.tensor(parents, dtype=torch.int32).cuda(), mask.tensor,
+                       pos.tensor)
+    _ok()
+    for b in range(5):
+        want = tree_ops.paths(parents[b], lens[b], cap)
+        got = [x % (1 << 64) for x in mask.tensor[b].tolist()]
+        assert got == [tree_ops.word(p) for p in want]
+        assert pos.tensor[b].tolist() == [lens[b] + len(p) - 1 if p else -1 for p in want]
+    mask.check("mask")
+    pos.check("positions")
+    _lib.msa_tree_mask(shape, lens_t, torch.tensor(parents, dtype=torch.int32).cuda(), mask.tensor)
+
+
+# ------------------------------------------------------------- 8-bit index keys
+
+def _special(x):
+    """Rows of zeros, one large value, tiny ones, the ends of the range, not finite ones."""
+    x = x.clone()
+    flat = x.view(-1, x.shape[-1])
+    for r, fill in enumerate([0.0, 2.0 ** -130, 3e38, 448.0, 450.0]):
+        if r < flat.shape[0]:
+            flat[r] = flat[r] * 0 + fill
+    if flat.shape[0] > 8:
+        flat[5, 3] = float("inf")
+        flat[6, 0] = float("nan")
+        flat[7] *= 2.0 ** -120
+        flat[8, 1] = 1e30
+    return x
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("idim", [64, 128])
+@pytest.mark.parametrize("n,cap,paged,starts", [
+    (1, 1, False, None), (1, 700, True, None), (130, 1000, True, [0, 127, 869, 500]),
+    (333, 333, False, [0, 0, 0, 0]), (700, 640, True, [-100, 3, 600, 639]), (64, 64, False, None)])
+def test_index_pack(dtype, idim, n, cap, paged, starts):
+    B, nB = 4, -(-cap // 128)
+    g = torch.Generator().manual_seed(n)
+    dt = DTYPES[dtype]
+    lens = [cap, max(0, cap - 1), cap // 2, 0]
+    x = _special((torch.randn(B, n, idim, generator=g) * torch.randn(B, n, 1, generator=g).exp()).to(dt))
+    shape = _lib.make_shape(B, 1, cap, 4, 4, 128, idim, 128, 1, 1, dtype)
+    n_phys = B * nB + 2 * paged
+    perm = torch.randperm(n_phys, generator=g)[:B * nB].view(B, nB)
+    table = perm.to(torch.int32).cuda() if paged else None
+    where = perm if paged else torch.arange(B * nB).view(B, nB)
+    rec = 128 * (idim + 1)
+    before = torch.randint(0, 256, (n_phys, rec), generator=g, dtype=torch.uint8)
+    cache = guarded_like((n_phys, rec), torch.uint8)
+    cache.tensor.copy_(before)
+    lens_t = torch.tensor(lens, dtype=torch.int32).cuda()
+    starts_t = torch.tensor(starts, dtype=torch.int32).cuda() if starts else None
+    args = starts_t, lens_t, table, n_phys
+    _lib.msa_index_pack(shape, n, *args, x.cuda(), cache.tensor)
+    out = guarded_like((B, n, idim), dt, fill=7.0)
+    _lib.msa_index_unpack(shape, n, *args, cache.tensor, out.tensor)
+    _ok()
+    codes, exps, val = tree_ops.quantise(x.float().numpy())
+    want, want_out = before.clone(), torch.full((B, n, idim), 7.0, dtype=torch.float64)
+    for b in range(B):
+        first = starts[b] if starts else lens[b] - n
+        for i in range(n):
+            pos = first + i
+            if not 0 <= pos < lens[b]:
+                continue
+            r = want[int(where[b, pos // 128])]
+            j = pos % 128
+            r[j * idim:(j + 1) * idim] = torch.tensor(codes[b, i])
+            r[128 * idim + j] = int(exps[b, i])
+            want_out[b, i] = torch.tensor(val[b, i])
+    got = cache.tensor.cpu()
+    # a zero's sign is kept too, so the bytes are equal; NaN rows hold NaN codes of either sign
+    assert torch.equal(got, want)
+    y = out.tensor.cpu().double()
+    assert torch.equal(torch.isnan(y), torch.isnan(want_out))
+    want_out = want_out.to(dt).double()            # 2^128 and above, and below the type's range
+    fine = ~torch.isnan(want_out)
+    assert torch.equal(y[fine], want_out[fine])
+    cache.check("cache")
+    out.check("rows")
+
+
+def test_index_pack_skips_bad_table_entries():
+    B, cap, idim = 2, 256, 128
+    shape = _lib.make_shape(B, 1, cap, 4, 4, 128, idim, 128, 1, 1)
+    table = torch.tensor([[0, 5], [-1, 2 ** 31 - 1]], dtype=torch.int32).cuda()
+    cache = guarded_like((3, 129 * 128), torch.uint8, fill=9)
+    x = torch.randn(B, cap, idim, device="cuda").bfloat16()
+    _lib.msa_index_pack(shape, cap, None, None, table, 3, x, cache.tensor)
+    y = torch.full_like(x, 5.0)
+    _lib.msa_index_unpack(shape, cap, None, None, table, 3, cache.tensor, y)
+    torch.cuda.synchronize()
+    assert (cache.tensor[1:] == 9).all() and not (cache.tensor[0] == 9).all()
+    assert (y[0, 128:] == 5).all() and (y[1] == 5).all() and not (y[0, :128] == 5).all()
+    cache.check()
+
+
+# ------------------------------------------------------------------ index scores
+
+SCORES = [
+    # the tensor-core form's shapes: lengths inside, at and past block ends; one token to 64
+    dict(lens=[0, 1, 127, 128], n=5, cap=300),
+    dict(lens=[1000, 129, 1023, 1024], n=16, cap=1100, paged=True),
+    dict(lens=[5000], n=1, cap=5001),
+    dict(lens=[3000, 17], n=64, cap=3100, kind="chain"),
+    dict(lens=[700, 250], n=64, cap=800, kind="bad", paged=True),
+    dict(lens=[100, 2000, 120], n=33, cap=2100, hkv=8, kind="chain", paged=True),
+    dict(lens=[600, 120], n=64, cap=700, hkv=8),
+    dict(lens=[600], n=7, cap=700, hkv=1),
+    dict(lens=[640, 640], n=9, cap=645, hkv=2, kind="chain"),           # the drafts fill the cache
+    dict(lens=[200] * 33, n=3, cap=260, hkv=3),
+    # 16-bit keys
+    dict(lens=[0, 1, 127, 128], n=5, cap=300, packed=False),
+    dict(lens=[1000, 129, 1023, 1024], n=16, cap=1100, packed=False, paged=True),
+    dict(lens=[2000, 20], n=64, cap=2100, kind="chain", packed=False),
+    dict(lens=[600, 100], n=64, cap=700, hkv=8, packed=False, kind="bad"),
+    # other dims, types and blocks
+    dict(lens=[700, 0, 130], n=6, cap=800, idim=64),
+    dict(lens=[700, 0, 130], n=6, cap=800, dtype="f32", paged=True),
+    dict(lens=[300, 64], n=40, cap=400, idim=64, packed=False, block=32, kind="chain"),
+    dict(lens=[300, 64], n=9, cap=400, dtype="f32", packed=False, block=200, paged=True),
+    dict(lens=[30, 4], n=20, cap=60, dtype="bf16", packed=False, block=1, kind="chain", paged=True),
+]
+
+
+@pytest.mark.parametrize("c", SCORES, ids=lambda c: "-".join(f"{k}{v if k != 'lens' else len(v)}" for k, v in c.items()))
+def test_scores(c):
+    t = Tree(seed=len(c["lens"]) * 100 + c["n"], **c)
+    s = t.shape
+    out = guarded_like((s.batch, s.n_heads_kv, t.n, t.nB), torch.float32)
+    d = t.dev
+    _lib.msa_index_scores_tree(s, t.seq_lens, t.table, t.n_phys, t.mask, d["iq"], d["ik"], d["ikd"],
+                               out.tensor, packed=t.packed)
+    _ok()
+    got, want = out.tensor.cpu().double().numpy(), t.scores()
+    assert np.array_equal(np.isneginf(got), np.isneginf(want))
+    assert not np.isnan(got).any()
+    fine = np.isfinite(want)
+    err = np.abs(np.where(fine, got, 0) - np.where(fine, want, 0))
+    assert (err <= t.score_bound() + 2.0 ** -23 * np.abs(np.where(fine, want, 0))).all(), err.max()
+    out.check("scores")
+
+
+# --------------------------------------------------------------------- selection
+
+@pytest.mark.parametrize("c,topk", [
+    (dict(lens=[1000, 129, 0, 1023], n=16, cap=1100), 3), (dict(lens=[900], n=64, cap=1000, kind="chain"), 1),
+    (dict(lens=[900, 5], n=20, cap=1000, kind="bad", hkv=2), 20), (dict(lens=[20], n=9, cap=40, block=2, packed=False, kind="chain"), 5),
+    (dict(lens=[300000], n=2, cap=300100, hkv=1, group=1, dim=64, idim=64), 64)])
+def test_selection(c, topk):
+    t = Tree(seed=3, topk=topk, **c)
+    s = t.shape
+    rng = np.random.default_rng(1)
+    x = rng.integers(-4, 4, (s.batch, s.n_heads_kv, t.n, t.nB)).astype(np.float32)   # many ties
+    x[rng.random(x.shape) < 0.1] = -np.inf
+    x[rng.random(x.shape) < 0.1] = -0.0
+    sel = guarded_like((s.batch, s.n_heads_kv, t.n, topk), torch.int32)
+    _lib.msa_block_topk_tree(s, t.seq_lens, t.mask, torch.tensor(x).cuda(), sel.tensor)
+    _ok()
+    for b in range(s.batch):
+        for h in range(s.n_heads_kv):
+            for i, path in enumerate(t.paths[b]):
+                pos = t.lens[b] + len(path) - 1 if path else -1
+                assert sel.tensor[b, h, i].tolist() == tree_ops.select(x[b, h, i], pos, s.block_size, topk)
+    sel.check("sel")
+
+
+# --------------------------------------------------------------------- attention
+
+ATTEND = [
+    dict(lens=[0, 1, 127, 128], n=5, cap=300),
+    dict(lens=[1000, 129, 1023, 1024], n=16, cap=1100, paged=True, topk=6),
+    dict(lens=[3000], n=1, cap=3001, topk=24),
+    dict(lens=[1500, 17], n=64, cap=1600, kind="chain", topk=5, sel_frac=0.6),
+    dict(lens=[700, 250], n=64, cap=800, kind="bad", paged=True, hkv=2),
+    dict(lens=[1990, 100], n=8, cap=2000, kind="star", topk=9, sel_frac=0.7),
+    dict(lens=[600], n=7, cap=700, hkv=1, group=1),
+    dict(lens=[600, 90], n=40, cap=700, hkv=2, group=5, kind="chain"),
+    dict(lens=[600], n=33, cap=700, hkv=2, group=33, paged=True),
+    dict(lens=[500], n=3, cap=600, hkv=1, group=64),
+    dict(lens=[640, 640], n=9, cap=645, hkv=2, kind="chain", topk=2),
+    dict(lens=[200] * 20, n=3, cap=260, hkv=8, group=2, topk=1),
+    dict(lens=[1200, 0], n=24, cap=1300, hkv=4, group=8, topk=300),
+    dict(lens=[900], n=12, cap=1000, topk=4, key_scale=12.0),            # peaked rows, rescaled often
+    dict(lens=[900, 140], n=20, cap=1000, dim=64, group=8, kind="chain"),
+    dict(lens=[900, 140], n=6, cap=1000, dtype="f32", group=16, paged=True),
+    dict(lens=[300, 64], n=40, cap=400, dtype="f32", dim=64, group=3, packed=False, block=32, kind="chain"),
+    dict(lens=[300, 64], n=9, cap=400, packed=False, block=200, paged=True, group=4),
+    dict(lens=[30, 4], n=20, cap=60, packed=False, block=1, kind="chain", paged=True, topk=30, group=2),
+]
+
+
+@pytest.mark.parametrize("c", ATTEND, ids=lambda c: "-".join(f"{k}{v if k != 'lens' else len(v)}" for k, v in c.items()))
+def test_attention(c):
+    t = Tree(seed=len(c["lens"]) * 100 + c["n"], **c)
+    s, d = t.shape, t.dev
+    out = guarded_like((s.batch, t.n, s.n_heads_q, s.head_dim), t.dt)
+    lse = guarded_like((s.batch, s.n_heads_q, t.n), torch.float32)
+    ws = guarded_like((_lib.msa_workspace_bytes(s, 5) // 4,), torch.float32)
+    args = (s, t.seq_lens, t.table, t.n_phys, t.mask, d["q"], d["k"], d["v"], d["kd"], d["vd"], d["sel"])
+    _lib.msa_sparse_decode_tree(*args, out.tensor, lse.tensor, ws.tensor)
+    _ok()
+    want, want_lse, tol, tol_lse = t.attend()
+    got, got_lse = out.tensor.cpu().double().numpy(), lse.tensor.cpu().double().numpy()
+    assert np.array_equal(np.isneginf(got_lse), np.isneginf(want_lse))
+    assert np.isfinite(got).all()
+    err = np.abs(got - want)
+    assert (err <= tol).all(), (err.max(), (err / np.maximum(tol, 1e-30)).max())
+    fine = np.isfinite(want_lse)
+    err = np.abs(np.where(fine, got_lse, 0) - np.where(fine, want_lse, 0))
+    assert (err <= tol_lse).all(), err.max()
+    for x in (out, lse, ws):
+        x.check()
+    # without lse, and again: the same bits
+    again = torch.empty_like(out.tensor)
+    _lib.msa_sparse_decode_tree(*args, again, None, ws.tensor)
+    torch.cuda.synchronize()
+    assert torch.equal(again, out.tensor)
+
+
+# ------------------------------------------------------------------------ commit
+
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_commit(paged, in_place, dtype):
+    t = Tree(lens=[0, 126, 290, 300, 255], n=11, cap=300, paged=paged, kind="star", hkv=3, group=1, dim=64, dtype=dtype)
+    s, d = t.shape, t.dev
+    accepted = [[3, 4, 10, -1, 2], [0, 0, 7, 7, 1], [5, 4, 3, 2, 1], [1, 2, 3, 4, 5], [-1, 3, 4, 5, 6]]
+    counts = [3, 5, 5, 0, 0]
+    acc = torch.tensor(accepted, dtype=torch.int32).cuda()
+    names = [("kd", "k"), ("vd", "v"), ("ikd", "ik")]
+    before = {n: d[n].clone() for _, n in names}
+    guards = {}
+    for _, n in names:
+        guards[n] = guarded_like(d[n].shape, d[n].dtype)
+        guards[n].tensor.copy_(d[n])
+    lens = t.seq_lens.clone()
+    new = lens if in_place else torch.full_like(lens, -5)
+    rows = [(d[a], guards[b].tensor) for a, b in names[:2]]
+    tensors = _lib.make_commit_tensors(rows, [(d["ikd"], guards["ik"].tensor)])
+    _lib.msa_tree_commit(s, lens, t.table, t.n_phys, acc, tensors, new)
+    _ok()
+    assert new.tolist() == [t.lens[b] + counts[b] for b in range(5)]
+    want = {n: x.clone() for n, x in before.items()}
+    for b in range(5):
+        for i in range(counts[b]):
+            pos, a = t.lens[b] + i, accepted[b][i]
+            phys = int(t.phys[b, pos // 128])
+            for src, dst in names[:2]:
+                if paged:
+                    want[dst][phys, :, pos % 128] = d[src][b, :, a]
+                else:
+                    want[dst][b, :, pos] = d[src][b, :, a]
+            r, q = want["ik"][phys], d["ikd"][b]
+            j = pos % 128
+            r[j * 128:(j + 1) * 128] = q[a * 128:(a + 1) * 128]
+            r[128 * 128 + j] = q[128 * 128 + a]
+    for _, n in names:
+        assert torch.equal(guards[n].tensor.view(torch.uint8), want[n].view(torch.uint8)), n
+        guards[n].check(n)
+
+
+def test_commit_bad_table_entry_and_long_lists():
+    n = 64
+    shape = _lib.make_shape(2, n, 512, 4, 4, 64, 128, 128, 1, 1)
+    src = torch.randn(2, 4, n, 64, device="cuda").bfloat16()
+    pool = guarded_like((5, 4, 128, 64), torch.bfloat16, fill=2.0)
+    table = torch.tensor([[3, 9, -1, 2 ** 30], [0, 1, 2, 4]], dtype=torch.int32).cuda()
+    acc = torch.arange(n, dtype=torch.int32).repeat(2, 1).cuda()
+    lens = torch.tensor([100, 470], dtype=torch.int32).cuda()
+    new = torch.zeros_like(lens)
+    _lib.msa_tree_commit(shape, lens, table, 5, acc, _lib.make_commit_tensors([(src, pool.tensor)]), new)
+    torch.cuda.synchronize()
+    assert new.tolist() == [164, 512]
+    want = torch.full_like(pool.tensor, 2.0)
+    want[3, :, 100:] = src[0, :, :28]
+    want[4, :, 86:] = src[1, :, :42]
+    assert torch.equal(pool.tensor, want)
+    pool.check()
