@@ -1,6 +1,503 @@
-// No shape runs on the tensor cores yet.
+// Index scores of drafted tokens on the tcgen05 tensor cores (bf16 queries, index_dim 128, blocks
+// of 128 keys, 8-bit or 16-bit index keys): every token's index queries against every cached index
+// key, max-pooled per block, and against the keys of its path.
+//
+// The scan is to be bound by HBM: a key is read once for all tokens, 129 bytes in 8 bits.  Each CTA
+// streams a contiguous range of one sequence's blocks through a TMA ring; one thread issues a
+// block's products with the 128 keys as M and the columns (token, head) as N, so that the cost
+// follows the number of tokens.  8-bit keys are operands as they lie in the cache: a key's scale is
+// a power of two of its own and is applied to the products.  The queries keep their precision by
+// being split in two 8-bit parts, x 2^-e = hi + lo, each rounded to 4 significant bits: a bf16 value
+// has 8, so the two hold it exactly while lo's last bit is 2^-9 or more, that is for dims of at
+// least 2^-10 of the query's largest; a smaller one is off by at most 2^-10 of the 448 that the
+// largest is scaled to.  Both parts accumulate in the same TMEM columns.
+//
+// Eight epilogue warps read the accumulator as fragments of 16 keys x 8 columns, in which a thread
+// holds four keys of a column: scale, maximum over the four, then over the lanes by halving (4
+// shuffles for 16 columns).  Eight blocks' maxima collect in shared memory before they are written,
+// 32 bytes of a score row at a time.
+// Warps: 0-7 epilogue (TMEM lane quadrant warp % 4, every other 16 columns), 8 TMA producer, 9 MMA
+// issuer.  Every wait is bounded.
+#include "index_cache.cuh"
+#include "launch.cuh"
+#include "ptx.cuh"
+#include "tma_host.cuh"
+#include "tree.cuh"
 #include "tree_scores_tc.cuh"
+
 namespace msa {
-bool tree_scores_tc_supported(const Dims&) { return false; }
-cudaError_t launch_tree_scores_tc(const Dims&, const void*, const void*, const void*, int, float*, cudaStream_t, int*) { return cudaErrorNotSupported; }
+
+namespace {
+
+constexpr int kBk = 128, kDI = 128, kRowBytes = 128;
+constexpr int kEpiWarps = 8;
+constexpr int kEpiThreads = kEpiWarps * 32;
+constexpr int kProducerWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = 10 * 32;
+constexpr int kMaxCols = 256;          // UMMA N
+constexpr int kMaxStages = 10;
+constexpr int kSmemLimit = 232448;
+
+// The small part of shared memory; the ring, the queries and the results lie before it.
+struct Small {
+  TreeWord path[64];
+  TreeWord late;                       // tokens whose position is in the block after the first's
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t acc_full[2], acc_empty[2];
+  int b, blk0, nblk, rank, cnt;        // the CTA's range, and its place among the sequence's CTAs
+  uint32_t tmem_base;
+  int abort;
+};
+
+// Bytes of each part, all multiples of 16; cols: padded to 16.
+struct Plan {
+  int cols, stages, stage_bytes;
+  __host__ __device__ int q_at() const { return stages * stage_bytes; }
+  __host__ __device__ int ex_at() const { return q_at() + cols * 2 * kRowBytes; }
+  __host__ __device__ int res_at() const { return ex_at() + stages * kBk; }
+  __host__ __device__ int res_row() const { return cols + 4; }          // spreads the banks
+  __host__ __device__ int dres_at() const { return res_at() + 32 * res_row() * 4; }
+  __host__ __device__ int scale_at() const { return dres_at() + 8 * cols * 4; }
+  __host__ __device__ int row_at() const { return scale_at() + cols * 4; }
+  __host__ __device__ int small_at() const { return row_at() + cols * 4; }
+  __host__ __device__ int bytes() const { return small_at() + (int)sizeof(Small); }
+};
+
+__device__ __forceinline__ void raise_abort(Small& s, int* status, int code) {
+  s.abort = 1;
+  if (status) atomicExch(status, code);
 }
+
+__device__ __forceinline__ void epi_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory");
+}
+
+// The CTA's blocks: the CTAs are shared out in proportion to the sequences' block counts, each
+// sequence getting at least one.  One warp.
+__device__ __forceinline__ void find_range(const Dims& p, Small& s, int lane) {
+  const int ctas = gridDim.x, c = blockIdx.x;              // ctas >= p.B
+  if (lane == 0) {                                         // nothing, where every sequence is empty
+    s.b = p.B - 1;
+    s.blk0 = s.nblk = 0;
+    s.rank = s.cnt = 1;
+  }
+  __syncwarp();
+  long long total = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    long long nb = b0 + lane < p.B ? (seq_len_of(p, b0 + lane) + kBk - 1) / kBk : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) nb += __shfl_xor_sync(0xffffffffu, nb, o);
+    total += nb;
+  }
+  if (total < 1) total = 1;
+  long long before = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int b = b0 + lane;
+    const int nb = b < p.B ? (seq_len_of(p, b) + kBk - 1) / kBk : 0;
+    long long incl = nb;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const long long prefix = before + incl - nb;
+    const int lo = b + (int)((ctas - p.B) * prefix / total);
+    const int hi = b + 1 + (int)((ctas - p.B) * (prefix + nb) / total);
+    if (b < p.B && c >= lo && c < hi) {                    // one lane of all
+      const int cnt = hi - lo, per = (nb + cnt - 1) / cnt;
+      s.b = b;
+      s.rank = c - lo;
+      s.cnt = cnt;
+      s.blk0 = min(nb, s.rank * per);
+      s.nblk = min(nb - s.blk0, per);
+    }
+    before += __shfl_sync(0xffffffffu, incl, 31);
+  }
+}
+
+// Maximum over lane / 4 of four values a lane, of columns 2 (lane % 4) + {0, 1, 8, 9}; the lane
+// returns that of column frag_col(lane).
+__device__ __forceinline__ int frag_col(int lane) {
+  return (lane & 16 ? 8 : 0) + 2 * (lane & 3) + (lane & 8 ? 1 : 0);
+}
+__device__ __forceinline__ float frag_max(const float (&v)[4], int lane) {
+  const bool u16 = lane & 16, u8 = lane & 8;
+  const float a = __shfl_xor_sync(0xffffffffu, u16 ? v[0] : v[2], 16);
+  const float b = __shfl_xor_sync(0xffffffffu, u16 ? v[1] : v[3], 16);
+  const float x = fmaxf(u16 ? v[2] : v[0], a), y = fmaxf(u16 ? v[3] : v[1], b);
+  const float c = __shfl_xor_sync(0xffffffffu, u8 ? x : y, 8);
+  const float z = fmaxf(u8 ? y : x, c);
+  return fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 4));
+}
+
+template <bool kPacked>
+__global__ void __launch_bounds__(kThreads, 1)
+tree_scores_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_d,
+                      const __nv_bfloat16* __restrict__ iq, const uint8_t* __restrict__ cache,
+                      const uint8_t* __restrict__ drafts, float* __restrict__ scores, Dims p,
+                      Plan plan, int per_group, uint32_t tmem_cols, int* status) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint8_t* qs = smem + plan.q_at();
+  uint8_t* ex = smem + plan.ex_at();
+  float* res = reinterpret_cast<float*>(smem + plan.res_at());     // [quadrant][8 blocks][cols]
+  float* dres = reinterpret_cast<float*>(smem + plan.dres_at());   // [2 blocks][quadrant][cols]
+  float* qscale = reinterpret_cast<float*>(smem + plan.scale_at());
+  int* rows = reinterpret_cast<int*>(smem + plan.row_at());        // score row of a column
+  Small& s = *reinterpret_cast<Small*>(smem + plan.small_at());
+  ptx::grid_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+  const int node0 = blockIdx.y * per_group;
+  const int n_nodes = min(per_group, p.nR - node0);
+  const int C = n_nodes * p.Hkv, Cp = plan.cols, stages = plan.stages;
+  const volatile int* abort = &s.abort;
+
+  if (warp == 0) find_range(p, s, lane);
+  if (tid == 32) {
+    for (int i = 0; i < stages; ++i) {
+      ptx::mbar_init(&s.full[i], 1);
+      ptx::mbar_init(&s.empty[i], kPacked ? 1 + kEpiWarps : 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&s.acc_full[i], 1);
+      ptx::mbar_init(&s.acc_empty[i], kEpiWarps);
+    }
+    s.abort = 0;
+    s.late = 0;
+    ptx::fence_barrier_init();
+  }
+  if (warp == 2) {
+    ptx::tmem_alloc(&s.tmem_base, tmem_cols);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before_sync();
+  __syncthreads();
+  ptx::tc_fence_after_sync();
+  const uint32_t tmem = s.tmem_base;
+  const int b = s.b, blk0 = s.blk0, nblk = s.nblk;
+  const int L = seq_len_of(p, b);
+  const int nB_b = (L + kBk - 1) / kBk;                    // blocks with cached keys
+  const int first = L / kBk;                               // block of the first drafted position
+  // the sequence's last range takes the drafted keys too, before its blocks
+  const int drafted = blk0 + nblk == nB_b && (nblk > 0 || s.rank == 0) ? 1 : 0;
+  const int items = nblk + drafted;
+  if (tid < 64) {
+    const TreeWord path = tid < p.nR ? tree_path(p, b, tid, L) : 0;
+    s.path[tid] = path;
+    if (path && tree_pos(path, L) / kBk == first + 1) atomicOr(&s.late, 1ull << tid);
+  }
+  __syncthreads();
+
+  if (warp == kProducerWarp) {
+    // ------------------------------------------------------------- TMA producer
+    int issued = 0;
+    bool ok = true;
+    if (lane == 0) ptx::tma_prefetch_desc(&tm_k);
+    for (int i = 0; i < items; ++i) {
+      const int st = i % stages;
+      if (p.inject == 2 && s.rank == 0 && i > 0) break;     // test hook: no copies any more
+      if (!ptx::mbar_wait(&s.empty[st], ((i / stages) & 1) ^ 1, abort)) { ok = false; break; }
+      if (lane == 0) {
+        uint8_t* to = smem + st * plan.stage_bytes;
+        const bool draft = drafted && i == 0;
+        const CUtensorMap* tm = draft ? &tm_d : &tm_k;
+        const int blk = blk0 + i - drafted;
+        ptx::mbar_arrive_expect_tx(&s.full[st], plan.stage_bytes + (kPacked ? kBk : 0));
+        int y = 0, z = b;                                  // row and outer index of the tile
+        if (!draft) {
+          if (p.block_table) z = p.block_table[(size_t)b * p.nB + blk];
+          else if (kPacked) z = b * p.nB + blk;
+          else y = blk * kBk;
+          debug_check(blk >= 0 && blk < nB_b && z >= 0 &&
+                          z < (p.block_table || kPacked ? p.n_phys : p.B),
+                      status, kDbgCoord);
+        }
+        if (kPacked) {
+          ptx::tma_load_3d(to, tm, &s.full[st], 0, 0, z);
+          // a table entry that is no block: zeros for the codes, some block's exponents
+          const int zc = draft ? z : min(max(z, 0), p.n_phys - 1);
+          ptx::bulk_load(ex + st * kBk, (draft ? drafts : cache) + (size_t)zc * index_record(kDI) + kBk * kDI,
+                         kBk, &s.full[st]);
+        } else {
+          ptx::tma_load_3d(to, tm, &s.full[st], 0, y, z);
+          ptx::tma_load_3d(to + kBk * kRowBytes, tm, &s.full[st], 64, y, z);
+        }
+      }
+      issued = i + 1;
+      __syncwarp();
+    }
+    if (!ok && lane == 0) raise_abort(s, status, 0x501);
+    // copies in flight land before the CTA leaves (after a full run they have been used)
+    if (lane == 0)
+      for (int i = issued > stages ? issued - stages : 0; i < issued; ++i)
+        ptx::mbar_wait_timed(&s.full[i % stages], (i / stages) & 1);
+  } else {
+    // ---- the queries as the B operand, K-major with the 128-byte swizzle (16-byte unit u of row c
+    // lies at unit u ^ (c % 8)); a warp a column
+    const int wq = warp > kProducerWarp ? warp - 1 : warp;
+    for (int c = wq; c < Cp; c += kThreads / 32 - 1) {
+      const int node = node0 + c / p.Hkv;
+      const bool there = c < C && s.path[node] != 0;
+      uint2 w = make_uint2(0, 0);                          // dims 4 lane .. 4 lane + 3
+      if (there)
+        w = *reinterpret_cast<const uint2*>(iq + (((size_t)b * p.nR + node0) * p.Hkv + c) * kDI + lane * 4);
+      float scale = p.index_scale;
+      if (kPacked) {
+        float x[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
+                      __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u)};
+        uint32_t amax = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) amax = max(amax, __float_as_uint(x[e]) & 0x7fffffffu);
+        amax = __reduce_max_sync(0xffffffffu, amax);
+        const uint32_t byte = index_exponent(amax);
+        const float inv = pow2_byte(254 - byte);
+        scale *= pow2_byte(byte);
+        uint32_t hi[2], lo[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float x0 = x[2 * e] * inv, x1 = x[2 * e + 1] * inv;
+          hi[e] = e4m3_pair(x0, x1);
+          const float2 h = from_e4m3_pair(hi[e]);
+          lo[e] = e4m3_pair(x0 - h.x, x1 - h.y);
+        }
+        uint8_t* to = qs + c * kRowBytes + (((lane >> 2) ^ (c & 7)) << 4) + (lane & 3) * 4;
+        *reinterpret_cast<uint32_t*>(to) = hi[0] | hi[1] << 16;
+        *reinterpret_cast<uint32_t*>(to + Cp * kRowBytes) = lo[0] | lo[1] << 16;
+      } else {
+        const int u = lane >> 1;                           // 16-byte unit of the 256-byte row
+        uint8_t* to = qs + (u >> 3) * Cp * kRowBytes + c * kRowBytes + (((u & 7) ^ (c & 7)) << 4) +
+                      (lane & 1) * 8;
+        *reinterpret_cast<uint2*>(to) = w;
+      }
+      if (lane == 0) {
+        qscale[c] = scale;
+        // -1: a column of no token, whose scores are -inf
+        rows[c] = c < C ? (b * p.Hkv + c % p.Hkv) * p.nR + node : -1;
+      }
+    }
+    // blocks that no key of this sequence can be in: its CTAs share them out
+    const int f0 = min(p.nB, first + 2);
+    for (int c = s.rank * (kThreads / 32 - 1) + wq; c < C; c += s.cnt * (kThreads / 32 - 1)) {
+      float* to = scores + (size_t)((b * p.Hkv + c % p.Hkv) * p.nR + node0 + c / p.Hkv) * p.nB;
+      for (int e = f0 + lane; e < p.nB; e += 32) to[e] = -INFINITY;
+    }
+    ptx::fence_proxy_async_smem();
+    asm volatile("bar.sync 2, %0;" ::"n"(kThreads - 32) : "memory");
+
+    if (warp == kMmaWarp) {
+      // ----------------------------------------------------------- MMA issuer
+      int issued = 0;
+      bool ok = true;
+      const uint32_t q0 = ptx::smem_u32(qs);
+      const uint32_t idesc = kPacked ? ptx::idesc_e4m3_f32(kBk, Cp) : ptx::idesc_bf16_f32(kBk, Cp);
+      for (int i = 0; i < items; ++i) {
+        const int st = i % stages, buf = i & 1;
+        if (!ptx::mbar_wait(&s.full[st], (i / stages) & 1, abort) ||
+            !ptx::mbar_wait(&s.acc_empty[buf], ((i >> 1) & 1) ^ 1, abort)) { ok = false; break; }
+        ptx::tc_fence_after_sync();
+        if (lane == 0) {
+          const uint32_t a0 = ptx::smem_u32(smem + st * plan.stage_bytes);
+          const uint32_t d = tmem + buf * Cp;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            // 8-bit: hi over the keys' 128 dims, then lo over the same; 16-bit: two halves of dims
+            const uint32_t q = q0 + (kk >> 2) * Cp * kRowBytes + (kk & 3) * 32;
+            if (kPacked)
+              ptx::umma_f8_ss(d, ptx::smem_desc_k_sw128(a0 + (kk & 3) * 32), ptx::smem_desc_k_sw128(q),
+                              idesc, kk > 0 ? 1u : 0u);
+            else
+              ptx::umma_bf16_ss(d, ptx::smem_desc_k_sw128(a0 + (kk >> 2) * kBk * kRowBytes + (kk & 3) * 32),
+                                ptx::smem_desc_k_sw128(q), idesc, kk > 0 ? 1u : 0u);
+          }
+          ptx::umma_commit(&s.empty[st]);
+          ptx::umma_commit(&s.acc_full[buf]);
+        }
+        issued = i + 1;
+        __syncwarp();
+      }
+      if (!ok && lane == 0) raise_abort(s, status, 0x502);
+      if (*abort && lane == 0 && issued > 0)
+        ptx::mbar_wait_timed(&s.acc_full[(issued - 1) & 1], ((issued - 1) >> 1) & 1);
+    } else {
+      // ------------------------------------------------------------- epilogue
+      const int quad = warp & 3, gr = lane >> 2;
+      bool ok = true;
+      int g0 = blk0;                                       // first block of the group of eight
+      for (int i = 0; i < items; ++i) {
+        const int buf = i & 1, st = i % stages;
+        const bool draft = drafted && i == 0;
+        const int blk = blk0 + i - drafted;
+        if (ok && !ptx::mbar_wait(&s.acc_full[buf], (i >> 1) & 1, abort)) ok = false;
+        if (ok) {
+          ptx::tc_fence_after_sync();
+          float sc[4] = {1.f, 1.f, 1.f, 1.f};
+          if (kPacked) {
+            ok = ptx::mbar_wait(&s.full[st], (i / stages) & 1, abort);   // the copy's own barrier
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sc[r] = pow2_byte(ex[st * kBk + quad * 32 + r * 8 + gr]);
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&s.empty[st]);
+          }
+          const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + buf * Cp;
+          const int seen = L - blk * kBk - quad * 32;      // keys of this warp's 32 (blocks only)
+          for (int c0 = (warp >> 2) * 16; c0 < Cp; c0 += 32) {
+            uint32_t a[8], d[8];                           // keys 0-15 and 16-31 of the quadrant
+            ptx::tmem_ld_frag16(at + c0, a);
+            ptx::tmem_ld_frag16(at + (16u << 16) + c0, d);
+            ptx::tmem_ld_wait();
+            float x[4][4];                                 // [key gr + 8 r][column]
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int e = (j >> 1) * 4 + (j & 1);
+              x[0][j] = __uint_as_float(a[e]) * sc[0];
+              x[1][j] = __uint_as_float(a[e + 2]) * sc[1];
+              x[2][j] = __uint_as_float(d[e]) * sc[2];
+              x[3][j] = __uint_as_float(d[e + 2]) * sc[3];
+            }
+            if (!draft) {
+              if (seen < 32) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                  for (int j = 0; j < 4; ++j)
+                    if (gr + 8 * r >= seen) x[r][j] = -INFINITY;
+              }
+              float v[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                v[j] = fmaxf(fmaxf(x[0][j], x[1][j]), fmaxf(x[2][j], x[3][j]));
+              const float top = frag_max(v, lane);
+              if (!(lane & 4))
+                res[(quad * 8 + (blk & 7)) * plan.res_row() + c0 + frag_col(lane)] = top;
+            } else {
+              // drafted keys: those on the column's path, in the first position's block or the next
+#pragma unroll
+              for (int late = 0; late < 2; ++late) {
+                float v[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const int col = c0 + (j >> 1) * 8 + 2 * (lane & 3) + (j & 1);
+                  TreeWord in = col < C ? s.path[node0 + col / p.Hkv] : 0;
+                  in &= late ? s.late : ~s.late;
+                  v[j] = -INFINITY;
+#pragma unroll
+                  for (int r = 0; r < 4; ++r) {
+                    const int t = quad * 32 + r * 8 + gr;
+                    if (t < 64 && (in >> t & 1) && s.path[t] != 0) v[j] = fmaxf(v[j], x[r][j]);
+                  }
+                }
+                const float top = frag_max(v, lane);
+                if (!(lane & 4)) dres[(late * 4 + quad) * Cp + c0 + frag_col(lane)] = top;
+              }
+            }
+          }
+          ptx::tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&s.acc_empty[buf]);
+        }
+        // write a group of eight blocks, or what there is of it at the end; blocks of drafted keys
+        // alone after the last item.  (Also after a wait was given up: the barriers pair up.)
+        const bool last = i + 1 == items;
+        if (last || (!draft && (blk & 7) == 7)) {
+          epi_sync();
+          const int n0 = last && nblk == 0 ? nB_b : g0;
+          const int n1 = last && drafted ? min(p.nB, max(first + 2, nB_b)) : blk + 1;
+          const int span = n1 - n0;                        // at most 8 + 2
+          for (int e = tid; e < C * 16; e += kEpiThreads) {
+            const int w = e & 15, c = e >> 4, to = n0 + w;
+            if (w >= span) continue;
+            float v = -INFINITY;
+            if (to < nB_b)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) v = fmaxf(v, res[(x * 8 + (to & 7)) * plan.res_row() + c]);
+            if (drafted && to >= first)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) v = fmaxf(v, dres[((to - first) * 4 + x) * Cp + c]);
+            if (s.path[node0 + c / p.Hkv] == 0) v = -INFINITY;
+            if (ok) scores[(size_t)rows[c] * p.nB + to] = v == -INFINITY ? v : v * qscale[c];
+          }
+          g0 = blk + 1;
+          epi_sync();
+        }
+      }
+      if (!ok && lane == 0) raise_abort(s, status, 0x503);
+    }
+  }
+
+  ptx::tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 2) {
+    ptx::tc_fence_after_sync();
+    ptx::tmem_dealloc(tmem, tmem_cols);
+  }
+}
+
+template <bool kPacked>
+cudaError_t launch(const Dims& p, const void* idx_q, const void* idx_k, const void* idx_draft,
+                   float* scores, cudaStream_t st, int* status, int sms) {
+  CUtensorMap tk, td;
+  cudaError_t e;
+  if (kPacked) {
+    // records as (128 dims, 128 keys, block), 129 * 128 bytes apart
+    const uint64_t stride[2] = {kRowBytes, index_record(kDI)};
+    const uint32_t box[3] = {kDI, kBk, 1};
+    uint64_t dims[3] = {kDI, kBk, (uint64_t)p.n_phys};
+    e = make_tensor_map(CU_TENSOR_MAP_DATA_TYPE_UINT8, &tk, idx_k, 3, dims, stride, box);
+    dims[2] = (uint64_t)p.B;
+    if (e == cudaSuccess)
+      e = make_tensor_map(CU_TENSOR_MAP_DATA_TYPE_UINT8, &td, idx_draft, 3, dims, stride, box);
+  } else {
+    const uint32_t box[3] = {64, kBk, 1};
+    const uint64_t r = p.block_table ? (uint64_t)kBk : (uint64_t)p.Sk;
+    const uint64_t kd[3] = {kDI, r, p.block_table ? (uint64_t)p.n_phys : (uint64_t)p.B};
+    const uint64_t ks[2] = {kDI * 2, r * kDI * 2};
+    const uint64_t dd[3] = {kDI, (uint64_t)p.nR, (uint64_t)p.B};
+    const uint64_t ds[2] = {kDI * 2, (uint64_t)p.nR * kDI * 2};
+    e = make_tensor_map_bf16(&tk, idx_k, 3, kd, ks, box);
+    if (e == cudaSuccess) e = make_tensor_map_bf16(&td, idx_draft, 3, dd, ds, box);
+  }
+  if (e != cudaSuccess) return e;
+  // tokens of a CTA: as many as give 256 columns
+  const int groups = (p.nR * p.Hkv + kMaxCols - 1) / kMaxCols;
+  int per = (p.nR + groups - 1) / groups;
+  if (per > kMaxCols / p.Hkv) per = kMaxCols / p.Hkv;
+  const int n_groups = (p.nR + per - 1) / per;
+  Plan plan;
+  plan.cols = (per * p.Hkv + 15) / 16 * 16;
+  plan.stage_bytes = kPacked ? kBk * kRowBytes : 2 * kBk * kRowBytes;
+  plan.stages = kMaxStages;
+  while (plan.stages > 2 && plan.bytes() + 1024 > kSmemLimit) --plan.stages;
+  uint32_t cols = 32;
+  while (cols < 2u * plan.cols) cols *= 2;
+  // the kernel's limit, the same in every call: host threads with other sizes share it
+  e = cudaFuncSetAttribute(tree_scores_tc_kernel<kPacked>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+  if (e != cudaSuccess) return e;
+  int ctas = sms / n_groups;
+  if (ctas < p.B) ctas = p.B;
+  return launch_after(tree_scores_tc_kernel<kPacked>, dim3((unsigned)ctas, (unsigned)n_groups), kThreads,
+                      (size_t)plan.bytes() + 1024, 0, st, tk, td, (const __nv_bfloat16*)idx_q,
+                      (const uint8_t*)idx_k, (const uint8_t*)idx_draft, scores, p, plan, per, cols,
+                      status);
+}
+
+}  // namespace
+
+bool tree_scores_tc_supported(const Dims& p) {
+  return p.dtype == 1 && p.dI == kDI && p.Bk == kBk && p.Hkv <= 64;
+}
+
+cudaError_t launch_tree_scores_tc(const Dims& p, const void* idx_q, const void* idx_k,
+                                  const void* idx_draft, int packed, float* scores,
+                                  cudaStream_t st, int* status) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  return packed ? launch<true>(p, idx_q, idx_k, idx_draft, scores, st, status, sms)
+                : launch<false>(p, idx_q, idx_k, idx_draft, scores, st, status, sms);
+}
+
+}  // namespace msa
