@@ -858,6 +858,8 @@ msa_status msa_sparse_decode_tree(const msa_shape* shape, const int32_t* seq_len
   MSA_TRY(make_tree_dims(shape, seq_lens, mask, &d));
   MSA_TRY(set_tree_table(block_table, n_phys, false, &d));
   if (d.G > 64) return fail(MSA_ERR_UNSUPPORTED, "decode needs n_heads_q / n_heads_kv <= 64");
+  if (d.k > kMaxMassBlocks)
+    return fail(MSA_ERR_UNSUPPORTED, "top_k %d: at most %d", d.k, kMaxMassBlocks);
   MSA_TRY(check_ptr(q, "q"));
   MSA_TRY(check_ptr(k, "k"));
   MSA_TRY(check_ptr(v, "v"));
@@ -955,7 +957,8 @@ msa_status msa_tree_commit(const msa_shape* shape, const int32_t* seq_lens,
 size_t msa_workspace_bytes(const msa_shape* shape, int which) {
   Dims d;
   if (which == 5)                                          // a tree's shape is no other call's
-    return make_tree_shape(shape, &d) == MSA_OK && d.G <= 64 ? tree_workspace_bytes(d) : 0;
+    return make_tree_shape(shape, &d) == MSA_OK && d.G <= 64 && d.k <= kMaxMassBlocks
+               ? tree_workspace_bytes(d) : 0;
   if (make_dims(shape, &d) != MSA_OK) return 0;
   if (which == 1 && d.decode) return decode_workspace_bytes(d);
   if (which == 2 && !d.decode) return backward_workspace_bytes(d);

@@ -1,7 +1,635 @@
-// No shape runs on the tensor cores yet.
+// Attention of a tree of drafted tokens on the tcgen05 tensor cores (bf16 inputs, fp32 softmax and
+// accumulation; head_dim 64 or 128, blocks of 128 keys).
+//
+// Bound by HBM: the tokens of a tree select mostly the same blocks, so a block is read once for
+// all of them.  CTA = (split, up to 256 rows, sequence x KV head), a row being a (token, query head)
+// of the KV head's group.  It forms the union of its tokens' selections (a bitmap of blocks in
+// shared memory), takes the split's share of it in order, streams these blocks through a TMA ring,
+// and multiplies all rows with each; rows whose token did not select a block get weight 0 there.
+// The drafted keys are one more block, with a mask of the path a row.
+//
+// More than 128 rows are two tiles that share each block (S0, S1, O0, O1 in TMEM); up to 128 rows
+// are one tile whose blocks alternate between two S buffers.  Warps: 0-3 and 4-7 softmax and
+// epilogue of a tile each, 8 TMA producer, 9 issues Q.K^T, 10 issues P.V.  P (bf16) is written over
+// S and read by the P.V product from TMEM.  Online softmax in the log2 domain; the running base
+// moves only when a block would push a row's weights past a bound, so O is rarely rescaled.
+// Every wait is bounded.
+#include "launch.cuh"
+#include "ptx.cuh"
+#include "tma_host.cuh"
+#include "tree.cuh"
 #include "tree_decode_tc.cuh"
+
 namespace msa {
-bool tree_decode_tc_supported(const Dims&) { return false; }
-int tree_decode_tc_splits(const Dims&) { return 1; }
-cudaError_t launch_tree_decode_tc(const Dims&, const void*, const void*, const void*, const void*, const void*, const int32_t*, float*, float*, cudaStream_t, int*) { return cudaErrorNotSupported; }
+
+namespace {
+
+constexpr int kBk = 128;
+constexpr int kTileRows = 128;
+constexpr int kRowBytes = 128;
+constexpr int kMaxItems = 1024;        // blocks of a split
+constexpr int kMaxWords = kMaxBlocks / 32;
+constexpr int kThreads = 352;
+constexpr int kProducerWarp = 8;
+constexpr int kMmaWarp = 9;            // issues the Q.K^T products; warp 10 the P.V ones
+constexpr uint32_t kTmemCols = 512;
+constexpr float kRescaleThreshold = 8.0f;   // log2 units, on a block's maximum
+constexpr float kSumThreshold = 512.0f;     // on a block's sum of weights
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <int kD, int kTiles>
+struct __align__(1024) Smem {
+  static constexpr int kChunks = kD / 64;
+  static constexpr int kTileBytes = kChunks * kTileRows * kRowBytes;   // [chunk][128 rows][128 B]
+  static constexpr int kStages = kD == 64 ? 4 : 2;
+  uint8_t q[kTiles][kTileBytes];
+  uint8_t k[kStages][kTileBytes];
+  uint8_t v[kStages][kTileBytes];
+  TreeWord mask[kMaxItems];            // tokens of the CTA that selected the item
+  TreeWord path[64];
+  int blocks[kMaxItems];
+  uint32_t bitmap[kMaxWords];
+  uint16_t before[kMaxWords];          // blocks in the words before
+  int warp_sum[11];
+  TreeWord sel[2];                     // tokens that selected the block of the first drafted position, the next
+  TreeWord late;                       // tokens whose position is in that next block
+  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  uint64_t s_full[2], p_full[2], pv_done[2], o_full[2], drain[2];
+  uint32_t tmem_base;
+  int abort;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// Packed pairs of fp32 (one 64-bit register) for the paired FMA / ADD instructions.
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 f32_pair(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.ftz.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.ftz.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// Rows of a token: the group's heads, padded to a power of two that divides the tile.
+__host__ __device__ inline int padded_heads(int G) {
+  int g = 1;
+  while (g < G) g *= 2;
+  return g;
+}
+
+template <typename S>
+__device__ __forceinline__ void raise_abort(S& s, int* status, int code) {
+  s.abort = 1;
+  if (status) atomicExch(status, code);
+}
+
+template <int kD, int kTiles>
+__global__ void __launch_bounds__(kThreads, 1)
+tree_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v,
+                      const __grid_constant__ CUtensorMap tm_kd,
+                      const __grid_constant__ CUtensorMap tm_vd,
+                      const __nv_bfloat16* __restrict__ q, const int32_t* __restrict__ sel,
+                      float* __restrict__ ws_o, float* __restrict__ ws_l, Dims p, int Gp, int* status) {
+  using S = Smem<kD, kTiles>;
+  constexpr int kStages = S::kStages, kTileBytes = S::kTileBytes;
+  constexpr uint32_t kIdescQK = ptx::idesc_bf16_f32(128, kBk, 0, 0);
+  constexpr uint32_t kIdescPV = ptx::idesc_bf16_f32(128, kD, 0, 1);
+  extern __shared__ uint8_t smem_raw[];
+  S& s = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  ptx::grid_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+  const int n_split = gridDim.x, split = blockIdx.x;
+  const int bg = blockIdx.z, b = bg / p.Hkv, g = bg % p.Hkv, G = p.G;
+  const int per_cta = kTiles * kTileRows / Gp;
+  const int node0 = blockIdx.y * per_cta;
+  const int n_nodes = min(per_cta, p.nR - node0);
+  const int L = seq_len_of(p, b);
+  const int first = L / kBk;                               // block of the first drafted position
+  const int words = (p.nB + 31) / 32;
+  const volatile int* abort = &s.abort;
+
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      ptx::mbar_init(&s.k_full[i], 1);
+      ptx::mbar_init(&s.k_empty[i], 1);
+      ptx::mbar_init(&s.v_full[i], 1);
+      ptx::mbar_init(&s.v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&s.s_full[i], 1);
+      ptx::mbar_init(&s.p_full[i], 4);
+      ptx::mbar_init(&s.pv_done[i], 1);
+      ptx::mbar_init(&s.o_full[i], 1);
+      ptx::mbar_init(&s.drain[i], 1);
+    }
+    s.abort = 0;
+    s.late = s.sel[0] = s.sel[1] = 0;
+    ptx::fence_barrier_init();
+  }
+  if (warp == 0) {
+    ptx::tmem_alloc(&s.tmem_base, kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  for (int w = tid; w < words; w += kThreads) s.bitmap[w] = 0;
+  if (tid < 64) s.path[tid] = tid < p.nR ? tree_path(p, b, tid, L) : 0;
+  __syncthreads();
+
+  // ---- union of the tokens' selections, over blocks with cached keys
+  if (tid < 64 && s.path[tid] && tree_pos(s.path[tid], L) / kBk == first + 1)
+    atomicOr(&s.late, 1ull << tid);
+  const int32_t* srow = sel + ((size_t)bg * p.nR + node0) * p.k;
+  const int entries = n_nodes * p.k;
+  for (int e = tid; e < entries; e += kThreads) {
+    const int blk = srow[e], t = node0 + e / p.k;
+    if (blk < 0 || blk >= p.nB || s.path[t] == 0) continue;
+    if (blk * kBk < L) atomicOr(&s.bitmap[blk >> 5], 1u << (blk & 31));
+    if (blk == first || blk == first + 1) atomicOr(&s.sel[blk - first], 1ull << t);
+  }
+  // Q as A operands: row r = token * Gp + head, K-major with the 128-byte swizzle (16-byte unit u of
+  // row r at unit u ^ (r % 8)); zero for heads past the group and absent tokens
+  for (int e = tid; e < kTiles * kTileRows * (kD / 8); e += kThreads) {
+    const int r = e / (kD / 8), u = e % (kD / 8);
+    const int t = node0 + r / Gp, h = r % Gp;
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (r / Gp < n_nodes && h < G && s.path[t] != 0)
+      x = *reinterpret_cast<const uint4*>(q + (((size_t)b * p.nR + t) * p.Hq + g * G + h) * kD + u * 8);
+    *reinterpret_cast<uint4*>(s.q[r / kTileRows] + (u >> 3) * kTileRows * kRowBytes +
+                              r % kTileRows * kRowBytes + (((u & 7) ^ (r & 7)) << 4)) = x;
+  }
+  ptx::fence_proxy_async_smem();
+  __syncthreads();
+  // blocks before each word of the bitmap: three words a thread
+  {
+    constexpr int kPer = (kMaxWords + kThreads - 1) / kThreads;
+    int c[kPer], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int w = tid * kPer + i;
+      c[i] = w < words ? __popc(s.bitmap[w]) : 0;
+      sum += c[i];
+    }
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) s.warp_sum[warp] = incl;
+    __syncthreads();
+    int at = incl - sum;
+    for (int w = 0; w < warp; ++w) at += s.warp_sum[w];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int w = tid * kPer + i;
+      if (w < words) s.before[w] = (uint16_t)at;
+      at += c[i];
+    }
+  }
+  int n_union = 0;
+  for (int w = 0; w < kThreads / 32; ++w) n_union += s.warp_sum[w];
+  // the drafted keys count as one more block, the last
+  const bool any_draft = s.sel[0] != 0 || s.sel[1] != 0;
+  const int total = n_union + (any_draft ? 1 : 0);
+  const int p0 = (int)((long long)total * split / n_split);
+  const int p1 = (int)((long long)total * (split + 1) / n_split);
+  const int n_items = p1 - p0;                             // at most kMaxItems, by the launcher
+  const int n_blk = min(p1, n_union) - p0;                 // items that are blocks (may be < 0: none)
+  const bool draft_here = any_draft && p1 == total && n_items > 0;
+  for (int i = tid; i < n_items; i += kThreads) s.mask[i] = 0;
+  __syncthreads();
+  for (int w = tid; w < words; w += kThreads) {
+    uint32_t bits = s.bitmap[w];
+    for (int at = (int)s.before[w] - p0; bits; bits &= bits - 1, ++at)
+      if (at >= 0 && at < n_blk) s.blocks[at] = w * 32 + __ffs(bits) - 1;
+  }
+  for (int e = tid; e < entries; e += kThreads) {
+    const int blk = srow[e], t = e / p.k;
+    if (blk < 0 || blk >= p.nB || blk * kBk >= L || s.path[node0 + t] == 0) continue;
+    const int at = (int)s.before[blk >> 5] +
+                   __popc(s.bitmap[blk >> 5] & ((1u << (blk & 31)) - 1)) - p0;
+    if (at >= 0 && at < n_blk) atomicOr(&s.mask[at], 1ull << t);
+  }
+  ptx::tc_fence_before_sync();
+  __syncthreads();
+  ptx::tc_fence_after_sync();
+  const uint32_t tmem = s.tmem_base;
+  // S buffer of tile i's block j, and how often it was used before
+  auto buf_of = [](int i, int j) { return kTiles == 2 ? i : j & 1; };
+  auto use_of = [](int j) { return kTiles == 2 ? j : j >> 1; };
+
+  if (warp == kProducerWarp) {
+    // ------------------------------------------------------------- TMA producer
+    int k_issued = 0, v_issued = 0;
+    bool ok = true;
+    if (lane == 0 && n_items > 0) {
+      ptx::tma_prefetch_desc(&tm_k);
+      ptx::tma_prefetch_desc(&tm_v);
+    }
+    for (int j = 0; j < n_items; ++j) {
+      if (p.inject == 2 && split == 0 && j > 0) break;      // test hook: no copies any more
+      const bool draft = draft_here && j == n_items - 1;
+      const int st = j % kStages;
+      // contiguous cache: (64 dims, key, half, sequence x head); pools: (.., key in block, .., block x head)
+      int y = 0, z = bg;
+      if (!draft) {
+        const int blk = s.blocks[j];
+        if (p.block_table) z = p.block_table[(size_t)b * p.nB + blk] * p.Hkv + g;
+        else y = blk * kBk;
+        debug_check(blk >= 0 && blk < p.nB && z >= 0 &&
+                        z < (p.block_table ? p.n_phys : p.B) * p.Hkv, status, kDbgCoord);
+      }
+      if (!ptx::mbar_wait(&s.k_empty[st], ((j / kStages) & 1) ^ 1, abort)) { ok = false; break; }
+      if (lane == 0) {
+        ptx::mbar_arrive_expect_tx(&s.k_full[st], kTileBytes);
+        ptx::tma_load_4d(s.k[st], draft ? &tm_kd : &tm_k, &s.k_full[st], 0, y, 0, z);
+      }
+      k_issued = j + 1;
+      if (!ptx::mbar_wait(&s.v_empty[st], ((j / kStages) & 1) ^ 1, abort)) { ok = false; break; }
+      if (lane == 0) {
+        ptx::mbar_arrive_expect_tx(&s.v_full[st], kTileBytes);
+        ptx::tma_load_4d(s.v[st], draft ? &tm_vd : &tm_v, &s.v_full[st], 0, y, 0, z);
+      }
+      v_issued = j + 1;
+      __syncwarp();
+    }
+    if (!ok && lane == 0) raise_abort(s, status, 0x601);
+    // copies in flight land before the CTA leaves (after a full run they have been used)
+    if (lane == 0) {
+      for (int j = k_issued > kStages ? k_issued - kStages : 0; j < k_issued; ++j)
+        ptx::mbar_wait_timed(&s.k_full[j % kStages], (j / kStages) & 1);
+      for (int j = v_issued > kStages ? v_issued - kStages : 0; j < v_issued; ++j)
+        ptx::mbar_wait_timed(&s.v_full[j % kStages], (j / kStages) & 1);
+    }
+  } else if (warp == kMmaWarp) {
+    // ---------------------------------------------------------- Q.K^T issuer
+    bool ok = true, issued_any = false;
+    for (int j = 0; ok && j < n_items; ++j) {
+      const int st = j % kStages;
+      if (!ptx::mbar_wait(&s.k_full[st], (j / kStages) & 1, abort)) { ok = false; break; }
+      for (int i = 0; i < kTiles; ++i) {
+        const int buf = buf_of(i, j), use = use_of(j);
+        // overwrites the S / P buffer, which the P.V product of its use before reads
+        if (use > 0 && !ptx::mbar_wait(&s.pv_done[buf], (use - 1) & 1, abort)) { ok = false; break; }
+        ptx::tc_fence_after_sync();
+        if (lane == 0) {
+          const uint32_t qa = ptx::smem_u32(s.q[i]);
+          const uint32_t kb = ptx::smem_u32(s.k[st]);
+#pragma unroll
+          for (int kk = 0; kk < kD / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * (kTileRows * kRowBytes) + (kk & 3) * 32;
+            ptx::umma_bf16_ss(tmem + buf * 128, ptx::smem_desc_k_sw128(qa + off),
+                              ptx::smem_desc_k_sw128(kb + off), kIdescQK, kk > 0 ? 1u : 0u);
+          }
+          ptx::umma_commit(&s.s_full[buf]);
+          if (i == kTiles - 1) ptx::umma_commit(&s.k_empty[st]);
+        }
+        issued_any = true;
+        __syncwarp();
+      }
+    }
+    if (!ok && lane == 0) raise_abort(s, status, 0x602);
+    if (*abort && lane == 0 && issued_any) {               // one more commit covers all issued here
+      ptx::umma_commit(&s.drain[0]);
+      ptx::mbar_wait_timed(&s.drain[0], 0);
+    }
+  } else if (warp == kMmaWarp + 1) {
+    // ------------------------------------------------------------ P.V issuer
+    bool ok = true, issued_any = false;
+    for (int j = 0; ok && j < n_items; ++j) {
+      const int st = j % kStages;
+      const bool draft = draft_here && j == n_items - 1;
+      if (!ptx::mbar_wait(&s.v_full[st], (j / kStages) & 1, abort)) { ok = false; break; }
+      // rows of V that no key of the sequence is in may hold anything, and 0 x NaN is NaN: zeros
+      const int keys = draft ? 64 : L - s.blocks[j] * kBk;
+      if (keys < kBk) {
+        for (int r = draft ? 0 : keys; r < (draft ? 64 : kBk); ++r) {
+          if (draft && s.path[r] != 0) continue;
+          for (int u = lane; u < kD / 8; u += 32)
+            *reinterpret_cast<uint4*>(s.v[st] + (u >> 3) * kBk * kRowBytes + r * kRowBytes + (u & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+      }
+      for (int i = 0; i < kTiles; ++i) {
+        const int buf = buf_of(i, j);
+        if (!ptx::mbar_wait(&s.p_full[buf], use_of(j) & 1, abort)) { ok = false; break; }
+        ptx::tc_fence_after_sync();
+        if (lane == 0) {
+          const uint32_t vb = ptx::smem_u32(s.v[st]);
+#pragma unroll
+          for (int kk = 0; kk < kBk / 16; ++kk)
+            ptx::umma_bf16_ts(tmem + 256 + i * 128, tmem + buf * 128 + kk * 8,
+                              ptx::smem_desc_mn_sw128(vb + kk * 16 * kRowBytes, kBk * kRowBytes, 1024),
+                              kIdescPV, (j > 0 || kk > 0) ? 1u : 0u);
+          ptx::umma_commit(&s.pv_done[buf]);
+          if (i == kTiles - 1) ptx::umma_commit(&s.v_empty[st]);
+          if (j + 1 == n_items) ptx::umma_commit(&s.o_full[i]);
+        }
+        issued_any = true;
+        __syncwarp();
+      }
+    }
+    if (!ok && lane == 0) raise_abort(s, status, 0x603);
+    if (*abort && lane == 0 && issued_any) {
+      ptx::umma_commit(&s.drain[1]);
+      ptx::mbar_wait_timed(&s.drain[1], 0);
+    }
+  } else if (warp < 4 * kTiles) {
+    // ------------------------------------------------------ softmax and epilogue
+    const int i = warp >> 2, quad = warp & 3;
+    const int R = i * kTileRows + quad * 32 + lane;          // row of the CTA
+    const int tl = R / Gp, t = node0 + tl, hl = R % Gp;      // its token (here, of the tree) and head
+    const bool valid = tl < n_nodes && hl < G;
+    const TreeWord path = tl < n_nodes ? s.path[t] : 0;
+    const float c1 = p.sm_scale * 1.4426950408889634f;       // to log2 units
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    const uint32_t o_addr = tmem + lane_off + 256 + i * 128;
+    float m_used = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int j = 0; j < n_items; ++j) {
+      const bool draft = draft_here && j == n_items - 1;
+      const int buf = buf_of(i, j);
+      const uint32_t s_addr = tmem + lane_off + buf * 128;
+      if (!ptx::mbar_wait(&s.s_full[buf], use_of(j) & 1, abort)) { ok = false; break; }
+      ptx::tc_fence_after_sync();
+      // keys that the row sees: the first `lim` columns, or for the drafts the bits of `in`
+      TreeWord in = 0;
+      int lim = 0;
+      if (draft) {
+        const TreeWord bit = 1ull << t;
+        if (path) in = path & ((s.sel[0] & bit ? ~s.late : 0) | (s.sel[1] & bit ? s.late : 0));
+        // path tokens that are not there
+        for (TreeWord w = in; w; w &= w - 1) {
+          const int a = __ffsll((long long)w) - 1;
+          if (s.path[a] == 0) in &= ~(1ull << a);
+        }
+      } else if (path && (s.mask[j] >> tl & 1)) {
+        lim = min(kBk, L - s.blocks[j] * kBk);
+      }
+      const bool some = draft ? in != 0 : lim > 0;
+      uint32_t sv[4][32];
+      const uint64_t c1x2 = f32x2(c1, c1);
+      // P = 2^(s * c1 - base) from the S values in sv, written over S as bf16; returns the row sum.
+      auto p_from_sv = [&](float base) {
+        const uint64_t negm = f32x2(-base, -base);
+        uint64_t acc[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+          acc[c] = f32x2(0.f, 0.f);
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float2 y = f32_pair(fma_f32x2(
+                f32x2(__uint_as_float(sv[c][e]), __uint_as_float(sv[c][e + 1])), c1x2, negm));
+            const float a0 = ex2(y.x), a1 = ex2(y.y);
+            acc[c] = add_f32x2(acc[c], f32x2(a0, a1));
+            pk[e >> 1] = pack_bf16x2(a0, a1);
+          }
+          ptx::tmem_st_x16(s_addr + c * 16, pk);
+        }
+        const float2 sum = f32_pair(add_f32x2(add_f32x2(acc[0], acc[1]), add_f32x2(acc[2], acc[3])));
+        return sum.x + sum.y;
+      };
+      // O *= alpha in every row of the warp (1 in rows that keep their base), once the P.V product
+      // of the block before is complete (with two S buffers nothing else has waited for it)
+      auto rescale_o = [&](float alpha) {
+        if (kTiles == 1 && j > 0) {
+          if (!ptx::mbar_wait(&s.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, abort)) ok = false;
+          ptx::tc_fence_after_sync();
+        }
+#pragma unroll 1
+        for (int c = 0; c < kD / 32; ++c) {
+          uint32_t ov[32];
+          ptx::tmem_ld_x32(o_addr + c * 32, ov);
+          ptx::tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+          ptx::tmem_st_x32(o_addr + c * 32, ov);
+        }
+      };
+      // tcgen05.ld/st are warp-collective, so every branch around them is warp-uniform.
+      if (!__any_sync(0xffffffffu, some)) {
+        // no row of the warp sees the block
+        uint32_t zero[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) zero[e] = 0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) ptx::tmem_st_x16(s_addr + c * 16, zero);
+      } else if (!draft && __all_sync(0xffffffffu, lim == 0 || (lim == kBk && m_used != -INFINITY))) {
+        // whole blocks for rows that have a base: P is formed with it while S streams in from TMEM,
+        // and the block's sum is checked afterwards; rows that do not see the block take an infinite
+        // base, which makes their weights 0.
+        const float base = lim == 0 ? INFINITY : m_used;
+        const uint64_t negm = f32x2(-base, -base);
+        uint64_t acc[4];
+        ptx::tmem_ld_x32(s_addr, sv[0]);
+        ptx::tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (c < 3) ptx::tmem_ld_x32(s_addr + (c + 1) * 32, sv[c + 1]);
+          uint32_t pk[16];
+          acc[c] = f32x2(0.f, 0.f);
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float2 y = f32_pair(fma_f32x2(
+                f32x2(__uint_as_float(sv[c][e]), __uint_as_float(sv[c][e + 1])), c1x2, negm));
+            const float a0 = ex2(y.x), a1 = ex2(y.y);
+            acc[c] = add_f32x2(acc[c], f32x2(a0, a1));
+            pk[e >> 1] = pack_bf16x2(a0, a1);
+          }
+          ptx::tmem_st_x16(s_addr + c * 16, pk);
+          if (c < 3) ptx::tmem_ld_wait();
+        }
+        const float2 sum = f32_pair(add_f32x2(add_f32x2(acc[0], acc[1]), add_f32x2(acc[2], acc[3])));
+        const float lb = sum.x + sum.y;
+        const bool redo = lim != 0 && !(lb <= kSumThreshold);
+        if (__any_sync(0xffffffffu, redo)) {
+          // rare: a row's weights grew past the bound; the warp redoes the block from its maximum
+          float alpha = 1.f;
+          if (redo) {
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int e = 0; e < 32; e += 2)
+                mx[c] = max3(mx[c], __uint_as_float(sv[c][e]), __uint_as_float(sv[c][e + 1]));
+            const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c1;
+            alpha = ex2(m_used - mb);
+            m_used = mb;
+          }
+          l = l * alpha + p_from_sv(lim == 0 ? INFINITY : m_used);
+          rescale_o(alpha);
+        } else {
+          l += lb;
+        }
+      } else {
+        // a row's first block, or keys that a row does not see: the block's maximum first
+#pragma unroll
+        for (int c = 0; c < 4; ++c) ptx::tmem_ld_x32(s_addr + c * 32, sv[c]);
+        ptx::tmem_ld_wait();
+        float mc[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        const uint32_t word[4] = {
+            draft ? (uint32_t)in : lim >= 32 ? 0xffffffffu : (1u << lim) - 1,
+            draft ? (uint32_t)(in >> 32) : lim >= 64 ? 0xffffffffu : lim > 32 ? (1u << (lim - 32)) - 1 : 0,
+            draft ? 0 : lim >= 96 ? 0xffffffffu : lim > 64 ? (1u << (lim - 64)) - 1 : 0,
+            draft ? 0 : lim >= 128 ? 0xffffffffu : lim > 96 ? (1u << (lim - 96)) - 1 : 0};
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float x = word[c] >> e & 1 ? __uint_as_float(sv[c][e]) : -INFINITY;
+            sv[c][e] = __float_as_uint(x);
+            mc[c] = fmaxf(mc[c], x);
+          }
+        const float mb = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3])) * c1;
+        float alpha = 1.f;
+        bool rescale = false;
+        if (mb > m_used + kRescaleThreshold) {
+          if (m_used != -INFINITY) {
+            alpha = ex2(m_used - mb);
+            rescale = true;
+            l *= alpha;
+          }
+          m_used = mb;
+        }
+        l += p_from_sv(m_used == -INFINITY ? 0.f : m_used);
+        if (__any_sync(0xffffffffu, rescale)) rescale_o(alpha);
+      }
+      ptx::tmem_st_wait();
+      ptx::tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&s.p_full[buf]);
+      if (!ok) break;
+    }
+    if (!ok && lane == 0) raise_abort(s, status, 0x604);
+    // the split's part of the row: O / l and its log-sum
+    bool have_o = ok && n_items > 0;
+    if (have_o) {
+      if (!ptx::mbar_wait(&s.o_full[i], 0, abort)) {
+        have_o = false;
+        if (lane == 0) raise_abort(s, status, 0x605);
+      }
+    }
+    if (have_o) ptx::tc_fence_after_sync();
+    const bool some = have_o && l > 0.f;
+    const float inv = some ? 1.f / l : 0.f;
+    const size_t row = ((size_t)b * p.nR + t) * p.Hq + (size_t)g * G + hl;
+    float* orow = ws_o + (row * n_split + split) * kD;
+    debug_check(!valid || (t < p.nR && hl < G), status, kDbgStore);
+#pragma unroll
+    for (int c = 0; c < kD / 32; ++c) {
+      uint32_t ov[32];
+      if (have_o) {
+        ptx::tmem_ld_x32(o_addr + c * 32, ov);
+        ptx::tmem_ld_wait();
+      }
+      if (valid) {
+        float4* dst = reinterpret_cast<float4*>(orow + c * 32);
+#pragma unroll
+        for (int w = 0; w < 8; ++w)
+          dst[w] = some ? make_float4(__uint_as_float(ov[4 * w]) * inv, __uint_as_float(ov[4 * w + 1]) * inv,
+                                      __uint_as_float(ov[4 * w + 2]) * inv, __uint_as_float(ov[4 * w + 3]) * inv)
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    }
+    if (valid) ws_l[row * n_split + split] = some ? (m_used + __log2f(l)) * kLn2 : -INFINITY;
+  }
+
+  ptx::tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 0) {
+    ptx::tc_fence_after_sync();
+    ptx::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+int tiles_of(const Dims& p) { return p.nR * padded_heads(p.G) > kTileRows ? 2 : 1; }
+
+template <int kD, int kTiles>
+cudaError_t launch(const Dims& p, const void* q, const void* k, const void* v, const void* kd,
+                   const void* vd, const int32_t* sel, float* ws_o, float* ws_l, int n_split,
+                   cudaStream_t st, int* status) {
+  CUtensorMap tk, tv, tkd, tvd;
+  // rows as (64 dims, key, half of the head, outer): one box {64, 128, halves, 1} lands a block as
+  // [half][128 keys][128 B], the swizzled chunks that the products read
+  constexpr uint64_t kHalves = kD / 64;
+  const uint64_t rows = p.block_table ? (uint64_t)kBk : (uint64_t)p.Sk;
+  const uint64_t outer = (uint64_t)p.Hkv * (p.block_table ? (uint64_t)p.n_phys : (uint64_t)p.B);
+  const uint64_t dims[4] = {64, rows, kHalves, outer};
+  const uint64_t stride[3] = {kD * 2, 128, rows * kD * 2};
+  const uint64_t ddims[4] = {64, (uint64_t)p.nR, kHalves, (uint64_t)p.B * p.Hkv};
+  const uint64_t dstride[3] = {kD * 2, 128, (uint64_t)p.nR * kD * 2};
+  const uint32_t box[4] = {64, (uint32_t)kBk, (uint32_t)kHalves, 1};
+  cudaError_t e = make_tensor_map_bf16(&tk, k, 4, dims, stride, box);
+  if (e == cudaSuccess) e = make_tensor_map_bf16(&tv, v, 4, dims, stride, box);
+  if (e == cudaSuccess) e = make_tensor_map_bf16(&tkd, kd, 4, ddims, dstride, box);
+  if (e == cudaSuccess) e = make_tensor_map_bf16(&tvd, vd, 4, ddims, dstride, box);
+  if (e != cudaSuccess) return e;
+  const size_t smem = sizeof(Smem<kD, kTiles>) + 1024;
+  e = cudaFuncSetAttribute(tree_decode_tc_kernel<kD, kTiles>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  const int Gp = padded_heads(p.G), per = kTiles * kTileRows / Gp;
+  const dim3 grid((unsigned)n_split, (unsigned)((p.nR + per - 1) / per), (unsigned)(p.B * p.Hkv));
+  return launch_after(tree_decode_tc_kernel<kD, kTiles>, grid, kThreads, smem, 0, st, tk, tv, tkd, tvd,
+                      (const __nv_bfloat16*)q, sel, ws_o, ws_l, p, Gp, status);
+}
+
+}  // namespace
+
+bool tree_decode_tc_supported(const Dims& p) {
+  return p.dtype == 1 && p.Bk == kBk && (p.d == 64 || p.d == 128) && p.G <= 64;
+}
+
+int tree_decode_tc_splits(const Dims& p) {
+  const int tiles = tiles_of(p), per = tiles * kTileRows / padded_heads(p.G);
+  const long long tokens = per < p.nR ? per : p.nR;
+  const long long units = (long long)p.B * p.Hkv * ((p.nR + per - 1) / per);
+  // one CTA a SM, no more than there can be blocks, and as many as keep a split's list in bounds
+  long long most = tokens * p.k;
+  if (most > p.nB) most = p.nB;
+  most += 1;
+  long long s = 152 / units;
+  if (s > most) s = most;
+  if (s < 1) s = 1;
+  const long long least = (most + kMaxItems - 1) / kMaxItems;
+  return (int)(s < least ? least : s);
+}
+
+cudaError_t launch_tree_decode_tc(const Dims& p, const void* q, const void* k, const void* v,
+                                  const void* k_draft, const void* v_draft, const int32_t* sel,
+                                  float* ws_o, float* ws_l, cudaStream_t st, int* status) {
+  const int n_split = tree_decode_tc_splits(p);
+  auto run = tiles_of(p) == 2 ? (p.d == 128 ? launch<128, 2> : launch<64, 2>)
+                              : (p.d == 128 ? launch<128, 1> : launch<64, 1>);
+  return run(p, q, k, v, k_draft, v_draft, sel, ws_o, ws_l, n_split, st, status);
+}
+
+}  // namespace msa

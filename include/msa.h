@@ -473,7 +473,7 @@ msa_status msa_block_topk_tree(const msa_shape* shape, const int32_t* seq_lens,
 /* Attention of the tree's tokens: msa_sparse_decode for each, over the keys it sees in its selected
  * blocks.  k, v: [batch, n_heads_kv, seq_k, head_dim], or pools [n_phys, n_heads_kv, block_size,
  * head_dim].  lse may be NULL.  Entries of sel outside [0, the token's own block] are skipped;
- * entries must be distinct.  At most 64 query heads per KV head.  bf16 in blocks of 128 runs on
+ * entries must be distinct.  At most 64 query heads per KV head, top_k at most 2^20.  bf16 in blocks of 128 runs on
  * the tensor cores, which read a block once for the tokens (256 query heads of a KV head at a
  * time) that selected it.  workspace: msa_workspace_bytes(shape, 5) bytes, 16-byte aligned. */
 msa_status msa_sparse_decode_tree(const msa_shape* shape, const int32_t* seq_lens,
