@@ -3,7 +3,7 @@
 // key, max-pooled per block, and against the keys of its path.
 //
 // The scan is to be bound by HBM: a key is read once for all tokens, 129 bytes in 8 bits.  Each CTA
-// streams a contiguous range of one sequence's blocks through a TMA ring; one thread issues a
+// streams a contiguous range of one sequence's blocks through a TMA ring; a thread issues a
 // block's products with the 128 keys as M and the columns (token, head) as N, so that the cost
 // follows the number of tokens.  8-bit keys are operands as they lie in the cache: a key's scale is
 // a power of two of its own and is applied to the products.  The queries keep their precision by
@@ -12,12 +12,13 @@
 // least 2^-10 of the query's largest; a smaller one is off by at most 2^-10 of the 448 that the
 // largest is scaled to.  Both parts accumulate in the same TMEM columns.
 //
-// Eight epilogue warps read the accumulator as fragments of 16 keys x 8 columns, in which a thread
-// holds four keys of a column: scale, maximum over the four, then over the lanes by halving (4
-// shuffles for 16 columns).  Eight blocks' maxima collect in shared memory before they are written,
-// 32 bytes of a score row at a time.
-// Warps: 0-7 epilogue (TMEM lane quadrant warp % 4, every other 16 columns), 8 TMA producer, 9 MMA
-// issuer.  Every wait is bounded.
+// Four groups of four epilogue warps take the blocks in turn (one group's chain of waits and loads
+// is longer than a block's share of the bandwidth).  They read the accumulator as fragments of 16
+// keys x 8 columns, in which a thread holds four keys of a column: scale, maximum over the four,
+// then over the lanes by halving (4 shuffles for 16 columns).  The maxima of eight blocks collect in
+// one of two buffers, which two further warps write out, 32 bytes of a score row at a time.
+// Warps: 0-15 epilogue (group warp / 4, TMEM lane quadrant warp % 4), 16 TMA producer, 17-18 MMA
+// issuers (every other block: one thread's products leave a gap after a commit), 19-20 writers.  Every wait is bounded.
 #include "index_cache.cuh"
 #include "launch.cuh"
 #include "ptx.cuh"
@@ -30,11 +31,17 @@ namespace msa {
 namespace {
 
 constexpr int kBk = 128, kDI = 128, kRowBytes = 128;
-constexpr int kEpiWarps = 8;
-constexpr int kEpiThreads = kEpiWarps * 32;
-constexpr int kProducerWarp = 8, kMmaWarp = 9;
-constexpr int kThreads = 10 * 32;
-constexpr int kMaxCols = 256;          // UMMA N
+constexpr int kAcc = 4;                // accumulators in TMEM
+constexpr int kGroups = 4;             // of epilogue warps
+constexpr int kIssuers = 2;            // warps that issue products
+// A barrier's phases are told apart by parity, so each waiter has to see them one by one: what
+// completes an accumulator's phases is waited for by one group and issued by one warp, and so is
+// a stage's (the number of stages is a multiple of the issuers').
+static_assert(kAcc % kGroups == 0 && kAcc % kIssuers == 0, "one group and issuer an accumulator");
+constexpr int kProducerWarp = 4 * kGroups, kMmaWarp = kProducerWarp + 1;
+constexpr int kWriterWarp = kMmaWarp + kIssuers, kWriters = 2;
+constexpr int kWarps = kWriterWarp + kWriters, kThreads = kWarps * 32;
+constexpr int kMaxCols = 128;          // UMMA N: four accumulators fill TMEM
 constexpr int kMaxStages = 10;
 constexpr int kSmemLimit = 232448;
 
@@ -43,7 +50,8 @@ struct Small {
   TreeWord path[64];
   TreeWord late;                       // tokens whose position is in the block after the first's
   uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t acc_full[2], acc_empty[2];
+  uint64_t acc_full[kAcc], acc_empty[kAcc];
+  uint64_t res_full[2], res_empty[2], dres_full;
   int b, blk0, nblk, rank, cnt;        // the CTA's range, and its place among the sequence's CTAs
   uint32_t tmem_base;
   int abort;
@@ -56,7 +64,7 @@ struct Plan {
   __host__ __device__ int ex_at() const { return q_at() + cols * 2 * kRowBytes; }
   __host__ __device__ int res_at() const { return ex_at() + stages * kBk; }
   __host__ __device__ int res_row() const { return cols + 4; }          // spreads the banks
-  __host__ __device__ int dres_at() const { return res_at() + 32 * res_row() * 4; }
+  __host__ __device__ int dres_at() const { return res_at() + 64 * res_row() * 4; }
   __host__ __device__ int scale_at() const { return dres_at() + 8 * cols * 4; }
   __host__ __device__ int row_at() const { return scale_at() + cols * 4; }
   __host__ __device__ int small_at() const { return row_at() + cols * 4; }
@@ -68,8 +76,9 @@ __device__ __forceinline__ void raise_abort(Small& s, int* status, int code) {
   if (status) atomicExch(status, code);
 }
 
-__device__ __forceinline__ void epi_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory");
+__device__ __forceinline__ void arrive_n(uint64_t* bar, int n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(ptx::smem_u32(bar)), "r"(n)
+               : "memory");
 }
 
 // The CTA's blocks: the CTAs are shared out in proportion to the sequences' block counts, each
@@ -115,19 +124,89 @@ __device__ __forceinline__ void find_range(const Dims& p, Small& s, int lane) {
   }
 }
 
-// Maximum over lane / 4 of four values a lane, of columns 2 (lane % 4) + {0, 1, 8, 9}; the lane
-// returns that of column frag_col(lane).
+// Maximum over lane / 4 (the rows of a fragment) of values v[4 c + j], c < N (1, 2 or 4), of the
+// columns 16 c + 2 (lane % 4) + {0, 1, 8, 9}[j].  Each step halves the values: the lane ends with
+// those of column frag_col(lane) of chunk 2 i + (lane & 4 ? 1 : 0) in v[i] (one chunk: all lanes).
 __device__ __forceinline__ int frag_col(int lane) {
   return (lane & 16 ? 8 : 0) + 2 * (lane & 3) + (lane & 8 ? 1 : 0);
 }
-__device__ __forceinline__ float frag_max(const float (&v)[4], int lane) {
-  const bool u16 = lane & 16, u8 = lane & 8;
-  const float a = __shfl_xor_sync(0xffffffffu, u16 ? v[0] : v[2], 16);
-  const float b = __shfl_xor_sync(0xffffffffu, u16 ? v[1] : v[3], 16);
-  const float x = fmaxf(u16 ? v[2] : v[0], a), y = fmaxf(u16 ? v[3] : v[1], b);
-  const float c = __shfl_xor_sync(0xffffffffu, u8 ? x : y, 8);
-  const float z = fmaxf(u8 ? y : x, c);
-  return fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 4));
+template <int N>
+__device__ __forceinline__ void frag_max(float (&v)[4 * N], int lane) {
+  const bool u16 = lane & 16, u8 = lane & 8, u4 = lane & 4;
+#pragma unroll
+  for (int c = 0; c < N; ++c) {
+    const float a = __shfl_xor_sync(0xffffffffu, u16 ? v[4 * c] : v[4 * c + 2], 16);
+    const float b = __shfl_xor_sync(0xffffffffu, u16 ? v[4 * c + 1] : v[4 * c + 3], 16);
+    v[4 * c] = fmaxf(u16 ? v[4 * c + 2] : v[4 * c], a);
+    v[4 * c + 1] = fmaxf(u16 ? v[4 * c + 3] : v[4 * c + 1], b);
+  }
+#pragma unroll
+  for (int c = 0; c < N; ++c) {
+    const float a = __shfl_xor_sync(0xffffffffu, u8 ? v[4 * c] : v[4 * c + 1], 8);
+    v[4 * c] = fmaxf(u8 ? v[4 * c + 1] : v[4 * c], a);
+  }
+  if (N == 1) {
+    v[0] = fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], 4));
+  } else {
+#pragma unroll
+    for (int c = 0; c < N; c += 2) {
+      const float a = __shfl_xor_sync(0xffffffffu, u4 ? v[4 * c] : v[4 * c + 4], 4);
+      v[c / 2] = fmaxf(u4 ? v[4 * c + 4] : v[4 * c], a);
+    }
+  }
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// Two fp32 products with one factor.
+__device__ __forceinline__ float2 mul2(uint32_t a, uint32_t b, uint64_t ss) {
+  uint64_t x;
+  float2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "r"(a), "r"(b));
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(ss));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+
+// Maxima over a quadrant's 32 keys of N x 16 accumulator columns from `at` on, each key's products
+// times its scale, into to[0 .. 16 N).
+template <int N, bool kScaled>
+__device__ __forceinline__ void block_max(uint32_t at, const float (&sc)[4], float* to, int lane) {
+  uint32_t a[N][8], d[N][8];                               // keys 0-15 and 16-31
+#pragma unroll
+  for (int c = 0; c < N; ++c) {
+    ptx::tmem_ld_frag16(at + 16 * c, a[c]);
+    ptx::tmem_ld_frag16(at + (16u << 16) + 16 * c, d[c]);
+  }
+  uint64_t ss[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) asm("mov.b64 %0, {%1, %1};" : "=l"(ss[r]) : "f"(sc[r]));
+  ptx::tmem_ld_wait();
+  float v[4 * N];
+#pragma unroll
+  for (int c = 0; c < N; ++c)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {                          // eight columns each
+      float2 x[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const uint32_t* f = r < 2 ? a[c] : d[c];
+        const uint32_t lo = f[4 * h + 2 * (r & 1)], hi = f[4 * h + 2 * (r & 1) + 1];
+        x[r] = kScaled ? mul2(lo, hi, ss[r]) : make_float2(__uint_as_float(lo), __uint_as_float(hi));
+      }
+      v[4 * c + 2 * h] = max3(x[0].x, x[1].x, fmaxf(x[2].x, x[3].x));
+      v[4 * c + 2 * h + 1] = max3(x[0].y, x[1].y, fmaxf(x[2].y, x[3].y));
+    }
+  frag_max<N>(v, lane);
+  if (N == 1) {
+    if (!(lane & 4)) to[frag_col(lane)] = v[0];
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) to[32 * i + (lane & 4 ? 16 : 0) + frag_col(lane)] = v[i];
+  }
 }
 
 template <bool kPacked>
@@ -142,7 +221,7 @@ tree_scores_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
                                              ~uintptr_t(1023));
   uint8_t* qs = smem + plan.q_at();
   uint8_t* ex = smem + plan.ex_at();
-  float* res = reinterpret_cast<float*>(smem + plan.res_at());     // [quadrant][8 blocks][cols]
+  float* res = reinterpret_cast<float*>(smem + plan.res_at());     // [2][quadrant][8 blocks][cols]
   float* dres = reinterpret_cast<float*>(smem + plan.dres_at());   // [2 blocks][quadrant][cols]
   float* qscale = reinterpret_cast<float*>(smem + plan.scale_at());
   int* rows = reinterpret_cast<int*>(smem + plan.row_at());        // score row of a column
@@ -158,12 +237,17 @@ tree_scores_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
   if (tid == 32) {
     for (int i = 0; i < stages; ++i) {
       ptx::mbar_init(&s.full[i], 1);
-      ptx::mbar_init(&s.empty[i], kPacked ? 1 + kEpiWarps : 1);
+      ptx::mbar_init(&s.empty[i], 4);                      // the epilogue's, after the products
+    }
+    for (int i = 0; i < kAcc; ++i) {
+      ptx::mbar_init(&s.acc_full[i], 1);
+      ptx::mbar_init(&s.acc_empty[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&s.acc_full[i], 1);
-      ptx::mbar_init(&s.acc_empty[i], kEpiWarps);
+      ptx::mbar_init(&s.res_full[i], 8 * 4);               // four warps a block
+      ptx::mbar_init(&s.res_empty[i], kWriters);
     }
+    ptx::mbar_init(&s.dres_full, 4);
     s.abort = 0;
     s.late = 0;
     ptx::fence_barrier_init();
@@ -237,7 +321,7 @@ tree_scores_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
     // ---- the queries as the B operand, K-major with the 128-byte swizzle (16-byte unit u of row c
     // lies at unit u ^ (c % 8)); a warp a column
     const int wq = warp > kProducerWarp ? warp - 1 : warp;
-    for (int c = wq; c < Cp; c += kThreads / 32 - 1) {
+    for (int c = wq; c < Cp; c += kWarps - 1) {
       const int node = node0 + c / p.Hkv;
       const bool there = c < C && s.path[node] != 0;
       uint2 w = make_uint2(0, 0);                          // dims 4 lane .. 4 lane + 3
@@ -273,29 +357,30 @@ tree_scores_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
       }
       if (lane == 0) {
         qscale[c] = scale;
-        // -1: a column of no token, whose scores are -inf
-        rows[c] = c < C ? (b * p.Hkv + c % p.Hkv) * p.nR + node : -1;
+        // the column's score row; of an absent token (scores -inf) its complement
+        const int row = (b * p.Hkv + c % p.Hkv) * p.nR + node;
+        rows[c] = there ? row : ~row;
       }
     }
     // blocks that no key of this sequence can be in: its CTAs share them out
     const int f0 = min(p.nB, first + 2);
-    for (int c = s.rank * (kThreads / 32 - 1) + wq; c < C; c += s.cnt * (kThreads / 32 - 1)) {
+    for (int c = s.rank * (kWarps - 1) + wq; c < C; c += s.cnt * (kWarps - 1)) {
       float* to = scores + (size_t)((b * p.Hkv + c % p.Hkv) * p.nR + node0 + c / p.Hkv) * p.nB;
       for (int e = f0 + lane; e < p.nB; e += 32) to[e] = -INFINITY;
     }
     ptx::fence_proxy_async_smem();
     asm volatile("bar.sync 2, %0;" ::"n"(kThreads - 32) : "memory");
 
-    if (warp == kMmaWarp) {
-      // ----------------------------------------------------------- MMA issuer
-      int issued = 0;
+    if (warp >= kMmaWarp && warp < kWriterWarp) {
+      // ---------------------------------------------------------- MMA issuers
+      int issued = -1;                                     // the last item issued here
       bool ok = true;
       const uint32_t q0 = ptx::smem_u32(qs);
       const uint32_t idesc = kPacked ? ptx::idesc_e4m3_f32(kBk, Cp) : ptx::idesc_bf16_f32(kBk, Cp);
-      for (int i = 0; i < items; ++i) {
-        const int st = i % stages, buf = i & 1;
+      for (int i = warp - kMmaWarp; i < items; i += kIssuers) {
+        const int st = i % stages, buf = i % kAcc;
         if (!ptx::mbar_wait(&s.full[st], (i / stages) & 1, abort) ||
-            !ptx::mbar_wait(&s.acc_empty[buf], ((i >> 1) & 1) ^ 1, abort)) { ok = false; break; }
+            !ptx::mbar_wait(&s.acc_empty[buf], ((i / kAcc) & 1) ^ 1, abort)) { ok = false; break; }
         ptx::tc_fence_after_sync();
         if (lane == 0) {
           const uint32_t a0 = ptx::smem_u32(smem + st * plan.stage_bytes);
@@ -311,115 +396,117 @@ tree_scores_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
               ptx::umma_bf16_ss(d, ptx::smem_desc_k_sw128(a0 + (kk >> 2) * kBk * kRowBytes + (kk & 3) * 32),
                                 ptx::smem_desc_k_sw128(q), idesc, kk > 0 ? 1u : 0u);
           }
-          ptx::umma_commit(&s.empty[st]);
           ptx::umma_commit(&s.acc_full[buf]);
         }
-        issued = i + 1;
+        issued = i;
         __syncwarp();
       }
       if (!ok && lane == 0) raise_abort(s, status, 0x502);
-      if (*abort && lane == 0 && issued > 0)
-        ptx::mbar_wait_timed(&s.acc_full[(issued - 1) & 1], ((issued - 1) >> 1) & 1);
+      if (lane == 0 && issued >= 0)                        // the last products here are complete
+        ptx::mbar_wait_timed(&s.acc_full[issued % kAcc], (issued / kAcc) & 1);
+    } else if (warp >= kWriterWarp) {
+      // -------------------------------------------------------------- writers
+      const int wt = tid - kWriterWarp * 32;
+      const int grp0 = blk0 >> 3, groups = nblk > 0 ? ((blk0 + nblk - 1) >> 3) - grp0 + 1 : 0;
+      bool ok = true;
+      // maxima of block `to` in column c, from the group's buffer and from the drafted keys
+      auto write = [&](int c, int to, bool cached) {
+        float v = -INFINITY;
+        if (cached) {
+          const float* r = res + (((((to >> 3) - grp0) & 1) * 4) * 8 + (to & 7)) * plan.res_row() + c;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) v = fmaxf(v, r[x * 8 * plan.res_row()]);
+        }
+        if (drafted && to >= first)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) v = fmaxf(v, dres[((to - first) * 4 + x) * Cp + c]);
+        const int row = rows[c];
+        v = row < 0 || v == -INFINITY ? -INFINITY : v * qscale[c];
+        scores[(size_t)(row < 0 ? ~row : row) * p.nB + to] = v;
+      };
+      for (int o = 0; ok && o < groups; ++o) {
+        const int base = (grp0 + o) * 8;
+        const int lo = max(base, blk0), hi = min(base + 8, blk0 + nblk);
+        if (wt == 0 && hi - lo < 8) arrive_n(&s.res_full[o & 1], (8 - (hi - lo)) * 4);
+        __syncwarp();
+        ok = ptx::mbar_wait(&s.res_full[o & 1], (o >> 1) & 1, abort);
+        if (ok && drafted && o + 1 == groups) ok = ptx::mbar_wait(&s.dres_full, 0, abort);
+        if (!ok) break;
+        for (int e = wt; e < C * 8; e += kWriters * 32)
+          if (base + (e & 7) >= lo && base + (e & 7) < hi) write(e >> 3, base + (e & 7), true);
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&s.res_empty[o & 1]);
+      }
+      if (ok && drafted && groups == 0) ok = ptx::mbar_wait(&s.dres_full, 0, abort);
+      if (ok && drafted) {                                 // blocks of drafted keys alone
+        const int n1 = min(p.nB, first + 2);
+        for (int e = wt; e < C * 2; e += kWriters * 32)
+          if (nB_b + (e & 1) < n1) write(e >> 1, nB_b + (e & 1), false);
+      }
+      if (!ok && lane == 0) raise_abort(s, status, 0x504);
     } else {
       // ------------------------------------------------------------- epilogue
       const int quad = warp & 3, gr = lane >> 2;
       bool ok = true;
-      int g0 = blk0;                                       // first block of the group of eight
-      for (int i = 0; i < items; ++i) {
-        const int buf = i & 1, st = i % stages;
+      for (int i = warp >> 2; i < items; i += kGroups) {
+        const int buf = i % kAcc, st = i % stages;
         const bool draft = drafted && i == 0;
         const int blk = blk0 + i - drafted;
-        if (ok && !ptx::mbar_wait(&s.acc_full[buf], (i >> 1) & 1, abort)) ok = false;
-        if (ok) {
-          ptx::tc_fence_after_sync();
-          float sc[4] = {1.f, 1.f, 1.f, 1.f};
-          if (kPacked) {
-            ok = ptx::mbar_wait(&s.full[st], (i / stages) & 1, abort);   // the copy's own barrier
+        const int o = (blk >> 3) - (blk0 >> 3);            // group of eight blocks
+        if (!ptx::mbar_wait(&s.acc_full[buf], (i / kAcc) & 1, abort)) { ok = false; break; }
+        ptx::tc_fence_after_sync();
+        float sc[4] = {1.f, 1.f, 1.f, 1.f};
+        if (kPacked) {
+          if (!ptx::mbar_wait(&s.full[st], (i / stages) & 1, abort)) { ok = false; break; }   // the copy's own barrier
 #pragma unroll
-            for (int r = 0; r < 4; ++r) sc[r] = pow2_byte(ex[st * kBk + quad * 32 + r * 8 + gr]);
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&s.empty[st]);
-          }
-          const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + buf * Cp;
-          const int seen = L - blk * kBk - quad * 32;      // keys of this warp's 32 (blocks only)
-          for (int c0 = (warp >> 2) * 16; c0 < Cp; c0 += 32) {
-            uint32_t a[8], d[8];                           // keys 0-15 and 16-31 of the quadrant
+          for (int r = 0; r < 4; ++r) sc[r] = pow2_byte(ex[st * kBk + quad * 32 + r * 8 + gr]);
+          __syncwarp();
+        }
+        // the products have read the tile and this warp the scales: the stage may be filled again
+        if (lane == 0) ptx::mbar_arrive(&s.empty[st]);
+        if (!draft && !ptx::mbar_wait(&s.res_empty[o & 1], ((o >> 1) & 1) ^ 1, abort)) { ok = false; break; }
+        const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + buf * Cp;
+        const int seen = L - blk * kBk - quad * 32;        // keys of this warp's 32 (blocks only)
+        float* to = res + (((o & 1) * 4 + quad) * 8 + (blk & 7)) * plan.res_row();
+        if (!draft && seen >= 32) {
+          int c0 = 0;
+          for (; c0 + 64 <= Cp; c0 += 64) block_max<4, kPacked>(at + c0, sc, to + c0, lane);
+          if (Cp & 32) block_max<2, kPacked>(at + c0, sc, to + c0, lane), c0 += 32;
+          if (Cp & 16) block_max<1, kPacked>(at + c0, sc, to + c0, lane);
+        } else {
+          // some keys only: those before the sequence's end, or drafted keys that are on the
+          // column's path, in the first position's block and (second turn) in the next
+#pragma unroll 1
+          for (int e = 0; e < Cp / 16 * (draft ? 2 : 1); ++e) {
+            const int c0 = (draft ? e >> 1 : e) * 16, late = draft ? e & 1 : 0;
+            uint32_t a[8], d[8];
             ptx::tmem_ld_frag16(at + c0, a);
             ptx::tmem_ld_frag16(at + (16u << 16) + c0, d);
             ptx::tmem_ld_wait();
-            float x[4][4];                                 // [key gr + 8 r][column]
+            float v[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const int e = (j >> 1) * 4 + (j & 1);
-              x[0][j] = __uint_as_float(a[e]) * sc[0];
-              x[1][j] = __uint_as_float(a[e + 2]) * sc[1];
-              x[2][j] = __uint_as_float(d[e]) * sc[2];
-              x[3][j] = __uint_as_float(d[e + 2]) * sc[3];
-            }
-            if (!draft) {
-              if (seen < 32) {
+              const int col = c0 + (j >> 1) * 8 + 2 * (lane & 3) + (j & 1);
+              TreeWord in = draft && col < C ? s.path[node0 + col / p.Hkv] : 0;
+              in &= late ? s.late : ~s.late;
+              v[j] = -INFINITY;
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-#pragma unroll
-                  for (int j = 0; j < 4; ++j)
-                    if (gr + 8 * r >= seen) x[r][j] = -INFINITY;
-              }
-              float v[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                v[j] = fmaxf(fmaxf(x[0][j], x[1][j]), fmaxf(x[2][j], x[3][j]));
-              const float top = frag_max(v, lane);
-              if (!(lane & 4))
-                res[(quad * 8 + (blk & 7)) * plan.res_row() + c0 + frag_col(lane)] = top;
-            } else {
-              // drafted keys: those on the column's path, in the first position's block or the next
-#pragma unroll
-              for (int late = 0; late < 2; ++late) {
-                float v[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const int col = c0 + (j >> 1) * 8 + 2 * (lane & 3) + (j & 1);
-                  TreeWord in = col < C ? s.path[node0 + col / p.Hkv] : 0;
-                  in &= late ? s.late : ~s.late;
-                  v[j] = -INFINITY;
-#pragma unroll
-                  for (int r = 0; r < 4; ++r) {
-                    const int t = quad * 32 + r * 8 + gr;
-                    if (t < 64 && (in >> t & 1) && s.path[t] != 0) v[j] = fmaxf(v[j], x[r][j]);
-                  }
-                }
-                const float top = frag_max(v, lane);
-                if (!(lane & 4)) dres[(late * 4 + quad) * Cp + c0 + frag_col(lane)] = top;
+              for (int r = 0; r < 4; ++r) {
+                const int t = quad * 32 + r * 8 + gr;      // drafted token of the key
+                const bool see = draft ? t < 64 && (in >> t & 1) && s.path[t] != 0 : gr + 8 * r < seen;
+                const uint32_t raw = r < 2 ? a[(j >> 1) * 4 + (j & 1) + 2 * r] : d[(j >> 1) * 4 + (j & 1) + 2 * (r - 2)];
+                if (see) v[j] = fmaxf(v[j], __uint_as_float(raw) * sc[r]);
               }
             }
+            frag_max<1>(v, lane);
+            if (!(lane & 4)) (draft ? dres + (late * 4 + quad) * Cp : to)[c0 + frag_col(lane)] = v[0];
           }
-          ptx::tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&s.acc_empty[buf]);
         }
-        // write a group of eight blocks, or what there is of it at the end; blocks of drafted keys
-        // alone after the last item.  (Also after a wait was given up: the barriers pair up.)
-        const bool last = i + 1 == items;
-        if (last || (!draft && (blk & 7) == 7)) {
-          epi_sync();
-          const int n0 = last && nblk == 0 ? nB_b : g0;
-          const int n1 = last && drafted ? min(p.nB, max(first + 2, nB_b)) : blk + 1;
-          const int span = n1 - n0;                        // at most 8 + 2
-          for (int e = tid; e < C * 16; e += kEpiThreads) {
-            const int w = e & 15, c = e >> 4, to = n0 + w;
-            if (w >= span) continue;
-            float v = -INFINITY;
-            if (to < nB_b)
-#pragma unroll
-              for (int x = 0; x < 4; ++x) v = fmaxf(v, res[(x * 8 + (to & 7)) * plan.res_row() + c]);
-            if (drafted && to >= first)
-#pragma unroll
-              for (int x = 0; x < 4; ++x) v = fmaxf(v, dres[((to - first) * 4 + x) * Cp + c]);
-            if (s.path[node0 + c / p.Hkv] == 0) v = -INFINITY;
-            if (ok) scores[(size_t)rows[c] * p.nB + to] = v == -INFINITY ? v : v * qscale[c];
-          }
-          g0 = blk + 1;
-          epi_sync();
+        ptx::tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          ptx::mbar_arrive(&s.acc_empty[buf]);
+          ptx::mbar_arrive(draft ? &s.dres_full : &s.res_full[o & 1]);
         }
       }
       if (!ok && lane == 0) raise_abort(s, status, 0x503);
@@ -459,7 +546,8 @@ cudaError_t launch(const Dims& p, const void* idx_q, const void* idx_k, const vo
     if (e == cudaSuccess) e = make_tensor_map_bf16(&td, idx_draft, 3, dd, ds, box);
   }
   if (e != cudaSuccess) return e;
-  // tokens of a CTA: as many as give 256 columns
+  // tokens of a CTA: as many as give 128 columns (more tokens: several CTAs read the same keys at
+  // about the same time, through L2)
   const int groups = (p.nR * p.Hkv + kMaxCols - 1) / kMaxCols;
   int per = (p.nR + groups - 1) / groups;
   if (per > kMaxCols / p.Hkv) per = kMaxCols / p.Hkv;
@@ -468,9 +556,9 @@ cudaError_t launch(const Dims& p, const void* idx_q, const void* idx_k, const vo
   plan.cols = (per * p.Hkv + 15) / 16 * 16;
   plan.stage_bytes = kPacked ? kBk * kRowBytes : 2 * kBk * kRowBytes;
   plan.stages = kMaxStages;
-  while (plan.stages > 2 && plan.bytes() + 1024 > kSmemLimit) --plan.stages;
+  while (plan.stages > kIssuers && plan.bytes() + 1024 > kSmemLimit) plan.stages -= kIssuers;
   uint32_t cols = 32;
-  while (cols < 2u * plan.cols) cols *= 2;
+  while (cols < (uint32_t)(kAcc * plan.cols)) cols *= 2;
   // the kernel's limit, the same in every call: host threads with other sizes share it
   e = cudaFuncSetAttribute(tree_scores_tc_kernel<kPacked>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);

@@ -306,3 +306,74 @@ def test_commit_bad_table_entry_and_long_lists():
     want[4, :, 86:] = src[1, :, :42]
     assert torch.equal(pool.tensor, want)
     pool.check()
+
+
+# ------------------------------------------- long ranges: many blocks for every CTA
+
+def _random_tree(batch, n, lens, cap, seed):
+    rng = np.random.default_rng(seed)
+    parents = random_parents(rng, batch, n, "tree")
+    paths = [tree_ops.paths(parents[b], lens[b], cap) for b in range(batch)]
+    words = [[tree_ops.word(p) for p in row] for row in paths]
+    return paths, torch.tensor([[w - (1 << 64) if w >> 63 else w for w in row] for row in words]).cuda()
+
+
+@pytest.mark.parametrize("n", [1, 5, 12, 16, 20, 28, 32, 64])
+@pytest.mark.parametrize("packed", [True, False])
+def test_scores_long_ranges(n, packed):
+    """160 sequences of up to 60 blocks: more sequences than SMs, so that every CTA's ring, its
+    accumulators and its result buffers wrap many times.  Cached blocks only; fp64 on the GPU."""
+    B, cap, d, h = 160, 7700, 128, 4
+    rng = np.random.default_rng(n)
+    lens = [int(x) for x in rng.integers(4000, cap - 64, B)]
+    _, mask = _random_tree(B, n, lens, cap, n)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    nB = -(-cap // 128)
+    ik = torch.randn(B, cap, d, generator=g, device="cuda").bfloat16()
+    iq = torch.randn(B, n, h, d, generator=g, device="cuda").bfloat16()
+    ikd = torch.randn(B, n, d, generator=g, device="cuda").bfloat16()
+    lens_t = torch.tensor(lens, dtype=torch.int32).cuda()
+    shape = _lib.make_shape(B, n, cap, h, h, d, d, 128, 1, 1)
+    cache, drafts, keys = ik, ikd, ik
+    if packed:
+        cache = torch.zeros(B * nB, 129 * 128, dtype=torch.uint8, device="cuda")
+        _lib.msa_index_pack(shape, cap, None, None, None, B * nB, ik, cache)
+        keys = torch.empty_like(ik)
+        _lib.msa_index_unpack(shape, cap, None, None, None, B * nB, cache, keys)
+        drafts = torch.zeros(B, 129 * 128, dtype=torch.uint8, device="cuda")
+        one = _lib.make_shape(B, 1, n, h, h, d, d, 128, 1, 1)
+        _lib.msa_index_pack(one, n, None, None, None, B, ikd, drafts)
+    out = guarded_like((B, h, n, nB), torch.float32)
+    _lib.msa_index_scores_tree(shape, lens_t, None, B * nB, mask, iq, cache, drafts, out.tensor, packed=packed)
+    _ok()
+    for b in range(B):
+        whole = lens[b] // 128
+        k = keys[b, :whole * 128].double()
+        z = (iq[b].double().flatten(0, 1) @ k.T) * d ** -0.5               # [n h, keys]
+        want = z.view(n, h, whole, 128).amax(-1).transpose(0, 1)
+        # fp32 sums of 128 products, twice over, and what the queries' two parts may miss
+        mag = (iq[b].double().abs().flatten(0, 1) @ k.abs().T).amax(-1)
+        lost = iq[b].double().abs().amax(-1).flatten() * k.abs().sum(-1).max() * (2.0 ** -18 if packed else 0)
+        tol = ((2 * 130 * 2.0 ** -24 * mag + lost) * d ** -0.5).view(n, h).T[..., None] + 2.0 ** -23 * want.abs()
+        got = out.tensor[b, :, :, :whole].double()
+        assert ((got - want).abs() <= tol).all(), (b, float((got - want).abs().max()))
+    out.check("scores")
+
+
+@pytest.mark.parametrize("c", [dict(n=4, group=16), dict(n=11, group=16, paged=True), dict(n=20, group=4, hkv=4, dim=64)],
+                         ids=["one-tile", "two-tiles", "dim64"])
+def test_attention_long_ranges(c):
+    """48 sequences x 4 KV heads: one CTA for each, so that its ring and buffers wrap many times."""
+    rng = np.random.default_rng(5)
+    lens = [int(x) for x in rng.integers(1500, 2900, 48)]
+    t = Tree(lens=lens, cap=3000, topk=14, sel_frac=0.9, seed=7, **{"hkv": 4, **c})
+    s, d = t.shape, t.dev
+    out, lse = torch.empty_like(d["q"]), torch.empty(s.batch, s.n_heads_q, t.n, device="cuda")
+    ws = torch.empty(_lib.msa_workspace_bytes(s, 5) // 4, device="cuda")
+    _lib.msa_sparse_decode_tree(s, t.seq_lens, t.table, t.n_phys, t.mask, d["q"], d["k"], d["v"], d["kd"], d["vd"],
+                                d["sel"], out, lse, ws)
+    _ok()
+    want, want_lse, tol, tol_lse = t.attend()
+    err = np.abs(out.cpu().double().numpy() - want)
+    assert (err <= tol).all(), (err.max(), (err / np.maximum(tol, 1e-30)).max())
+    assert (np.abs(lse.cpu().double().numpy() - want_lse) <= tol_lse).all()
