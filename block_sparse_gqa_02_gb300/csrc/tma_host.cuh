@@ -23,7 +23,8 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return fn;
 }
 
-// A rank-`rank` tensor map of `type`.  dims[0] is the innermost (contiguous) dimension;
+// A rank-`rank` tensor map of `type` (8-bit records start at odd multiples of 128 bytes, so their
+// L2 fetches are of 128).  dims[0] is the innermost (contiguous) dimension;
 // strides_bytes[i] is the byte stride of dimension i+1; box[] is the tile each copy moves
 // (its first side must be at most 128 bytes for the 128-byte swizzle).  Out-of-range elements of a
 // box read as zero.
@@ -42,7 +43,9 @@ inline cudaError_t make_tensor_map(CUtensorMapDataType type, CUtensorMap* map, c
   }
   CUresult r = enc(map, type, (cuuint32_t)rank,
                    const_cast<void*>(base), gd, gs, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_SWIZZLE_128B,
+                   type == CU_TENSOR_MAP_DATA_TYPE_UINT8 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                                         : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }

@@ -42,7 +42,9 @@ constexpr int kProducerWarp = 4 * kGroups, kMmaWarp = kProducerWarp + 1;
 constexpr int kWriterWarp = kMmaWarp + kIssuers, kWriters = 2;
 constexpr int kWarps = kWriterWarp + kWriters, kThreads = kWarps * 32;
 constexpr int kMaxCols = 128;          // UMMA N: four accumulators fill TMEM
-constexpr int kMaxStages = 10;
+constexpr int kMaxStages = 12;
+constexpr int kScaleSlots = 16;        // a power of two, kMaxStages + kAcc or more: see the producer
+static_assert(kScaleSlots >= kMaxStages + kAcc && (kScaleSlots & (kScaleSlots - 1)) == 0, "slots");
 constexpr int kSmemLimit = 232448;
 
 // The small part of shared memory; the ring, the queries and the results lie before it.
@@ -62,10 +64,10 @@ struct Plan {
   int cols, stages, stage_bytes;
   __host__ __device__ int q_at() const { return stages * stage_bytes; }
   __host__ __device__ int ex_at() const { return q_at() + cols * 2 * kRowBytes; }
-  __host__ __device__ int res_at() const { return ex_at() + stages * kBk; }
+  __host__ __device__ int res_at() const { return ex_at() + kScaleSlots * kBk; }
   __host__ __device__ int res_row() const { return cols + 4; }          // spreads the banks
-  __host__ __device__ int dres_at() const { return res_at() + 64 * res_row() * 4; }
-  __host__ __device__ int scale_at() const { return dres_at() + 8 * cols * 4; }
+  __host__ __device__ int dres_at() const { return res_at() + 16 * res_row() * 4; }
+  __host__ __device__ int scale_at() const { return dres_at() + 2 * cols * 4; }
   __host__ __device__ int row_at() const { return scale_at() + cols * 4; }
   __host__ __device__ int small_at() const { return row_at() + cols * 4; }
   __host__ __device__ int bytes() const { return small_at() + (int)sizeof(Small); }
@@ -156,6 +158,16 @@ __device__ __forceinline__ void frag_max(float (&v)[4 * N], int lane) {
   }
 }
 
+// Integers in the order of the floats, and back.
+__device__ __forceinline__ int order_key(float x) {
+  const int i = __float_as_int(x);
+  return i ^ ((i >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float from_order_key(int k) {
+  return __int_as_float(k ^ ((k >> 31) & 0x7fffffff));
+}
+constexpr int kNothing = (int)0x807fffff;                  // of -inf
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -172,9 +184,9 @@ __device__ __forceinline__ float2 mul2(uint32_t a, uint32_t b, uint64_t ss) {
 }
 
 // Maxima over a quadrant's 32 keys of N x 16 accumulator columns from `at` on, each key's products
-// times its scale, into to[0 .. 16 N).
+// times its scale, joined into to[0 .. 16 N) (a maximum: no order of the warps shows).
 template <int N, bool kScaled>
-__device__ __forceinline__ void block_max(uint32_t at, const float (&sc)[4], float* to, int lane) {
+__device__ __forceinline__ void block_max(uint32_t at, const float (&sc)[4], int* to, int lane) {
   uint32_t a[N][8], d[N][8];                               // keys 0-15 and 16-31
 #pragma unroll
   for (int c = 0; c < N; ++c) {
@@ -202,10 +214,10 @@ __device__ __forceinline__ void block_max(uint32_t at, const float (&sc)[4], flo
     }
   frag_max<N>(v, lane);
   if (N == 1) {
-    if (!(lane & 4)) to[frag_col(lane)] = v[0];
+    if (!(lane & 4)) atomicMax(to + frag_col(lane), order_key(v[0]));
   } else {
 #pragma unroll
-    for (int i = 0; i < N / 2; ++i) to[32 * i + (lane & 4 ? 16 : 0) + frag_col(lane)] = v[i];
+    for (int i = 0; i < N / 2; ++i) atomicMax(to + 32 * i + (lane & 4 ? 16 : 0) + frag_col(lane), order_key(v[i]));
   }
 }
 
@@ -221,8 +233,8 @@ tree_scores_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
                                              ~uintptr_t(1023));
   uint8_t* qs = smem + plan.q_at();
   uint8_t* ex = smem + plan.ex_at();
-  float* res = reinterpret_cast<float*>(smem + plan.res_at());     // [2][quadrant][8 blocks][cols]
-  float* dres = reinterpret_cast<float*>(smem + plan.dres_at());   // [2 blocks][quadrant][cols]
+  int* res = reinterpret_cast<int*>(smem + plan.res_at());         // [2][8 blocks][cols], order_key
+  int* dres = reinterpret_cast<int*>(smem + plan.dres_at());       // [2 blocks][cols]
   float* qscale = reinterpret_cast<float*>(smem + plan.scale_at());
   int* rows = reinterpret_cast<int*>(smem + plan.row_at());        // score row of a column
   Small& s = *reinterpret_cast<Small*>(smem + plan.small_at());
@@ -237,10 +249,10 @@ tree_scores_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
   if (tid == 32) {
     for (int i = 0; i < stages; ++i) {
       ptx::mbar_init(&s.full[i], 1);
-      ptx::mbar_init(&s.empty[i], 4);                      // the epilogue's, after the products
+      ptx::mbar_init(&s.empty[i], 1);
     }
     for (int i = 0; i < kAcc; ++i) {
-      ptx::mbar_init(&s.acc_full[i], 1);
+      ptx::mbar_init(&s.acc_full[i], 2);                   // products done; their issuer
       ptx::mbar_init(&s.acc_empty[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
@@ -267,6 +279,8 @@ tree_scores_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
   // the sequence's last range takes the drafted keys too, before its blocks
   const int drafted = blk0 + nblk == nB_b && (nblk > 0 || s.rank == 0) ? 1 : 0;
   const int items = nblk + drafted;
+  for (int e = tid; e < 16 * plan.res_row(); e += kThreads) res[e] = kNothing;
+  for (int e = tid; e < 2 * Cp; e += kThreads) dres[e] = kNothing;
   if (tid < 64) {
     const TreeWord path = tid < p.nR ? tree_path(p, b, tid, L) : 0;
     s.path[tid] = path;
@@ -276,40 +290,46 @@ tree_scores_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
 
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------- TMA producer
-    int issued = 0;
+    // (The loops of this kernel turn once in 700 cycles: stages and phases are counted, not divided
+    // out, and a table's entries are read 32 at a time.)
+    int issued = 0, st = 0, entry = 0;
+    uint32_t phase = 1;
     bool ok = true;
     if (lane == 0) ptx::tma_prefetch_desc(&tm_k);
+    const int32_t* table = p.block_table ? p.block_table + (size_t)b * p.nB + blk0 : nullptr;
     for (int i = 0; i < items; ++i) {
-      const int st = i % stages;
       if (p.inject == 2 && s.rank == 0 && i > 0) break;     // test hook: no copies any more
-      if (!ptx::mbar_wait(&s.empty[st], ((i / stages) & 1) ^ 1, abort)) { ok = false; break; }
+      const bool draft = drafted && i == 0;
+      const int n = i - drafted;                           // block of the range
+      if (table && !draft && (n & 31) == 0) entry = n + lane < nblk ? table[n + lane] : 0;
+      int y = 0, z = b;                                    // row and outer index of the tile
+      if (!draft) {
+        if (table) z = __shfl_sync(0xffffffffu, entry, n & 31);
+        else if (kPacked) z = b * p.nB + blk0 + n;
+        else y = (blk0 + n) * kBk;
+        debug_check(z >= 0 && z < (table || kPacked ? p.n_phys : p.B), status, kDbgCoord);
+      }
+      if (!ptx::mbar_wait(&s.empty[st], phase, abort)) { ok = false; break; }
       if (lane == 0) {
         uint8_t* to = smem + st * plan.stage_bytes;
-        const bool draft = drafted && i == 0;
         const CUtensorMap* tm = draft ? &tm_d : &tm_k;
-        const int blk = blk0 + i - drafted;
         ptx::mbar_arrive_expect_tx(&s.full[st], plan.stage_bytes + (kPacked ? kBk : 0));
-        int y = 0, z = b;                                  // row and outer index of the tile
-        if (!draft) {
-          if (p.block_table) z = p.block_table[(size_t)b * p.nB + blk];
-          else if (kPacked) z = b * p.nB + blk;
-          else y = blk * kBk;
-          debug_check(blk >= 0 && blk < nB_b && z >= 0 &&
-                          z < (p.block_table || kPacked ? p.n_phys : p.B),
-                      status, kDbgCoord);
-        }
         if (kPacked) {
           ptx::tma_load_3d(to, tm, &s.full[st], 0, 0, z);
-          // a table entry that is no block: zeros for the codes, some block's exponents
+          // a table entry that is no block: zeros for the codes, some block's exponents.  The slot was
+          // read kScaleSlots items ago: the stage is free since the products of the item `stages`
+          // before this one, whose accumulator was free since the epilogue of kAcc items before that
           const int zc = draft ? z : min(max(z, 0), p.n_phys - 1);
-          ptx::bulk_load(ex + st * kBk, (draft ? drafts : cache) + (size_t)zc * index_record(kDI) + kBk * kDI,
-                         kBk, &s.full[st]);
+          ptx::bulk_load(ex + (i & (kScaleSlots - 1)) * kBk,
+                         (draft ? drafts : cache) + (size_t)zc * index_record(kDI) + kBk * kDI, kBk,
+                         &s.full[st]);
         } else {
           ptx::tma_load_3d(to, tm, &s.full[st], 0, y, z);
           ptx::tma_load_3d(to + kBk * kRowBytes, tm, &s.full[st], 64, y, z);
         }
       }
       issued = i + 1;
+      if (++st == stages) st = 0, phase ^= 1;
       __syncwarp();
     }
     if (!ok && lane == 0) raise_abort(s, status, 0x501);
@@ -373,32 +393,40 @@ tree_scores_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
 
     if (warp >= kMmaWarp && warp < kWriterWarp) {
       // ---------------------------------------------------------- MMA issuers
+      const int m = warp - kMmaWarp;
       int issued = -1;                                     // the last item issued here
       bool ok = true;
-      const uint32_t q0 = ptx::smem_u32(qs);
+      int st = m;
+      uint32_t phase = 0;
+      const uint64_t a_desc = ptx::smem_desc_k_sw128(ptx::smem_u32(smem));
+      const uint64_t q_desc = ptx::smem_desc_k_sw128(ptx::smem_u32(qs));
+      const int q_half = Cp * kRowBytes;                   // 8-bit: hi, lo; 16-bit: halves of the dims
       const uint32_t idesc = kPacked ? ptx::idesc_e4m3_f32(kBk, Cp) : ptx::idesc_bf16_f32(kBk, Cp);
-      for (int i = warp - kMmaWarp; i < items; i += kIssuers) {
-        const int st = i % stages, buf = i % kAcc;
-        if (!ptx::mbar_wait(&s.full[st], (i / stages) & 1, abort) ||
+      for (int i = m; i < items; i += kIssuers) {
+        const int buf = i % kAcc;
+        if (!ptx::mbar_wait(&s.full[st], phase, abort) ||
             !ptx::mbar_wait(&s.acc_empty[buf], ((i / kAcc) & 1) ^ 1, abort)) { ok = false; break; }
         ptx::tc_fence_after_sync();
         if (lane == 0) {
-          const uint32_t a0 = ptx::smem_u32(smem + st * plan.stage_bytes);
           const uint32_t d = tmem + buf * Cp;
+          const uint64_t a = a_desc + ((uint32_t)(st * plan.stage_bytes) >> 4);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
-            // 8-bit: hi over the keys' 128 dims, then lo over the same; 16-bit: two halves of dims
-            const uint32_t q = q0 + (kk >> 2) * Cp * kRowBytes + (kk & 3) * 32;
-            if (kPacked)
-              ptx::umma_f8_ss(d, ptx::smem_desc_k_sw128(a0 + (kk & 3) * 32), ptx::smem_desc_k_sw128(q),
-                              idesc, kk > 0 ? 1u : 0u);
+            const uint64_t q = q_desc + ((uint32_t)((kk >> 2) * q_half + (kk & 3) * 32) >> 4);
+            if (kPacked)                                   // both parts against the same 128 dims
+              ptx::umma_f8_ss(d, a + ((kk & 3) * 32 >> 4), q, idesc, kk > 0 ? 1u : 0u);
             else
-              ptx::umma_bf16_ss(d, ptx::smem_desc_k_sw128(a0 + (kk >> 2) * kBk * kRowBytes + (kk & 3) * 32),
-                                ptx::smem_desc_k_sw128(q), idesc, kk > 0 ? 1u : 0u);
+              ptx::umma_bf16_ss(d, a + (((kk >> 2) * kBk * kRowBytes + (kk & 3) * 32) >> 4), q, idesc,
+                                kk > 0 ? 1u : 0u);
           }
+          ptx::umma_commit(&s.empty[st]);
           ptx::umma_commit(&s.acc_full[buf]);
+          // this thread has seen the copies land: passes on what the epilogue reads of them
+          ptx::mbar_arrive(&s.acc_full[buf]);
         }
         issued = i;
+        st += kIssuers;
+        if (st >= stages) st -= stages, phase ^= 1;
         __syncwarp();
       }
       if (!ok && lane == 0) raise_abort(s, status, 0x502);
@@ -409,17 +437,17 @@ tree_scores_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
       const int wt = tid - kWriterWarp * 32;
       const int grp0 = blk0 >> 3, groups = nblk > 0 ? ((blk0 + nblk - 1) >> 3) - grp0 + 1 : 0;
       bool ok = true;
-      // maxima of block `to` in column c, from the group's buffer and from the drafted keys
+      // maxima of block `to` in column c, from the group's buffer (left empty for the next) and from
+      // the drafted keys
       auto write = [&](int c, int to, bool cached) {
-        float v = -INFINITY;
+        int key = kNothing;
         if (cached) {
-          const float* r = res + (((((to >> 3) - grp0) & 1) * 4) * 8 + (to & 7)) * plan.res_row() + c;
-#pragma unroll
-          for (int x = 0; x < 4; ++x) v = fmaxf(v, r[x * 8 * plan.res_row()]);
+          int* r = res + ((((to >> 3) - grp0) & 1) * 8 + (to & 7)) * plan.res_row() + c;
+          key = *r;
+          *r = kNothing;
         }
-        if (drafted && to >= first)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) v = fmaxf(v, dres[((to - first) * 4 + x) * Cp + c]);
+        if (drafted && to >= first) key = max(key, dres[(to - first) * Cp + c]);
+        float v = from_order_key(key);
         const int row = rows[c];
         v = row < 0 || v == -INFINITY ? -INFINITY : v * qscale[c];
         scores[(size_t)(row < 0 ? ~row : row) * p.nB + to] = v;
@@ -449,25 +477,21 @@ tree_scores_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
       const int quad = warp & 3, gr = lane >> 2;
       bool ok = true;
       for (int i = warp >> 2; i < items; i += kGroups) {
-        const int buf = i % kAcc, st = i % stages;
+        const int buf = i % kAcc;
         const bool draft = drafted && i == 0;
         const int blk = blk0 + i - drafted;
         const int o = (blk >> 3) - (blk0 >> 3);            // group of eight blocks
         if (!ptx::mbar_wait(&s.acc_full[buf], (i / kAcc) & 1, abort)) { ok = false; break; }
         ptx::tc_fence_after_sync();
         float sc[4] = {1.f, 1.f, 1.f, 1.f};
-        if (kPacked) {
-          if (!ptx::mbar_wait(&s.full[st], (i / stages) & 1, abort)) { ok = false; break; }   // the copy's own barrier
+        if (kPacked)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) sc[r] = pow2_byte(ex[st * kBk + quad * 32 + r * 8 + gr]);
-          __syncwarp();
-        }
-        // the products have read the tile and this warp the scales: the stage may be filled again
-        if (lane == 0) ptx::mbar_arrive(&s.empty[st]);
+          for (int r = 0; r < 4; ++r)
+            sc[r] = pow2_byte(ex[(i & (kScaleSlots - 1)) * kBk + quad * 32 + r * 8 + gr]);
         if (!draft && !ptx::mbar_wait(&s.res_empty[o & 1], ((o >> 1) & 1) ^ 1, abort)) { ok = false; break; }
         const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + buf * Cp;
         const int seen = L - blk * kBk - quad * 32;        // keys of this warp's 32 (blocks only)
-        float* to = res + (((o & 1) * 4 + quad) * 8 + (blk & 7)) * plan.res_row();
+        int* to = res + ((o & 1) * 8 + (blk & 7)) * plan.res_row();
         if (!draft && seen >= 32) {
           int c0 = 0;
           for (; c0 + 64 <= Cp; c0 += 64) block_max<4, kPacked>(at + c0, sc, to + c0, lane);
@@ -499,7 +523,7 @@ tree_scores_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
               }
             }
             frag_max<1>(v, lane);
-            if (!(lane & 4)) (draft ? dres + (late * 4 + quad) * Cp : to)[c0 + frag_col(lane)] = v[0];
+            if (!(lane & 4)) atomicMax((draft ? dres + late * Cp : to) + c0 + frag_col(lane), order_key(v[0]));
           }
         }
         ptx::tc_fence_before_sync();
