@@ -229,33 +229,49 @@ tree_decode_simt(const T* __restrict__ q, const T* __restrict__ k, const T* __re
   }
 }
 
-// o = sum_s exp(lse_s - lse) o_s with lse = log sum_s exp(lse_s): a warp a row of out
-// [B, nR, Hq, D].
-template <typename T, int D>
+// o = sum_s exp(lse_s - lse) o_s with lse = log sum_s exp(lse_s), of a row of out [B, nR, Hq, D].
+// kRowWarps warps a row take every kRowWarps-th split each: one warp while there are few splits, all
+// eight of the CTA when the loads of many would follow one another (34 splits: 17 -> 4 us).
+template <typename T, int D, int kRowWarps>
 __global__ void __launch_bounds__(256)
 tree_combine(const float* __restrict__ ws_o, const float* __restrict__ ws_l, T* __restrict__ out,
              float* __restrict__ lse, Dims p, int n_split) {
-  constexpr int kVec = D / 32;
+  constexpr int kVec = D / 32, kRows = 8 / kRowWarps;
+  __shared__ float part[kRowWarps > 1 ? kRowWarps : 1][D + 1];
   ptx::grid_wait();
-  const long long row = (long long)blockIdx.x * 8 + threadIdx.x / 32;
-  if (row >= (long long)p.B * p.nR * p.Hq) return;
-  const int lane = threadIdx.x % 32;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, sub = warp % kRowWarps;
+  const long long row = (long long)blockIdx.x * kRows + warp / kRowWarps;
+  if (row >= (long long)p.B * p.nR * p.Hq) return;         // whole CTAs where warps share a row
   const float* l = ws_l + row * n_split;
   float top = -INFINITY;
-#pragma unroll 4
-  for (int s = 0; s < n_split; ++s) top = fmaxf(top, l[s]);
+  for (int s = lane; s < n_split; s += 32) top = fmaxf(top, l[s]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   float acc[kVec], den = 0.f;
 #pragma unroll
   for (int i = 0; i < kVec; ++i) acc[i] = 0.f;
   if (top != -INFINITY) {
 #pragma unroll 4
-    for (int s = 0; s < n_split; ++s) {
+    for (int s = sub; s < n_split; s += kRowWarps) {
       const float w = expf(l[s] - top);
       float x[kVec];
       load_dims<float, kVec>(ws_o + (row * n_split + s) * D + lane * kVec, x);
       den += w;
 #pragma unroll
       for (int i = 0; i < kVec; ++i) acc[i] = fmaf(w, x[i], acc[i]);
+    }
+  }
+  if (kRowWarps > 1) {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) part[sub][lane * kVec + i] = acc[i];
+    if (lane == 0) part[sub][D] = den;
+    __syncthreads();
+    if (sub) return;
+#pragma unroll
+    for (int x = 1; x < kRowWarps; ++x) {
+      den += part[x][D];
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) acc[i] += part[x][lane * kVec + i];
     }
   }
   const float inv = den > 0.f ? 1.f / den : 0.f;
@@ -313,8 +329,11 @@ cudaError_t decode(const Dims& p, const void* q, const void* k, const void* v, c
     e = run(p, q, k, v, kd, vd, sel, ws_o, ws_l, n_split, st);
   }
   if (e != cudaSuccess) return e;
-  return launch_after(tree_combine<T, D>, dim3((unsigned)((rows + 7) / 8)), 256, 0, 0, st, ws_o, ws_l,
-                      (T*)out, lse, p, n_split);
+  if (n_split <= 8)
+    return launch_after(tree_combine<T, D, 1>, dim3((unsigned)((rows + 7) / 8)), 256, 0, 0, st, ws_o,
+                        ws_l, (T*)out, lse, p, n_split);
+  return launch_after(tree_combine<T, D, 8>, dim3((unsigned)rows), 256, 0, 0, st, ws_o, ws_l, (T*)out,
+                      lse, p, n_split);
 }
 
 }  // namespace

@@ -115,7 +115,7 @@ tree_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_kd,
                       const __grid_constant__ CUtensorMap tm_vd,
                       const __nv_bfloat16* __restrict__ q, const int32_t* __restrict__ sel,
-                      float* __restrict__ ws_o, float* __restrict__ ws_l, Dims p, int Gp, int* status) {
+                      float* __restrict__ ws_o, float* __restrict__ ws_l, Dims p, int lg, int* status) {
   using S = Smem<kD, kTiles>;
   constexpr int kStages = S::kStages, kTileBytes = S::kTileBytes;
   constexpr uint32_t kIdescQK = ptx::idesc_bf16_f32(128, kBk, 0, 0);
@@ -126,7 +126,7 @@ tree_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
   const int n_split = gridDim.x, split = blockIdx.x;
   const int bg = blockIdx.z, b = bg / p.Hkv, g = bg % p.Hkv, G = p.G;
-  const int per_cta = kTiles * kTileRows / Gp;
+  const int Gp = 1 << lg, per_cta = kTiles * kTileRows >> lg;   // rows of a token, tokens
   const int node0 = blockIdx.y * per_cta;
   const int n_nodes = min(per_cta, p.nR - node0);
   const int L = seq_len_of(p, b);
@@ -134,6 +134,22 @@ tree_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
   const int words = (p.nB + 31) / 32;
   const volatile int* abort = &s.abort;
 
+  // Q and the first entries of the selections are on their way while the rest is set up
+  constexpr int kQ = (kTiles * kTileRows * (kD / 8) + kThreads - 1) / kThreads, kSel = 4;
+  uint4 qv[kQ];
+#pragma unroll
+  for (int i = 0; i < kQ; ++i) {
+    const int e = tid + i * kThreads, r = e / (kD / 8), u = e % (kD / 8), h = r & (Gp - 1);
+    qv[i] = make_uint4(0, 0, 0, 0);
+    if (r >> lg < n_nodes && h < G)
+      qv[i] = *reinterpret_cast<const uint4*>(
+          q + (((size_t)b * p.nR + node0 + (r >> lg)) * p.Hq + g * G + h) * kD + u * 8);
+  }
+  const int32_t* srow = sel + ((size_t)bg * p.nR + node0) * p.k;
+  const int entries = n_nodes * p.k;
+  int sv0[kSel];
+#pragma unroll
+  for (int i = 0; i < kSel; ++i) sv0[i] = tid + i * kThreads < entries ? srow[tid + i * kThreads] : -1;
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       ptx::mbar_init(&s.k_full[i], 1);
@@ -152,7 +168,7 @@ tree_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
     s.late = s.sel[0] = s.sel[1] = 0;
     ptx::fence_barrier_init();
   }
-  if (warp == 0) {
+  if (warp == 2) {
     ptx::tmem_alloc(&s.tmem_base, kTmemCols);
     ptx::tmem_relinquish();
   }
@@ -163,24 +179,29 @@ tree_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
   // ---- union of the tokens' selections, over blocks with cached keys
   if (tid < 64 && s.path[tid] && tree_pos(s.path[tid], L) / kBk == first + 1)
     atomicOr(&s.late, 1ull << tid);
-  const int32_t* srow = sel + ((size_t)bg * p.nR + node0) * p.k;
-  const int entries = n_nodes * p.k;
-  for (int e = tid; e < entries; e += kThreads) {
-    const int blk = srow[e], t = node0 + e / p.k;
-    if (blk < 0 || blk >= p.nB || s.path[t] == 0) continue;
+  // calls f(entry's block, token of the CTA) for every entry
+  auto each_entry = [&](auto f) {
+#pragma unroll
+    for (int i = 0; i < kSel; ++i) {
+      const int e = tid + i * kThreads;
+      if (e < entries) f(sv0[i], e / p.k);
+    }
+    for (int e = tid + kSel * kThreads; e < entries; e += kThreads) f(srow[e], e / p.k);
+  };
+  each_entry([&](int blk, int t) {
+    if (blk < 0 || blk >= p.nB || s.path[node0 + t] == 0) return;
     if (blk * kBk < L) atomicOr(&s.bitmap[blk >> 5], 1u << (blk & 31));
-    if (blk == first || blk == first + 1) atomicOr(&s.sel[blk - first], 1ull << t);
-  }
+    if (blk == first || blk == first + 1) atomicOr(&s.sel[blk - first], 1ull << (node0 + t));
+  });
   // Q as A operands: row r = token * Gp + head, K-major with the 128-byte swizzle (16-byte unit u of
   // row r at unit u ^ (r % 8)); zero for heads past the group and absent tokens
-  for (int e = tid; e < kTiles * kTileRows * (kD / 8); e += kThreads) {
-    const int r = e / (kD / 8), u = e % (kD / 8);
-    const int t = node0 + r / Gp, h = r % Gp;
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (r / Gp < n_nodes && h < G && s.path[t] != 0)
-      x = *reinterpret_cast<const uint4*>(q + (((size_t)b * p.nR + t) * p.Hq + g * G + h) * kD + u * 8);
+#pragma unroll
+  for (int i = 0; i < kQ; ++i) {
+    const int e = tid + i * kThreads, r = e / (kD / 8), u = e % (kD / 8);
+    if (r >= kTiles * kTileRows) continue;
+    if (r >> lg < n_nodes && s.path[node0 + (r >> lg)] == 0) qv[i] = make_uint4(0, 0, 0, 0);
     *reinterpret_cast<uint4*>(s.q[r / kTileRows] + (u >> 3) * kTileRows * kRowBytes +
-                              r % kTileRows * kRowBytes + (((u & 7) ^ (r & 7)) << 4)) = x;
+                              r % kTileRows * kRowBytes + (((u & 7) ^ (r & 7)) << 4)) = qv[i];
   }
   ptx::fence_proxy_async_smem();
   __syncthreads();
@@ -228,13 +249,12 @@ tree_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
     for (int at = (int)s.before[w] - p0; bits; bits &= bits - 1, ++at)
       if (at >= 0 && at < n_blk) s.blocks[at] = w * 32 + __ffs(bits) - 1;
   }
-  for (int e = tid; e < entries; e += kThreads) {
-    const int blk = srow[e], t = e / p.k;
-    if (blk < 0 || blk >= p.nB || blk * kBk >= L || s.path[node0 + t] == 0) continue;
+  each_entry([&](int blk, int t) {
+    if (blk < 0 || blk >= p.nB || blk * kBk >= L || s.path[node0 + t] == 0) return;
     const int at = (int)s.before[blk >> 5] +
                    __popc(s.bitmap[blk >> 5] & ((1u << (blk & 31)) - 1)) - p0;
     if (at >= 0 && at < n_blk) atomicOr(&s.mask[at], 1ull << t);
-  }
+  });
   ptx::tc_fence_before_sync();
   __syncthreads();
   ptx::tc_fence_after_sync();
@@ -365,9 +385,7 @@ tree_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
     // ------------------------------------------------------ softmax and epilogue
     const int i = warp >> 2, quad = warp & 3;
     const int R = i * kTileRows + quad * 32 + lane;          // row of the CTA
-    const int tl = R / Gp, t = node0 + tl, hl = R % Gp;      // its token (here, of the tree) and head
-    const bool valid = tl < n_nodes && hl < G;
-    const TreeWord path = tl < n_nodes ? s.path[t] : 0;
+    const int tl = R >> lg;                                  // its token
     const float c1 = p.sm_scale * 1.4426950408889634f;       // to log2 units
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
     const uint32_t o_addr = tmem + lane_off + 256 + i * 128;
@@ -383,14 +401,15 @@ tree_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
       TreeWord in = 0;
       int lim = 0;
       if (draft) {
-        const TreeWord bit = 1ull << t;
-        if (path) in = path & ((s.sel[0] & bit ? ~s.late : 0) | (s.sel[1] & bit ? s.late : 0));
-        // path tokens that are not there
-        for (TreeWord w = in; w; w &= w - 1) {
+        const int t = node0 + tl;
+        const TreeWord bit = 1ull << (t & 63);
+        if (tl < n_nodes && s.path[t])
+          in = s.path[t] & ((s.sel[0] & bit ? ~s.late : 0) | (s.sel[1] & bit ? s.late : 0));
+        for (TreeWord w = in; w; w &= w - 1) {               // path tokens that are not there
           const int a = __ffsll((long long)w) - 1;
           if (s.path[a] == 0) in &= ~(1ull << a);
         }
-      } else if (path && (s.mask[j] >> tl & 1)) {
+      } else if (tl < n_nodes && (s.mask[j] >> tl & 1)) {
         lim = min(kBk, L - s.blocks[j] * kBk);
       }
       const bool some = draft ? in != 0 : lim > 0;
@@ -540,31 +559,49 @@ tree_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
     if (have_o) ptx::tc_fence_after_sync();
     const bool some = have_o && l > 0.f;
     const float inv = some ? 1.f / l : 0.f;
-    const size_t row = ((size_t)b * p.nR + t) * p.Hq + (size_t)g * G + hl;
-    float* orow = ws_o + (row * n_split + split) * kD;
-    debug_check(!valid || (t < p.nR && hl < G), status, kDbgStore);
+    // Half of the dims at a time through shared memory, so that a row is written in runs: the tile's
+    // own Q is no longer read (its last Q.K^T was before its last P.V), and its rows of 2 kD bytes
+    // hold kD / 2 values, 16-byte unit u of row r at u ^ (r % units).
+    constexpr int kPass = kD / 2, kUnits = kPass / 4;
+    uint8_t* stage = s.q[i] + quad * 32 * kD * 2;
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
 #pragma unroll
-    for (int c = 0; c < kD / 32; ++c) {
-      uint32_t ov[32];
-      if (have_o) {
-        ptx::tmem_ld_x32(o_addr + c * 32, ov);
-        ptx::tmem_ld_wait();
-      }
-      if (valid) {
-        float4* dst = reinterpret_cast<float4*>(orow + c * 32);
+      for (int c = 0; c < kPass / 32; ++c) {
+        uint32_t ov[32];
+        if (have_o) {
+          ptx::tmem_ld_x32(o_addr + half * kPass + c * 32, ov);
+          ptx::tmem_ld_wait();
+        }
 #pragma unroll
         for (int w = 0; w < 8; ++w)
-          dst[w] = some ? make_float4(__uint_as_float(ov[4 * w]) * inv, __uint_as_float(ov[4 * w + 1]) * inv,
-                                      __uint_as_float(ov[4 * w + 2]) * inv, __uint_as_float(ov[4 * w + 3]) * inv)
-                        : make_float4(0.f, 0.f, 0.f, 0.f);
+          *reinterpret_cast<float4*>(stage + lane * kD * 2 + (((c * 8 + w) ^ (lane & (kUnits - 1))) << 4)) =
+              some ? make_float4(__uint_as_float(ov[4 * w]) * inv, __uint_as_float(ov[4 * w + 1]) * inv,
+                                 __uint_as_float(ov[4 * w + 2]) * inv, __uint_as_float(ov[4 * w + 3]) * inv)
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
       }
+      __syncwarp();
+#pragma unroll 4
+      for (int r = lane / kUnits; r < 32; r += 32 / kUnits) {
+        const int u = lane % kUnits, row = i * kTileRows + quad * 32 + r;
+        const int tr = row >> lg, hr = row & (Gp - 1);
+        if (tr >= n_nodes || hr >= G) continue;
+        debug_check(node0 + tr < p.nR, status, kDbgStore);
+        const size_t at = (((size_t)b * p.nR + node0 + tr) * p.Hq + (size_t)g * G + hr) * n_split + split;
+        *reinterpret_cast<float4*>(ws_o + at * kD + half * kPass + u * 4) =
+            *reinterpret_cast<const float4*>(stage + r * kD * 2 + ((u ^ (r & (kUnits - 1))) << 4));
+      }
+      __syncwarp();
     }
-    if (valid) ws_l[row * n_split + split] = some ? (m_used + __log2f(l)) * kLn2 : -INFINITY;
+    const int hl = R & (Gp - 1);
+    if (tl < n_nodes && hl < G)
+      ws_l[(((size_t)b * p.nR + node0 + tl) * p.Hq + (size_t)g * G + hl) * n_split + split] =
+          some ? (m_used + __log2f(l)) * kLn2 : -INFINITY;
   }
 
   ptx::tc_fence_before_sync();
   __syncthreads();
-  if (warp == 0) {
+  if (warp == 2) {
     ptx::tc_fence_after_sync();
     ptx::tmem_dealloc(tmem, kTmemCols);
   }
@@ -597,9 +634,11 @@ cudaError_t launch(const Dims& p, const void* q, const void* k, const void* v, c
                            cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const int Gp = padded_heads(p.G), per = kTiles * kTileRows / Gp;
+  int lg = 0;
+  while (1 << lg < Gp) ++lg;
   const dim3 grid((unsigned)n_split, (unsigned)((p.nR + per - 1) / per), (unsigned)(p.B * p.Hkv));
   return launch_after(tree_decode_tc_kernel<kD, kTiles>, grid, kThreads, smem, 0, st, tk, tv, tkd, tvd,
-                      (const __nv_bfloat16*)q, sel, ws_o, ws_l, p, Gp, status);
+                      (const __nv_bfloat16*)q, sel, ws_o, ws_l, p, lg, status);
 }
 
 }  // namespace
