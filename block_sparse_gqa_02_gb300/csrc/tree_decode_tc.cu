@@ -8,8 +8,10 @@
 // and multiplies all rows with each; rows whose token did not select a block get weight 0 there.
 // The drafted keys are one more block, with a mask of the path a row.
 //
-// More than 128 rows are two tiles that share each block (S0, S1, O0, O1 in TMEM); up to 128 rows
-// are one tile whose blocks alternate between two S buffers.  Warps: 0-3 and 4-7 softmax and
+// More than 128 rows are two tiles that share each block (O0 and O1 take half of TMEM), fewer are
+// one.  A tile has two S buffers, so that the next Q.K^T runs under the softmax: of a whole block for
+// one tile, of half a block's keys for two (with whole blocks and one buffer a tile the tensor cores
+// wait for the softmax: 83 us where this takes 79, ragged 8 x 128K).  Warps: 0-3 and 4-7 softmax and
 // epilogue of a tile each, 8 TMA producer, 9 issues Q.K^T, 10 issues P.V.  P (bf16) is written over
 // S and read by the P.V product from TMEM.  Online softmax in the log2 domain; the running base
 // moves only when a block would push a row's weights past a bound, so O is rarely rescaled.
@@ -54,7 +56,7 @@ struct __align__(1024) Smem {
   TreeWord sel[2];                     // tokens that selected the block of the first drafted position, the next
   TreeWord late;                       // tokens whose position is in that next block
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-  uint64_t s_full[2], p_full[2], pv_done[2], o_full[2], drain[2];
+  uint64_t s_full[2 * kTiles], p_full[2 * kTiles], pv_done[2 * kTiles], o_full[2], drain[2];
   uint32_t tmem_base;
   int abort;
 };
@@ -95,6 +97,11 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
+// Sets bit t of a word in shared memory (32-bit halves: their atomics are single instructions).
+__device__ __forceinline__ void set_bit(TreeWord& w, int t) {
+  atomicOr(reinterpret_cast<uint32_t*>(&w) + (t >> 5), 1u << (t & 31));
+}
+
 // Rows of a token: the group's heads, padded to a power of two that divides the tile.
 __host__ __device__ inline int padded_heads(int G) {
   int g = 1;
@@ -118,7 +125,8 @@ tree_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
                       float* __restrict__ ws_o, float* __restrict__ ws_l, Dims p, int lg, int* status) {
   using S = Smem<kD, kTiles>;
   constexpr int kStages = S::kStages, kTileBytes = S::kTileBytes;
-  constexpr uint32_t kIdescQK = ptx::idesc_bf16_f32(128, kBk, 0, 0);
+  constexpr int kCols = kBk / kTiles, kSteps = kTiles;       // keys of a step, steps of a block
+  constexpr uint32_t kIdescQK = ptx::idesc_bf16_f32(128, kCols, 0, 0);
   constexpr uint32_t kIdescPV = ptx::idesc_bf16_f32(128, kD, 0, 1);
   extern __shared__ uint8_t smem_raw[];
   S& s = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -147,7 +155,7 @@ tree_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
   }
   const int32_t* srow = sel + ((size_t)bg * p.nR + node0) * p.k;
   const int entries = n_nodes * p.k;
-  int sv0[kSel];
+  int sv0[kSel], st0[kSel];                                // block and token of this thread's first entries
 #pragma unroll
   for (int i = 0; i < kSel; ++i) sv0[i] = tid + i * kThreads < entries ? srow[tid + i * kThreads] : -1;
   if (tid == 0) {
@@ -157,10 +165,12 @@ tree_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
       ptx::mbar_init(&s.v_full[i], 1);
       ptx::mbar_init(&s.v_empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 2 * kTiles; ++i) {
       ptx::mbar_init(&s.s_full[i], 1);
       ptx::mbar_init(&s.p_full[i], 4);
       ptx::mbar_init(&s.pv_done[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&s.o_full[i], 1);
       ptx::mbar_init(&s.drain[i], 1);
     }
@@ -174,24 +184,25 @@ tree_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
   }
   for (int w = tid; w < words; w += kThreads) s.bitmap[w] = 0;
   if (tid < 64) s.path[tid] = tid < p.nR ? tree_path(p, b, tid, L) : 0;
+#pragma unroll
+  for (int i = 0; i < kSel; ++i) st0[i] = (tid + i * kThreads) / p.k;
   __syncthreads();
 
   // ---- union of the tokens' selections, over blocks with cached keys
   if (tid < 64 && s.path[tid] && tree_pos(s.path[tid], L) / kBk == first + 1)
-    atomicOr(&s.late, 1ull << tid);
+    set_bit(s.late, tid);
   // calls f(entry's block, token of the CTA) for every entry
   auto each_entry = [&](auto f) {
 #pragma unroll
     for (int i = 0; i < kSel; ++i) {
-      const int e = tid + i * kThreads;
-      if (e < entries) f(sv0[i], e / p.k);
+      if (sv0[i] >= 0) f(sv0[i], st0[i]);
     }
     for (int e = tid + kSel * kThreads; e < entries; e += kThreads) f(srow[e], e / p.k);
   };
   each_entry([&](int blk, int t) {
     if (blk < 0 || blk >= p.nB || s.path[node0 + t] == 0) return;
     if (blk * kBk < L) atomicOr(&s.bitmap[blk >> 5], 1u << (blk & 31));
-    if (blk == first || blk == first + 1) atomicOr(&s.sel[blk - first], 1ull << (node0 + t));
+    if (blk == first || blk == first + 1) set_bit(s.sel[blk - first], node0 + t);
   });
   // Q as A operands: row r = token * Gp + head, K-major with the 128-byte swizzle (16-byte unit u of
   // row r at unit u ^ (r % 8)); zero for heads past the group and absent tokens
@@ -253,15 +264,15 @@ tree_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
     if (blk < 0 || blk >= p.nB || blk * kBk >= L || s.path[node0 + t] == 0) return;
     const int at = (int)s.before[blk >> 5] +
                    __popc(s.bitmap[blk >> 5] & ((1u << (blk & 31)) - 1)) - p0;
-    if (at >= 0 && at < n_blk) atomicOr(&s.mask[at], 1ull << t);
+    if (at >= 0 && at < n_blk) set_bit(s.mask[at], t);
   });
   ptx::tc_fence_before_sync();
   __syncthreads();
   ptx::tc_fence_after_sync();
   const uint32_t tmem = s.tmem_base;
-  // S buffer of tile i's block j, and how often it was used before
-  auto buf_of = [](int i, int j) { return kTiles == 2 ? i : j & 1; };
-  auto use_of = [](int j) { return kTiles == 2 ? j : j >> 1; };
+  // steps, and the S buffer of tile i in step n (its use number n / 2); the drafts fill half a block
+  const int n_steps = n_items * kSteps - (draft_here && kSteps == 2 ? 1 : 0);
+  auto buf_of = [](int i, int n) { return 2 * i + (n & 1); };
 
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------- TMA producer
@@ -309,25 +320,25 @@ tree_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------- Q.K^T issuer
     bool ok = true, issued_any = false;
-    for (int j = 0; ok && j < n_items; ++j) {
-      const int st = j % kStages;
-      if (!ptx::mbar_wait(&s.k_full[st], (j / kStages) & 1, abort)) { ok = false; break; }
+    for (int n = 0; ok && n < n_steps; ++n) {
+      const int j = n / kSteps, half = n % kSteps, st = j % kStages;
+      if (half == 0 && !ptx::mbar_wait(&s.k_full[st], (j / kStages) & 1, abort)) { ok = false; break; }
       for (int i = 0; i < kTiles; ++i) {
-        const int buf = buf_of(i, j), use = use_of(j);
+        const int buf = buf_of(i, n), use = n >> 1;
         // overwrites the S / P buffer, which the P.V product of its use before reads
         if (use > 0 && !ptx::mbar_wait(&s.pv_done[buf], (use - 1) & 1, abort)) { ok = false; break; }
         ptx::tc_fence_after_sync();
         if (lane == 0) {
           const uint32_t qa = ptx::smem_u32(s.q[i]);
-          const uint32_t kb = ptx::smem_u32(s.k[st]);
+          const uint32_t kb = ptx::smem_u32(s.k[st]) + half * kCols * kRowBytes;
 #pragma unroll
           for (int kk = 0; kk < kD / 16; ++kk) {
             const uint32_t off = (kk >> 2) * (kTileRows * kRowBytes) + (kk & 3) * 32;
-            ptx::umma_bf16_ss(tmem + buf * 128, ptx::smem_desc_k_sw128(qa + off),
+            ptx::umma_bf16_ss(tmem + buf * kCols, ptx::smem_desc_k_sw128(qa + off),
                               ptx::smem_desc_k_sw128(kb + off), kIdescQK, kk > 0 ? 1u : 0u);
           }
           ptx::umma_commit(&s.s_full[buf]);
-          if (i == kTiles - 1) ptx::umma_commit(&s.k_empty[st]);
+          if (i == kTiles - 1 && (half == kSteps - 1 || n + 1 == n_steps)) ptx::umma_commit(&s.k_empty[st]);
         }
         issued_any = true;
         __syncwarp();
@@ -341,13 +352,13 @@ tree_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
   } else if (warp == kMmaWarp + 1) {
     // ------------------------------------------------------------ P.V issuer
     bool ok = true, issued_any = false;
-    for (int j = 0; ok && j < n_items; ++j) {
-      const int st = j % kStages;
+    for (int n = 0; ok && n < n_steps; ++n) {
+      const int j = n / kSteps, half = n % kSteps, st = j % kStages;
       const bool draft = draft_here && j == n_items - 1;
-      if (!ptx::mbar_wait(&s.v_full[st], (j / kStages) & 1, abort)) { ok = false; break; }
+      if (half == 0 && !ptx::mbar_wait(&s.v_full[st], (j / kStages) & 1, abort)) { ok = false; break; }
       // rows of V that no key of the sequence is in may hold anything, and 0 x NaN is NaN: zeros
       const int keys = draft ? 64 : L - s.blocks[j] * kBk;
-      if (keys < kBk) {
+      if (half == 0 && keys < kBk) {
         for (int r = draft ? 0 : keys; r < (draft ? 64 : kBk); ++r) {
           if (draft && s.path[r] != 0) continue;
           for (int u = lane; u < kD / 8; u += 32)
@@ -358,19 +369,19 @@ tree_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
         __syncwarp();
       }
       for (int i = 0; i < kTiles; ++i) {
-        const int buf = buf_of(i, j);
-        if (!ptx::mbar_wait(&s.p_full[buf], use_of(j) & 1, abort)) { ok = false; break; }
+        const int buf = buf_of(i, n);
+        if (!ptx::mbar_wait(&s.p_full[buf], (n >> 1) & 1, abort)) { ok = false; break; }
         ptx::tc_fence_after_sync();
         if (lane == 0) {
-          const uint32_t vb = ptx::smem_u32(s.v[st]);
+          const uint32_t vb = ptx::smem_u32(s.v[st]) + half * kCols * kRowBytes;
 #pragma unroll
-          for (int kk = 0; kk < kBk / 16; ++kk)
-            ptx::umma_bf16_ts(tmem + 256 + i * 128, tmem + buf * 128 + kk * 8,
+          for (int kk = 0; kk < kCols / 16; ++kk)
+            ptx::umma_bf16_ts(tmem + 256 + i * 128, tmem + buf * kCols + kk * 8,
                               ptx::smem_desc_mn_sw128(vb + kk * 16 * kRowBytes, kBk * kRowBytes, 1024),
-                              kIdescPV, (j > 0 || kk > 0) ? 1u : 0u);
+                              kIdescPV, (n > 0 || kk > 0) ? 1u : 0u);
           ptx::umma_commit(&s.pv_done[buf]);
-          if (i == kTiles - 1) ptx::umma_commit(&s.v_empty[st]);
-          if (j + 1 == n_items) ptx::umma_commit(&s.o_full[i]);
+          if (i == kTiles - 1 && (half == kSteps - 1 || n + 1 == n_steps)) ptx::umma_commit(&s.v_empty[st]);
+          if (n + 1 == n_steps) ptx::umma_commit(&s.o_full[i]);
         }
         issued_any = true;
         __syncwarp();
@@ -391,13 +402,15 @@ tree_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
     const uint32_t o_addr = tmem + lane_off + 256 + i * 128;
     float m_used = -INFINITY, l = 0.f;
     bool ok = true;
-    for (int j = 0; j < n_items; ++j) {
+    constexpr int kChunk = kCols / 32;                       // 32 columns each
+    for (int n = 0; n < n_steps; ++n) {
+      const int j = n / kSteps, key0 = n % kSteps * kCols;   // the block, the step's first key in it
       const bool draft = draft_here && j == n_items - 1;
-      const int buf = buf_of(i, j);
-      const uint32_t s_addr = tmem + lane_off + buf * 128;
-      if (!ptx::mbar_wait(&s.s_full[buf], use_of(j) & 1, abort)) { ok = false; break; }
+      const int buf = buf_of(i, n);
+      const uint32_t s_addr = tmem + lane_off + buf * kCols;
+      if (!ptx::mbar_wait(&s.s_full[buf], (n >> 1) & 1, abort)) { ok = false; break; }
       ptx::tc_fence_after_sync();
-      // keys that the row sees: the first `lim` columns, or for the drafts the bits of `in`
+      // keys that the row sees: the first `lim` of the step, or for the drafts the bits of `in`
       TreeWord in = 0;
       int lim = 0;
       if (draft) {
@@ -410,17 +423,22 @@ tree_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
           if (s.path[a] == 0) in &= ~(1ull << a);
         }
       } else if (tl < n_nodes && (s.mask[j] >> tl & 1)) {
-        lim = min(kBk, L - s.blocks[j] * kBk);
+        lim = max(0, min(kCols, L - s.blocks[j] * kBk - key0));
       }
       const bool some = draft ? in != 0 : lim > 0;
-      uint32_t sv[4][32];
+      uint32_t sv[kChunk][32];
       const uint64_t c1x2 = f32x2(c1, c1);
+      auto sum_of = [](const uint64_t (&a)[kChunk]) {
+        uint64_t x = add_f32x2(a[0], a[1]);
+        if constexpr (kChunk == 4) x = add_f32x2(x, add_f32x2(a[2], a[3]));
+        return x;
+      };
       // P = 2^(s * c1 - base) from the S values in sv, written over S as bf16; returns the row sum.
       auto p_from_sv = [&](float base) {
         const uint64_t negm = f32x2(-base, -base);
-        uint64_t acc[4];
+        uint64_t acc[kChunk];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < kChunk; ++c) {
           uint32_t pk[16];
           acc[c] = f32x2(0.f, 0.f);
 #pragma unroll
@@ -433,14 +451,14 @@ tree_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
           }
           ptx::tmem_st_x16(s_addr + c * 16, pk);
         }
-        const float2 sum = f32_pair(add_f32x2(add_f32x2(acc[0], acc[1]), add_f32x2(acc[2], acc[3])));
+        const float2 sum = f32_pair(sum_of(acc));
         return sum.x + sum.y;
       };
       // O *= alpha in every row of the warp (1 in rows that keep their base), once the P.V product
-      // of the block before is complete (with two S buffers nothing else has waited for it)
+      // of the step before is complete (with two S buffers nothing else has waited for it)
       auto rescale_o = [&](float alpha) {
-        if (kTiles == 1 && j > 0) {
-          if (!ptx::mbar_wait(&s.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, abort)) ok = false;
+        if (n > 0) {
+          if (!ptx::mbar_wait(&s.pv_done[buf_of(i, n - 1)], ((n - 1) >> 1) & 1, abort)) ok = false;
           ptx::tc_fence_after_sync();
         }
 #pragma unroll 1
@@ -460,19 +478,19 @@ tree_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
         for (int e = 0; e < 16; ++e) zero[e] = 0;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) ptx::tmem_st_x16(s_addr + c * 16, zero);
-      } else if (!draft && __all_sync(0xffffffffu, lim == 0 || (lim == kBk && m_used != -INFINITY))) {
+        for (int c = 0; c < kChunk; ++c) ptx::tmem_st_x16(s_addr + c * 16, zero);
+      } else if (!draft && __all_sync(0xffffffffu, lim == 0 || (lim == kCols && m_used != -INFINITY))) {
         // whole blocks for rows that have a base: P is formed with it while S streams in from TMEM,
         // and the block's sum is checked afterwards; rows that do not see the block take an infinite
         // base, which makes their weights 0.
         const float base = lim == 0 ? INFINITY : m_used;
         const uint64_t negm = f32x2(-base, -base);
-        uint64_t acc[4];
+        uint64_t acc[kChunk];
         ptx::tmem_ld_x32(s_addr, sv[0]);
         ptx::tmem_ld_wait();
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (c < 3) ptx::tmem_ld_x32(s_addr + (c + 1) * 32, sv[c + 1]);
+        for (int c = 0; c < kChunk; ++c) {
+          if (c < kChunk - 1) ptx::tmem_ld_x32(s_addr + (c + 1) * 32, sv[c + 1]);
           uint32_t pk[16];
           acc[c] = f32x2(0.f, 0.f);
 #pragma unroll
@@ -484,22 +502,25 @@ tree_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
             pk[e >> 1] = pack_bf16x2(a0, a1);
           }
           ptx::tmem_st_x16(s_addr + c * 16, pk);
-          if (c < 3) ptx::tmem_ld_wait();
+          if (c < kChunk - 1) ptx::tmem_ld_wait();
         }
-        const float2 sum = f32_pair(add_f32x2(add_f32x2(acc[0], acc[1]), add_f32x2(acc[2], acc[3])));
+        const float2 sum = f32_pair(sum_of(acc));
         const float lb = sum.x + sum.y;
         const bool redo = lim != 0 && !(lb <= kSumThreshold);
         if (__any_sync(0xffffffffu, redo)) {
           // rare: a row's weights grew past the bound; the warp redoes the block from its maximum
           float alpha = 1.f;
           if (redo) {
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            float mx[kChunk], mb = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < kChunk; ++c) {
+              mx[c] = -INFINITY;
 #pragma unroll
               for (int e = 0; e < 32; e += 2)
                 mx[c] = max3(mx[c], __uint_as_float(sv[c][e]), __uint_as_float(sv[c][e + 1]));
-            const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c1;
+              mb = fmaxf(mb, mx[c]);
+            }
+            mb *= c1;
             alpha = ex2(m_used - mb);
             m_used = mb;
           }
@@ -511,23 +532,24 @@ tree_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
       } else {
         // a row's first block, or keys that a row does not see: the block's maximum first
 #pragma unroll
-        for (int c = 0; c < 4; ++c) ptx::tmem_ld_x32(s_addr + c * 32, sv[c]);
+        for (int c = 0; c < kChunk; ++c) ptx::tmem_ld_x32(s_addr + c * 32, sv[c]);
         ptx::tmem_ld_wait();
-        float mc[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        const uint32_t word[4] = {
-            draft ? (uint32_t)in : lim >= 32 ? 0xffffffffu : (1u << lim) - 1,
-            draft ? (uint32_t)(in >> 32) : lim >= 64 ? 0xffffffffu : lim > 32 ? (1u << (lim - 32)) - 1 : 0,
-            draft ? 0 : lim >= 96 ? 0xffffffffu : lim > 64 ? (1u << (lim - 64)) - 1 : 0,
-            draft ? 0 : lim >= 128 ? 0xffffffffu : lim > 96 ? (1u << (lim - 96)) - 1 : 0};
+        float mc[kChunk], mb = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < kChunk; ++c) {
+          const int in_chunk = lim - 32 * c;
+          const uint32_t word = draft ? (c < 2 ? (uint32_t)(in >> (32 * (c & 1))) : 0)
+                                      : in_chunk >= 32 ? 0xffffffffu : in_chunk > 0 ? (1u << in_chunk) - 1 : 0;
+          mc[c] = -INFINITY;
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            const float x = word[c] >> e & 1 ? __uint_as_float(sv[c][e]) : -INFINITY;
+            const float x = word >> e & 1 ? __uint_as_float(sv[c][e]) : -INFINITY;
             sv[c][e] = __float_as_uint(x);
             mc[c] = fmaxf(mc[c], x);
           }
-        const float mb = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3])) * c1;
+          mb = fmaxf(mb, mc[c]);
+        }
+        mb *= c1;
         float alpha = 1.f;
         bool rescale = false;
         if (mb > m_used + kRescaleThreshold) {
