@@ -11,6 +11,8 @@
 // selected blocks are then compacted in index order, which writes them ascending without
 // a sort.  Bit-exact and deterministic.
 #include "common.cuh"
+#include "launch.cuh"
+#include "ptx.cuh"
 #include "tree.cuh"
 
 namespace msa {
@@ -72,12 +74,7 @@ __global__ void __launch_bounds__(kThreads) block_topk_kernel(const float* __res
   const int m = row % p.nR;
   const int b = shared ? row / p.nR : row / (p.Hkv * p.nR);
   // ragged decode: the query of sequence b sits at its own cache length - 1
-  int last = p.seq_lens ? seq_len_of(p, b) - 1 : row_last_pos(p, m);
-  if (p.tree_mask) {                                        // row m: a drafted token, or none
-    const int L = seq_len_of(p, b);
-    const TreeWord path = tree_path(p, b, m, L);
-    last = path ? tree_pos(path, L) : -1;
-  }
+  const int last = p.seq_lens ? seq_len_of(p, b) - 1 : row_last_pos(p, m);
   const float* srow = scores + (size_t)row * p.nB;
   int32_t* out = sel + (size_t)row * p.k;
   const size_t head_stride = (size_t)p.nR * p.nB;           // between heads, same (b, m)
@@ -210,6 +207,129 @@ __global__ void __launch_bounds__(kThreads) block_topk_kernel(const float* __res
   if (threadIdx.x < n_out) out[threadIdx.x * out_stride + want] = cb;   // cb > every earlier
 }
 
+// The rows of a tree's tokens: many rows of few selected blocks each.  The same selection with the
+// keys in registers (key j of thread t is candidate j kThreads + t).  At least `want` keys are no
+// smaller than the want-th largest of the threads' maxima, so that bound, found to 16 bits by counting,
+// leaves little more than `want` candidates; these are ranked by comparing each with each.  Where ties
+// or a large `want` leave more than kMaxRanked, the threshold is found by counting all keys, bit by
+// bit, and ties are taken in index order.  8 x 16 tokens x 4 heads of 8192 candidates: SELNEW us, where
+// the radix select above, whose histograms collide in a few bins, takes 26.
+constexpr int kMaxRanked = 512;
+
+template <int kThreads, int kKeys>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) tree_topk_kernel(const float* __restrict__ scores,
+                                                             int32_t* __restrict__ sel, Dims p) {
+  constexpr int kWarps = kThreads / 32;
+  __shared__ uint32_t c_key[kMaxRanked];
+  __shared__ int c_idx[kMaxRanked];
+  __shared__ uint8_t c_take[kMaxRanked];
+  __shared__ int warp_sums[kWarps];
+  __shared__ int s_count;
+  ptx::grid_wait();
+  const int row = blockIdx.x, tid = threadIdx.x;
+  const int m = row % p.nR, b = row / (p.Hkv * p.nR);
+  const int L = seq_len_of(p, b);
+  const TreeWord path = tree_path(p, b, m, L);
+  const float* srow = scores + (size_t)row * p.nB;
+  int32_t* out = sel + (size_t)row * p.k;
+  const int cb = path ? tree_pos(path, L) / p.Bk : -1;     // no token: nothing
+  if (cb + 1 <= p.k) {                                     // every candidate fits
+    for (int i = tid; i < p.k; i += kThreads) out[i] = i <= cb ? i : -1;
+    return;
+  }
+  const int want = p.k - 1, n = cb;
+  if (tid == 0) {
+    s_count = 0;
+    out[want] = cb;                                        // after every earlier block
+  }
+  if (want == 0) return;
+  uint32_t key[kKeys];
+#pragma unroll
+  for (int j = 0; j < kKeys; ++j) {
+    const int i = j * kThreads + tid;
+    key[j] = i < n ? order_key(__ldg(srow + i)) : 0u;
+  }
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < kKeys; ++j) top = max(top, key[j]);
+  uint32_t bound = 0;
+#pragma unroll 1
+  for (int bit = 31; bit >= 16; --bit) {
+    const uint32_t next = bound | 1u << bit;
+    if (__syncthreads_count(top >= next) >= want) bound = next;
+  }
+#pragma unroll
+  for (int j = 0; j < kKeys; ++j) {
+    const int i = j * kThreads + tid;
+    if (i < n && key[j] >= bound) {
+      const int at = atomicAdd(&s_count, 1);
+      if (at < kMaxRanked) {
+        c_key[at] = key[j];
+        c_idx[at] = i;
+      }
+    }
+  }
+  __syncthreads();
+  const int nc = s_count;
+  if (nc <= kMaxRanked) {
+    for (int c = tid; c < nc; c += kThreads) {
+      const uint32_t k = c_key[c];
+      const int i = c_idx[c];
+      int better = 0;
+#pragma unroll 4
+      for (int x = 0; x < nc; ++x) better += c_key[x] > k || (c_key[x] == k && c_idx[x] < i);
+      c_take[c] = better < want;
+    }
+    __syncthreads();
+    for (int c = tid; c < nc; c += kThreads) {
+      if (!c_take[c]) continue;
+      const int i = c_idx[c];
+      int at = 0;
+#pragma unroll 4
+      for (int x = 0; x < nc; ++x) at += c_take[x] && c_idx[x] < i;
+      out[at] = i;
+    }
+    return;
+  }
+  // the want-th largest key exactly, how many are above it, and index order by rounds of kThreads keys
+  auto count = [&](auto f) {
+    int c = 0;
+#pragma unroll
+    for (int j = 0; j < kKeys; ++j) c += j * kThreads + tid < n && f(key[j]) ? 1 : 0;
+    int total;
+    cta_exclusive_scan<kThreads>(c, warp_sums, total);
+    return total;
+  };
+  uint32_t tau = 0;
+#pragma unroll 1
+  for (int bit = 31; bit >= 0; --bit) {
+    const uint32_t next = tau | 1u << bit;
+    if (count([&](uint32_t x) { return x >= next; }) >= want) tau = next;
+  }
+  int ties = want - count([&](uint32_t x) { return x > tau; });   // keys equal to tau still to take
+  int base = 0;
+#pragma unroll 1
+  for (int j = 0; j < kKeys; ++j) {
+    uint32_t k = 0;
+#pragma unroll
+    for (int x = 0; x < kKeys; ++x) k = x == j ? key[x] : k;      // registers are not indexed
+    const bool in = j * kThreads + tid < n;
+    int total;
+    const int before = cta_exclusive_scan<kThreads>(in && k == tau ? 1 : 0, warp_sums, total);
+    const bool take = in && (k > tau || (k == tau && before < ties));
+    ties -= min(ties, total);
+    const int at = cta_exclusive_scan<kThreads>(take ? 1 : 0, warp_sums, total);
+    if (take) out[base + at] = j * kThreads + tid;
+    base += total;
+  }
+}
+
+template <int kThreads, int kKeys>
+cudaError_t launch_tree_rows(const Dims& p, const float* scores, int32_t* sel, cudaStream_t st) {
+  return launch_after(tree_topk_kernel<kThreads, kKeys>, dim3((unsigned)(p.B * p.Hkv * p.nR)), kThreads,
+                      0, 0, st, scores, sel, p);
+}
+
 }  // namespace
 
 template <int kThreads>
@@ -231,6 +351,11 @@ static cudaError_t launch_rows(const Dims& p, const float* scores, int32_t* sel,
 cudaError_t launch_block_topk(const Dims& p, const float* scores, int32_t* sel,
                               cudaStream_t st, int shared) {
   if (p.B * p.Hkv * p.nR == 0) return cudaSuccess;
+  if (p.tree_mask) {                                       // as few keys a thread as hold a row
+    if (p.nB <= 1024) return launch_tree_rows<256, 4>(p, scores, sel, st);
+    if (p.nB <= 8192 + 1) return launch_tree_rows<256, 32>(p, scores, sel, st);
+    return launch_tree_rows<1024, 32>(p, scores, sel, st);
+  }
   // long rows (decode at 1M context: 8192 candidates) get more threads per row
   if (p.nB > 2048) return launch_rows<1024>(p, scores, sel, st, shared);
   return launch_rows<256>(p, scores, sel, st, shared);

@@ -97,8 +97,8 @@ index_pack_kernel(const T* __restrict__ x, const int32_t* __restrict__ starts,
 #pragma unroll
     for (int s = 1; s < kLanes; s <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, s));
     if (pos[f] < 0) continue;
-    const int blk = (int)(pos[f] / kIndexBlock), r = (int)(pos[f] % kIndexBlock);
-    const int phys = physical_index_block(p, b, blk);
+    const int r = (int)(pos[f] % kIndexBlock);
+    const int phys = physical_index_block(p, b, (int)(pos[f] / kIndexBlock));
     if (phys < 0) continue;
     uint8_t* rec = cache + (size_t)phys * index_record(D);
     uint2 c = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);        // NaN codes of a row that is not finite

@@ -193,6 +193,30 @@ def test_selection(c, topk):
     sel.check("sel")
 
 
+@pytest.mark.parametrize("lens,n,topk", [([1_199_000, 700_000], 2, 64), ([1_199_000], 1, 700), ([140_000, 90_000], 3, 300),
+                                         ([1_040_000], 3, 64), ([127_000], 5, 129)])
+def test_selection_of_many_blocks(lens, n, topk):
+    """Distinct scores (ranked candidates), and scores with few values (ties over the whole row)."""
+    cap = max(lens) + 64
+    shape = _lib.make_shape(len(lens), n, cap, 2, 2, 64, 64, 128, topk, 1)
+    paths, mask = _random_tree(len(lens), n, lens, cap, 1)
+    lens_t = torch.tensor(lens, dtype=torch.int32).cuda()
+    rng = np.random.default_rng(2)
+    shp = (len(lens), 2, n, shape.n_blocks)
+    for x in (rng.standard_normal(shp), rng.integers(0, 5, shp), np.full(shp, -np.inf),
+              np.where(rng.random(shp) < 0.01, rng.standard_normal(shp), -1.0)):
+        x = x.astype(np.float32)
+        sel = guarded_like((*shp[:3], topk), torch.int32)
+        _lib.msa_block_topk_tree(shape, lens_t, mask, torch.tensor(x).cuda(), sel.tensor)
+        _ok()
+        for b, length in enumerate(lens):
+            for h in range(2):
+                for i, path in enumerate(paths[b]):
+                    want = tree_ops.select(x[b, h, i], length + len(path) - 1, 128, topk)
+                    assert sel.tensor[b, h, i].tolist() == want
+        sel.check("sel")
+
+
 # --------------------------------------------------------------------- attention
 
 ATTEND = [
