@@ -11,6 +11,6 @@ from ._lib import (MsaError, MsaShape, make_commit_tensors, make_gather_tensors,
                    msa_sparse_decode_mass, msa_sparse_decode_packed, msa_sparse_decode_tree,
                    msa_sparse_prefill, msa_tree_commit, msa_tree_mask, msa_workspace_bytes,
                    shape_from_config)
-from .api import (Rope, alloc_decode_outputs, alloc_packed_cache, alloc_prefill_outputs, decode,
-                  decode_packed, evict, evict_paged, prefill, rope, rope_freqs, run_decode,
-                  run_prefill)
+from .api import (Rope, alloc_decode_outputs, alloc_index_cache, alloc_packed_cache,
+                  alloc_prefill_outputs, commit_tree, decode, decode_packed, decode_tree, evict,
+                  evict_paged, pack_index, prefill, rope, rope_freqs, run_decode, run_prefill)

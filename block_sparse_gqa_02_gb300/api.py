@@ -9,11 +9,12 @@ from dataclasses import dataclass
 import torch
 
 from . import _lib
-from ._lib import (make_gather_tensors, make_rope, make_rope_tensors, make_shape, msa_block_topk,
-                   msa_block_topk_ragged, msa_cache_evict, msa_cache_gather, msa_cache_pack,
-                   msa_index_scores, msa_index_scores_paged, msa_rope, msa_sparse_decode,
-                   msa_sparse_decode_mass, msa_sparse_decode_packed, msa_sparse_prefill,
-                   msa_workspace_bytes)
+from ._lib import (make_commit_tensors, make_gather_tensors, make_rope, make_rope_tensors, make_shape,
+                   msa_block_topk, msa_block_topk_ragged, msa_block_topk_tree, msa_cache_evict,
+                   msa_cache_gather, msa_cache_pack, msa_index_pack, msa_index_scores,
+                   msa_index_scores_paged, msa_index_scores_tree, msa_rope, msa_sparse_decode,
+                   msa_sparse_decode_mass, msa_sparse_decode_packed, msa_sparse_decode_tree,
+                   msa_sparse_prefill, msa_tree_commit, msa_tree_mask, msa_workspace_bytes)
 
 _DT = {torch.float32: "f32", torch.bfloat16: "bf16"}
 
@@ -284,6 +285,125 @@ def evict(k_cache, v_cache, idx_k, mass, keep, n_first=1, n_recent=2, block_size
                 mass=out[:, :, :blocks].contiguous(), kept=kept)
 
 
+def alloc_index_cache(n_phys, index_dim=128, device="cuda"):
+    """An 8-bit index-key cache of n_phys blocks of 128 keys (layout in include/msa.h)."""
+    return torch.zeros((n_phys, 128 * (index_dim + 1)), dtype=torch.uint8, device=device)
+
+
+def pack_index(idx_k, cache, seq_lens=None, block_table=None, starts=None, capacity=None):
+    """Packs index keys idx_k [B,n,dI] into an 8-bit cache (alloc_index_cache): token i of sequence
+    b at position starts[b] + i, or at seq_lens[b] - n + i without starts; positions outside
+    [0, seq_lens[b]) are not stored.  capacity: positions of a sequence (default: whole blocks)."""
+    B, n, dI = idx_k.shape
+    n_phys = cache.shape[0]
+    if capacity is None:
+        capacity = 128 * (block_table.shape[1] if block_table is not None else n_phys // B)
+    shape = make_shape(B, 1, capacity, 1, 1, 128, dI, 128, 1, 1, _DT[idx_k.dtype])
+    if block_table is not None:
+        _check_shape(block_table, "block_table", (B, shape.n_blocks))
+    _check_shape(cache, "cache", (n_phys, 128 * (dI + 1)))
+    msa_index_pack(shape, n, starts, seq_lens, block_table, n_phys, idx_k, cache)
+
+
+def decode_tree(q, k, v, idx_q, idx_k, k_cache, v_cache, idx_cache, seq_lens, parents,
+                block_table=None, capacity=None, block_size=128, top_k=64, sm_scale=0.0,
+                index_scale=0.0, rope=None, positions=None):
+    """One MSA decode step over a tree of N <= 64 drafted tokens a sequence (N = 1: a decode step of
+    the new token, which is not in the caches yet).  q [B,N,Hq,d]; k, v [B,Hkv,N,d];
+    idx_q [B,N,Hkv,dI]; idx_k [B,N,dI]; parents int32 [B,N]: an earlier token of the tree, -1 for
+    the last cached token (any other value: the sequence has no such token).  Every token gets
+    what decode gives it with its path from the root appended to the caches.
+
+    seq_lens int32 [B]: cached tokens, the drafts not counted.  k_cache, v_cache [B,Hkv,L,d], or
+    with a block_table (int32 [B, blocks]) pools [P,Hkv,block_size,d].  idx_cache: [B,L,dI] or
+    [P,block_size,dI] of q's type, or an 8-bit cache (alloc_index_cache), whose drafts are packed
+    first.  capacity: positions of a sequence (default: L, or all that the table holds); tokens
+    past it are absent.  With a Rope, q, k, idx_q and idx_k are rotated (copies) to the tokens'
+    positions: seq_lens + depth, or with positions (int32 [B]) positions + depth, for caches that
+    were cut by evict or evict_paged.
+
+    Nothing is written to the caches: commit_tree does that for the tokens that are accepted.
+    Returns a dict with out [B,N,Hq,d], lse [B,Hq,N], scores, sel, mask, positions, and the
+    drafts as the caches hold them (k, v, idx_k)."""
+    B, N, Hq, d = q.shape
+    Hkv, dI = k.shape[1], idx_q.shape[-1]
+    packed = idx_cache.dtype is torch.uint8
+    if capacity is None:
+        capacity = k_cache.shape[2] if block_table is None else block_table.shape[1] * block_size
+    shape = make_shape(B, N, capacity, Hq, Hkv, d, dI, block_size, top_k, 1, _DT[q.dtype], sm_scale,
+                       index_scale)
+    _check_shape(parents, "parents", (B, N))
+    _check_shape(k, "k", (B, Hkv, N, d))
+    _check_shape(v, "v", (B, Hkv, N, d))
+    _check_shape(idx_q, "idx_q", (B, N, Hkv, dI))
+    _check_shape(idx_k, "idx_k", (B, N, dI))
+    _check_positions(positions, rope, B)
+    n_phys = _tree_caches(shape, k_cache, v_cache, idx_cache, block_table, packed)
+    dev = q.device
+    mask = torch.empty((B, N), dtype=torch.int64, device=dev)
+    pos = torch.empty((B, N), dtype=torch.int32, device=dev)
+    ws = torch.empty(max(16, msa_workspace_bytes(shape, 5)) // 4 + 4, dtype=torch.float32, device=dev)
+    msa_tree_mask(shape, seq_lens, parents, mask, pos)
+    if rope is not None:
+        at = pos if positions is None else pos + (positions - seq_lens)[:, None]
+        index = rope.freqs if rope.index_freqs is None else rope.index_freqs
+        rows = [(x, torch.empty_like(x), f, h)
+                for x, f, h in ((q, rope.freqs, False), (k, rope.freqs, True),
+                                (idx_q, index, False), (idx_k, index, False))]
+        msa_rope(make_rope(B, N, _DT[q.dtype], 0, rope.scale, rope.interleaved),
+                 make_rope_tensors(rows), at)
+        q, k, idx_q, idx_k = (y for _, y, _, _ in rows)
+    if packed:
+        drafts = torch.empty((B, 128 * (dI + 1)), dtype=torch.uint8, device=dev)
+        msa_index_pack(make_shape(B, 1, N, Hq, Hkv, d, dI, 128, 1, 1, _DT[q.dtype]), N, None, None,
+                       None, B, idx_k, drafts)
+        idx_k = drafts
+    bufs = alloc_prefill_outputs(shape, dev, q.dtype)
+    msa_index_scores_tree(shape, seq_lens, block_table, n_phys, mask, idx_q, idx_cache, idx_k,
+                          bufs["scores"], packed=packed)
+    msa_block_topk_tree(shape, seq_lens, mask, bufs["scores"], bufs["sel"])
+    msa_sparse_decode_tree(shape, seq_lens, block_table, n_phys, mask, q, k_cache, v_cache, k, v,
+                           bufs["sel"], bufs["out"], bufs["lse"], ws)
+    bufs.update(mask=mask, positions=pos, k=k, v=v, idx_k=idx_k)
+    return bufs
+
+
+def _tree_caches(shape, k_cache, v_cache, idx_cache, block_table, packed):
+    """Checks the caches of a tree step against each other; the number of physical blocks."""
+    B, Hkv, d, dI, bs = shape.batch, shape.n_heads_kv, shape.head_dim, shape.index_dim, shape.block_size
+    rows = (B, Hkv, shape.seq_k, d)
+    index = (B, shape.seq_k, dI)
+    n_phys = B * shape.n_blocks
+    if block_table is not None:
+        _check_shape(block_table, "block_table", (B, shape.n_blocks))
+        n_phys = k_cache.shape[0]
+        rows, index = (n_phys, Hkv, bs, d), (n_phys, bs, dI)
+    _check_shape(k_cache, "k_cache", rows)
+    _check_shape(v_cache, "v_cache", rows)
+    _check_shape(idx_cache, "idx_cache", (n_phys, 128 * (dI + 1)) if packed else index)
+    return n_phys
+
+
+def commit_tree(step, accepted, k_cache, v_cache, idx_cache, seq_lens, block_table=None,
+                capacity=None, block_size=128):
+    """Moves the accepted tokens of a decode_tree step into its caches, in place: token
+    accepted[b, i] (int32 [B,n]; a list ends at its first entry outside [0, N)) becomes position
+    seq_lens[b] + i, and seq_lens grows by the number of them.  The tokens should be a path of
+    the tree, root first: they are stored as they were rotated."""
+    k, v, idx_k = step["k"], step["v"], step["idx_k"]
+    B, Hkv, N, d = k.shape
+    packed = idx_cache.dtype is torch.uint8
+    dI = idx_cache.shape[-1] // 128 - 1 if packed else idx_cache.shape[-1]
+    if capacity is None:
+        capacity = k_cache.shape[2] if block_table is None else block_table.shape[1] * block_size
+    shape = make_shape(B, N, capacity, Hkv, Hkv, d, dI, block_size, 1, 1, _DT[k.dtype])
+    n_phys = _tree_caches(shape, k_cache, v_cache, idx_cache, block_table, packed)
+    rows = [(k, k_cache), (v, v_cache)] + ([] if packed else [(idx_k, idx_cache)])
+    msa_tree_commit(shape, seq_lens, block_table, n_phys, accepted,
+                    make_commit_tensors(rows, [(idx_k, idx_cache)] if packed else []), seq_lens)
+
+
 __all__ = ["prefill", "decode", "run_prefill", "run_decode", "alloc_prefill_outputs",
            "alloc_decode_outputs", "Rope", "rope", "rope_freqs", "alloc_packed_cache",
-           "decode_packed", "evict", "evict_paged", "_lib"]
+           "decode_packed", "evict", "evict_paged", "alloc_index_cache", "pack_index", "decode_tree",
+           "commit_tree", "_lib"]
