@@ -226,6 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) tree_topk_kernel(co
   __shared__ int warp_sums[kWarps];
   __shared__ int s_count;
   ptx::grid_wait();
+  ptx::launch_dependents();
   const int row = blockIdx.x, tid = threadIdx.x;
   const int m = row % p.nR, b = row / (p.Hkv * p.nR);
   const int L = seq_len_of(p, b);

@@ -75,6 +75,7 @@ index_pack_kernel(const T* __restrict__ x, const int32_t* __restrict__ starts,
                   uint8_t* __restrict__ cache, Dims p, int n, int per_seq) {
   constexpr int kLanes = D / 8, kRows = kThreads / kLanes;
   ptx::grid_wait();
+  ptx::launch_dependents();
   const int b = blockIdx.x / per_seq, part = blockIdx.x % per_seq;
   const int L = seq_len_of(p, b), sub = threadIdx.x % kLanes;
   const long long start = starts ? (long long)starts[b] : (long long)L - n;
@@ -120,6 +121,7 @@ index_unpack_kernel(const uint8_t* __restrict__ cache, const int32_t* __restrict
                     T* __restrict__ x, Dims p, int n, int per_seq) {
   constexpr int kLanes = D / 8, kRows = kThreads / kLanes;
   ptx::grid_wait();
+  ptx::launch_dependents();
   const int b = blockIdx.x / per_seq, part = blockIdx.x % per_seq;
   const int L = seq_len_of(p, b), sub = threadIdx.x % kLanes;
   const long long start = starts ? (long long)starts[b] : (long long)L - n;

@@ -22,6 +22,7 @@ tree_mask_kernel(const int32_t* __restrict__ parents, TreeWord* __restrict__ mas
   __shared__ TreeWord path[64];
   __shared__ int up[64];
   ptx::grid_wait();
+  ptx::launch_dependents();
   const int b = blockIdx.x, lane = threadIdx.x, n = p.nR;
   const int L = seq_len_of(p, b);
 #pragma unroll
@@ -82,6 +83,7 @@ tree_commit_kernel(const __grid_constant__ CommitArgs a, const int32_t* __restri
   __shared__ int s_count;
   cg::cluster_group cluster = cg::this_cluster();
   ptx::grid_wait();
+  ptx::launch_dependents();
   const int parts = (int)cluster.num_blocks(), part = (int)cluster.block_rank();
   const int b = blockIdx.x / parts, tid = threadIdx.x;
   const int L = seq_len_of(p, b);

@@ -7,13 +7,16 @@ namespace msa {
 
 using TreeWord = unsigned long long;   // bit a: drafted token a
 
-// Path of drafted token i of sequence b with cache length L, 0 when the tree has no such token
+// Path of drafted token i (mask word m) of a sequence with cache length L, 0 when the tree has no such token
 // there: bits past the tree's tokens are dropped, and a token past the capacity has no place.
-__device__ __forceinline__ TreeWord tree_path(const Dims& p, int b, int i, int L) {
-  TreeWord m = p.tree_mask[(size_t)b * p.nR + i];
+__device__ __forceinline__ TreeWord tree_path_of(const Dims& p, TreeWord m, int i, int L) {
   if (p.nR < 64) m &= (1ull << p.nR) - 1;
   if (!(m >> i & 1)) return 0;
   return L + __popcll(m) - 1 < p.Sk ? m : 0;
+}
+
+__device__ __forceinline__ TreeWord tree_path(const Dims& p, int b, int i, int L) {
+  return tree_path_of(p, p.tree_mask[(size_t)b * p.nR + i], i, L);
 }
 
 // Position of a token from its path (which is not 0).

@@ -70,6 +70,7 @@ tree_decode_simt(const T* __restrict__ q, const T* __restrict__ k, const T* __re
   constexpr int kChunk = 16 / (int)sizeof(T);
   extern __shared__ __align__(16) unsigned char smem[];
   ptx::grid_wait();
+  ptx::launch_dependents();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int split = blockIdx.x, bg = blockIdx.z, b = bg / p.Hkv, g = bg % p.Hkv;
   const int node = blockIdx.y % p.nR, h0 = blockIdx.y / p.nR * kH;
@@ -239,6 +240,7 @@ tree_combine(const float* __restrict__ ws_o, const float* __restrict__ ws_l, T* 
   constexpr int kVec = D / 32, kRows = 8 / kRowWarps;
   __shared__ float part[kRowWarps > 1 ? kRowWarps : 1][D + 1];
   ptx::grid_wait();
+  ptx::launch_dependents();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, sub = warp % kRowWarps;
   const long long row = (long long)blockIdx.x * kRows + warp / kRowWarps;
   if (row >= (long long)p.B * p.nR * p.Hq) return;         // whole CTAs where warps share a row

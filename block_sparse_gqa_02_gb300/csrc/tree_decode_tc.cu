@@ -52,7 +52,6 @@ struct __align__(1024) Smem {
   int blocks[kMaxItems];
   uint32_t bitmap[kMaxWords];
   uint16_t before[kMaxWords];          // blocks in the words before
-  int warp_sum[11];
   TreeWord sel[2];                     // tokens that selected the block of the first drafted position, the next
   TreeWord late;                       // tokens whose position is in that next block
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
@@ -131,33 +130,38 @@ tree_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
   extern __shared__ uint8_t smem_raw[];
   S& s = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   ptx::grid_wait();
+  ptx::launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
   const int n_split = gridDim.x, split = blockIdx.x;
   const int bg = blockIdx.z, b = bg / p.Hkv, g = bg % p.Hkv, G = p.G;
   const int Gp = 1 << lg, per_cta = kTiles * kTileRows >> lg;   // rows of a token, tokens
   const int node0 = blockIdx.y * per_cta;
   const int n_nodes = min(per_cta, p.nR - node0);
-  const int L = seq_len_of(p, b);
-  const int first = L / kBk;                               // block of the first drafted position
   const int words = (p.nB + 31) / 32;
   const volatile int* abort = &s.abort;
 
-  // Q and the first entries of the selections are on their way while the rest is set up
-  constexpr int kQ = (kTiles * kTileRows * (kD / 8) + kThreads - 1) / kThreads, kSel = 4;
-  uint4 qv[kQ];
-#pragma unroll
-  for (int i = 0; i < kQ; ++i) {
-    const int e = tid + i * kThreads, r = e / (kD / 8), u = e % (kD / 8), h = r & (Gp - 1);
-    qv[i] = make_uint4(0, 0, 0, 0);
-    if (r >> lg < n_nodes && h < G)
-      qv[i] = *reinterpret_cast<const uint4*>(
-          q + (((size_t)b * p.nR + node0 + (r >> lg)) * p.Hq + g * G + h) * kD + u * 8);
-  }
+  // The set-up works on all warps but the producer's, which starts its copies as soon as the union
+  // is known.  What comes from memory is on its way first, all at once.
+  constexpr int kOthers = kThreads - 32;
+  const int me = warp == kProducerWarp ? -1 : warp < kProducerWarp ? tid : tid - 32;
+  const int length = p.seq_lens[b];
+  const TreeWord word = me >= 0 && me < p.nR ? p.tree_mask[(size_t)b * p.nR + me] : 0;
+  constexpr int kQ = (kTiles * kTileRows * (kD / 8) + kOthers - 1) / kOthers, kSel = 4;
   const int32_t* srow = sel + ((size_t)bg * p.nR + node0) * p.k;
   const int entries = n_nodes * p.k;
   int sv0[kSel], st0[kSel];                                // block and token of this thread's first entries
 #pragma unroll
-  for (int i = 0; i < kSel; ++i) sv0[i] = tid + i * kThreads < entries ? srow[tid + i * kThreads] : -1;
+  for (int i = 0; i < kSel; ++i)
+    sv0[i] = me >= 0 && me + i * kOthers < entries ? srow[me + i * kOthers] : -1;
+  uint4 qv[kQ];
+#pragma unroll
+  for (int i = 0; i < kQ; ++i) {
+    const int e = me + i * kOthers, r = e / (kD / 8), u = e % (kD / 8), h = r & (Gp - 1);
+    qv[i] = make_uint4(0, 0, 0, 0);
+    if (me >= 0 && r >> lg < n_nodes && h < G)
+      qv[i] = *reinterpret_cast<const uint4*>(
+          q + (((size_t)b * p.nR + node0 + (r >> lg)) * p.Hq + g * G + h) * kD + u * 8);
+  }
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       ptx::mbar_init(&s.k_full[i], 1);
@@ -183,68 +187,37 @@ tree_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
     ptx::tmem_relinquish();
   }
   for (int w = tid; w < words; w += kThreads) s.bitmap[w] = 0;
-  if (tid < 64) s.path[tid] = tid < p.nR ? tree_path(p, b, tid, L) : 0;
+  for (int i = tid; i < kMaxItems; i += kThreads) s.mask[i] = 0;
 #pragma unroll
-  for (int i = 0; i < kSel; ++i) st0[i] = (tid + i * kThreads) / p.k;
+  for (int i = 0; i < kSel; ++i) st0[i] = (me + i * kOthers) / p.k;
+  const int L = length < 0 ? 0 : length > p.Sk ? p.Sk : length;
+  const int first = L / kBk;                               // block of the first drafted position
+  if (me >= 0 && me < 64) s.path[me] = me < p.nR ? tree_path_of(p, word, me, L) : 0;
+  ptx::tc_fence_before_sync();
   __syncthreads();
+  ptx::tc_fence_after_sync();
 
   // ---- union of the tokens' selections, over blocks with cached keys
-  if (tid < 64 && s.path[tid] && tree_pos(s.path[tid], L) / kBk == first + 1)
-    set_bit(s.late, tid);
   // calls f(entry's block, token of the CTA) for every entry
   auto each_entry = [&](auto f) {
 #pragma unroll
-    for (int i = 0; i < kSel; ++i) {
+    for (int i = 0; i < kSel; ++i)
       if (sv0[i] >= 0) f(sv0[i], st0[i]);
-    }
-    for (int e = tid + kSel * kThreads; e < entries; e += kThreads) f(srow[e], e / p.k);
+    for (int e = me + kSel * kOthers; e < entries; e += kOthers) f(srow[e], e / p.k);
   };
-  each_entry([&](int blk, int t) {
-    if (blk < 0 || blk >= p.nB || s.path[node0 + t] == 0) return;
-    if (blk * kBk < L) atomicOr(&s.bitmap[blk >> 5], 1u << (blk & 31));
-    if (blk == first || blk == first + 1) set_bit(s.sel[blk - first], node0 + t);
-  });
-  // Q as A operands: row r = token * Gp + head, K-major with the 128-byte swizzle (16-byte unit u of
-  // row r at unit u ^ (r % 8)); zero for heads past the group and absent tokens
-#pragma unroll
-  for (int i = 0; i < kQ; ++i) {
-    const int e = tid + i * kThreads, r = e / (kD / 8), u = e % (kD / 8);
-    if (r >= kTiles * kTileRows) continue;
-    if (r >> lg < n_nodes && s.path[node0 + (r >> lg)] == 0) qv[i] = make_uint4(0, 0, 0, 0);
-    *reinterpret_cast<uint4*>(s.q[r / kTileRows] + (u >> 3) * kTileRows * kRowBytes +
-                              r % kTileRows * kRowBytes + (((u & 7) ^ (r & 7)) << 4)) = qv[i];
+  if (me >= 0) {
+    if (me < 64 && s.path[me] && tree_pos(s.path[me], L) / kBk == first + 1) set_bit(s.late, me);
+    each_entry([&](int blk, int t) {
+      if (blk < 0 || blk >= p.nB || s.path[node0 + t] == 0) return;
+      if (blk * kBk < L) atomicOr(&s.bitmap[blk >> 5], 1u << (blk & 31));
+      if (blk == first || blk == first + 1) set_bit(s.sel[blk - first], node0 + t);
+    });
   }
-  ptx::fence_proxy_async_smem();
   __syncthreads();
-  // blocks before each word of the bitmap: three words a thread
-  {
-    constexpr int kPer = (kMaxWords + kThreads - 1) / kThreads;
-    int c[kPer], sum = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int w = tid * kPer + i;
-      c[i] = w < words ? __popc(s.bitmap[w]) : 0;
-      sum += c[i];
-    }
-    int incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    if (lane == 31) s.warp_sum[warp] = incl;
-    __syncthreads();
-    int at = incl - sum;
-    for (int w = 0; w < warp; ++w) at += s.warp_sum[w];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int w = tid * kPer + i;
-      if (w < words) s.before[w] = (uint16_t)at;
-      at += c[i];
-    }
-  }
-  int n_union = 0;
-  for (int w = 0; w < kThreads / 32; ++w) n_union += s.warp_sum[w];
+  const uint32_t tmem = s.tmem_base;
+  int n_union = 0;                                         // every warp counts for itself
+  for (int w = lane; w < words; w += 32) n_union += __popc(s.bitmap[w]);
+  n_union = __reduce_add_sync(0xffffffffu, n_union);
   // the drafted keys count as one more block, the last
   const bool any_draft = s.sel[0] != 0 || s.sel[1] != 0;
   const int total = n_union + (any_draft ? 1 : 0);
@@ -253,23 +226,51 @@ tree_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
   const int n_items = p1 - p0;                             // at most kMaxItems, by the launcher
   const int n_blk = min(p1, n_union) - p0;                 // items that are blocks (may be < 0: none)
   const bool draft_here = any_draft && p1 == total && n_items > 0;
-  for (int i = tid; i < n_items; i += kThreads) s.mask[i] = 0;
-  __syncthreads();
-  for (int w = tid; w < words; w += kThreads) {
-    uint32_t bits = s.bitmap[w];
-    for (int at = (int)s.before[w] - p0; bits; bits &= bits - 1, ++at)
-      if (at >= 0 && at < n_blk) s.blocks[at] = w * 32 + __ffs(bits) - 1;
+  // calls f(word, its bits, blocks before it) for the bitmap's words, by one warp
+  auto each_word = [&](auto f) {
+    int base = 0;
+    for (int w0 = 0; w0 < words; w0 += 32) {
+      const uint32_t bits = w0 + lane < words ? s.bitmap[w0 + lane] : 0;
+      int incl = __popc(bits);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (w0 + lane < words) f(w0 + lane, bits, base + incl - __popc(bits));
+      base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+  };
+  if (me < 0) {
+    each_word([&](int w, uint32_t bits, int at) {          // the split's blocks, in order
+      for (at -= p0; bits; bits &= bits - 1, ++at)
+        if (at >= 0 && at < n_blk) s.blocks[at] = w * 32 + __ffs(bits) - 1;
+    });
+    __syncwarp();
+    asm volatile("bar.arrive 3, %0;" ::"n"(kThreads) : "memory");
+  } else {
+    if (warp == kMmaWarp)
+      each_word([&](int w, uint32_t, int at) { s.before[w] = (uint16_t)at; });
+    // Q as A operands: row r = token * Gp + head, K-major with the 128-byte swizzle (16-byte unit u of
+    // row r at unit u ^ (r % 8)); zero for heads past the group and absent tokens
+#pragma unroll
+    for (int i = 0; i < kQ; ++i) {
+      const int e = me + i * kOthers, r = e / (kD / 8), u = e % (kD / 8);
+      if (r >= kTiles * kTileRows) continue;
+      if (r >> lg < n_nodes && s.path[node0 + (r >> lg)] == 0) qv[i] = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(s.q[r / kTileRows] + (u >> 3) * kTileRows * kRowBytes +
+                                r % kTileRows * kRowBytes + (((u & 7) ^ (r & 7)) << 4)) = qv[i];
+    }
+    ptx::fence_proxy_async_smem();
+    asm volatile("bar.sync 4, %0;" ::"n"(kOthers) : "memory");
+    each_entry([&](int blk, int t) {
+      if (blk < 0 || blk >= p.nB || blk * kBk >= L || s.path[node0 + t] == 0) return;
+      const int at = (int)s.before[blk >> 5] +
+                     __popc(s.bitmap[blk >> 5] & ((1u << (blk & 31)) - 1)) - p0;
+      if (at >= 0 && at < n_blk) set_bit(s.mask[at], t);
+    });
+    asm volatile("bar.sync 3, %0;" ::"n"(kThreads) : "memory");
   }
-  each_entry([&](int blk, int t) {
-    if (blk < 0 || blk >= p.nB || blk * kBk >= L || s.path[node0 + t] == 0) return;
-    const int at = (int)s.before[blk >> 5] +
-                   __popc(s.bitmap[blk >> 5] & ((1u << (blk & 31)) - 1)) - p0;
-    if (at >= 0 && at < n_blk) set_bit(s.mask[at], t);
-  });
-  ptx::tc_fence_before_sync();
-  __syncthreads();
-  ptx::tc_fence_after_sync();
-  const uint32_t tmem = s.tmem_base;
   // steps, and the S buffer of tile i in step n (its use number n / 2); the drafts fill half a block
   const int n_steps = n_items * kSteps - (draft_here && kSteps == 2 ? 1 : 0);
   auto buf_of = [](int i, int n) { return 2 * i + (n & 1); };
@@ -585,6 +586,12 @@ tree_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
     // own Q is no longer read (its last Q.K^T was before its last P.V), and its rows of 2 kD bytes
     // hold kD / 2 values, 16-byte unit u of row r at u ^ (r % units).
     constexpr int kPass = kD / 2, kUnits = kPass / 4;
+    const int hl = R & (Gp - 1);
+    const long long slot =                                   // of this thread's row; -1: none
+        tl < n_nodes && hl < G
+            ? (long long)((((size_t)b * p.nR + node0 + tl) * p.Hq + (size_t)g * G + hl) * n_split + split)
+            : -1;
+    debug_check(slot < 0 || node0 + tl < p.nR, status, kDbgStore);
     uint8_t* stage = s.q[i] + quad * 32 * kD * 2;
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {
@@ -604,21 +611,16 @@ tree_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
       }
       __syncwarp();
 #pragma unroll 4
-      for (int r = lane / kUnits; r < 32; r += 32 / kUnits) {
-        const int u = lane % kUnits, row = i * kTileRows + quad * 32 + r;
-        const int tr = row >> lg, hr = row & (Gp - 1);
-        if (tr >= n_nodes || hr >= G) continue;
-        debug_check(node0 + tr < p.nR, status, kDbgStore);
-        const size_t at = (((size_t)b * p.nR + node0 + tr) * p.Hq + (size_t)g * G + hr) * n_split + split;
+      for (int r0 = 0; r0 < 32; r0 += 32 / kUnits) {
+        const int u = lane % kUnits, r = r0 + lane / kUnits;
+        const long long at = __shfl_sync(0xffffffffu, slot, r);
+        if (at < 0) continue;
         *reinterpret_cast<float4*>(ws_o + at * kD + half * kPass + u * 4) =
             *reinterpret_cast<const float4*>(stage + r * kD * 2 + ((u ^ (r & (kUnits - 1))) << 4));
       }
       __syncwarp();
     }
-    const int hl = R & (Gp - 1);
-    if (tl < n_nodes && hl < G)
-      ws_l[(((size_t)b * p.nR + node0 + tl) * p.Hq + (size_t)g * G + hl) * n_split + split] =
-          some ? (m_used + __log2f(l)) * kLn2 : -INFINITY;
+    if (slot >= 0) ws_l[slot] = some ? (m_used + __log2f(l)) * kLn2 : -INFINITY;
   }
 
   ptx::tc_fence_before_sync();

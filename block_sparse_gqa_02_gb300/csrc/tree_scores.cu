@@ -74,6 +74,7 @@ tree_scores_simt(const T* __restrict__ iq, const void* __restrict__ idx_k,
   float* best = smem + kCols * D;                          // [kWarps][cols rounded up to kCols]
   const int padded = (cols + kCols - 1) / kCols * kCols;
   ptx::grid_wait();
+  ptx::launch_dependents();
   const int blk = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int L = seq_len_of(p, b);
   if (tid < 64) path[tid] = tid < p.nR ? tree_path(p, b, tid, L) : 0;

@@ -12,13 +12,13 @@
 // least 2^-10 of the query's largest; a smaller one is off by at most 2^-10 of the 448 that the
 // largest is scaled to.  Both parts accumulate in the same TMEM columns.
 //
-// Four groups of four epilogue warps take the blocks in turn (one group's chain of waits and loads
+// Two groups of four epilogue warps take the blocks in turn (one group's chain of waits and loads
 // is longer than a block's share of the bandwidth).  They read the accumulator as fragments of 16
 // keys x 8 columns, in which a thread holds four keys of a column: scale, maximum over the four,
 // then over the lanes by halving (4 shuffles for 16 columns).  The maxima of eight blocks collect in
 // one of two buffers, which two further warps write out, 32 bytes of a score row at a time.
-// Warps: 0-15 epilogue (group warp / 4, TMEM lane quadrant warp % 4), 16 TMA producer, 17-18 MMA
-// issuers (every other block: one thread's products leave a gap after a commit), 19-20 writers.  Every wait is bounded.
+// Warps: 0-7 epilogue (group warp / 4, TMEM lane quadrant warp % 4), 8 TMA producer, 9-10 MMA
+// issuers (every other block: one alone takes 260 us where two take 203), 11-12 writers.  Every wait is bounded.
 #include "index_cache.cuh"
 #include "launch.cuh"
 #include "ptx.cuh"
@@ -32,7 +32,7 @@ namespace {
 
 constexpr int kBk = 128, kDI = 128, kRowBytes = 128;
 constexpr int kAcc = 4;                // accumulators in TMEM
-constexpr int kGroups = 4;             // of epilogue warps
+constexpr int kGroups = 2;             // of epilogue warps (with 4: 209 us at 8 x 1M, 16 drafts, with 2 203)
 constexpr int kIssuers = 2;            // warps that issue products
 // A barrier's phases are told apart by parity, so each waiter has to see them one by one: what
 // completes an accumulator's phases is waited for by one group and issued by one warp, and so is
@@ -239,6 +239,7 @@ tree_scores_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
   int* rows = reinterpret_cast<int*>(smem + plan.row_at());        // score row of a column
   Small& s = *reinterpret_cast<Small*>(smem + plan.small_at());
   ptx::grid_wait();
+  ptx::launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
   const int node0 = blockIdx.y * per_group;
   const int n_nodes = min(per_group, p.nR - node0);
