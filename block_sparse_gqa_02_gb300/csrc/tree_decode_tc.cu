@@ -9,13 +9,16 @@
 // The drafted keys are one more block, with a mask of the path a row.
 //
 // More than 128 rows are two tiles that share each block (O0 and O1 take half of TMEM), fewer are
-// one.  A tile has two S buffers, so that the next Q.K^T runs under the softmax: of a whole block for
-// one tile, of half a block's keys for two (with whole blocks and one buffer a tile the tensor cores
-// wait for the softmax: 83 us where this takes 79, ragged 8 x 128K).  Warps: 0-3 and 4-7 softmax and
-// epilogue of a tile each, 8 TMA producer, 9 issues Q.K^T, 10 issues P.V.  P (bf16) is written over
-// S and read by the P.V product from TMEM.  Online softmax in the log2 domain; the running base
-// moves only when a block would push a row's weights past a bound, so O is rarely rescaled.
-// Every wait is bounded.
+// one.  A step is half a block's keys: a tile has two S buffers of 64 columns, so that the next
+// Q.K^T runs under the softmax, and the copies' ring has slots of half a block, freed as soon as
+// they can be.  What bounds it is the bytes in flight: Q takes 32 KiB a tile, so that 144 KiB (two
+// tiles) or 176 KiB (one) are left for keys and values, which at 128 SMs is less than the memory
+// holds back under load.  (With two slots of whole blocks for K and V each, and the block table read
+// in the copies' loop, a ragged 8 x 128K batch of 16 drafts took 78 us.)
+// Warps: 0-3 and 4-7 softmax and epilogue of a tile each, 8 TMA producer, 9 issues Q.K^T, 10 issues
+// P.V.  P (bf16) is written over S and read by the P.V product from TMEM.  Online softmax in the
+// log2 domain; the running base moves only when a step would push a row's weights past a bound, so O
+// is rarely rescaled.  Every wait is bounded.
 #include "launch.cuh"
 #include "ptx.cuh"
 #include "tma_host.cuh"
@@ -29,7 +32,9 @@ namespace {
 constexpr int kBk = 128;
 constexpr int kTileRows = 128;
 constexpr int kRowBytes = 128;
-constexpr int kMaxItems = 1024;        // blocks of a split
+constexpr int kMaxItems = 512;         // blocks of a split
+constexpr int kCols = 64;              // keys of a step
+constexpr int kSteps = kBk / kCols;
 constexpr int kMaxWords = kMaxBlocks / 32;
 constexpr int kThreads = 352;
 constexpr int kProducerWarp = 8;
@@ -43,18 +48,21 @@ template <int kD, int kTiles>
 struct __align__(1024) Smem {
   static constexpr int kChunks = kD / 64;
   static constexpr int kTileBytes = kChunks * kTileRows * kRowBytes;   // [chunk][128 rows][128 B]
-  static constexpr int kStages = kD == 64 ? 4 : 2;
+  static constexpr int kSlotBytes = kChunks * kCols * kRowBytes;       // [chunk][64 keys][128 B]
+  // slots: K is copied a step ahead of V, which is used after the softmax
+  static constexpr int kK = kD == 64 ? 10 : kTiles == 2 ? 5 : 6, kV = kK - 1;
   uint8_t q[kTiles][kTileBytes];
-  uint8_t k[kStages][kTileBytes];
-  uint8_t v[kStages][kTileBytes];
+  uint8_t k[kK][kSlotBytes];
+  uint8_t v[kV][kSlotBytes];
   TreeWord mask[kMaxItems];            // tokens of the CTA that selected the item
   TreeWord path[64];
-  int blocks[kMaxItems];
+  int blocks[kMaxItems];               // the item's block, and where its keys are (outer coordinate)
+  int outer[kMaxItems];
   uint32_t bitmap[kMaxWords];
   uint16_t before[kMaxWords];          // blocks in the words before
   TreeWord sel[2];                     // tokens that selected the block of the first drafted position, the next
   TreeWord late;                       // tokens whose position is in that next block
-  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  uint64_t k_full[kK], k_empty[kK], v_full[kV], v_empty[kV];
   uint64_t s_full[2 * kTiles], p_full[2 * kTiles], pv_done[2 * kTiles], o_full[2], drain[2];
   uint32_t tmem_base;
   int abort;
@@ -123,8 +131,7 @@ tree_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
                       const __nv_bfloat16* __restrict__ q, const int32_t* __restrict__ sel,
                       float* __restrict__ ws_o, float* __restrict__ ws_l, Dims p, int lg, int* status) {
   using S = Smem<kD, kTiles>;
-  constexpr int kStages = S::kStages, kTileBytes = S::kTileBytes;
-  constexpr int kCols = kBk / kTiles, kSteps = kTiles;       // keys of a step, steps of a block
+  constexpr int kK = S::kK, kV = S::kV, kSlotBytes = S::kSlotBytes;
   constexpr uint32_t kIdescQK = ptx::idesc_bf16_f32(128, kCols, 0, 0);
   constexpr uint32_t kIdescPV = ptx::idesc_bf16_f32(128, kD, 0, 1);
   extern __shared__ uint8_t smem_raw[];
@@ -163,9 +170,11 @@ tree_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
           q + (((size_t)b * p.nR + node0 + (r >> lg)) * p.Hq + g * G + h) * kD + u * 8);
   }
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < kK; ++i) {
       ptx::mbar_init(&s.k_full[i], 1);
       ptx::mbar_init(&s.k_empty[i], 1);
+    }
+    for (int i = 0; i < kV; ++i) {
       ptx::mbar_init(&s.v_full[i], 1);
       ptx::mbar_init(&s.v_empty[i], 1);
     }
@@ -247,6 +256,11 @@ tree_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
         if (at >= 0 && at < n_blk) s.blocks[at] = w * 32 + __ffs(bits) - 1;
     });
     __syncwarp();
+    // contiguous cache: (64 dims, key, half of the dims, sequence x head); pools: (.., key in block, ..,
+    // block x head), the table's entries read here, all at once
+    for (int i = lane; i < n_blk; i += 32)
+      s.outer[i] = p.block_table ? p.block_table[(size_t)b * p.nB + s.blocks[i]] * p.Hkv + g : bg;
+    __syncwarp();
     asm volatile("bar.arrive 3, %0;" ::"n"(kThreads) : "memory");
   } else {
     if (warp == kMmaWarp)
@@ -272,58 +286,68 @@ tree_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
     asm volatile("bar.sync 3, %0;" ::"n"(kThreads) : "memory");
   }
   // steps, and the S buffer of tile i in step n (its use number n / 2); the drafts fill half a block
-  const int n_steps = n_items * kSteps - (draft_here && kSteps == 2 ? 1 : 0);
+  const int n_steps = n_items * kSteps - (draft_here ? 1 : 0);
   auto buf_of = [](int i, int n) { return 2 * i + (n & 1); };
 
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------- TMA producer
-    int k_issued = 0, v_issued = 0;
+    // K of step n goes out before V of step n - 1
+    int k_issued = 0, v_issued = 0, ks = 0, vs = 0;
+    uint32_t k_phase = 1, v_phase = 1;
     bool ok = true;
     if (lane == 0 && n_items > 0) {
       ptx::tma_prefetch_desc(&tm_k);
       ptx::tma_prefetch_desc(&tm_v);
     }
-    for (int j = 0; j < n_items; ++j) {
-      if (p.inject == 2 && split == 0 && j > 0) break;      // test hook: no copies any more
-      const bool draft = draft_here && j == n_items - 1;
-      const int st = j % kStages;
-      // contiguous cache: (64 dims, key, half, sequence x head); pools: (.., key in block, .., block x head)
-      int y = 0, z = bg;
-      if (!draft) {
-        const int blk = s.blocks[j];
-        if (p.block_table) z = p.block_table[(size_t)b * p.nB + blk] * p.Hkv + g;
-        else y = blk * kBk;
-        debug_check(blk >= 0 && blk < p.nB && z >= 0 &&
-                        z < (p.block_table ? p.n_phys : p.B) * p.Hkv, status, kDbgCoord);
+    for (int n = 0; n <= n_steps && n_steps > 0; ++n) {
+      if (p.inject == 2 && split == 0 && n > 1) break;      // test hook: no copies any more
+      // coordinates of a step's keys
+      auto place = [&](int step, int& y, int& z) {
+        const int j = step / kSteps;
+        const bool draft = draft_here && j == n_items - 1;
+        y = draft ? 0 : step % kSteps * kCols + (p.block_table ? 0 : s.blocks[j] * kBk);
+        z = draft ? bg : s.outer[j];
+        debug_check(draft || (s.blocks[j] >= 0 && s.blocks[j] < p.nB && z >= 0 &&
+                              z < (p.block_table ? p.n_phys : p.B) * p.Hkv), status, kDbgCoord);
+        return draft;
+      };
+      int y, z;
+      if (n < n_steps) {
+        const bool draft = place(n, y, z);
+        if (!ptx::mbar_wait(&s.k_empty[ks], k_phase, abort)) { ok = false; break; }
+        if (lane == 0) {
+          ptx::mbar_arrive_expect_tx(&s.k_full[ks], kSlotBytes);
+          ptx::tma_load_4d(s.k[ks], draft ? &tm_kd : &tm_k, &s.k_full[ks], 0, y, 0, z);
+        }
+        k_issued = n + 1;
+        if (++ks == kK) ks = 0, k_phase ^= 1;
       }
-      if (!ptx::mbar_wait(&s.k_empty[st], ((j / kStages) & 1) ^ 1, abort)) { ok = false; break; }
-      if (lane == 0) {
-        ptx::mbar_arrive_expect_tx(&s.k_full[st], kTileBytes);
-        ptx::tma_load_4d(s.k[st], draft ? &tm_kd : &tm_k, &s.k_full[st], 0, y, 0, z);
+      if (n > 0) {
+        const bool draft = place(n - 1, y, z);
+        if (!ptx::mbar_wait(&s.v_empty[vs], v_phase, abort)) { ok = false; break; }
+        if (lane == 0) {
+          ptx::mbar_arrive_expect_tx(&s.v_full[vs], kSlotBytes);
+          ptx::tma_load_4d(s.v[vs], draft ? &tm_vd : &tm_v, &s.v_full[vs], 0, y, 0, z);
+        }
+        v_issued = n;
+        if (++vs == kV) vs = 0, v_phase ^= 1;
       }
-      k_issued = j + 1;
-      if (!ptx::mbar_wait(&s.v_empty[st], ((j / kStages) & 1) ^ 1, abort)) { ok = false; break; }
-      if (lane == 0) {
-        ptx::mbar_arrive_expect_tx(&s.v_full[st], kTileBytes);
-        ptx::tma_load_4d(s.v[st], draft ? &tm_vd : &tm_v, &s.v_full[st], 0, y, 0, z);
-      }
-      v_issued = j + 1;
       __syncwarp();
     }
     if (!ok && lane == 0) raise_abort(s, status, 0x601);
     // copies in flight land before the CTA leaves (after a full run they have been used)
     if (lane == 0) {
-      for (int j = k_issued > kStages ? k_issued - kStages : 0; j < k_issued; ++j)
-        ptx::mbar_wait_timed(&s.k_full[j % kStages], (j / kStages) & 1);
-      for (int j = v_issued > kStages ? v_issued - kStages : 0; j < v_issued; ++j)
-        ptx::mbar_wait_timed(&s.v_full[j % kStages], (j / kStages) & 1);
+      for (int j = k_issued > kK ? k_issued - kK : 0; j < k_issued; ++j)
+        ptx::mbar_wait_timed(&s.k_full[j % kK], (j / kK) & 1);
+      for (int j = v_issued > kV ? v_issued - kV : 0; j < v_issued; ++j)
+        ptx::mbar_wait_timed(&s.v_full[j % kV], (j / kV) & 1);
     }
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------- Q.K^T issuer
     bool ok = true, issued_any = false;
     for (int n = 0; ok && n < n_steps; ++n) {
-      const int j = n / kSteps, half = n % kSteps, st = j % kStages;
-      if (half == 0 && !ptx::mbar_wait(&s.k_full[st], (j / kStages) & 1, abort)) { ok = false; break; }
+      const int st = n % kK;
+      if (!ptx::mbar_wait(&s.k_full[st], (n / kK) & 1, abort)) { ok = false; break; }
       for (int i = 0; i < kTiles; ++i) {
         const int buf = buf_of(i, n), use = n >> 1;
         // overwrites the S / P buffer, which the P.V product of its use before reads
@@ -331,15 +355,17 @@ tree_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
         ptx::tc_fence_after_sync();
         if (lane == 0) {
           const uint32_t qa = ptx::smem_u32(s.q[i]);
-          const uint32_t kb = ptx::smem_u32(s.k[st]) + half * kCols * kRowBytes;
+          const uint32_t kb = ptx::smem_u32(s.k[st]);
 #pragma unroll
           for (int kk = 0; kk < kD / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * (kTileRows * kRowBytes) + (kk & 3) * 32;
-            ptx::umma_bf16_ss(tmem + buf * kCols, ptx::smem_desc_k_sw128(qa + off),
-                              ptx::smem_desc_k_sw128(kb + off), kIdescQK, kk > 0 ? 1u : 0u);
+            const uint32_t off = (kk & 3) * 32;
+            ptx::umma_bf16_ss(tmem + buf * kCols,
+                              ptx::smem_desc_k_sw128(qa + (kk >> 2) * (kTileRows * kRowBytes) + off),
+                              ptx::smem_desc_k_sw128(kb + (kk >> 2) * (kCols * kRowBytes) + off), kIdescQK,
+                              kk > 0 ? 1u : 0u);
           }
           ptx::umma_commit(&s.s_full[buf]);
-          if (i == kTiles - 1 && (half == kSteps - 1 || n + 1 == n_steps)) ptx::umma_commit(&s.k_empty[st]);
+          if (i == kTiles - 1) ptx::umma_commit(&s.k_empty[st]);
         }
         issued_any = true;
         __syncwarp();
@@ -354,16 +380,17 @@ tree_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
     // ------------------------------------------------------------ P.V issuer
     bool ok = true, issued_any = false;
     for (int n = 0; ok && n < n_steps; ++n) {
-      const int j = n / kSteps, half = n % kSteps, st = j % kStages;
+      const int j = n / kSteps, st = n % kV;
       const bool draft = draft_here && j == n_items - 1;
-      if (half == 0 && !ptx::mbar_wait(&s.v_full[st], (j / kStages) & 1, abort)) { ok = false; break; }
+      if (!ptx::mbar_wait(&s.v_full[st], (n / kV) & 1, abort)) { ok = false; break; }
       // rows of V that no key of the sequence is in may hold anything, and 0 x NaN is NaN: zeros
-      const int keys = draft ? 64 : L - s.blocks[j] * kBk;
-      if (half == 0 && keys < kBk) {
-        for (int r = draft ? 0 : keys; r < (draft ? 64 : kBk); ++r) {
-          if (draft && s.path[r] != 0) continue;
-          for (int u = lane; u < kD / 8; u += 32)
-            *reinterpret_cast<uint4*>(s.v[st] + (u >> 3) * kBk * kRowBytes + r * kRowBytes + (u & 7) * 16) =
+      const int keys = draft ? 0 : L - s.blocks[j] * kBk - n % kSteps * kCols;
+      if (keys < kCols) {
+#pragma unroll 8
+        for (int e = lane; e < kCols * (kD / 8); e += 32) {
+          const int r = e / (kD / 8), u = e % (kD / 8);
+          if (draft ? s.path[r] == 0 : r >= keys)
+            *reinterpret_cast<uint4*>(s.v[st] + (u >> 3) * kCols * kRowBytes + r * kRowBytes + (u & 7) * 16) =
                 make_uint4(0, 0, 0, 0);
         }
         ptx::fence_proxy_async_smem();
@@ -374,14 +401,14 @@ tree_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
         if (!ptx::mbar_wait(&s.p_full[buf], (n >> 1) & 1, abort)) { ok = false; break; }
         ptx::tc_fence_after_sync();
         if (lane == 0) {
-          const uint32_t vb = ptx::smem_u32(s.v[st]) + half * kCols * kRowBytes;
+          const uint32_t vb = ptx::smem_u32(s.v[st]);
 #pragma unroll
           for (int kk = 0; kk < kCols / 16; ++kk)
             ptx::umma_bf16_ts(tmem + 256 + i * 128, tmem + buf * kCols + kk * 8,
-                              ptx::smem_desc_mn_sw128(vb + kk * 16 * kRowBytes, kBk * kRowBytes, 1024),
+                              ptx::smem_desc_mn_sw128(vb + kk * 16 * kRowBytes, kCols * kRowBytes, 1024),
                               kIdescPV, (n > 0 || kk > 0) ? 1u : 0u);
           ptx::umma_commit(&s.pv_done[buf]);
-          if (i == kTiles - 1 && (half == kSteps - 1 || n + 1 == n_steps)) ptx::umma_commit(&s.v_empty[st]);
+          if (i == kTiles - 1) ptx::umma_commit(&s.v_empty[st]);
           if (n + 1 == n_steps) ptx::umma_commit(&s.o_full[i]);
         }
         issued_any = true;
@@ -638,8 +665,8 @@ cudaError_t launch(const Dims& p, const void* q, const void* k, const void* v, c
                    const void* vd, const int32_t* sel, float* ws_o, float* ws_l, int n_split,
                    cudaStream_t st, int* status) {
   CUtensorMap tk, tv, tkd, tvd;
-  // rows as (64 dims, key, half of the head, outer): one box {64, 128, halves, 1} lands a block as
-  // [half][128 keys][128 B], the swizzled chunks that the products read
+  // rows as (64 dims, key, half of the head, outer): one box {64, 64, halves, 1} lands half a block as
+  // [half of the dims][64 keys][128 B], the swizzled chunks that the products read
   constexpr uint64_t kHalves = kD / 64;
   const uint64_t rows = p.block_table ? (uint64_t)kBk : (uint64_t)p.Sk;
   const uint64_t outer = (uint64_t)p.Hkv * (p.block_table ? (uint64_t)p.n_phys : (uint64_t)p.B);
@@ -647,13 +674,14 @@ cudaError_t launch(const Dims& p, const void* q, const void* k, const void* v, c
   const uint64_t stride[3] = {kD * 2, 128, rows * kD * 2};
   const uint64_t ddims[4] = {64, (uint64_t)p.nR, kHalves, (uint64_t)p.B * p.Hkv};
   const uint64_t dstride[3] = {kD * 2, 128, (uint64_t)p.nR * kD * 2};
-  const uint32_t box[4] = {64, (uint32_t)kBk, (uint32_t)kHalves, 1};
+  const uint32_t box[4] = {64, (uint32_t)kCols, (uint32_t)kHalves, 1};
   cudaError_t e = make_tensor_map_bf16(&tk, k, 4, dims, stride, box);
   if (e == cudaSuccess) e = make_tensor_map_bf16(&tv, v, 4, dims, stride, box);
   if (e == cudaSuccess) e = make_tensor_map_bf16(&tkd, kd, 4, ddims, dstride, box);
   if (e == cudaSuccess) e = make_tensor_map_bf16(&tvd, vd, 4, ddims, dstride, box);
   if (e != cudaSuccess) return e;
-  const size_t smem = sizeof(Smem<kD, kTiles>) + 1024;
+  constexpr size_t smem = sizeof(Smem<kD, kTiles>) + 1024;
+  static_assert(smem <= 232448, "shared memory of a CTA");
   e = cudaFuncSetAttribute(tree_decode_tc_kernel<kD, kTiles>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
