@@ -1,6 +1,6 @@
 // Attention of a tree of drafted tokens over the selected blocks and its own tokens: the
-// CUDA-core kernel (fp32, other block sizes, more than 64 heads a group's shapes do not occur)
-// and the join of the splits.  (bf16 in blocks of 128: tree_decode_tc.cu.)
+// CUDA-core kernel (fp32, other block sizes) and the join of the splits.  (bf16 in blocks of 128:
+// tree_decode_tc.cu.)
 //
 // CTA = (split of the token's selection, token x heads, sequence x KV head).  A warp takes 32 keys
 // at a time and keeps the running maximum, sum and output of kH heads by itself: scores with a
@@ -231,8 +231,9 @@ tree_decode_simt(const T* __restrict__ q, const T* __restrict__ k, const T* __re
 }
 
 // o = sum_s exp(lse_s - lse) o_s with lse = log sum_s exp(lse_s), of a row of out [B, nR, Hq, D].
-// kRowWarps warps a row take every kRowWarps-th split each: one warp while there are few splits, all
-// eight of the CTA when the loads of many would follow one another (34 splits: 17 -> 4 us).
+// kRowWarps warps a row take every kRowWarps-th split each, with the loads of eight in flight: one
+// warp while there are few splits, all eight of the CTA when there are many (34 splits of 128 rows,
+// cold: 17 us with one warp a row, 6 with eight).
 template <typename T, int D, int kRowWarps>
 __global__ void __launch_bounds__(256)
 tree_combine(const float* __restrict__ ws_o, const float* __restrict__ ws_l, T* __restrict__ out,
@@ -244,23 +245,36 @@ tree_combine(const float* __restrict__ ws_o, const float* __restrict__ ws_l, T* 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, sub = warp % kRowWarps;
   const long long row = (long long)blockIdx.x * kRows + warp / kRowWarps;
   if (row >= (long long)p.B * p.nR * p.Hq) return;         // whole CTAs where warps share a row
+  constexpr int kFlight = 8;
   const float* l = ws_l + row * n_split;
-  float top = -INFINITY;
-  for (int s = lane; s < n_split; s += 32) top = fmaxf(top, l[s]);
+  const float* o = ws_o + row * n_split * D + lane * kVec;
+  float x[kFlight][kVec];
+  auto load = [&](int s0) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int i = 0; i < kFlight; ++i)
+      if (s0 + i * kRowWarps < n_split) load_dims<float, kVec>(o + (size_t)(s0 + i * kRowWarps) * D, x[i]);
+  };
+  float top = lane < n_split ? l[lane] : -INFINITY;
+  load(sub);
+  for (int s = lane + 32; s < n_split; s += 32) top = fmaxf(top, l[s]);
+#pragma unroll
+  for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
   float acc[kVec], den = 0.f;
 #pragma unroll
   for (int i = 0; i < kVec; ++i) acc[i] = 0.f;
   if (top != -INFINITY) {
-#pragma unroll 4
-    for (int s = sub; s < n_split; s += kRowWarps) {
-      const float w = expf(l[s] - top);
-      float x[kVec];
-      load_dims<float, kVec>(ws_o + (row * n_split + s) * D + lane * kVec, x);
-      den += w;
+    for (int s0 = sub; s0 < n_split; s0 += kFlight * kRowWarps) {
+      if (s0 != sub) load(s0);
+      const int mine = s0 + lane * kRowWarps;
+      const float w = lane < kFlight && mine < n_split ? expf(l[mine] - top) : 0.f;
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) acc[i] = fmaf(w, x[i], acc[i]);
+      for (int i = 0; i < kFlight; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, w, i);
+        if (s0 + i * kRowWarps >= n_split) continue;
+        den += wi;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) acc[e] = fmaf(wi, x[i][e], acc[e]);
+      }
     }
   }
   if (kRowWarps > 1) {

@@ -10,11 +10,13 @@
 //
 // More than 128 rows are two tiles that share each block (O0 and O1 take half of TMEM), fewer are
 // one.  A step is half a block's keys: a tile has two S buffers of 64 columns, so that the next
-// Q.K^T runs under the softmax, and the copies' ring has slots of half a block, freed as soon as
-// they can be.  What bounds it is the bytes in flight: Q takes 32 KiB a tile, so that 144 KiB (two
-// tiles) or 176 KiB (one) are left for keys and values, which at 128 SMs is less than the memory
-// holds back under load.  (With two slots of whole blocks for K and V each, and the block table read
-// in the copies' loop, a ragged 8 x 128K batch of 16 drafts took 78 us.)
+// Q.K^T runs under the softmax, and the copies' ring has slots of half a block: Q takes 32 KiB a
+// tile, which leaves 144 KiB (two tiles) or 176 KiB (one) for keys and values.
+// Measured, ragged 8 x 128K, 16 drafts of 16 heads a KV head (206 MB, 128 CTAs): 67 us, of which 4.7
+// set-up, 2.3 to the first S, 46 for 48 steps, 3.5 epilogue and 5 the join; without the products and
+// exponentials (timing only) it takes 8 us less: the steps are bound by the copies' latency at
+// 128 SMs as much as by the tensor cores, which multiply all 256 rows with every block of the union.
+// 2 x 64K, 64 drafts (72 MB from HBM, read by four CTAs each): 79 us, bound by the products.
 // Warps: 0-3 and 4-7 softmax and epilogue of a tile each, 8 TMA producer, 9 issues Q.K^T, 10 issues
 // P.V.  P (bf16) is written over S and read by the P.V product from TMEM.  Online softmax in the
 // log2 domain; the running base moves only when a step would push a row's weights past a bound, so O
