@@ -93,6 +93,14 @@ __device__ __forceinline__ void find_range(const Dims& p, Small& s, int lane) {
     s.rank = s.cnt = 1;
   }
   __syncwarp();
+  if (ctas == p.B) {                                       // a CTA a sequence
+    if (lane == 0) {
+      s.b = c;
+      s.rank = 0;
+      s.nblk = (seq_len_of(p, c) + kBk - 1) / kBk;
+    }
+    return;
+  }
   long long total = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     long long nb = b0 + lane < p.B ? (seq_len_of(p, b0 + lane) + kBk - 1) / kBk : 0;

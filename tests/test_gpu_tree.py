@@ -142,6 +142,12 @@ SCORES = [
     dict(lens=[1000, 129, 1023, 1024], n=16, cap=1100, packed=False, paged=True),
     dict(lens=[2000, 20], n=64, cap=2100, kind="chain", packed=False),
     dict(lens=[600, 100], n=64, cap=700, hkv=8, packed=False, kind="bad"),
+    # caches shorter than a tile, odd head counts, more sequences than SMs
+    dict(lens=[0, 1, 2], n=1, cap=3),
+    dict(lens=[0, 1, 2], n=2, cap=3, packed=False, kind="chain"),
+    dict(lens=[300, 260], n=5, cap=310, hkv=33, group=1, packed=False),
+    dict(lens=[i % 140 for i in range(170)], n=3, cap=150, hkv=2, paged=True),
+    dict(lens=[0] * 160, n=2, cap=129),
     # other dims, types and blocks
     dict(lens=[700, 0, 130], n=6, cap=800, idim=64),
     dict(lens=[700, 0, 130], n=6, cap=800, dtype="f32", paged=True),
@@ -234,6 +240,8 @@ ATTEND = [
     dict(lens=[200] * 20, n=3, cap=260, hkv=8, group=2, topk=1),
     dict(lens=[1200, 0], n=24, cap=1300, hkv=4, group=8, topk=300),
     dict(lens=[900], n=12, cap=1000, topk=4, key_scale=12.0),            # peaked rows, rescaled often
+    dict(lens=[0, 1, 2], n=2, cap=3, kind="chain"),
+    dict(lens=[i % 140 for i in range(90)], n=3, cap=150, hkv=2, paged=True),
     dict(lens=[900, 140], n=20, cap=1000, dim=64, group=8, kind="chain"),
     dict(lens=[900, 140], n=6, cap=1000, dtype="f32", group=16, paged=True),
     dict(lens=[300, 64], n=40, cap=400, dtype="f32", dim=64, group=3, packed=False, block=32, kind="chain"),
