@@ -668,7 +668,8 @@ class CommitTensors:
         self.device = dev = _device()
         self.rows, self.packed = rows, packed
         self.array = (MsaCommitTensor * max(1, len(rows) + len(packed)))()
-        self.shapes = []                     # (batch, tokens or None, first axis and rows of dst)
+        # (batch, tokens, first axis and rows of dst) of the rows, (batch, blocks) of 8-bit keys
+        self.row_shapes, self.packed_shapes = set(), set()
         for i, (src, dst) in enumerate(rows):
             heads = 1 if src.dim() == 3 else src.shape[1]
             if src.dim() not in (3, 4) or dst.dim() != src.dim() or dst.dtype != src.dtype or \
@@ -679,7 +680,7 @@ class CommitTensors:
                 _arg(src, f"src of commit tensor {i}", None, 0, dev),
                 _arg(dst, f"dst of commit tensor {i}", None, 0, dev), heads,
                 src.shape[-1] * src.element_size(), 0)
-            self.shapes.append((src.shape[0], src.shape[-2], dst.shape[0], dst.shape[-2]))
+            self.row_shapes.add((src.shape[0], src.shape[-2], dst.shape[0], dst.shape[-2]))
         for j, (src, dst) in enumerate(packed):
             i = len(rows) + j
             n = src.shape[-1]
@@ -689,10 +690,10 @@ class CommitTensors:
             self.array[i] = MsaCommitTensor(_arg(src, f"src of commit tensor {i}", _U8, 0, dev),
                                             _arg(dst, f"dst of commit tensor {i}", _U8, 0, dev), 1,
                                             n // 128 - 1, 1)
-            self.shapes.append((src.shape[0], None, dst.shape[0], 128))
+            self.packed_shapes.add((src.shape[0], dst.shape[0]))
 
     def __len__(self):
-        return len(self.shapes)
+        return len(self.rows) + len(self.packed)
 
 
 def make_commit_tensors(rows, packed=()) -> CommitTensors:
@@ -706,15 +707,14 @@ def msa_tree_commit(shape: MsaShape, seq_lens, block_table, n_phys, accepted,
     if tensors.device != dev:
         raise ValueError(f"the commit tensors are on CUDA device {tensors.device}, the current one "
                          f"is {dev}")
-    for i, (b, tokens, lead, rows) in enumerate(tensors.shapes):
-        if tokens is None:
-            want, have = (batch, n_phys), (b, lead)
-        elif block_table is None:
-            want, have = (batch, shape.seq_q, batch, shape.seq_k), (b, tokens, lead, rows)
-        else:
-            want, have = (batch, shape.seq_q, n_phys, shape.block_size), (b, tokens, lead, rows)
-        if want != have:
-            raise ValueError(f"commit tensor {i} has (batch, tokens, cache axes) {have}, the call {want}")
+    paged = block_table is not None
+    want = (batch, shape.seq_q) + ((n_phys, shape.block_size) if paged else (batch, shape.seq_k))
+    if tensors.row_shapes and tensors.row_shapes != {want}:
+        raise ValueError(f"commit tensors with (batch, tokens, cache axes) {tensors.row_shapes}, the "
+                         f"call has {want}")
+    if tensors.packed_shapes and tensors.packed_shapes != {(batch, n_phys)}:
+        raise ValueError(f"8-bit index keys with (batch, blocks) {tensors.packed_shapes}, the call has "
+                         f"{(batch, n_phys)}")
     if accepted.dim() != 2 or accepted.shape[0] != batch:
         raise ValueError(f"accepted is {tuple(accepted.shape)}, expected [{batch}, tokens]")
     _check(load().msa_tree_commit(

@@ -340,8 +340,11 @@ cudaError_t decode(const Dims& p, const void* q, const void* k, const void* v, c
   if (tree_decode_tc_supported(p)) {
     e = launch_tree_decode_tc(p, q, k, v, kd, vd, sel, ws_o, ws_l, st, dev_status);
   } else {
-    auto run = p.G <= 2 ? launch_simt<T, D, 2> : p.G <= 4 ? launch_simt<T, D, 4>
-                                                         : launch_simt<T, D, 8>;
+    // heads of a CTA: as many as the group has, up to 16 (each chunk reads K and V again)
+    auto run = p.G <= 2   ? launch_simt<T, D, 2>
+               : p.G <= 4 ? launch_simt<T, D, 4>
+               : p.G <= 8 ? launch_simt<T, D, 8>
+                          : launch_simt<T, D, 16>;
     e = run(p, q, k, v, kd, vd, sel, ws_o, ws_l, n_split, st);
   }
   if (e != cudaSuccess) return e;

@@ -288,15 +288,6 @@ tree_scores_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
   // the sequence's last range takes the drafted keys too, before its blocks
   const int drafted = blk0 + nblk == nB_b && (nblk > 0 || s.rank == 0) ? 1 : 0;
   const int items = nblk + drafted;
-  for (int e = tid; e < 16 * plan.res_row(); e += kThreads) res[e] = kNothing;
-  for (int e = tid; e < 2 * Cp; e += kThreads) dres[e] = kNothing;
-  if (tid < 64) {
-    const TreeWord path = tid < p.nR ? tree_path(p, b, tid, L) : 0;
-    s.path[tid] = path;
-    if (path && tree_pos(path, L) / kBk == first + 1) atomicOr(&s.late, 1ull << tid);
-  }
-  __syncthreads();
-
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------- TMA producer
     // (The loops of this kernel turn once in 700 cycles: stages and phases are counted, not divided
@@ -347,6 +338,16 @@ tree_scores_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
       for (int i = issued > stages ? issued - stages : 0; i < issued; ++i)
         ptx::mbar_wait_timed(&s.full[i % stages], (i / stages) & 1);
   } else {
+    // the producer has started; the other warps set up the tree and the results first
+    const int me = warp > kProducerWarp ? tid - 32 : tid;
+    for (int e = me; e < 16 * plan.res_row(); e += kThreads - 32) res[e] = kNothing;
+    for (int e = me; e < 2 * Cp; e += kThreads - 32) dres[e] = kNothing;
+    if (me < 64) {
+      const TreeWord path = me < p.nR ? tree_path(p, b, me, L) : 0;
+      s.path[me] = path;
+      if (path && tree_pos(path, L) / kBk == first + 1) atomicOr(&s.late, 1ull << me);
+    }
+    asm volatile("bar.sync 4, %0;" ::"n"(kThreads - 32) : "memory");
     // ---- the queries as the B operand, K-major with the 128-byte swizzle (16-byte unit u of row c
     // lies at unit u ^ (c % 8)); a warp a column
     const int wq = warp > kProducerWarp ? warp - 1 : warp;
