@@ -409,3 +409,55 @@ def test_attention_long_ranges(c):
     err = np.abs(out.cpu().double().numpy() - want)
     assert (err <= tol).all(), (err.max(), (err / np.maximum(tol, 1e-30)).max())
     assert (np.abs(lse.cpu().double().numpy() - want_lse) <= tol_lse).all()
+
+
+def test_attention_more_blocks_than_a_list_holds():
+    """Selections of 650 of 700 blocks on 160 (sequence, KV head) pairs: one CTA a pair would need a
+    longer list of blocks than it has, so the selection is split.  The sequences share the pools'
+    blocks.  fp64 on the GPU for some of the pairs."""
+    B, h, g, d, n, nB, topk = 40, 4, 4, 128, 2, 700, 650
+    cap = nB * 128
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    rng = np.random.default_rng(3)
+    lens = [int(x) for x in rng.integers(cap - 3000, cap - 2, B)]
+    paths, mask = _random_tree(B, n, lens, cap, 3)
+    k, v = (torch.randn(nB, h, 128, d, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    kd, vd = (torch.randn(B, h, n, d, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    q = torch.randn(B, n, h * g, d, generator=gen, device="cuda").bfloat16()
+    table = torch.stack([torch.randperm(nB, generator=gen, device="cuda") for _ in range(B)]).to(torch.int32)
+    sel = np.full((B, h, n, topk), -1, dtype=np.int32)
+    for b in range(B):
+        for j in range(h):
+            for i, path in enumerate(paths[b]):
+                cur = (lens[b] + len(path) - 1) // 128
+                got = sorted(rng.permutation(cur)[:topk - 1].tolist() + [cur])
+                sel[b, j, i, :len(got)] = got
+    shape = _lib.make_shape(B, n, cap, h * g, h, d, d, 128, topk, 1)
+    lens_t = torch.tensor(lens, dtype=torch.int32).cuda()
+    sel_t = torch.tensor(sel).cuda()
+    out, lse = torch.empty_like(q), torch.empty(B, h * g, n, device="cuda")
+    ws = torch.empty(_lib.msa_workspace_bytes(shape, 5) // 4, device="cuda")
+    assert ws.numel() >= 2 * B * n * h * g * (d + 1)                       # two splits or more
+    _lib.msa_sparse_decode_tree(shape, lens_t, table, nB, mask, q, k, v, kd, vd, sel_t, out, lse, ws)
+    _ok()
+    for b, j in ((0, 0), (7, 3), (19, 1), (39, 2)):
+        for i, path in enumerate(paths[b]):
+            chosen = [x for x in sel[b, j, i].tolist() if x >= 0]
+            at = torch.tensor(chosen, device="cuda")
+            keep = ((at[:, None] * 128 + torch.arange(128, device="cuda")) < lens[b]).flatten()
+            phys = table[b].long()[at]
+            mine = [a for a in path if (lens[b] + len(paths[b][a]) - 1) // 128 in chosen]
+            kk = torch.cat([k[phys, j].flatten(0, 1)[keep], kd[b, j][mine]]).double()
+            vv = torch.cat([v[phys, j].flatten(0, 1)[keep], vd[b, j][mine]]).double()
+            heads = slice(j * g, (j + 1) * g)
+            qq = q[b, i, heads].double()
+            z = qq @ kk.T * d ** -0.5
+            norm = torch.logsumexp(z, 1)
+            w = torch.exp(z - norm[:, None])
+            want, mag = w @ vv, w @ vv.abs()
+            # as in tree_cases: scores off by e, weights and result rounded to bf16
+            e = 2 * (d + 4) * 2.0 ** -24 * (qq.abs() @ kk.abs().T).amax(1) * d ** -0.5 + 2.0 ** -20
+            tol = mag * (2 * e[:, None] + 2.0 ** -8 + 2.0 ** -20 + 2.0 ** -18) + 2.0 ** -8 * want.abs()
+            assert ((out[b, i, heads].double() - want).abs() <= tol).all()
+            # sums of 83,000 weights in fp32 chains of 64 and 1300: 2^-18 and 2^-22 of the log-sum
+            assert ((lse[b, heads, i].double() - norm).abs() <= e + 2.0 ** -16 + 2.0 ** -22 * norm.abs()).all()
