@@ -515,7 +515,9 @@ def _plan(s):
     if c["op"] == "attend":
         more = torch.empty(_lib.msa_workspace_bytes(shape, 5) // 4 + 4, device=DEV)
     if c["op"] == "commit":
-        more = _lib.make_commit_tensors([(s["kd"], s["k"]), (s["vd"], s["v"])], [(s["drafts"], s["cache"])])
+        more = (_lib.make_commit_tensors([(s["kd"], s["k"]), (s["vd"], s["v"])], [(s["drafts"], s["cache"])]),
+                # the index keys are bf16 whatever K and V are
+                _lib.make_shape(c["batch"], 1, c["cap"], hkv, hkv, c["dim"], 128, BLOCK, 1, 1, "bf16"))
     if c["op"] == "pack":
         shape.seq_q = 1
     return _lib, shape, more
@@ -542,9 +544,10 @@ def _run_own(s):
         lib.msa_sparse_decode_tree(shape, s["lens"], s["table"], s["n_phys"], s["mask"], s["q"], s["k"], s["v"],
                                    s["kd"], s["vd"], s["sel"], s["out"], s["lse"], more)
         return [s["out"], s["lse"]]
-    lib.msa_tree_commit(shape, s["lens"], s["table"], s["n_phys"], s["accepted"], more, s["new_lens"])
+    tensors, index = more
+    lib.msa_tree_commit(shape, s["lens"], s["table"], s["n_phys"], s["accepted"], tensors, s["new_lens"])
     # the committed tokens' index keys as the cache now holds them
-    lib.msa_index_unpack(shape, c["accept"], s["lens"], s["new_lens"], s["table"], s["n_phys"], s["cache"], s["out"])
+    lib.msa_index_unpack(index, c["accept"], s["lens"], s["new_lens"], s["table"], s["n_phys"], s["cache"], s["out"])
     return [s["k"], s["v"], s["new_lens"], s["out"]]
 
 
