@@ -19,11 +19,12 @@ __device__ __forceinline__ int physical_index_block(const Dims& p, int b, int bl
 }
 
 // Exponent byte of a row from its largest magnitude (finite): the least e, at least -126, with
-// magnitude <= 448 * 2^e, plus 127.  448 is 1.75 * 2^8, so it is the magnitude's exponent less 8,
-// or less 7 where its fraction is above 1.75.
+// magnitude <= 1.75 * 2^kTop * 2^e, plus 127: the magnitude's exponent less kTop, or less kTop - 1
+// where its fraction is above 1.75.  kTop 8: 448, the largest e4m3 value; 15: 57344, the largest of e5m2.
+template <int kTop = 8>
 __host__ __device__ __forceinline__ uint32_t index_exponent(uint32_t amax_bits) {
   const uint32_t e = (amax_bits >> 23) + ((amax_bits & 0x7fffffu) > 0x600000u ? 1 : 0);
-  return e > 8 ? e - 8 : 1;
+  return e > kTop ? e - kTop : 1;
 }
 
 __device__ __forceinline__ float pow2_byte(uint32_t byte) { return __uint_as_float(byte << 23); }
@@ -35,6 +36,14 @@ __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
 __device__ __forceinline__ float2 from_e4m3_pair(uint32_t codes) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
   return __half22float2(__half2(h));
+}
+
+// The same with three significant bits and a wider range, 2^-16 to 57344, from and to fp16 values.
+__device__ __forceinline__ uint32_t e5m2_pair(__half2 x) {
+  return __nv_cvt_halfraw2_to_fp8x2(x, __NV_SATFINITE, __NV_E5M2);
+}
+__device__ __forceinline__ __half2 from_e5m2_pair(uint32_t codes) {
+  return __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E5M2));
 }
 
 }  // namespace msa

@@ -209,9 +209,11 @@ __device__ __forceinline__ void umma_bf16_ss(uint32_t d_tmem, uint64_t a_desc, u
       : "memory");
 }
 
-// Instruction descriptor of tcgen05.mma kind::f8f6f4 with e4m3 A/B (both K-major), fp32 accumulate.
-__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
-  return (1u << 4)                      // D format: f32 (A and B formats 0: e4m3)
+// Instruction descriptor of tcgen05.mma kind::f8f6f4 with e4m3 A and e5m2 B (both K-major), fp32
+// accumulate.
+__host__ __device__ constexpr uint32_t idesc_e4m3_e5m2_f32(int M, int N) {
+  return (1u << 4)                      // D format: f32 (A format 0: e4m3)
+         | (1u << 10)                   // B format: e5m2
          | ((uint32_t)(N >> 3) << 17)
          | ((uint32_t)(M >> 4) << 24);
 }

@@ -7,10 +7,13 @@
 // block's products with the 128 keys as M and the columns (token, head) as N, so that the cost
 // follows the number of tokens.  8-bit keys are operands as they lie in the cache: a key's scale is
 // a power of two of its own and is applied to the products.  The queries keep their precision by
-// being split in two 8-bit parts, x 2^-e = hi + lo, each rounded to 4 significant bits: a bf16 value
-// has 8, so the two hold it exactly while lo's last bit is 2^-9 or more, that is for dims of at
-// least 2^-10 of the query's largest; a smaller one is off by at most 2^-10 of the 448 that the
-// largest is scaled to.  Both parts accumulate in the same TMEM columns.
+// being split in three 8-bit parts, x 2^-e = hi + mid + lo, each the nearest e5m2 value (3 significant
+// bits, 2^-16 to 57344) to what the ones before leave.  A bf16 value is m units of its last bit,
+// m < 2^8: hi leaves at most 16 units, mid at most one, lo nothing.  That holds while the last bit
+// is 2^-16 or more; with the largest dim scaled to (28672, 57344] it is so for dims of at least 2^-9,
+// 2^-23.8 of the largest.  A smaller dim is off by at most 2^-17, 2^-31.8 of the largest.  (Two e4m3
+// parts, a third less of products, keep the digits to 2^-9.8 of the largest only: one large dim then
+// costs the others theirs.)  All parts accumulate in the same TMEM columns.
 //
 // Two groups of four epilogue warps take the blocks in turn (one group's chain of waits and loads
 // is longer than a block's share of the bandwidth).  They read the accumulator as fragments of 16
@@ -49,6 +52,7 @@ constexpr int kMaxStages = 12;
 constexpr int kScaleSlots = 16;        // a power of two, kMaxStages + kAcc or more: see the producer
 static_assert(kScaleSlots >= kMaxStages + kAcc && (kScaleSlots & (kScaleSlots - 1)) == 0, "slots");
 constexpr int kSmemLimit = 232448;
+constexpr int kParts = 3;              // of a query beside 8-bit keys; 16-bit ones: two halves of the dims
 
 // The small part of shared memory; the ring, the queries and the results lie before it.
 struct Small {
@@ -64,9 +68,9 @@ struct Small {
 
 // Bytes of each part, all multiples of 16; cols: padded to 16.
 struct Plan {
-  int cols, stages, stage_bytes;
+  int cols, stages, stage_bytes, q_tiles;                  // q_tiles: of cols x 128 bytes of queries
   __host__ __device__ int q_at() const { return stages * stage_bytes; }
-  __host__ __device__ int ex_at() const { return q_at() + cols * 2 * kRowBytes; }
+  __host__ __device__ int ex_at() const { return q_at() + cols * q_tiles * kRowBytes; }
   __host__ __device__ int res_at() const { return ex_at() + kScaleSlots * kBk; }
   __host__ __device__ int res_row() const { return cols + 4; }          // spreads the banks
   __host__ __device__ int dres_at() const { return res_at() + 16 * res_row() * 4; }
@@ -346,14 +350,16 @@ tree_scores_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
     // the copies)
     const int me = warp > kProducerWarp ? tid - 32 : tid;
     const int wq = warp > kProducerWarp ? warp - 1 : warp;
-    constexpr int kOwn = (kMaxCols + kWarps - 2) / (kWarps - 1);   // columns of a warp
-    uint2 qv[kOwn];                                        // dims 4 lane .. 4 lane + 3
+    constexpr int kPass = 2 * (kWarps - 1);                // columns at a time, half a warp each
+    constexpr int kOwn = (kMaxCols + kPass - 1) / kPass;
+    const int sub = lane & 15, c_own = 2 * wq + (lane >> 4);
+    uint4 qv[kOwn];                                        // dims 8 sub .. 8 sub + 7
 #pragma unroll
     for (int x = 0; x < kOwn; ++x) {
-      const int c = wq + x * (kWarps - 1);
-      qv[x] = make_uint2(0, 0);
+      const int c = c_own + x * kPass;
+      qv[x] = make_uint4(0, 0, 0, 0);
       if (c < C)
-        qv[x] = *reinterpret_cast<const uint2*>(iq + (((size_t)b * p.nR + node0) * p.Hkv + c) * kDI + lane * 4);
+        qv[x] = *reinterpret_cast<const uint4*>(iq + (((size_t)b * p.nR + node0) * p.Hkv + c) * kDI + sub * 8);
     }
     for (int e = me; e < 16 * plan.res_row(); e += kThreads - 32) res[e] = kNothing;
     for (int e = me; e < 2 * Cp; e += kThreads - 32) dres[e] = kNothing;
@@ -364,43 +370,47 @@ tree_scores_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
     }
     asm volatile("bar.sync 4, %0;" ::"n"(kThreads - 32) : "memory");
     // ---- the queries as the B operand, K-major with the 128-byte swizzle (16-byte unit u of row c
-    // lies at unit u ^ (c % 8)); a warp a column
+    // lies at unit u ^ (c % 8)); half a warp a column, and Cp is even, so a warp leaves as a whole
 #pragma unroll
     for (int x = 0; x < kOwn; ++x) {
-      const int c = wq + x * (kWarps - 1);
+      const int c = c_own + x * kPass;
       if (c >= Cp) break;
       const int node = node0 + c / p.Hkv;
       const bool there = c < C && s.path[node] != 0;
-      const uint2 w = there ? qv[x] : make_uint2(0, 0);
+      const uint4 w = there ? qv[x] : make_uint4(0, 0, 0, 0);
       float scale = p.index_scale;
       if (kPacked) {
-        const float v[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
-                            __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u)};
+        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
         uint32_t amax = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) amax = max(amax, __float_as_uint(v[e]) & 0x7fffffffu);
-        amax = __reduce_max_sync(0xffffffffu, amax);
-        const uint32_t byte = index_exponent(amax);
+        for (int e = 0; e < 4; ++e) amax = max(amax, max(v[e] << 16 & 0x7fffffffu, v[e] & 0x7fff0000u));
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const uint32_t byte = index_exponent<15>(amax);
         const float inv = pow2_byte(254 - byte);
         scale *= pow2_byte(byte);
-        uint32_t hi[2], lo[2];
+        // fp16 holds the scaled dims and what the parts leave of them: 8 bits, the last at 2^-24 or more
+        __half2 rest[4];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float x0 = v[2 * e] * inv, x1 = v[2 * e + 1] * inv;
-          hi[e] = e4m3_pair(x0, x1);
-          const float2 h = from_e4m3_pair(hi[e]);
-          lo[e] = e4m3_pair(x0 - h.x, x1 - h.y);
+        for (int e = 0; e < 4; ++e)
+          rest[e] = __floats2half2_rn(__uint_as_float(v[e] << 16) * inv, __uint_as_float(v[e] & 0xffff0000u) * inv);
+        uint8_t* to = qs + c * kRowBytes + (((sub >> 1) ^ (c & 7)) << 4) + (sub & 1) * 8;
+#pragma unroll
+        for (int part = 0; part < kParts; ++part) {
+          uint32_t code[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            code[e] = e5m2_pair(rest[e]);
+            rest[e] = __hsub2(rest[e], from_e5m2_pair(code[e]));
+          }
+          *reinterpret_cast<uint2*>(to + part * Cp * kRowBytes) =
+              make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
         }
-        uint8_t* to = qs + c * kRowBytes + (((lane >> 2) ^ (c & 7)) << 4) + (lane & 3) * 4;
-        *reinterpret_cast<uint32_t*>(to) = hi[0] | hi[1] << 16;
-        *reinterpret_cast<uint32_t*>(to + Cp * kRowBytes) = lo[0] | lo[1] << 16;
       } else {
-        const int u = lane >> 1;                           // 16-byte unit of the 256-byte row
-        uint8_t* to = qs + (u >> 3) * Cp * kRowBytes + c * kRowBytes + (((u & 7) ^ (c & 7)) << 4) +
-                      (lane & 1) * 8;
-        *reinterpret_cast<uint2*>(to) = w;
+        *reinterpret_cast<uint4*>(qs + (sub >> 3) * Cp * kRowBytes + c * kRowBytes +
+                                  (((sub & 7) ^ (c & 7)) << 4)) = w;
       }
-      if (lane == 0) {
+      if (sub == 0) {
         qscale[c] = scale;
         // the column's score row; of an absent token (scores -inf) its complement
         const int row = (b * p.Hkv + c % p.Hkv) * p.nR + node;
@@ -425,8 +435,8 @@ tree_scores_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
       uint32_t phase = 0;
       const uint64_t a_desc = ptx::smem_desc_k_sw128(ptx::smem_u32(smem));
       const uint64_t q_desc = ptx::smem_desc_k_sw128(ptx::smem_u32(qs));
-      const int q_half = Cp * kRowBytes;                   // 8-bit: hi, lo; 16-bit: halves of the dims
-      const uint32_t idesc = kPacked ? ptx::idesc_e4m3_f32(kBk, Cp) : ptx::idesc_bf16_f32(kBk, Cp);
+      const int q_tile = Cp * kRowBytes;                   // 8-bit: a part; 16-bit: half of the dims
+      const uint32_t idesc = kPacked ? ptx::idesc_e4m3_e5m2_f32(kBk, Cp) : ptx::idesc_bf16_f32(kBk, Cp);
       for (int i = m; i < items; i += kIssuers) {
         const int buf = i % kAcc;
         if (!ptx::mbar_wait(&s.full[st], phase, abort) ||
@@ -436,9 +446,9 @@ tree_scores_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
           const uint32_t d = tmem + buf * Cp;
           const uint64_t a = a_desc + ((uint32_t)(st * plan.stage_bytes) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint64_t q = q_desc + ((uint32_t)((kk >> 2) * q_half + (kk & 3) * 32) >> 4);
-            if (kPacked)                                   // both parts against the same 128 dims
+          for (int kk = 0; kk < 4 * (kPacked ? kParts : 2); ++kk) {
+            const uint64_t q = q_desc + ((uint32_t)((kk >> 2) * q_tile + (kk & 3) * 32) >> 4);
+            if (kPacked)                                   // all parts against the same 128 dims
               ptx::umma_f8_ss(d, a + ((kk & 3) * 32 >> 4), q, idesc, kk > 0 ? 1u : 0u);
             else
               ptx::umma_bf16_ss(d, a + (((kk >> 2) * kBk * kRowBytes + (kk & 3) * 32) >> 4), q, idesc,
@@ -604,6 +614,7 @@ cudaError_t launch(const Dims& p, const void* idx_q, const void* idx_k, const vo
   Plan plan;
   plan.cols = (per * p.Hkv + 15) / 16 * 16;
   plan.stage_bytes = kPacked ? kBk * kRowBytes : 2 * kBk * kRowBytes;
+  plan.q_tiles = kPacked ? kParts : 2;
   plan.stages = kMaxStages;
   while (plan.stages > kIssuers && plan.bytes() + 1024 > kSmemLimit) plan.stages -= kIssuers;
   uint32_t cols = 32;
