@@ -473,35 +473,38 @@ tree_scores_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
       const int grp0 = blk0 >> 3, groups = nblk > 0 ? ((blk0 + nblk - 1) >> 3) - grp0 + 1 : 0;
       bool ok = true;
       // maxima of block `to` in column c, from the group's buffer (left empty for the next) and from
-      // the drafted keys
+      // the drafted keys; -inf once a wait was given up
       auto write = [&](int c, int to, bool cached) {
         int key = kNothing;
-        if (cached) {
+        if (ok && cached) {
           int* r = res + ((((to >> 3) - grp0) & 1) * 8 + (to & 7)) * plan.res_row() + c;
           key = *r;
           *r = kNothing;
         }
-        if (drafted && to >= first) key = max(key, dres[(to - first) * Cp + c]);
+        if (ok && drafted && to >= first) key = max(key, dres[(to - first) * Cp + c]);
         float v = from_order_key(key);
         const int row = rows[c];
         v = row < 0 || v == -INFINITY ? -INFINITY : v * qscale[c];
         scores[(size_t)(row < 0 ? ~row : row) * p.nB + to] = v;
       };
-      for (int o = 0; ok && o < groups; ++o) {
+      for (int o = 0; o < groups; ++o) {
         const int base = (grp0 + o) * 8;
         const int lo = max(base, blk0), hi = min(base + 8, blk0 + nblk);
-        if (wt == 0 && hi - lo < 8) arrive_n(&s.res_full[o & 1], (8 - (hi - lo)) * 4);
-        __syncwarp();
-        ok = ptx::mbar_wait(&s.res_full[o & 1], (o >> 1) & 1, abort);
-        if (ok && drafted && o + 1 == groups) ok = ptx::mbar_wait(&s.dres_full, 0, abort);
-        if (!ok) break;
+        if (ok) {
+          if (wt == 0 && hi - lo < 8) arrive_n(&s.res_full[o & 1], (8 - (hi - lo)) * 4);
+          __syncwarp();
+          ok = ptx::mbar_wait(&s.res_full[o & 1], (o >> 1) & 1, abort);
+          if (ok && drafted && o + 1 == groups) ok = ptx::mbar_wait(&s.dres_full, 0, abort);
+          ok = __all_sync(0xffffffffu, ok);
+        }
         for (int e = wt; e < C * 8; e += kWriters * 32)
           if (base + (e & 7) >= lo && base + (e & 7) < hi) write(e >> 3, base + (e & 7), true);
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&s.res_empty[o & 1]);
+        if (ok && lane == 0) ptx::mbar_arrive(&s.res_empty[o & 1]);
       }
-      if (ok && drafted && groups == 0) ok = ptx::mbar_wait(&s.dres_full, 0, abort);
-      if (ok && drafted) {                                 // blocks of drafted keys alone
+      if (ok && drafted && groups == 0)
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&s.dres_full, 0, abort));
+      if (drafted) {                                       // blocks of drafted keys alone
         const int n1 = min(p.nB, first + 2);
         for (int e = wt; e < C * 2; e += kWriters * 32)
           if (nB_b + (e & 1) < n1) write(e >> 1, nB_b + (e & 1), false);

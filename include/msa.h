@@ -529,9 +529,12 @@ const char* msa_last_error(void);
  * wait for the copies give up after their one-second bound, the kernel writes zeros and
  * -inf, and the next msa_get_device_status() reports MSA_ERR_TIMEOUT.  No copy or MMA is
  * ever in flight in this mode, and the CUDA context stays usable.  mode 2: in every tensor-core
- * decode launch (over drafted tokens too, and their index scores), the CTA of a row's first split
- * issues only the copy of its first block, so it gives up in the same way if it has another.  mode 0 (default): normal operation.  Any other
- * mode: MSA_ERR_INVALID_ARG. */
+ * decode launch, the CTA of a row's first split issues only the copy of its first block, so it
+ * gives up in the same way if it has another.  Over drafted tokens: attention issues K of its first
+ * block and V of half of it, and gives up on that block too; index scores issue the first tile of a
+ * sequence's first range (the drafts, where the range is the sequence's last) and write -inf for
+ * the blocks they have not reached.  mode 0 (default): normal operation.  Any other mode:
+ * MSA_ERR_INVALID_ARG. */
 msa_status msa_debug_set_fault(int32_t mode);
 
 /* MSA_ABI_VERSION of the loaded library. */
