@@ -100,6 +100,8 @@ SIGNATURES = {
                                       _vp, _vp, _vp, _vp, _sz, _vp]),
     "msa_tree_commit": (_i32, [_SHAPE_P, _vp, _vp, _i32, _vp, _i32,
                                ctypes.POINTER(MsaCommitTensor), _i32, _vp, _vp]),
+    "msa_tree_commit_masked": (_i32, [_SHAPE_P, _vp, _vp, _i32, _vp, _vp, _i32,
+                                      ctypes.POINTER(MsaCommitTensor), _i32, _vp, _vp]),
     "msa_workspace_bytes": (_sz, [_SHAPE_P, ctypes.c_int]),
     "msa_get_device_status": (_i32, [_vp]),
     "msa_status_string": (ctypes.c_char_p, [_i32]),
@@ -701,7 +703,8 @@ def make_commit_tensors(rows, packed=()) -> CommitTensors:
 
 
 def msa_tree_commit(shape: MsaShape, seq_lens, block_table, n_phys, accepted,
-                    tensors: CommitTensors, new_lens, stream=None):
+                    tensors: CommitTensors, new_lens, stream=None, mask=None):
+    """With the tree's mask (int64 [batch, tokens]) a list ends at a token that the tree does not have."""
     dev, st = _place(stream)
     batch, n_phys = shape.batch, int(n_phys)
     if tensors.device != dev:
@@ -717,9 +720,10 @@ def msa_tree_commit(shape: MsaShape, seq_lens, block_table, n_phys, accepted,
                          f"{(batch, n_phys)}")
     if accepted.dim() != 2 or accepted.shape[0] != batch:
         raise ValueError(f"accepted is {tuple(accepted.shape)}, expected [{batch}, tokens]")
-    _check(load().msa_tree_commit(
+    _check(load().msa_tree_commit_masked(
         ctypes.byref(shape), _arg(seq_lens, "seq_lens", _I32, batch, dev, batch),
         _arg(block_table, "block_table", _I32, batch * shape.n_blocks, dev, batch), n_phys,
+        _arg(mask, "mask", _I64, batch * shape.seq_q, dev, batch),
         _arg(accepted, "accepted", _I32, 0, dev), accepted.shape[1], tensors.array, len(tensors),
         _arg(new_lens, "new_lens", _I32, batch, dev, batch), st), "msa_tree_commit")
 

@@ -387,9 +387,10 @@ def _tree_caches(shape, k_cache, v_cache, idx_cache, block_table, packed):
 def commit_tree(step, accepted, k_cache, v_cache, idx_cache, seq_lens, block_table=None,
                 capacity=None, block_size=128):
     """Moves the accepted tokens of a decode_tree step into its caches, in place: token
-    accepted[b, i] (int32 [B,n]; a list ends at its first entry outside [0, N)) becomes position
-    seq_lens[b] + i, and seq_lens grows by the number of them.  The tokens should be a path of
-    the tree, root first: they are stored as they were rotated."""
+    accepted[b, i] (int32 [B,n]; a list ends at its first entry outside [0, N), or that the tree does
+    not have) becomes position seq_lens[b] + i, and seq_lens grows by the number of them.  seq_lens
+    is as it was in the step.  The tokens should be a path of the tree, root first: they are
+    stored as they were rotated."""
     k, v, idx_k = step["k"], step["v"], step["idx_k"]
     B, Hkv, N, d = k.shape
     packed = idx_cache.dtype is torch.uint8
@@ -400,7 +401,8 @@ def commit_tree(step, accepted, k_cache, v_cache, idx_cache, seq_lens, block_tab
     n_phys = _tree_caches(shape, k_cache, v_cache, idx_cache, block_table, packed)
     rows = [(k, k_cache), (v, v_cache)] + ([] if packed else [(idx_k, idx_cache)])
     msa_tree_commit(shape, seq_lens, block_table, n_phys, accepted,
-                    make_commit_tensors(rows, [(idx_k, idx_cache)] if packed else []), seq_lens)
+                    make_commit_tensors(rows, [(idx_k, idx_cache)] if packed else []), seq_lens,
+                    mask=step.get("mask"))
 
 
 __all__ = ["prefill", "decode", "run_prefill", "run_decode", "alloc_prefill_outputs",

@@ -887,9 +887,18 @@ msa_status msa_tree_commit(const msa_shape* shape, const int32_t* seq_lens,
                            const int32_t* block_table, int32_t n_phys, const int32_t* accepted,
                            int32_t n_accept, const msa_commit_tensor* tensors, int32_t n_tensors,
                            int32_t* new_lens, void* stream) {
+  return msa_tree_commit_masked(shape, seq_lens, block_table, n_phys, nullptr, accepted, n_accept,
+                                tensors, n_tensors, new_lens, stream);
+}
+
+msa_status msa_tree_commit_masked(const msa_shape* shape, const int32_t* seq_lens,
+                                  const int32_t* block_table, int32_t n_phys, const uint64_t* mask,
+                                  const int32_t* accepted, int32_t n_accept,
+                                  const msa_commit_tensor* tensors, int32_t n_tensors,
+                                  int32_t* new_lens, void* stream) {
   g_last_error[0] = 0;
   Dims d;
-  MSA_TRY(make_tree_dims(shape, seq_lens, nullptr, &d));
+  MSA_TRY(make_tree_dims(shape, seq_lens, mask, &d));
   if (!tensors) return fail(MSA_ERR_INVALID_ARG, "tensors is NULL");
   if (n_tensors < 1 || n_tensors > MSA_COMMIT_MAX_TENSORS)
     return fail(MSA_ERR_INVALID_ARG, "n_tensors must be in [1, %d] (got %d)",
@@ -900,14 +909,15 @@ msa_status msa_tree_commit(const msa_shape* shape, const int32_t* seq_lens,
   MSA_TRY(set_tree_table(block_table, n_phys, true, &d));
   MSA_TRY(check_ptr(accepted, "accepted"));
   MSA_TRY(check_ptr(new_lens, "new_lens"));
-  // buffers of the call: [start, bytes) of lengths, list and table, then sources and destinations
+  // buffers of the call: [start, bytes) of lengths, list, masks and table, then sources and destinations
   struct Span { __int128 at, bytes; const char* name; };
-  Span in[3 + MSA_COMMIT_MAX_TENSORS], out[1 + MSA_COMMIT_MAX_TENSORS];
+  Span in[4 + MSA_COMMIT_MAX_TENSORS], out[1 + MSA_COMMIT_MAX_TENSORS];
   int n_in = 0, n_out = 0;
   auto span = [](const void* ptr, __int128 bytes, const char* name) {
     return Span{(__int128)(uintptr_t)ptr, bytes, name};
   };
   in[n_in++] = span(accepted, (__int128)d.B * n_accept * 4, "accepted");
+  if (mask) in[n_in++] = span(mask, (__int128)d.B * d.nR * 8, "mask");
   if (new_lens != seq_lens) in[n_in++] = span(seq_lens, (__int128)d.B * 4, "seq_lens");
   if (block_table) in[n_in++] = span(block_table, (__int128)d.B * d.nB * 4, "block_table");
   out[n_out++] = span(new_lens, (__int128)d.B * 4, "new_lens");

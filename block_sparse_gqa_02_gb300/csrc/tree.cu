@@ -93,7 +93,8 @@ tree_commit_kernel(const __grid_constant__ CommitArgs a, const int32_t* __restri
     for (int i0 = 0; i0 < a.n_accept; i0 += 32) {
       const int i = i0 + tid;
       const int x = i < a.n_accept ? accepted[(size_t)b * a.n_accept + i] : -1;
-      const bool ok = x >= 0 && x < p.nR && L + i < p.Sk;
+      // with the masks: a token that the tree has
+      const bool ok = x >= 0 && x < p.nR && L + i < p.Sk && (!p.tree_mask || tree_path(p, b, x, L));
       const unsigned bad = ~__ballot_sync(0xffffffffu, ok);
       const int good = bad ? __ffs(bad) - 1 : 32;
       if (ok && tid < good) {

@@ -486,7 +486,10 @@ msa_status msa_sparse_decode_tree(const msa_shape* shape, const int32_t* seq_len
  * position seq_lens[b] + i, and new_lens[b] = seq_lens[b] + the number of them.  accepted int32
  * [batch, n_accept] (n_accept at most 64): a sequence's list ends at its first entry outside [0,
  * n_tokens), or where the cache is full.  Nothing else in the caches changes.  new_lens may be
- * seq_lens itself.  Up to MSA_COMMIT_MAX_TENSORS caches a call:
+ * seq_lens itself.  The rows are stored as they are, so the tokens must be ones that the tree has: an
+ * absent token's may hold anything, and cached rows must be finite.  msa_tree_commit_masked, given
+ * the tree's mask [batch, n_tokens] and the step's seq_lens, ends a list at an absent token too (mask
+ * NULL: it is msa_tree_commit).  Up to MSA_COMMIT_MAX_TENSORS caches a call:
  *   packed = 0: src [batch, n_heads, n_tokens, row_bytes]; dst [batch, n_heads, seq_k, row_bytes],
  *               or with a block_table pools [n_phys, n_heads, block_size, row_bytes];
  *   packed = 1: 8-bit index keys (n_heads 1, row_bytes = index_dim 64 or 128, block_size 128):
@@ -506,6 +509,11 @@ msa_status msa_tree_commit(const msa_shape* shape, const int32_t* seq_lens,
                            const int32_t* block_table, int32_t n_phys, const int32_t* accepted,
                            int32_t n_accept, const msa_commit_tensor* tensors, int32_t n_tensors,
                            int32_t* new_lens, void* stream);
+msa_status msa_tree_commit_masked(const msa_shape* shape, const int32_t* seq_lens,
+                                  const int32_t* block_table, int32_t n_phys, const uint64_t* mask,
+                                  const int32_t* accepted, int32_t n_accept,
+                                  const msa_commit_tensor* tensors, int32_t n_tensors,
+                                  int32_t* new_lens, void* stream);
 
 /* Scratch bytes msa_sparse_prefill (which = 0), msa_sparse_decode (which = 1),
  * msa_sparse_prefill_backward (which = 2), msa_index_kl_loss (which = 3),
