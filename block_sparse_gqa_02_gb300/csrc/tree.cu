@@ -60,10 +60,9 @@ tree_mask_kernel(const int32_t* __restrict__ parents, TreeWord* __restrict__ mas
   for (int h = 0; h < 2; ++h) {
     const int i = lane + 32 * h;
     if (i >= n) continue;
-    const int pos = tree_pos(path[i], L);
-    const bool there = up[i] == kRoot && pos < p.Sk;
+    const bool there = up[i] == kRoot && __popcll(path[i]) - 1 < p.Sk - L;
     mask[(size_t)b * n + i] = there ? path[i] : 0;
-    if (positions) positions[(size_t)b * n + i] = there ? pos : -1;
+    if (positions) positions[(size_t)b * n + i] = there ? tree_pos(path[i], L) : -1;
   }
 }
 
@@ -94,7 +93,7 @@ tree_commit_kernel(const __grid_constant__ CommitArgs a, const int32_t* __restri
       const int i = i0 + tid;
       const int x = i < a.n_accept ? accepted[(size_t)b * a.n_accept + i] : -1;
       // with the masks: a token that the tree has
-      const bool ok = x >= 0 && x < p.nR && L + i < p.Sk && (!p.tree_mask || tree_path(p, b, x, L));
+      const bool ok = x >= 0 && x < p.nR && i < p.Sk - L && (!p.tree_mask || tree_path(p, b, x, L));
       const unsigned bad = ~__ballot_sync(0xffffffffu, ok);
       const int good = bad ? __ffs(bad) - 1 : 32;
       if (ok && tid < good) {

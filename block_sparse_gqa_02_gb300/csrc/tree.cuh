@@ -12,7 +12,7 @@ using TreeWord = unsigned long long;   // bit a: drafted token a
 __device__ __forceinline__ TreeWord tree_path_of(const Dims& p, TreeWord m, int i, int L) {
   if (p.nR < 64) m &= (1ull << p.nR) - 1;
   if (!(m >> i & 1)) return 0;
-  return L + __popcll(m) - 1 < p.Sk ? m : 0;
+  return __popcll(m) - 1 < p.Sk - L ? m : 0;               // L + depth may pass 32 bits
 }
 
 __device__ __forceinline__ TreeWord tree_path(const Dims& p, int b, int i, int L) {
