@@ -312,7 +312,8 @@ def decode_tree(q, k, v, idx_q, idx_k, k_cache, v_cache, idx_cache, seq_lens, pa
     the new token, which is not in the caches yet).  q [B,N,Hq,d]; k, v [B,Hkv,N,d];
     idx_q [B,N,Hkv,dI]; idx_k [B,N,dI]; parents int32 [B,N]: an earlier token of the tree, -1 for
     the last cached token (any other value: the sequence has no such token).  Every token gets
-    what decode gives it with its path from the root appended to the caches.
+    what decode gives it with its path from the root appended to the caches; over an 8-bit idx_cache
+    its blocks are selected by the keys' values there (include/msa.h has the rounding).
 
     seq_lens int32 [B]: cached tokens, the drafts not counted.  k_cache, v_cache [B,Hkv,L,d], or
     with a block_table (int32 [B, blocks]) pools [P,Hkv,block_size,d].  idx_cache: [B,L,dI] or

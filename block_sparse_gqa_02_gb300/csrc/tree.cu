@@ -1,6 +1,6 @@
 // Around a decode step over drafted tokens: the paths of a tree from its parents, and the rows of
 // the accepted tokens into the caches.  Both are small and bound by latency: one launch each (cold, 8
-// sequences: 2.8 us for the paths, 8.5 for the rows, a chain of length, list, table and row).
+// sequences: 2.8 us for the paths, 8.5 for the rows, a chain of length, list, (mask,) table and row).
 #include <cooperative_groups.h>
 
 #include "index_cache.cuh"

@@ -1,8 +1,8 @@
 // Attention of a tree of drafted tokens on the tcgen05 tensor cores (bf16 inputs, fp32 softmax and
 // accumulation; head_dim 64 or 128, blocks of 128 keys).
 //
-// Bound by HBM: the tokens of a tree select mostly the same blocks, so a block is read once for
-// all of them.  CTA = (split, up to 256 rows, sequence x KV head), a row being a (token, query head)
+// The tokens of a tree select mostly the same blocks, so a block is read once for all of
+// them.  CTA = (split, up to 256 rows, sequence x KV head), a row being a (token, query head)
 // of the KV head's group.  It forms the union of its tokens' selections (a bitmap of blocks in
 // shared memory), takes the split's share of it in order, streams these blocks through a TMA ring,
 // and multiplies all rows with each; rows whose token did not select a block get weight 0 there.
@@ -13,13 +13,16 @@
 // Q.K^T runs under the softmax, and the copies' ring has slots of half a block: Q takes 32 KiB a
 // tile, which leaves 144 KiB (two tiles) or 176 KiB (one) for keys and values.
 // Measured, ragged 8 x 128K, 16 drafts of 16 heads a KV head (206 MB, 128 CTAs): 67 us, of which 4.7
-// set-up, 2.3 to the first S, 46 for 48 steps, 3.5 epilogue and 5 the join; without the products and
-// exponentials (timing only) it takes 8 us less: the steps are bound by the copies' latency at
-// 128 SMs as much as by the tensor cores, which multiply all 256 rows with every block of the union.
-// 2 x 64K, 64 drafts (72 MB from HBM, read by four CTAs each): 79 us, bound by the products.
+// set-up, 2.3 to the first S, 46 for 48 steps, 3.5 epilogue and 5 the join.  A step takes some 1,830
+// cycles.  In 1,030 of them shared memory serves the products' operands, 128 bytes a cycle (Q again for
+// every half block: 64 KiB; K and V once a tile: 64 KiB), and in 256 the copies land; HBM is busy 38 %
+// of the time.  So a step waits for shared memory first, the rest is the chain of copy, product and
+// softmax.  2 x 64K, 64 drafts (72 MB from HBM, read by four CTAs each): 79 us, 1.0 us a step, though it
+// reads a third as much.
 // Warps: 0-3 and 4-7 softmax and epilogue of a tile each, 8 TMA producer, 9 issues Q.K^T, 10 issues
-// P.V.  P (bf16) is written over S and read by the P.V product from TMEM.  Online softmax in the
-// log2 domain; the running base moves only when a step would push a row's weights past a bound, so O
+// P.V.  P is written over S and read by the P.V product from TMEM, rounded to bf16 (by at most 2^-8 of
+// each weight: the product takes V's type; its sum is not rounded).  Online softmax in the log2
+// domain; the running base moves only when a step would push a row's weights past a bound, so O
 // is rarely rescaled.  Every wait is bounded.
 #include "launch.cuh"
 #include "ptx.cuh"

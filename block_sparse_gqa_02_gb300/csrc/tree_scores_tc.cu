@@ -22,9 +22,10 @@
 // one of two buffers, which two further warps write out, 32 bytes of a score row at a time.
 // Warps: 0-7 epilogue (group warp / 4, TMEM lane quadrant warp % 4), 8 TMA producer, 9-10 MMA
 // issuers (every other block: one alone takes 58 us more), 11-12 writers.  Every wait is bounded.
-// Measured: 16 drafts, 8-bit keys, 8 x 1M tokens 188 us (5.8 TB/s, 86 % of the copy bandwidth; the
-// copies without the epilogue's work take 15 less); 12 drafts, 16-bit keys, ragged 8 x 128K 32 us
-// (5.2 TB/s with 5 us of set-up); 5 drafts, 1 x 8K 10 us, of which a CTA's work is 5.
+// Measured: 16 drafts, 8-bit keys, 8 x 1M tokens 192 us (5.7 TB/s, 85 % of the copy bandwidth; two parts
+// of the queries: 189; shared memory serves operands in 66 % of the cycles, the issue slots are 40 %
+// busy); 32 drafts 258, 64 drafts 508; 12 drafts, 16-bit keys, ragged 8 x 128K 32 us (5.2 TB/s with 5 us
+// of set-up); 5 drafts, 1 x 8K 10.5 us, of which a CTA's work is 5.
 #include "index_cache.cuh"
 #include "launch.cuh"
 #include "ptx.cuh"

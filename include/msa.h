@@ -458,7 +458,8 @@ msa_status msa_index_unpack(const msa_shape* shape, int32_t n_out, const int32_t
  *               index_dim]; idx_draft [batch, n_tokens, index_dim].
  * Products are exact and accumulated in fp32 (bf16 queries of 128 dims against 8-bit keys take
  * three 8-bit parts that hold all of a dim's digits if it is 2^-23 of the query's largest or more;
- * smaller ones are off by at most 2^-31 of the largest; 8-bit keys are below 2^100 in magnitude). */
+ * smaller ones are off by at most 2^-31 of the largest, which is 2^-110 or more; 8-bit keys are below
+ * 2^100 in magnitude). */
 msa_status msa_index_scores_tree(const msa_shape* shape, const int32_t* seq_lens,
                                  const int32_t* block_table, int32_t n_phys, const uint64_t* mask,
                                  const void* idx_q, const void* idx_k, const void* idx_draft,
